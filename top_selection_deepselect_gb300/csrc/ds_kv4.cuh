@@ -1,0 +1,61 @@
+// ds_kv4.cuh -- the 4-bit cache as the kernels see it: record layout, page
+// lookup, conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ds_topk.h"
+
+namespace ds {
+namespace kv4 {
+
+constexpr int kGroup = 32;  // channels that share a scale
+
+__host__ __device__ constexpr int data_bytes(int d) { return d + 4 * (d / kGroup); }
+__host__ __device__ constexpr int record_bytes(int d) { return (data_bytes(d) + 15) / 16 * 16; }
+
+struct Cache {
+    unsigned char *pool;
+    long long page_stride;
+    const int32_t *table;
+    long long table_stride;
+    int n_pages, page_size, kv_heads, max_seqs, max_pages;
+};
+
+// Token slot (page * page_size + offset) of position `pos` of sequence `seq`,
+// or -1 where the sequence, the position or the page is out of range.
+__device__ __forceinline__ int token_slot(const Cache &c, int seq, int pos)
+{
+    if ((unsigned)seq >= (unsigned)c.max_seqs || pos < 0)
+        return -1;
+    const int col = pos / c.page_size;
+    if (col >= c.max_pages)
+        return -1;
+    const int page = __ldg(c.table + seq * c.table_stride + col);
+    if ((unsigned)page >= (unsigned)c.n_pages)
+        return -1;
+    return page * c.page_size + (pos - col * c.page_size);
+}
+
+// Byte offset of the record of (slot, head) in the pool: 64 bits, a pool may
+// be hundreds of gigabytes.
+template <int D>
+__device__ __forceinline__ long long record_offset(const Cache &c, int slot, int head)
+{
+    const int page = slot / c.page_size;
+    return page * c.page_stride +
+           ((long long)head * c.page_size + (slot - page * c.page_size)) * record_bytes(D);
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_float(float &y, float x) { y = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16 &y, float x) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_float(__half &y, float x) { y = __float2half_rn(x); }
+
+}  // namespace kv4
+}  // namespace ds

@@ -14,14 +14,13 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "ds_host.h"
 #include "ds_stream.cuh"
 
 // ===========================================================================
 // Host side: argument checks, launch planning, C ABI.
 // ===========================================================================
-namespace {
-
-using ds::Params;
+namespace ds {
 
 thread_local char g_detail[512];
 
@@ -38,6 +37,16 @@ int fail_cuda(cudaError_t e, const char *what)
 {
     return fail(DS_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+}  // namespace ds
+
+namespace {
+
+using ds::Params;
+
+using ds::fail;
+using ds::fail_cuda;
+using ds::g_detail;
 
 struct ClusterFit {
     const void *fn;
