@@ -165,7 +165,7 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
         return fail(DS_EINVAL, "bytes must be non-NULL");
     if ((rc = sm_count(&sms)) != DS_OK)
         return rc;
-    *bytes = ds::kv4::attention_workspace(c, cache->head_dim, batch, queries, heads, k, sms);
+    *bytes = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
     return DS_OK;
 }
 
@@ -195,7 +195,7 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
         return fail(DS_EINVAL, "q must be aligned to its elements and out to 16 bytes");
     if ((rc = sm_count(&sms)) != DS_OK)
         return rc;
-    const size_t need = ds::kv4::attention_workspace(c, cache->head_dim, batch, queries, heads, k, sms);
+    const size_t need = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
     if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
         return fail(DS_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)",
                     need, workspace_bytes);

@@ -32,8 +32,7 @@ struct Attend {
     int bf16;        // 1: q and out are bf16, 0: fp16
 };
 
-size_t attention_workspace(const Cache &c, int head_dim, int batch, int queries, int heads, int k,
-                           int sms);
+size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads, int k, int sms);
 cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int sms,
                              cudaStream_t stream);
 
