@@ -232,6 +232,15 @@ def test_size_of_the_queries(ds, size, scale):
     check_attention(ds, q, "bf16", pool, table, lengths, scale=scale)
 
 
+def test_a_scale_of_zero_is_the_mean(ds):
+    rng = np.random.default_rng(4)
+    lengths = np.array([45, 7], dtype=np.int32)
+    table, n_pages = make_table(rng, lengths, 16, wide=3)
+    pool = random_pool(rng, n_pages, 1, 16, 64)
+    q = rng.standard_normal((2, 2, 4, 64)).astype(np.float32)
+    check_attention(ds, q, "bf16", pool, table, lengths, scale=0.0)
+
+
 def test_what_is_masked_is_not_read_into_the_result(ds):
     """NaN records past the ends, in free pages and at unlisted positions leave no trace."""
     rng = np.random.default_rng(5)

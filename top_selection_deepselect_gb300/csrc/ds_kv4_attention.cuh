@@ -79,7 +79,6 @@ struct Shape {
     static constexpr int kMT = D == 256 ? 1 : 2;                // 16-token steps of a tile
     static constexpr int kTile = 16 * kMT;
     static constexpr int kRecord = record_bytes(D);
-    static constexpr int kPieces = kRecord / 16;
     // Distance of records in shared memory: the operand loads of a warp then
     // touch every bank once.
     static constexpr int kStride = D == 256 ? kRecord + 16 : kRecord;
@@ -96,8 +95,9 @@ struct Shape {
     static constexpr int kOffQ = kAttendWarps * kWarpBytes;            // query operands
     static constexpr int kOffFactor = kOffQ + kGroups * 2 * NT * 32 * 8;
     static constexpr int kOffLimit = kOffFactor + kRows * 4;
-    static constexpr int kOffMask = kOffLimit + kRows * 4;
-    static constexpr int kOffScan = kOffMask + kAttendWarps * kStages * 4;
+    static constexpr int kOffBarrier = (kOffLimit + kRows * 4 + 15) / 16 * 16;
+    static constexpr int kOffMask = kOffBarrier + kAttendWarps * kStages * 8;
+    static constexpr int kOffScan = (kOffMask + kAttendWarps * kStages * 4 + 15) / 16 * 16;
     static constexpr int kSmem = (kOffScan + 16 * 8 + 15) / 16 * 16;
     static constexpr int kPartial = kRows * (D + 2);                   // floats of a partial result
 };
@@ -107,16 +107,58 @@ struct AttendArgs {
     Attend a;
     Divider by_page;
     long long sel_tiles;  // tiles of a unit when tokens are listed
+    int run;              // tokens of a tile that lie side by side in a page, a power of two
     int group;            // query heads of a key/value head
     int rows;             // query rows of a unit before it is cut into blocks
     int blocks;           // blocks of kRows rows
     int units;            // units of a batch entry
 };
 
+__device__ __forceinline__ uint32_t shared_address(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// Arrival barriers of the rings: one arrival (lane 0's, with the bytes to
+// come) and the bytes themselves complete a phase.
+__device__ __forceinline__ void barrier_init(uint32_t bar)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void barrier_expect(uint32_t bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Whether the phase ended; gives up after kPatience tries (far beyond any
+// copy's time), so that a copy that never ends cannot hang the GPU.
+constexpr int kPatience = 1 << 20;
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, unsigned phase)
+{
+    for (int i = 0; i < kPatience; ++i) {
+        unsigned done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
+// Asynchronous copy of `bytes` (a multiple of 16) from global to shared memory.
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, unsigned bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -337,7 +379,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u,
         odd = __any_sync(~0u, odd);
         int up = most > 0.f && !odd ? 14 - ((int)(__float_as_uint(most) >> 23) - 127) : 0;
         up = up > 100 ? 100 : up;
-        const float lift = __uint_as_float((unsigned)(up + 127) << 23);
+        const float lift = copysignf(__uint_as_float((unsigned)(up + 127) << 23), p.a.scale);
 #pragma unroll
         for (int e = 0; e < kMine; ++e) {
             const int d = lane * kMine + e, w = d / 8, n = d % 8;
@@ -346,8 +388,8 @@ __device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u,
                 __float2half_rn(x[e] * lift * (reg ? 0.0625f : 1.f));
         }
         if (lane == 0) {
-            // score in base-2 units = sum * factor
-            factor[r] = ldexpf(p.a.scale * 1.4426950408889634f, 24 - up);
+            // score in base-2 units = sum * factor, which is not negative
+            factor[r] = ldexpf(fabsf(p.a.scale) * 1.4426950408889634f, 24 - up);
             const int see = u.len - p.a.queries + 1 + j;
             limit[r] = in && see > 0 ? see : 0;
         }
@@ -373,6 +415,19 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     auto wsum = [&](int w, int r) -> float & {
         return *reinterpret_cast<float *>(smem + w * S::kWarpBytes + S::kOffSum + r * 4);
     };
+
+    // state of the warp's ring: the stage filled and the one used next, the
+    // phase of the latter; lost: a copy did not arrive, the results become NaN
+    const uint32_t barriers = shared_address(smem + S::kOffBarrier) + warp * S::kStages * 8;
+    int fill = 0, use = 0;
+    unsigned phase = 0;
+    bool lost = false;
+    if (lane == 0) {
+        for (int s = 0; s < S::kStages; ++s)
+            barrier_init(barriers + s * 8);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
 
     dependent_grid_wait();
     allow_dependent_grid();
@@ -431,30 +486,30 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         auto page_of = [&](int pos) -> int {
             return pos >= 0 ? __ldg(row_table + p.by_page(pos)) : -1;
         };
-        auto issue = [&](int i, int pos, int page) {
-            const int slot = i % S::kStages;
-            unsigned char *dst = ring + slot * S::kStageBytes;
+        // Copies the records of a tile: a lane each, or, where `run` neighbours
+        // lie side by side in a page, one lane for all of them.  A run's tokens
+        // past the sequence's end are in the page too; the mask leaves them out.
+        auto issue = [&](int pos, int page) {
+            const uint32_t bar = barriers + fill * 8, dst = shared_address(ring + fill * S::kStageBytes);
             const bool ok = (unsigned)page < (unsigned)p.c.n_pages;   // page is -1 where pos is
-            const unsigned mask = __ballot_sync(~0u, ok);
-            if (lane == 0)
-                masks[slot] = mask;
-            // Source of a 16-byte piece c of the tile is that of its record
-            // plus the rest of c: src + 16 c with the record's start moved back.
-            const int in_page = pos - p.by_page(pos < 0 ? 0 : pos) * p.c.page_size;
-            const long long src = ok ? page * p.c.page_stride + (long long)(in_page - lane) * S::kRecord : 0;
-            const unsigned lo = (unsigned)src, hi = (unsigned)(src >> 32);
-#pragma unroll
-            for (int it = 0; it < S::kTile * S::kPieces / 32 + (S::kTile * S::kPieces % 32 != 0); ++it) {
-                const int c = it * 32 + lane, rec = c / S::kPieces;
-                const unsigned slo = __shfl_sync(~0u, lo, rec & 31), shi = __shfl_sync(~0u, hi, rec & 31);
-                if (c < S::kTile * S::kPieces && mask >> rec & 1) {
-                    const long long from = (long long)((unsigned long long)shi << 32 | slo) + c * 16;
-                    cp_async16((uint32_t)__cvta_generic_to_shared(dst + c * 16 + rec * (S::kStride - S::kRecord)),
-                               head_pool + from);
-                }
+            const bool leads = ok && (lane & (p.run - 1)) == 0;
+            const unsigned mask = __ballot_sync(~0u, ok), leaders = __ballot_sync(~0u, leads);
+            if (lane == 0) {
+                masks[fill] = mask;
+                barrier_expect(bar, __popc(leaders) * p.run * S::kRecord);
             }
+            __syncwarp();
+            if (leads) {
+                const int in_page = pos - p.by_page(pos) * p.c.page_size;
+                copy_bulk(dst + lane * S::kStride,
+                          head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
+                          p.run * S::kRecord, bar);
+            }
+            fill = fill + 1 == S::kStages ? 0 : fill + 1;
         };
 
+        // the ring held the last unit's results
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         int pos_next, page_next;
         {
             int pos[S::kStages], page[S::kStages];
@@ -467,8 +522,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
                 if (s < mine)
-                    issue(s, pos[s], page[s]);
-                cp_async_commit();
+                    issue(pos[s], page[s]);
             }
             pos_next = pos[S::kStages - 1];
             page_next = page[S::kStages - 1];
@@ -566,7 +620,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[mt][nt][e] *= fac[nt][e & 1];
                         if (kMasked && !there(mt, e, nt))
                             sc[mt][nt][e] = -INFINITY;
                         best[nt][e & 1] = fmaxf(best[nt][e & 1], sc[mt][nt][e]);
@@ -584,7 +637,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         b = fmaxf(b, __shfl_xor_sync(~0u, b, 4));
                         b = fmaxf(b, __shfl_xor_sync(~0u, b, 8));
                         b = fmaxf(b, __shfl_xor_sync(~0u, b, 16));
-                        const float down = top[nt][c] == b ? 1.f : exp2_fast(top[nt][c] - b);
+                        const float down =
+                            top[nt][c] == -INFINITY ? 0.f : exp2_fast((top[nt][c] - b) * fac[nt][c]);
                         top[nt][c] = b;
                         sum[nt][c] *= down;
 #pragma unroll
@@ -596,6 +650,12 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             }
                     }
             }
+            float low[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    low[nt][c] = top[nt][c] == -INFINITY ? 0.f : top[nt][c] * fac[nt][c];
             // probabilities, times the value scales, as operands; then the values
 #pragma unroll
             for (int mt = 0; mt < S::kMT; ++mt) {
@@ -608,8 +668,9 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float m = top[nt][e & 1] == -INFINITY ? 0.f : top[nt][e & 1];
-                        pr[nt][e] = exp2_fast(sc[mt][nt][e] - m);
+                        pr[nt][e] = exp2_fast(sc[mt][nt][e] * fac[nt][e & 1] - low[nt][e & 1]);
+                        if (kMasked && !there(mt, e, nt))
+                            pr[nt][e] = 0.f;
                         sum[nt][e & 1] += pr[nt][e];
                     }
                 const unsigned char *va = tile + (mt * 16 + tok_a) * S::kStride + D / 2;
@@ -657,27 +718,29 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         };
 
         for (int i = 0; i < mine; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+            // every lane is done with the stage that is filled next
             __syncwarp();
             if (i + S::kStages - 1 < mine)
-                issue(i + S::kStages - 1, pos_next, page_next);
-            cp_async_commit();
+                issue(pos_next, page_next);
             pos_next = pos_after;
             page_next = page_of(pos_next);
             pos_after = position(i + S::kStages + 1);
 
-            const int slot = i % S::kStages;
-            const unsigned mask = masks[slot];
+            const unsigned mask = masks[use];
+            const bool came = barrier_wait(barriers + use * 8, phase);
+            const unsigned char *data = ring + use * S::kStageBytes;
+            if (++use == S::kStages)
+                use = 0, phase ^= 1;
+            if (!came)
+                lost = true;
             const long long tile = tile0 + warp + (long long)i * kAttendWarps;
             const int base = kListed ? 0 : (int)(tile * S::kTile);
-            const unsigned char *data = ring + slot * S::kStageBytes;
             if (mask == (S::kTile == 32 ? ~0u : (1u << (S::kTile & 31)) - 1) &&
                 (kListed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
             else if (mask)
                 consume(std::true_type{}, data, mask, base);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
 
         // ---- the warps' results, side by side in the rings' place ----------
@@ -685,13 +748,13 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float s = sum[nt][c];
+                float s = lost ? __int_as_float(0x7fffffff) : sum[nt][c];
                 s += __shfl_xor_sync(~0u, s, 4);
                 s += __shfl_xor_sync(~0u, s, 8);
                 s += __shfl_xor_sync(~0u, s, 16);
                 const int r = nt * 8 + 2 * t + c;
                 if (g == 0) {
-                    wmax(warp, r) = top[nt][c];
+                    wmax(warp, r) = top[nt][c] == -INFINITY ? -INFINITY : top[nt][c] * fac[nt][c];
                     wsum(warp, r) = s;
                 }
                 float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride + 4 * g;
@@ -906,6 +969,10 @@ cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t st
     p.a = a;
     p.by_page.set(c.page_size);
     p.group = a.heads / c.kv_heads;
+    p.run = 1;
+    if (!a.indices && Shape<D, 1>::kStride == Shape<D, 1>::kRecord)
+        while (p.run < Shape<D, 1>::kTile && c.page_size % (2 * p.run) == 0)
+            p.run *= 2;
     p.rows = a.indices ? p.group : p.group * a.queries;
     const int nt = row_tiles<D>(p.rows);
     if (a.indices)
