@@ -5,16 +5,15 @@
 // codes into operands and the softmax cost few instructions, so everything
 // here is laid out for that.
 //
-// Codes become operands with one AND.  A code u (0..15) in the low bits of a
-// 16-bit half is the fp16 subnormal u 2^-24, in bits 4..7 it is u 2^-20; the
-// tensor cores take subnormals exactly.  A word of eight codes gives four
-// operand registers with four ANDs and one shift, no conversion.  The factors
-// 2^-24 and 2^-20 are powers of two: the query (2^-4 where the code stands
-// high) and the epilogue take them back.  What u stands for is u - 8; one packed
-// addition per operand register makes it that, exactly (subnormals again).
-// Starting the accumulator at -8 sum(q) instead would save the addition for
-// keys, but the matrix unit cuts addends off below the largest one: scores were
-// off by up to 2^-17 of the sum of their terms' sizes, which is too much.
+// Codes become operands with one logical operation and one packed addition.  A
+// code u (0..15) in the low bits of an fp16 of value 1024 makes it 1024 + u, in
+// bits 4..7 it makes it 1024 + 16 u; subtracting 1032 or 1152 leaves u - 8 or
+// 16 (u - 8), exactly.  A word of eight codes gives four operand registers with
+// one shift and four of each, no conversion.  The factor 16 is taken back by
+// the query (2^-4 there) and the epilogue.  Without the addition, on the fp16
+// subnormals u 2^-24 and with -8 sum(q) as the accumulator's start, scores were
+// off by up to 2^-17 of the sum of their terms' sizes: the matrix unit aligns
+// its addends by exponent and cuts them off below the largest one.
 //
 // Both products have tokens or channels as the 16 rows and up to 8 (query,
 // head) rows of one key/value head as the 8 columns of m16n8k16:
@@ -178,12 +177,20 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// u 2^-24 - 8 2^-24 (codes in the low bits of each half), and 16 times that.
-constexpr uint32_t kEight = 0x80088008u, kEight16 = 0x80808080u;
-__device__ __forceinline__ uint32_t minus8(uint32_t x, uint32_t eight)
+// u - 8 of the codes in the low four bits of each half, and 16 (u - 8) of those
+// in the four bits above.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w)
 {
-    uint32_t y;
-    asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(eight));
+    uint32_t x, y;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x) : "r"(w));  // (w & mask) | 1024
+    asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xe408e408u));         // - 1032
+    return y;
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w)
+{
+    uint32_t x, y;
+    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
+    asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xe480e480u));         // - 1152
     return y;
 }
 
@@ -272,55 +279,70 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
     return all;
 }
 
-// All tiles of the call.
-template <int kTile, bool kListed>
-__device__ __forceinline__ long long all_tiles(const AttendArgs &p, long long *scratch)
-{
-    if (kListed)
-        return p.sel_tiles * p.units * p.a.batch;
-    long long all = 0, before;
-    for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
-        const int b = b0 + threadIdx.x;
-        all += scan_cta(b < p.a.batch ? tiles_of<kTile, kListed>(p, b) * p.units : 0, &before, scratch);
-    }
-    return all;
-}
+// The line of work: each unit takes kUnitCost places and one for each of its
+// tiles.  A unit's start and end (its queries, the first copies' latency, the
+// meeting of the warps) cost a CTA as much as some tiles do; without these
+// places the CTA that met 24 empty sequences in a row took four times as long
+// as the others.
+constexpr int kUnitCost = 12;
 
-// Tiles that each of `ctas` CTAs takes: two a warp at least where there is
-// little, so that a CTA's start and its join are shared.
-__device__ __forceinline__ long long tiles_per_cta(long long all, int ctas)
+// Places of the line for each of `ctas` CTAs: two tiles a warp at least, so
+// that there are not more parts to join than the work is worth.
+__device__ __forceinline__ long long places_per_cta(long long all, int ctas)
 {
     const long long even = (all + ctas - 1) / ctas;
     return even > 2 * kAttendWarps ? even : 2 * kAttendWarps;
 }
 
-// Batch entry that tile x of the line belongs to, and the entry's first tile.
+// The line's length and, for batch entry `entry`, its first place; with entry
+// < 0 the entry that place `per * cta` belongs to and that one's first place.
+struct Line {
+    long long all, per, first;
+    int entry;
+};
+
 template <int kTile, bool kListed>
-__device__ __forceinline__ void locate(const AttendArgs &p, long long x, int *entry, long long *first,
-                                       long long *scratch)
+__device__ __forceinline__ Line line_of(const AttendArgs &p, int ctas, int cta, int entry,
+                                        long long *scratch)
 {
+    Line n;
     if (kListed) {
-        const long long each = p.sel_tiles * p.units;
-        *entry = (int)(x / each);
-        *first = *entry * each;
-        return;
+        const long long each = (p.sel_tiles + kUnitCost) * p.units;
+        n.all = each * p.a.batch;
+        n.per = places_per_cta(n.all, ctas);
+        n.entry = entry >= 0 ? entry : (int)(n.per * cta / each);
+        n.first = n.entry * each;
+        return n;
     }
-    long long at = 0, before;
+    const bool once = p.a.batch <= (int)blockDim.x;   // then one scan answers both
+    long long mine = 0, before = 0;
+    n.all = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
-        const long long mine = b < p.a.batch ? tiles_of<kTile, kListed>(p, b) * p.units : 0;
-        const long long sum = scan_cta(mine, &before, scratch);
-        if (x >= at + before && x < at + before + mine) {
-            scratch[8] = b;
-            scratch[9] = at + before;
-        }
-        __syncthreads();
-        at += sum;
-        if (x < at)
-            break;
+        mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
+        n.all += scan_cta(mine, &before, scratch);
     }
-    *entry = (int)scratch[8];
-    *first = scratch[9];
+    n.per = places_per_cta(n.all, ctas);
+    const long long x = n.per * cta;
+    long long at = 0;
+    for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        long long sum = n.all;
+        if (!once) {
+            mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
+            sum = scan_cta(mine, &before, scratch);
+        }
+        const long long mine0 = at + before;
+        if (entry >= 0 ? b == entry : x >= mine0 && x < mine0 + mine) {
+            scratch[8] = b;
+            scratch[9] = mine0;
+        }
+        at += sum;
+    }
+    __syncthreads();
+    n.entry = (int)scratch[8];
+    n.first = scratch[9];
+    return n;
 }
 
 // Which rows of q a unit's block covers.
@@ -389,7 +411,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u,
         }
         if (lane == 0) {
             // score in base-2 units = sum * factor, which is not negative
-            factor[r] = ldexpf(fabsf(p.a.scale) * 1.4426950408889634f, 24 - up);
+            factor[r] = ldexpf(fabsf(p.a.scale) * 1.4426950408889634f, -up);
             const int see = u.len - p.a.queries + 1 + j;
             limit[r] = in && see > 0 ? see : 0;
         }
@@ -432,15 +454,12 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     dependent_grid_wait();
     allow_dependent_grid();
 
-    const long long all = all_tiles<S::kTile, kListed>(p, scratch);
-    const long long per = tiles_per_cta(all, gridDim.x);
-    long long x = per * blockIdx.x;
-    const long long end = x + per < all ? x + per : all;
+    const Line line = line_of<S::kTile, kListed>(p, gridDim.x, blockIdx.x, -1, scratch);
+    long long x = line.per * blockIdx.x, first = line.first;
+    const long long end = x + line.per < line.all ? x + line.per : line.all;
     if (x >= end)
         return;
-    int entry;
-    long long first;
-    locate<S::kTile, kListed>(p, x, &entry, &first, scratch);
+    int entry = line.entry;
 
     // Tokens of the rows of the operands: row r of a 16-token step is token
     // tok(r) of it, rows 8..15 the tokens after those of rows 0..7; an order
@@ -449,12 +468,21 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     const int tok_a = 2 * t, tok_b = 8 + ((2 * t + 4) & 7);
 
     while (x < end) {
-        const long long tiles = tiles_of<S::kTile, kListed>(p, entry);
-        const long long at = x - first;
-        const int u_in = (int)(at / tiles);
-        const long long tile0 = at - u_in * tiles;
-        const long long count = tiles - tile0 < end - x ? tiles - tile0 : end - x;
+        // the part of the unit at x that is this CTA's
+        const long long tiles = tiles_of<S::kTile, kListed>(p, entry), each = tiles + kUnitCost;
+        const int u_in = (int)((x - first) / each);
+        const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
+        const long long tile0 = x > zero ? x - zero : 0;
+        const long long stop = zero + tiles < end ? zero + tiles : end;
+        const long long count = stop - zero - tile0;
         const Unit u(p, kListed, entry, u_in, S::kRows);
+        x = zero + tiles;
+        if (x - first == each * p.units) {
+            first = x;
+            ++entry;
+        }
+        if (count <= 0)
+            break;      // only the unit's first places: its tiles are the next CTA's
 
         if (p.a.bf16)
             load_queries<D, NT, __nv_bfloat16>(p, u, smem);
@@ -471,16 +499,16 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         const unsigned char *head_pool =
             p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
 
+        // tokens and list entries are below 2^31; the last tile may end above
+        const unsigned e0 = (unsigned)((tile0 + warp) * S::kTile) + lane;
         // position of this lane's token of the warp's tile i, -1: none
         auto position = [&](int i) -> int {
             if (i >= mine || lane >= S::kTile)
                 return -1;
-            const long long e = (tile0 + warp + (long long)i * kAttendWarps) * S::kTile + lane;
-            int pos = -1;
-            if (!kListed)
-                pos = e < seen ? (int)e : -1;
-            else if (e < p.a.k)
-                pos = __ldg(list + e);
+            const unsigned e = e0 + i * (kAttendWarps * S::kTile);
+            int pos = (int)e;
+            if (kListed)
+                pos = e < (unsigned)p.a.k ? __ldg(list + e) : -1;
             return pos < seen ? pos : -1;
         };
         auto page_of = [&](int pos) -> int {
@@ -582,14 +610,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     for (int i = 0; i < S::kPer; ++i) {
                         const int group = st * S::kPer + i;
                         const uint32_t ha = wa[i] >> 8, hb = wb[i] >> 8;
-                        const uint32_t a00 = minus8(wa[i] & 0x000f000fu, kEight);
-                        const uint32_t a01 = minus8(wb[i] & 0x000f000fu, kEight);
-                        const uint32_t a02 = minus8(wa[i] & 0x00f000f0u, kEight16);
-                        const uint32_t a03 = minus8(wb[i] & 0x00f000f0u, kEight16);
-                        const uint32_t a10 = minus8(ha & 0x000f000fu, kEight);
-                        const uint32_t a11 = minus8(hb & 0x000f000fu, kEight);
-                        const uint32_t a12 = minus8(ha & 0x00f000f0u, kEight16);
-                        const uint32_t a13 = minus8(hb & 0x00f000f0u, kEight16);
+                        const uint32_t a00 = low_codes(wa[i]);
+                        const uint32_t a01 = low_codes(wb[i]);
+                        const uint32_t a02 = high_codes(wa[i]);
+                        const uint32_t a03 = high_codes(wb[i]);
+                        const uint32_t a10 = low_codes(ha);
+                        const uint32_t a11 = low_codes(hb);
+                        const uint32_t a12 = high_codes(ha);
+                        const uint32_t a13 = high_codes(hb);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint2 *qf = reinterpret_cast<const uint2 *>(smem + S::kOffQ) +
@@ -690,14 +718,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], pick);
                         const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], pick);
                         const uint32_t z8 = z >> 8, y8 = y >> 8;
-                        const uint32_t a00 = minus8(z & 0x000f000fu, kEight);
-                        const uint32_t a01 = minus8(z & 0x00f000f0u, kEight16);
-                        const uint32_t a02 = minus8(y & 0x000f000fu, kEight);
-                        const uint32_t a03 = minus8(y & 0x00f000f0u, kEight16);
-                        const uint32_t a10 = minus8(z8 & 0x000f000fu, kEight);
-                        const uint32_t a11 = minus8(z8 & 0x00f000f0u, kEight16);
-                        const uint32_t a12 = minus8(y8 & 0x000f000fu, kEight);
-                        const uint32_t a13 = minus8(y8 & 0x00f000f0u, kEight16);
+                        const uint32_t a00 = low_codes(z);
+                        const uint32_t a01 = high_codes(z);
+                        const uint32_t a02 = low_codes(y);
+                        const uint32_t a03 = high_codes(y);
+                        const uint32_t a10 = low_codes(z8);
+                        const uint32_t a11 = high_codes(z8);
+                        const uint32_t a12 = low_codes(y8);
+                        const uint32_t a13 = high_codes(y8);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float w[4];
@@ -733,8 +761,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 use = 0, phase ^= 1;
             if (!came)
                 lost = true;
-            const long long tile = tile0 + warp + (long long)i * kAttendWarps;
-            const int base = kListed ? 0 : (int)(tile * S::kTile);
+            const int base = kListed ? 0 : (int)(e0 - lane + i * (kAttendWarps * S::kTile));
             if (mask == (S::kTile == 32 ? ~0u : (1u << (S::kTile & 31)) - 1) &&
                 (kListed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
@@ -761,8 +788,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
                 for (int i = 0; i < S::kGroups; ++i)
                     *reinterpret_cast<float4 *>(dst + i * kGroup) =
-                        make_float4(o[i][0][nt][c] * 16777216.f, o[i][0][nt][c + 2] * 1048576.f,
-                                    o[i][1][nt][c] * 16777216.f, o[i][1][nt][c + 2] * 1048576.f);
+                        make_float4(o[i][0][nt][c], o[i][0][nt][c + 2] * 0.0625f,
+                                    o[i][1][nt][c], o[i][1][nt][c + 2] * 0.0625f);
             }
         __syncthreads();
 
@@ -832,12 +859,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
         }
         __syncthreads();
-
-        x += count;
-        if (x - first == tiles * p.units) {
-            first = x;
-            ++entry;
-        }
     }
 }
 
@@ -850,35 +871,21 @@ join_kernel(const __grid_constant__ AttendArgs p, int ctas)
     using S = Shape<D, NT>;
     __shared__ long long scratch[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    dependent_grid_wait();
     // blocks of 8 rows of a unit
     const long long unit = blockIdx.x / NT;
-    const int entry = (int)(unit / p.units), u_in = (int)(unit % p.units);
-    long long all = 0, first = 0;
-    if (kListed) {
-        all = p.sel_tiles * p.units * p.a.batch;
-        first = p.sel_tiles * p.units * entry;
-    } else {
-        for (int b0 = 0; b0 < p.a.batch; b0 += kAttendThreads) {
-            const int b = b0 + threadIdx.x;
-            long long before;
-            const long long mine = b < p.a.batch ? tiles_of<S::kTile, kListed>(p, b) * p.units : 0;
-            const long long sum = scan_cta(mine, &before, scratch);
-            if (b == entry)
-                scratch[8] = all + before;
-            all += sum;
-        }
-        __syncthreads();
-        first = scratch[8];
-    }
-    const long long per = tiles_per_cta(all, ctas);
-    const long long tiles = tiles_of<S::kTile, kListed>(p, entry);
-    const long long from = first + u_in * tiles;
+    const int u_in = (int)(unit % p.units);
+    const Line line = line_of<S::kTile, kListed>(p, ctas, 0, (int)(unit / p.units), scratch);
+    const int entry = line.entry;
+    const long long per = line.per, tiles = tiles_of<S::kTile, kListed>(p, entry);
+    const long long from = line.first + u_in * (tiles + kUnitCost) + kUnitCost;
     const long long c0 = from / per, c1 = (from + tiles - 1) / per;
     const int r = blockIdx.x % NT * 8 + warp;
     const Unit u(p, kListed, entry, u_in, S::kRows);
     if (c0 == c1 || r >= u.rows)
         return;
+    // Up to here only what the launch before the attention left is read: this
+    // launch starts when that one has been waited for.
+    dependent_grid_wait();
     // a CTA's second place holds the unit that begins in it
     auto place = [&](long long c) { return p.a.partial + (c * 2 + (c == c0)) * S::kPartial; };
     float m = -INFINITY;
