@@ -15,19 +15,22 @@
 // off by up to 2^-17 of the sum of their terms' sizes: the matrix unit aligns
 // its addends by exponent and cuts them off below the largest one.
 //
-// Both products have tokens or channels as the 16 rows and up to 8 (query,
-// head) rows of one key/value head as the 8 columns of m16n8k16:
-//   S^T = K Q^T   rows are tokens; for each group of 32 channels the sum is
-//                 multiplied by the token's key scale in 32 bits
-//   O^T = V^T P^T rows are channels; the probabilities carry the value scale
-//                 of (token, group): fp16(p * scale), the only rounding of the
-//                 inner loop.  2^-11 relative on each token's share, less than
-//                 the output's own rounding; 32-bit operands would halve the
-//                 rate of the matrix instructions.  Denominators are summed in
-//                 32 bits from unrounded p.
-// The transposition of P between the two is one movmatrix per 8 x 8.  m64+ tile
-// instructions (tcgen05) would leave 7/8 of their rows empty at 8 query rows and
-// need the operands written back to shared memory after the expansion.
+// A unit is up to kRows (query, head) rows that share a key/value head.  With 8
+// rows the matrix instructions (m16n8k16) have tokens or channels as their 16
+// rows and the query rows as their 8 columns:
+//   S^T = K Q^T,  O^T = V^T P^T
+// and P is transposed between the two by a movmatrix per 8 x 8.  With 16 or 32
+// rows (grouped heads, drafted tokens) the query rows are the 16 rows instead,
+//   S = Q K^T,  O = P V
+// the same number of instructions for 16 rows, and P comes out as it goes in.
+// Either way the sum over each group of 32 channels is multiplied by the key
+// scale of (token, group) in 32 bits, and the probabilities carry the value
+// scale: fp16(p * scale), the only rounding of the inner loop.  2^-11 relative on
+// each token's share, less than the output's own rounding; 32-bit operands
+// would halve the rate of the matrix instructions.  Denominators are summed in
+// 32 bits from unrounded p.  Instructions on 64 and more rows (tcgen05) would
+// leave most of them empty and need the operands written back to shared memory
+// after the expansion.
 //
 // Work is cut into tiles of kTile tokens; all tiles of all (sequence, head)
 // units stand in one line that is divided evenly among the CTAs, whatever the
@@ -47,9 +50,6 @@
 namespace ds {
 namespace kv4 {
 
-constexpr int kAttendWarps = 8;
-constexpr int kAttendThreads = kAttendWarps * 32;
-
 // Quotient by a fixed divisor of numbers below 2^31.
 struct Divider {
     unsigned mul;
@@ -68,37 +68,54 @@ struct Divider {
     }
 };
 
-// Shape of one instantiation.
-template <int D, int NT>
+// Shape of one instantiation: head dimension, query rows of a unit (8, 16, 32).
+template <int D, int Rows>
 struct Shape {
+    static constexpr bool kWide = Rows > 8;                      // query rows are the operands' rows
+    static constexpr int kRows = Rows;
+    static constexpr int kBlocks = kWide ? Rows / 16 : 1;        // row blocks of an instruction
+    static constexpr int kSubs = kWide ? 4 : 2;                  // instructions of a group's values
     static constexpr int kGroups = D / kGroup;
-    static constexpr int kStretches = D > 128 ? D / 128 : 1;   // of up to 128 channels
-    static constexpr int kPer = kGroups / kStretches;           // groups of a stretch
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kMT = D == 256 ? 1 : 2;                // 16-token steps of a tile
+    static constexpr int kStretches = D > 128 ? D / 128 : 1;    // of up to 128 channels
+    static constexpr int kPer = kGroups / kStretches;            // groups of a stretch
+    static constexpr int kMT = D == 256 ? 1 : 2;                 // 16-token steps of a tile
     static constexpr int kTile = 16 * kMT;
     static constexpr int kRecord = record_bytes(D);
-    // Distance of records in shared memory: the operand loads of a warp then
-    // touch every bank once.
-    static constexpr int kStride = D == 256 ? kRecord + 16 : kRecord;
-    static constexpr int kStageBytes = kTile * kStride;
-    static constexpr bool kTwoCtas = D * NT <= 256;             // output registers of a thread: D NT / 4
-    static constexpr int kStages = D == 64 ? 4 : D == 128 ? (kTwoCtas ? 3 : 5) : (kTwoCtas ? 2 : 4);
-    static constexpr int kOutStride = D + 4;                    // floats of an output row in shared memory
+    static constexpr int kStageBytes = kTile * kRecord;
+    static constexpr int kOutRegs = kGroups * kSubs * kBlocks * 4;
+    // Warps of a CTA and CTAs of an SM, by what the output leaves of the
+    // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.
+    static constexpr int kWarps = kOutRegs == 64 ? 12 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? (kCtas == 2 ? 4 : 6) : kCtas == 2 ? 3 : kWarps == 12 ? 4 : 5;
+    static constexpr int kOutStride = D + 4;                     // floats of an output row in shared memory
     // A warp's ring; at a unit's end its output, the rows' maxima and sums.
     static constexpr int kOffMax = kRows * kOutStride * 4;
     static constexpr int kOffSum = kOffMax + kRows * 4;
     static constexpr int kWarpBytes = kStages * kStageBytes > kOffSum + kRows * 4
                                           ? kStages * kStageBytes : kOffSum + kRows * 4;
     // shared memory behind the rings
-    static constexpr int kOffQ = kAttendWarps * kWarpBytes;            // query operands
-    static constexpr int kOffFactor = kOffQ + kGroups * 2 * NT * 32 * 8;
+    static constexpr int kOffQ = kWarps * kWarpBytes;             // query operands
+    static constexpr int kOffFactor = kOffQ + kRows * D * 2;
     static constexpr int kOffLimit = kOffFactor + kRows * 4;
     static constexpr int kOffBarrier = (kOffLimit + kRows * 4 + 15) / 16 * 16;
-    static constexpr int kOffMask = kOffBarrier + kAttendWarps * kStages * 8;
-    static constexpr int kOffScan = (kOffMask + kAttendWarps * kStages * 4 + 15) / 16 * 16;
-    static constexpr int kSmem = (kOffScan + 16 * 8 + 15) / 16 * 16;
-    static constexpr int kPartial = kRows * (D + 2);                   // floats of a partial result
+    static constexpr int kOffMask = kOffBarrier + kWarps * kStages * 8;
+    static constexpr int kOffScan = (kOffMask + kWarps * kStages * 4 + 15) / 16 * 16;
+    static constexpr int kOffPart = kOffScan + 16 * 8;
+    static constexpr int kSmem = kOffPart + 128;
+    static constexpr int kPartial = kRows * (D + 2);                    // floats of a partial result
+
+    // Order of the 16 tokens of a step in the operands: places 2 t and 2 t + 1
+    // (t < 4) hold tokens even(t) and odd(t), places 8 above hold the tokens
+    // kNext after those.  With records of 80, 144 and 288 bytes the operand
+    // loads of a warp then touch every bank equally often.
+    static constexpr int kNext = D == 256 ? 8 : 1;
+    static __device__ __forceinline__ int even(int t) { return D == 256 ? t : 2 * t; }
+    static __device__ __forceinline__ int odd(int t)
+    {
+        return D == 256 ? 4 + ((t + 2) & 3) : 8 + ((2 * t + 4) & 7);
+    }
 };
 
 struct AttendArgs {
@@ -106,10 +123,11 @@ struct AttendArgs {
     Attend a;
     Divider by_page;
     long long sel_tiles;  // tiles of a unit when tokens are listed
+    long long parts;      // floats of the workspace before the partial results
     int run;              // tokens of a tile that lie side by side in a page, a power of two
     int group;            // query heads of a key/value head
     int rows;             // query rows of a unit before it is cut into blocks
-    int blocks;           // blocks of kRows rows
+    int blocks;           // blocks of kRows rows, a unit each
     int units;            // units of a batch entry
 };
 
@@ -253,8 +271,7 @@ __device__ __forceinline__ long long tiles_of(const AttendArgs &p, int b)
     return n > kTile ? (n + kTile - 1LL) / kTile : 1;
 }
 
-// Sum over the CTA (a power of two of at most 8 warps), and in *before the sum
-// of the threads below.
+// Sum over the CTA, and in *before the sum of the threads below.
 __device__ __forceinline__ long long scan_cta(long long v, long long *before, long long *scratch)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -288,29 +305,29 @@ constexpr int kUnitCost = 12;
 
 // Places of the line for each of `ctas` CTAs: two tiles a warp at least, so
 // that there are not more parts to join than the work is worth.
-__device__ __forceinline__ long long places_per_cta(long long all, int ctas)
+__device__ __forceinline__ long long places_per_cta(long long all, int ctas, int warps)
 {
     const long long even = (all + ctas - 1) / ctas;
-    return even > 2 * kAttendWarps ? even : 2 * kAttendWarps;
+    return even > 2 * warps ? even : 2 * warps;
 }
 
-// The line's length and, for batch entry `entry`, its first place; with entry
-// < 0 the entry that place `per * cta` belongs to and that one's first place.
+// The line's length, places for each CTA, and the batch entry that this CTA's
+// first place belongs to with the entry's own first place.
 struct Line {
     long long all, per, first;
     int entry;
 };
 
 template <int kTile, bool kListed>
-__device__ __forceinline__ Line line_of(const AttendArgs &p, int ctas, int cta, int entry,
-                                        long long *scratch)
+__device__ __forceinline__ Line line_of(const AttendArgs &p, long long *scratch)
 {
     Line n;
+    const int warps = blockDim.x / 32;
     if (kListed) {
         const long long each = (p.sel_tiles + kUnitCost) * p.units;
         n.all = each * p.a.batch;
-        n.per = places_per_cta(n.all, ctas);
-        n.entry = entry >= 0 ? entry : (int)(n.per * cta / each);
+        n.per = places_per_cta(n.all, gridDim.x, warps);
+        n.entry = (int)(n.per * blockIdx.x / each);
         n.first = n.entry * each;
         return n;
     }
@@ -322,8 +339,8 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, int ctas, int cta, 
         mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
         n.all += scan_cta(mine, &before, scratch);
     }
-    n.per = places_per_cta(n.all, ctas);
-    const long long x = n.per * cta;
+    n.per = places_per_cta(n.all, gridDim.x, warps);
+    const long long x = n.per * blockIdx.x;
     long long at = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
@@ -332,31 +349,29 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, int ctas, int cta, 
             mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
             sum = scan_cta(mine, &before, scratch);
         }
-        const long long mine0 = at + before;
-        if (entry >= 0 ? b == entry : x >= mine0 && x < mine0 + mine) {
-            scratch[8] = b;
-            scratch[9] = mine0;
+        if (x >= at + before && x < at + before + mine) {
+            scratch[14] = b;
+            scratch[15] = at + before;
         }
         at += sum;
     }
     __syncthreads();
-    n.entry = (int)scratch[8];
-    n.first = scratch[9];
+    n.entry = (int)scratch[14];
+    n.first = scratch[15];
     return n;
 }
 
-// Which rows of q a unit's block covers.
+// Which query rows unit u of a batch entry covers.
 struct Unit {
-    int b, seq, head, query, row0, len, rows;
-    __device__ __forceinline__ Unit(const AttendArgs &p, bool listed, int entry, int u, int block_rows)
+    int b, head, query, row0, rows;
+    __device__ __forceinline__ Unit() {}
+    __device__ __forceinline__ Unit(const AttendArgs &p, int entry, int u, int block_rows)
     {
         b = entry;
-        seq = sequence_of(p, b);
-        len = length_of(p, seq);
         const int block = u % p.blocks;
         u /= p.blocks;
         head = u % p.c.kv_heads;
-        query = listed ? u / p.c.kv_heads : 0;
+        query = p.a.indices ? u / p.c.kv_heads : 0;
         row0 = block * block_rows;
         rows = p.rows - row0 < block_rows ? p.rows - row0 : block_rows;
     }
@@ -369,19 +384,37 @@ struct Unit {
     }
 };
 
+// What a CTA works on, kept in shared memory so that the loop over tiles has
+// the registers for itself.
+struct Part {
+    const int32_t *list, *row_table;     // listed positions; the sequence's row of the table
+    const unsigned char *head_pool;      // records of the head in page 0
+    long long next, next_first;          // place of the line to go on at, its entry's first place
+    Unit u;
+    int next_entry, seen;                // positions attended are below `seen`
+    int whole, begins;                   // all of the unit's tiles are this CTA's; its first one is
+};
+static_assert(sizeof(Part) <= 128, "room in Shape");
+
+// Left for the join: the unit that begins in a CTA and goes on in others.
+struct alignas(16) Split {
+    int b, unit, parts, pad;
+};
+
 // Query operands of a unit, the rows' factors and limits.  A row is scaled by a
 // power of two to magnitudes of 2^14 to 2^15, so that fp16 holds every bf16 and
 // fp16 value of it (down to 2^-39 of the largest, below which it adds nothing).
-template <int D, int NT, typename T>
-__device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u, unsigned char *smem)
+template <int D, int Rows, typename T>
+__device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u, int len,
+                                             unsigned char *smem)
 {
-    using S = Shape<D, NT>;
+    using S = Shape<D, Rows>;
     constexpr int kMine = D / 32;                  // channels of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     __half *frag = reinterpret_cast<__half *>(smem + S::kOffQ);
     float *factor = reinterpret_cast<float *>(smem + S::kOffFactor);
     int *limit = reinterpret_cast<int *>(smem + S::kOffLimit);
-    for (int r = warp; r < S::kRows; r += kAttendWarps) {
+    for (int r = warp; r < S::kRows; r += S::kWarps) {
         float x[kMine];
         int j = 0, h = 0;
         const bool in = r < u.rows;
@@ -406,23 +439,27 @@ __device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u,
         for (int e = 0; e < kMine; ++e) {
             const int d = lane * kMine + e, w = d / 8, n = d % 8;
             const int group = d / kGroup, t = w % 4, half = n / 4, reg = n % 2, second = n % 4 / 2;
-            frag[((((group * 2 + second) * NT + r / 8) * 32 + r % 8 * 4 + t) * 2 + reg) * 2 + half] =
-                __float2half_rn(x[e] * lift * (reg ? 0.0625f : 1.f));
+            // operand register of the lane that holds row r % 8, place 2 t:
+            // narrow {reg}, wide {reg, row / 8 % 2}
+            const int at = S::kWide ? (((group * 2 + second) * S::kBlocks + r / 16) * 32 + r % 8 * 4 + t) * 4 +
+                                          reg * 2 + r / 8 % 2
+                                    : ((group * 2 + second) * 32 + r * 4 + t) * 2 + reg;
+            frag[at * 2 + half] = __float2half_rn(x[e] * lift * (reg ? 0.0625f : 1.f));
         }
         if (lane == 0) {
             // score in base-2 units = sum * factor, which is not negative
             factor[r] = ldexpf(fabsf(p.a.scale) * 1.4426950408889634f, -up);
-            const int see = u.len - p.a.queries + 1 + j;
+            const int see = len - p.a.queries + 1 + j;
             limit[r] = in && see > 0 ? see : 0;
         }
     }
 }
 
-template <int D, int NT, bool kListed>
-__global__ void __launch_bounds__(kAttendThreads, Shape<D, NT>::kTwoCtas ? 2 : 1)
+template <int D, int Rows, bool kListed>
+__global__ void __launch_bounds__((Shape<D, Rows>::kThreads), (Shape<D, Rows>::kCtas))
 attend_kernel(const __grid_constant__ AttendArgs p)
 {
-    using S = Shape<D, NT>;
+    using S = Shape<D, Rows>;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     long long *scratch = reinterpret_cast<long long *>(smem + S::kOffScan);
@@ -454,65 +491,84 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     dependent_grid_wait();
     allow_dependent_grid();
 
-    const Line line = line_of<S::kTile, kListed>(p, gridDim.x, blockIdx.x, -1, scratch);
-    long long x = line.per * blockIdx.x, first = line.first;
-    const long long end = x + line.per < line.all ? x + line.per : line.all;
-    if (x >= end)
-        return;
-    int entry = line.entry;
+    volatile Part &part = *reinterpret_cast<Part *>(smem + S::kOffPart);
+    Split *split = reinterpret_cast<Split *>(p.a.partial) + blockIdx.x;
+    if (threadIdx.x == 0)
+        split->parts = 0;
 
-    // Tokens of the rows of the operands: row r of a 16-token step is token
-    // tok(r) of it, rows 8..15 the tokens after those of rows 0..7; an order
-    // that spreads the records of a load over all banks.
-    const int tok_row = g & 1 ? 8 + ((g + 3) & 7) : g;
-    const int tok_a = 2 * t, tok_b = 8 + ((2 * t + 4) & 7);
+    long long x, per, end, first;
+    int entry;
+    {
+        const Line line = line_of<S::kTile, kListed>(p, scratch);
+        per = line.per;
+        x = per * blockIdx.x;
+        end = x + per < line.all ? x + per : line.all;
+        first = line.first;
+        entry = line.entry;
+    }
+
+    const int tok_row = g & 1 ? S::odd(g / 2) : S::even(g / 2);   // token at place g
+    const int tok_a = S::even(t), tok_b = S::odd(t);              // at places 2 t and 2 t + 1
 
     while (x < end) {
         // the part of the unit at x that is this CTA's
-        const long long tiles = tiles_of<S::kTile, kListed>(p, entry), each = tiles + kUnitCost;
-        const int u_in = (int)((x - first) / each);
-        const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
-        const long long tile0 = x > zero ? x - zero : 0;
-        const long long stop = zero + tiles < end ? zero + tiles : end;
-        const long long count = stop - zero - tile0;
-        const Unit u(p, kListed, entry, u_in, S::kRows);
-        x = zero + tiles;
-        if (x - first == each * p.units) {
-            first = x;
-            ++entry;
+        int mine;
+        unsigned e0;
+        {
+            const int seq = sequence_of(p, entry), len = length_of(p, seq);
+            const long long tiles = tiles_of<S::kTile, kListed>(p, entry), each = tiles + kUnitCost;
+            const int u_in = (int)((x - first) / each);
+            const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
+            const long long tile0 = x > zero ? x - zero : 0;
+            const long long stop = zero + tiles < end ? zero + tiles : end;
+            const long long count = stop - zero - tile0;
+            if (count <= 0)
+                break;      // only the unit's first places: its tiles are the next CTA's
+            const Unit u(p, entry, u_in, S::kRows);
+            if (threadIdx.x == 0) {
+                part.list = kListed ? p.a.indices + ((long long)entry * p.a.queries + u.query) * p.a.k
+                                    : nullptr;
+                part.row_table =
+                    p.c.table + ((unsigned)seq < (unsigned)p.c.max_seqs ? seq * p.c.table_stride : 0);
+                part.head_pool = p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
+                const bool last = zero + tiles - first == each * p.units;
+                part.next = zero + tiles;
+                part.next_first = last ? zero + tiles : first;
+                part.next_entry = entry + last;
+                part.seen = kListed ? len - p.a.queries + 1 + u.query : len;
+                part.u.b = u.b, part.u.head = u.head, part.u.query = u.query;
+                part.u.row0 = u.row0, part.u.rows = u.rows;
+                part.whole = count == tiles;
+                part.begins = tile0 == 0;
+                if (tile0 == 0 && count < tiles) {
+                    split->b = entry;
+                    split->unit = u_in;
+                    split->parts = (int)((zero + tiles - 1) / per - blockIdx.x) + 1;
+                }
+            }
+            if (p.a.bf16)
+                load_queries<D, Rows, __nv_bfloat16>(p, u, len, smem);
+            else
+                load_queries<D, Rows, __half>(p, u, len, smem);
+            // the warp's tiles: warp, warp + kWarps, ... of `count`
+            mine = count > warp ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
+            // tokens and list entries are below 2^31; the last tile may end above
+            e0 = (unsigned)((tile0 + warp) * S::kTile) + lane;
         }
-        if (count <= 0)
-            break;      // only the unit's first places: its tiles are the next CTA's
+        __syncthreads();   // query operands and `part` are there
 
-        if (p.a.bf16)
-            load_queries<D, NT, __nv_bfloat16>(p, u, smem);
-        else
-            load_queries<D, NT, __half>(p, u, smem);
-
-        // ---- the warp's tiles: warp, warp + 8, ... of `count` -------------
-        const int mine = count > warp ? (int)((count - warp + kAttendWarps - 1) / kAttendWarps) : 0;
-        const int32_t *list = kListed ? p.a.indices + ((long long)u.b * p.a.queries + u.query) * p.a.k
-                                      : nullptr;
-        const int seen = kListed ? u.len - p.a.queries + 1 + u.query : u.len;
-        const int32_t *row_table =
-            p.c.table + ((unsigned)u.seq < (unsigned)p.c.max_seqs ? u.seq * p.c.table_stride : 0);
-        const unsigned char *head_pool =
-            p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
-
-        // tokens and list entries are below 2^31; the last tile may end above
-        const unsigned e0 = (unsigned)((tile0 + warp) * S::kTile) + lane;
         // position of this lane's token of the warp's tile i, -1: none
         auto position = [&](int i) -> int {
             if (i >= mine || lane >= S::kTile)
                 return -1;
-            const unsigned e = e0 + i * (kAttendWarps * S::kTile);
+            const unsigned e = e0 + i * (S::kWarps * S::kTile);
             int pos = (int)e;
             if (kListed)
-                pos = e < (unsigned)p.a.k ? __ldg(list + e) : -1;
-            return pos < seen ? pos : -1;
+                pos = e < (unsigned)p.a.k ? __ldg(part.list + e) : -1;
+            return pos < part.seen ? pos : -1;
         };
         auto page_of = [&](int pos) -> int {
-            return pos >= 0 ? __ldg(row_table + p.by_page(pos)) : -1;
+            return pos >= 0 ? __ldg(part.row_table + p.by_page(pos)) : -1;
         };
         // Copies the records of a tile: a lane each, or, where `run` neighbours
         // lie side by side in a page, one lane for all of them.  A run's tokens
@@ -529,8 +585,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             __syncwarp();
             if (leads) {
                 const int in_page = pos - p.by_page(pos) * p.c.page_size;
-                copy_bulk(dst + lane * S::kStride,
-                          head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
+                copy_bulk(dst + lane * S::kRecord,
+                          part.head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
                           p.run * S::kRecord, bar);
             }
             fill = fill + 1 == S::kStages ? 0 : fill + 1;
@@ -557,188 +613,291 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         }
         int pos_after = position(S::kStages);
 
-        __syncthreads();   // query operands are there
-
-        float o[S::kGroups][2][NT][4];
-        float top[NT][2], sum[NT][2], fac[NT][2];
-        int least = 0x7fffffff, lim[NT][2];
+        // Output; two rows of the unit for each block of it that this lane
+        // shares: row(b, c).
+        float o[S::kGroups][S::kSubs][S::kBlocks][4];
+        float top[S::kBlocks][2], sum[S::kBlocks][2], fac[S::kBlocks][2];
+        auto row = [&](int b, int c) { return S::kWide ? b * 16 + g + 8 * c : 2 * t + c; };
+        int least = 0x7fffffff;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                top[nt][c] = -INFINITY;
-                sum[nt][c] = 0.f;
-                fac[nt][c] = factor[nt * 8 + 2 * t + c];
-                lim[nt][c] = limit[nt * 8 + 2 * t + c];
-                if (nt * 8 + 2 * t + c < u.rows)
-                    least = min(least, lim[nt][c]);
+                top[b][c] = -INFINITY;
+                sum[b][c] = 0.f;
+                fac[b][c] = factor[row(b, c)];
+                if (row(b, c) < part.u.rows)
+                    least = min(least, limit[row(b, c)]);
             }
         // tiles below the lowest limit of any row need no comparison
         least = __reduce_min_sync(~0u, least);
 #pragma unroll
         for (int i = 0; i < S::kGroups; ++i)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < S::kSubs; ++s)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        o[i][s][nt][e] = 0.f;
+                        o[i][s][b][e] = 0.f;
+
+        // largest of the lanes that share a row
+        auto row_max = [&](float v) {
+#pragma unroll
+            for (int step = S::kWide ? 1 : 4; step < (S::kWide ? 4 : 32); step *= 2)
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, step));
+            return v;
+        };
+        // state of accumulator register e: columns 2 t, 2 t + 1 of rows g, g + 8
+        auto state = [](int e) { return S::kWide ? e / 2 : e & 1; };
+        // New maxima `best` of the lane's scores.  One is rare after the first
+        // tiles: only then the rows' maxima are joined and the sums brought down.
+        auto raise = [&](const float (&best)[S::kBlocks][2]) {
+            bool higher = false;
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b)
+                higher |= best[b][0] > top[b][0] || best[b][1] > top[b][1];
+            if (!__any_sync(~0u, higher))
+                return;
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b) {
+                float down[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float m = row_max(fmaxf(best[b][c], top[b][c]));
+                    down[c] = top[b][c] == -INFINITY ? 0.f : exp2_fast((top[b][c] - m) * fac[b][c]);
+                    top[b][c] = m;
+                    sum[b][c] *= down[c];
+                }
+#pragma unroll
+                for (int i = 0; i < S::kGroups; ++i)
+#pragma unroll
+                    for (int s = 0; s < S::kSubs; ++s)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[i][s][b][e] *= down[state(e)];
+            }
+        };
+        auto low = [&](int b, int c) { return top[b][c] == -INFINITY ? 0.f : top[b][c] * fac[b][c]; };
+        // operands of the four codes of each of two tokens in z: codes j of both
+        auto value_codes = [](uint32_t z, int j) {
+            return j == 0 ? low_codes(z) : j == 1 ? high_codes(z) : j == 2 ? low_codes(z >> 8)
+                                                                          : high_codes(z >> 8);
+        };
 
         auto consume = [&](auto masked_tag, const unsigned char *tile, unsigned mask, int base) {
             constexpr bool kMasked = decltype(masked_tag)::value;
-            // scores
-            float sc[S::kMT][NT][4];
+            auto seen_by = [&](int token, int r) -> bool {
+                return (mask >> token & 1) && (kListed || base + token < limit[r]);
+            };
+            if constexpr (!S::kWide) {
+                float sc[S::kMT][4];
 #pragma unroll
-            for (int mt = 0; mt < S::kMT; ++mt) {
-                const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kStride;
-                const unsigned char *rb = ra + S::kStride;
-                float sa[S::kGroups], sb[S::kGroups];
-                load_scales(sa, ra + D);
-                load_scales(sb, rb + D);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int mt = 0; mt < S::kMT; ++mt) {
+                    const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kRecord;
+                    const unsigned char *rb = ra + S::kNext * S::kRecord;
+                    float sa[S::kGroups], sb[S::kGroups];
+                    load_scales(sa, ra + D);
+                    load_scales(sb, rb + D);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sc[mt][nt][e] = 0.f;
+                        sc[mt][e] = 0.f;
 #pragma unroll
-                for (int st = 0; st < S::kStretches; ++st) {
-                    uint32_t wa[S::kPer], wb[S::kPer];
-                    load_words(wa, ra + st * 64 + t * S::kPer * 4);
-                    load_words(wb, rb + st * 64 + t * S::kPer * 4);
+                    for (int st = 0; st < S::kStretches; ++st) {
+                        uint32_t wa[S::kPer], wb[S::kPer];
+                        load_words(wa, ra + st * 64 + t * S::kPer * 4);
+                        load_words(wb, rb + st * 64 + t * S::kPer * 4);
 #pragma unroll
-                    for (int i = 0; i < S::kPer; ++i) {
-                        const int group = st * S::kPer + i;
-                        const uint32_t ha = wa[i] >> 8, hb = wb[i] >> 8;
-                        const uint32_t a00 = low_codes(wa[i]);
-                        const uint32_t a01 = low_codes(wb[i]);
-                        const uint32_t a02 = high_codes(wa[i]);
-                        const uint32_t a03 = high_codes(wb[i]);
-                        const uint32_t a10 = low_codes(ha);
-                        const uint32_t a11 = low_codes(hb);
-                        const uint32_t a12 = high_codes(ha);
-                        const uint32_t a13 = high_codes(hb);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int i = 0; i < S::kPer; ++i) {
+                            const int group = st * S::kPer + i;
                             const uint2 *qf = reinterpret_cast<const uint2 *>(smem + S::kOffQ) +
-                                              (group * 2 * NT + nt) * 32 + lane;
-                            const uint2 q0 = qf[0], q1 = qf[NT * 32];
+                                              group * 2 * 32 + lane;
+                            const uint2 q0 = qf[0], q1 = qf[32];
+                            const uint32_t ha = wa[i] >> 8, hb = wb[i] >> 8;
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(acc, a00, a01, a02, a03, q0.x, q0.y);
-                            mma16816(acc, a10, a11, a12, a13, q1.x, q1.y);
-                            sc[mt][nt][0] += sa[group] * acc[0];
-                            sc[mt][nt][1] += sa[group] * acc[1];
-                            sc[mt][nt][2] += sb[group] * acc[2];
-                            sc[mt][nt][3] += sb[group] * acc[3];
+                            mma16816(acc, low_codes(wa[i]), low_codes(wb[i]), high_codes(wa[i]),
+                                     high_codes(wb[i]), q0.x, q0.y);
+                            mma16816(acc, low_codes(ha), low_codes(hb), high_codes(ha), high_codes(hb),
+                                     q1.x, q1.y);
+                            sc[mt][0] += sa[group] * acc[0];
+                            sc[mt][1] += sa[group] * acc[1];
+                            sc[mt][2] += sb[group] * acc[2];
+                            sc[mt][3] += sb[group] * acc[3];
                         }
                     }
                 }
-            }
-            // which of the lane's tokens (step mt, row g or g + 8) rows see
-            auto there = [&](int mt, int e, int nt) -> bool {
-                const int token = mt * 16 + tok_row + (e >= 2);
-                return (mask >> token & 1) && (kListed || base + token < lim[nt][e & 1]);
-            };
-            bool higher = false;
-            float best[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                best[nt][0] = best[nt][1] = -INFINITY;
+                float best[1][2] = {{-INFINITY, -INFINITY}};
 #pragma unroll
                 for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (kMasked && !there(mt, e, nt))
-                            sc[mt][nt][e] = -INFINITY;
-                        best[nt][e & 1] = fmaxf(best[nt][e & 1], sc[mt][nt][e]);
+                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                            sc[mt][e] = -INFINITY;
+                        best[0][e & 1] = fmaxf(best[0][e & 1], sc[mt][e]);
                     }
-                higher |= best[nt][0] > top[nt][0] || best[nt][1] > top[nt][1];
-            }
-            // a new maximum is rare after the first tiles: only then the
-            // columns' maxima are joined and the sums brought down
-            if (__any_sync(~0u, higher)) {
+                raise(best);
+                const float low0 = low(0, 0), low1 = low(0, 1);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float b = fmaxf(best[nt][c], top[nt][c]);
-                        b = fmaxf(b, __shfl_xor_sync(~0u, b, 4));
-                        b = fmaxf(b, __shfl_xor_sync(~0u, b, 8));
-                        b = fmaxf(b, __shfl_xor_sync(~0u, b, 16));
-                        const float down =
-                            top[nt][c] == -INFINITY ? 0.f : exp2_fast((top[nt][c] - b) * fac[nt][c]);
-                        top[nt][c] = b;
-                        sum[nt][c] *= down;
-#pragma unroll
-                        for (int i = 0; i < S::kGroups; ++i)
-#pragma unroll
-                            for (int s = 0; s < 2; ++s) {
-                                o[i][s][nt][c] *= down;
-                                o[i][s][nt][c + 2] *= down;
-                            }
-                    }
-            }
-            float low[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    low[nt][c] = top[nt][c] == -INFINITY ? 0.f : top[nt][c] * fac[nt][c];
-            // probabilities, times the value scales, as operands; then the values
-#pragma unroll
-            for (int mt = 0; mt < S::kMT; ++mt) {
-                const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kStride;
-                float sa[S::kGroups], sb[S::kGroups];
-                load_scales(sa, ra + D + 2 * S::kGroups);
-                load_scales(sb, ra + S::kStride + D + 2 * S::kGroups);
-                float pr[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int mt = 0; mt < S::kMT; ++mt) {
+                    const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kRecord;
+                    float sa[S::kGroups], sb[S::kGroups], pr[4];
+                    load_scales(sa, ra + D + 2 * S::kGroups);
+                    load_scales(sb, ra + S::kNext * S::kRecord + D + 2 * S::kGroups);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        pr[nt][e] = exp2_fast(sc[mt][nt][e] * fac[nt][e & 1] - low[nt][e & 1]);
-                        if (kMasked && !there(mt, e, nt))
-                            pr[nt][e] = 0.f;
-                        sum[nt][e & 1] += pr[nt][e];
+                        pr[e] = exp2_fast(sc[mt][e] * fac[0][e & 1] - (e & 1 ? low1 : low0));
+                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                            pr[e] = 0.f;
+                        sum[0][e & 1] += pr[e];
                     }
-                const unsigned char *va = tile + (mt * 16 + tok_a) * S::kStride + D / 2;
-                const unsigned char *vb = tile + (mt * 16 + tok_b) * S::kStride + D / 2;
+                    const unsigned char *va = tile + (mt * 16 + tok_a) * S::kRecord + D / 2;
+                    const unsigned char *vb = tile + (mt * 16 + tok_b) * S::kRecord + D / 2;
 #pragma unroll
-                for (int st = 0; st < S::kStretches; ++st) {
-                    constexpr int kW = S::kPer / 2;
-                    uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
-                    load_words(wa, va + st * 64 + g * kW * 4);
-                    load_words(wb, vb + st * 64 + g * kW * 4);
-                    load_words(xa, va + S::kStride + st * 64 + g * kW * 4);
-                    load_words(xb, vb + S::kStride + st * 64 + g * kW * 4);
+                    for (int st = 0; st < S::kStretches; ++st) {
+                        constexpr int kW = S::kPer / 2;
+                        uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
+                        load_words(wa, va + st * 64 + g * kW * 4);
+                        load_words(wb, vb + st * 64 + g * kW * 4);
+                        load_words(xa, va + S::kNext * S::kRecord + st * 64 + g * kW * 4);
+                        load_words(xb, vb + S::kNext * S::kRecord + st * 64 + g * kW * 4);
 #pragma unroll
-                    for (int i = 0; i < S::kPer; ++i) {
-                        const int group = st * S::kPer + i;
-                        const unsigned pick = i & 1 ? 0x7632 : 0x5410;
-                        const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], pick);
-                        const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], pick);
-                        const uint32_t z8 = z >> 8, y8 = y >> 8;
-                        const uint32_t a00 = low_codes(z);
-                        const uint32_t a01 = high_codes(z);
-                        const uint32_t a02 = low_codes(y);
-                        const uint32_t a03 = high_codes(y);
-                        const uint32_t a10 = low_codes(z8);
-                        const uint32_t a11 = high_codes(z8);
-                        const uint32_t a12 = low_codes(y8);
-                        const uint32_t a13 = high_codes(y8);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int i = 0; i < S::kPer; ++i) {
+                            const int group = st * S::kPer + i;
+                            const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                            const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
                             float w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                w[e] = pr[nt][e] * (e < 2 ? sa[group] : sb[group]);
-                                if (kMasked && !there(mt, e, nt))
-                                    w[e] = 0.f;   // whatever the record holds
+                                w[e] = pr[e] * (e < 2 ? sa[group] : sb[group]);
+                                // whatever the record holds
+                                if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                                    w[e] = 0.f;
                             }
                             const uint32_t b0 = transpose8x8(pack_half2(w[0], w[1]));
                             const uint32_t b1 = transpose8x8(pack_half2(w[2], w[3]));
-                            mma16816(o[group][0][nt], a00, a01, a02, a03, b0, b1);
-                            mma16816(o[group][1][nt], a10, a11, a12, a13, b0, b1);
+                            mma16816(o[group][0][0], value_codes(z, 0), value_codes(z, 1),
+                                     value_codes(y, 0), value_codes(y, 1), b0, b1);
+                            mma16816(o[group][1][0], value_codes(z, 2), value_codes(z, 3),
+                                     value_codes(y, 2), value_codes(y, 3), b0, b1);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int mt = 0; mt < S::kMT; ++mt) {
+                    // scores of the step's places 2 t, 2 t + 1 (half 0) and those + 8
+                    float sc[S::kBlocks][2][4];
+                    const unsigned char *step = tile + mt * 16 * S::kRecord;
+                    const unsigned char *ra = step + tok_a * S::kRecord, *rb = step + tok_b * S::kRecord;
+#pragma unroll
+                    for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[b][0][e] = sc[b][1][e] = 0.f;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const unsigned char *rk = step + (tok_row + half * S::kNext) * S::kRecord;
+                        float sa[S::kGroups], sb[S::kGroups];
+                        load_scales(sa, ra + half * S::kNext * S::kRecord + D);
+                        load_scales(sb, rb + half * S::kNext * S::kRecord + D);
+#pragma unroll
+                        for (int st = 0; st < S::kStretches; ++st) {
+                            uint32_t wk[S::kPer];
+                            load_words(wk, rk + st * 64 + t * S::kPer * 4);
+#pragma unroll
+                            for (int i = 0; i < S::kPer; ++i) {
+                                const int group = st * S::kPer + i;
+                                const uint32_t k0 = low_codes(wk[i]), k1 = high_codes(wk[i]);
+                                const uint32_t k2 = low_codes(wk[i] >> 8), k3 = high_codes(wk[i] >> 8);
+#pragma unroll
+                                for (int b = 0; b < S::kBlocks; ++b) {
+                                    const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kOffQ) +
+                                                      (group * 2 * S::kBlocks + b) * 32 + lane;
+                                    const uint4 q0 = qf[0], q1 = qf[S::kBlocks * 32];
+                                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816(acc, q0.x, q0.y, q0.z, q0.w, k0, k1);
+                                    mma16816(acc, q1.x, q1.y, q1.z, q1.w, k2, k3);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        sc[b][half][e] += (e & 1 ? sb[group] : sa[group]) * acc[e];
+                                }
+                            }
+                        }
+                    }
+                    auto token = [&](int half, int e) {
+                        return mt * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
+                    };
+                    float best[S::kBlocks][2];
+#pragma unroll
+                    for (int b = 0; b < S::kBlocks; ++b) {
+                        best[b][0] = best[b][1] = -INFINITY;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
+                                    sc[b][half][e] = -INFINITY;
+                                best[b][e / 2] = fmaxf(best[b][e / 2], sc[b][half][e]);
+                            }
+                    }
+                    raise(best);
+#pragma unroll
+                    for (int b = 0; b < S::kBlocks; ++b) {
+                        const float low0 = low(b, 0), low1 = low(b, 1);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float pr = exp2_fast(sc[b][half][e] * fac[b][e / 2] - (e / 2 ? low1 : low0));
+                                if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
+                                    pr = 0.f;
+                                sum[b][e / 2] += pr;
+                                sc[b][half][e] = pr;
+                            }
+                    }
+#pragma unroll
+                    for (int st = 0; st < S::kStretches; ++st) {
+                        constexpr int kW = S::kPer / 2;
+                        const int at = D / 2 + st * 64 + g * kW * 4, next = S::kNext * S::kRecord;
+                        uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
+                        load_words(wa, ra + at);
+                        load_words(wb, rb + at);
+                        load_words(xa, ra + next + at);
+                        load_words(xb, rb + next + at);
+#pragma unroll
+                        for (int i = 0; i < S::kPer; ++i) {
+                            const int group = st * S::kPer + i;
+                            const int vs = D + 2 * S::kGroups + 2 * group;
+                            const float s0 = __half2float(*reinterpret_cast<const __half *>(ra + vs));
+                            const float s1 = __half2float(*reinterpret_cast<const __half *>(rb + vs));
+                            const float s2 = __half2float(*reinterpret_cast<const __half *>(ra + next + vs));
+                            const float s3 = __half2float(*reinterpret_cast<const __half *>(rb + next + vs));
+                            const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                            const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                            uint32_t pa[S::kBlocks][4];
+#pragma unroll
+                            for (int b = 0; b < S::kBlocks; ++b) {
+                                float w[2][4];
+#pragma unroll
+                                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        w[half][e] = sc[b][half][e] * (half ? (e & 1 ? s3 : s2) : (e & 1 ? s1 : s0));
+                                        if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
+                                            w[half][e] = 0.f;
+                                    }
+                                pa[b][0] = pack_half2(w[0][0], w[0][1]);
+                                pa[b][1] = pack_half2(w[0][2], w[0][3]);
+                                pa[b][2] = pack_half2(w[1][0], w[1][1]);
+                                pa[b][3] = pack_half2(w[1][2], w[1][3]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t b0 = value_codes(z, j), b1 = value_codes(y, j);
+#pragma unroll
+                                for (int b = 0; b < S::kBlocks; ++b)
+                                    mma16816(o[group][j][b], pa[b][0], pa[b][1], pa[b][2], pa[b][3], b0, b1);
+                            }
                         }
                     }
                 }
@@ -761,7 +920,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 use = 0, phase ^= 1;
             if (!came)
                 lost = true;
-            const int base = kListed ? 0 : (int)(e0 - lane + i * (kAttendWarps * S::kTile));
+            const int base = kListed ? 0 : (int)(e0 - lane + i * (S::kWarps * S::kTile));
             if (mask == (S::kTile == 32 ? ~0u : (1u << (S::kTile & 31)) - 1) &&
                 (kListed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
@@ -772,36 +931,54 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
         // ---- the warps' results, side by side in the rings' place ----------
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float s = lost ? __int_as_float(0x7fffffff) : sum[nt][c];
-                s += __shfl_xor_sync(~0u, s, 4);
-                s += __shfl_xor_sync(~0u, s, 8);
-                s += __shfl_xor_sync(~0u, s, 16);
-                const int r = nt * 8 + 2 * t + c;
-                if (g == 0) {
-                    wmax(warp, r) = top[nt][c] == -INFINITY ? -INFINITY : top[nt][c] * fac[nt][c];
+                const int r = row(b, c);
+                float s = lost ? __int_as_float(0x7fffffff) : sum[b][c];
+#pragma unroll
+                for (int step = S::kWide ? 1 : 4; step < (S::kWide ? 4 : 32); step *= 2)
+                    s += __shfl_xor_sync(~0u, s, step);
+                if (S::kWide ? t == 0 : g == 0) {
+                    wmax(warp, r) = low(b, c);
+                    if (top[b][c] == -INFINITY)
+                        wmax(warp, r) = -INFINITY;
                     wsum(warp, r) = s;
                 }
-                float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride + 4 * g;
+                // narrow: rows of the instruction are channels 4 g + {0, 1} and
+                // 4 g + {2, 3}; wide: columns 2 t, 2 t + 1 of instruction j are
+                // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large.
+                float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride;
 #pragma unroll
-                for (int i = 0; i < S::kGroups; ++i)
-                    *reinterpret_cast<float4 *>(dst + i * kGroup) =
-                        make_float4(o[i][0][nt][c], o[i][0][nt][c + 2] * 0.0625f,
-                                    o[i][1][nt][c], o[i][1][nt][c + 2] * 0.0625f);
+                for (int i = 0; i < S::kGroups; ++i) {
+                    if constexpr (S::kWide) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<float4 *>(dst + i * kGroup + 8 * t + 4 * k) = make_float4(
+                                o[i][0][b][2 * c + k], o[i][1][b][2 * c + k] * 0.0625f,
+                                o[i][2][b][2 * c + k], o[i][3][b][2 * c + k] * 0.0625f);
+                    } else {
+                        *reinterpret_cast<float4 *>(dst + i * kGroup + 4 * g) =
+                            make_float4(o[i][0][b][c], o[i][0][b][c + 2] * 0.0625f, o[i][1][b][c],
+                                        o[i][1][b][c + 2] * 0.0625f);
+                    }
+                }
             }
         __syncthreads();
 
-        const bool whole = count == tiles;
-        float *part = p.a.partial + (blockIdx.x * 2LL + (tile0 == 0)) * S::kPartial;
+        Unit u;
+        u.b = part.u.b, u.head = part.u.head, u.query = part.u.query;
+        u.row0 = part.u.row0, u.rows = part.u.rows;
+        const bool whole = part.whole;
+        // a CTA's second place is for the unit that begins in it
+        float *to_join = p.a.partial + p.parts + (blockIdx.x * 2LL + part.begins) * S::kPartial;
         // weights of the warps' results: 2^(max - largest max)
         if (threadIdx.x < S::kRows) {
             const int r = threadIdx.x;
             float m = -INFINITY, l = 0.f;
-            for (int w = 0; w < kAttendWarps; ++w)
+            for (int w = 0; w < S::kWarps; ++w)
                 m = fmaxf(m, wmax(w, r));
-            for (int w = 0; w < kAttendWarps; ++w) {
+            for (int w = 0; w < S::kWarps; ++w) {
                 const float f = wmax(w, r);
                 // a warp that saw nothing has sum 0; one whose scores are NaN
                 // has a maximum of -inf, and its NaN goes on
@@ -819,18 +996,18 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 }
             } else {
-                part[r] = m;
-                part[S::kRows + r] = l;
+                to_join[r] = m;
+                to_join[S::kRows + r] = l;
             }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < S::kRows * D / 4; e += kAttendThreads) {
+        for (int e = threadIdx.x; e < S::kRows * D / 4; e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             if (r >= u.rows)
                 break;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kAttendWarps; ++w) {
+            for (int w = 0; w < S::kWarps; ++w) {
                 const float4 f = *reinterpret_cast<const float4 *>(
                     smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
                 const float weight = wmax(w, r);
@@ -855,99 +1032,125 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         *reinterpret_cast<const uint2 *>(y);
                 }
             } else {
-                *reinterpret_cast<float4 *>(part + 2 * S::kRows + r * D + d) = v;
+                *reinterpret_cast<float4 *>(to_join + 2 * S::kRows + r * D + d) = v;
             }
         }
+        x = part.next;
+        first = part.next_first;
+        entry = part.next_entry;
         __syncthreads();
     }
 }
 
-// Joins the partial results of units that several CTAs worked on: one warp a
-// query row, CTAs' shares in order.
-template <int D, int NT, bool kListed>
-__global__ void __launch_bounds__(kAttendThreads)
-join_kernel(const __grid_constant__ AttendArgs p, int ctas)
+// Joins the partial results of units that several CTAs worked on, a CTA for
+// each query row of the unit that began in attending CTA blockIdx.x / Rows: the
+// weights of the parts first, then D/4 threads for a part's row, the parts
+// dealt out to the rest and their sums added in order.
+constexpr int kJoinThreads = 128;
+
+template <int D, int Rows>
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(const __grid_constant__ AttendArgs p)
 {
-    using S = Shape<D, NT>;
-    __shared__ long long scratch[16];
+    using S = Shape<D, Rows>;
+    constexpr int kLanes = D / 4, kTeams = kJoinThreads / kLanes;
+    __shared__ float weight[kJoinThreads], red[kJoinThreads / 32], teams[kTeams][D + 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    // blocks of 8 rows of a unit
-    const long long unit = blockIdx.x / NT;
-    const int u_in = (int)(unit % p.units);
-    const Line line = line_of<S::kTile, kListed>(p, ctas, 0, (int)(unit / p.units), scratch);
-    const int entry = line.entry;
-    const long long per = line.per, tiles = tiles_of<S::kTile, kListed>(p, entry);
-    const long long from = line.first + u_in * (tiles + kUnitCost) + kUnitCost;
-    const long long c0 = from / per, c1 = (from + tiles - 1) / per;
-    const int r = blockIdx.x % NT * 8 + warp;
-    const Unit u(p, kListed, entry, u_in, S::kRows);
-    if (c0 == c1 || r >= u.rows)
-        return;
-    // Up to here only what the launch before the attention left is read: this
-    // launch starts when that one has been waited for.
+    const int cta = blockIdx.x / Rows, r = blockIdx.x % Rows;
     dependent_grid_wait();
-    // a CTA's second place holds the unit that begins in it
-    auto place = [&](long long c) { return p.a.partial + (c * 2 + (c == c0)) * S::kPartial; };
-    float m = -INFINITY;
-    for (long long c = c0 + lane; c <= c1; c += 32)
-        m = fmaxf(m, place(c)[r]);
+    const int4 split = reinterpret_cast<const int4 *>(p.a.partial)[cta];
+    const int parts = split.z;
+    if (parts == 0)
+        return;
+    const Unit u(p, split.x, split.y, Rows);
+    if (r >= u.rows)
+        return;
+    const float *base = p.a.partial + p.parts + 2LL * cta * S::kPartial;
+    auto place = [&](int i) { return base + (i == 0 ? 1 : 2 * i) * (long long)S::kPartial; };
+    auto joined = [&](float v, auto add) {
 #pragma unroll
-    for (int step = 16; step; step /= 2)
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, step));
+        for (int step = 16; step; step /= 2)
+            v = add(v, __shfl_xor_sync(~0u, v, step));
+        __syncthreads();
+        if (lane == 0)
+            red[warp] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < kJoinThreads / 32; ++w)
+            v = add(v, red[w]);
+        return v;
+    };
+    const int team = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    float m = -INFINITY, l = 0.f;
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads)
+        m = fmaxf(m, place(i)[r]);
+    m = joined(m, [](float a, float b) { return fmaxf(a, b); });
     const float low = m == -INFINITY ? 0.f : m;
-    float l = 0.f, v[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        v[i] = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kJoinThreads) {
+        __syncthreads();
+        const int i = i0 + threadIdx.x;
+        if (i < parts) {
+            const float s = place(i)[S::kRows + r];
+            weight[threadIdx.x] = s != s ? 1.f : exp2_fast(place(i)[r] - low);
+            l += s * weight[threadIdx.x];
+        }
+        __syncthreads();
+        const int n = parts - i0 < kJoinThreads ? parts - i0 : kJoinThreads;
 #pragma unroll 4
-    for (long long c = c0; c <= c1; ++c) {
-        const float *q = place(c);
-        const float s = q[S::kRows + r];
-        const float weight = s != s ? 1.f : exp2_fast(q[r] - low);
-        l += s * weight;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            v[i] += q[2 * S::kRows + r * D + i * 32 + lane] * weight;
+        for (int i = team; i < n; i += kTeams) {
+            const float4 f =
+                *reinterpret_cast<const float4 *>(place(i0 + i) + 2 * S::kRows + r * D + d);
+            v.x += f.x * weight[i], v.y += f.y * weight[i];
+            v.z += f.z * weight[i], v.w += f.w * weight[i];
+        }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<float4 *>(&teams[team][d]) = v;
+    l = joined(l, [](float a, float b) { return a + b; });
     int j, h;
     u.row(p, r, &j, &h);
     const long long row = ((long long)u.b * p.a.queries + j) * p.a.heads + h;
+    for (int c = threadIdx.x; c < D; c += kJoinThreads) {
+        float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+        for (int k = 0; k < kTeams; ++k)
+            x += teams[k][c];
+        x = l == 0.f ? 0.f : x / l;
         if (p.a.bf16)
-            from_float(((__nv_bfloat16 *)p.a.out)[row * D + i * 32 + lane], v[i] * inv);
+            from_float(((__nv_bfloat16 *)p.a.out)[row * D + c], x);
         else
-            from_float(((__half *)p.a.out)[row * D + i * 32 + lane], v[i] * inv);
+            from_float(((__half *)p.a.out)[row * D + c], x);
     }
-    if (p.a.lse && lane == 0)
+    if (p.a.lse && threadIdx.x == 0)
         p.a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // ---- host ----------------------------------------------------------------------
-// Columns of eight rows that a unit works on at once: as many as its rows
-// fill, up to 4 (2 for D = 256, whose outputs would not fit the registers).
+// Query rows of a unit: as many as there are, up to 32 (16 for D = 256, whose
+// outputs would not fit the registers).
 template <int D>
-int row_tiles(int rows)
+int unit_rows(int rows)
 {
-    return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+    return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
 }
 
-template <int D, int NT>
+template <int D, int Rows>
 int attend_grid(int sms)
 {
-    return sms * (Shape<D, NT>::kTwoCtas ? 2 : 1);
+    return sms * Shape<D, Rows>::kCtas;
 }
 
-template <int D, int NT, bool kListed>
+template <int D, int Rows, bool kListed>
 cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
 {
-    using S = Shape<D, NT>;
-    const int ctas = attend_grid<D, NT>(sms);
+    using S = Shape<D, Rows>;
+    const int ctas = attend_grid<D, Rows>(sms);
     p.blocks = (p.rows + S::kRows - 1) / S::kRows;
     p.units = p.c.kv_heads * p.blocks * (kListed ? p.a.queries : 1);
     p.sel_tiles = ((long long)p.a.k + S::kTile - 1) / S::kTile;
-    auto fn = attend_kernel<D, NT, kListed>;
+    p.parts = ctas * (long long)(sizeof(Split) / sizeof(float));
+    auto fn = attend_kernel<D, Rows, kListed>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
@@ -956,50 +1159,55 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kAttendThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, fn, (const AttendArgs)p)) != cudaSuccess)
         return e;
-    cfg.gridDim = dim3((unsigned)((long long)p.a.batch * p.units * NT));
+    cfg.gridDim = dim3((unsigned)(ctas * Rows));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, NT, kListed>, (const AttendArgs)p, ctas);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, Rows>, (const AttendArgs)p);
 }
 
 template <int D>
 cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t stream)
 {
+    constexpr int kMost = D == 256 ? 16 : 32;
     AttendArgs p;
     p.c = c;
     p.a = a;
     p.by_page.set(c.page_size);
     p.group = a.heads / c.kv_heads;
     p.run = 1;
-    if (!a.indices && Shape<D, 1>::kStride == Shape<D, 1>::kRecord)
-        while (p.run < Shape<D, 1>::kTile && c.page_size % (2 * p.run) == 0)
-            p.run *= 2;
+    while (!a.indices && p.run < Shape<D, 8>::kTile && c.page_size % (2 * p.run) == 0)
+        p.run *= 2;
     p.rows = a.indices ? p.group : p.group * a.queries;
-    const int nt = row_tiles<D>(p.rows);
+    const int rows = unit_rows<D>(p.rows);
     if (a.indices)
-        return nt == 1   ? launch_shape<D, 1, true>(p, sms, stream)
-               : nt == 2 ? launch_shape<D, 2, true>(p, sms, stream)
-                         : launch_shape<D, D == 256 ? 2 : 4, true>(p, sms, stream);
-    return nt == 1   ? launch_shape<D, 1, false>(p, sms, stream)
-           : nt == 2 ? launch_shape<D, 2, false>(p, sms, stream)
-                     : launch_shape<D, D == 256 ? 2 : 4, false>(p, sms, stream);
+        return rows == 8    ? launch_shape<D, 8, true>(p, sms, stream)
+               : rows == 16 ? launch_shape<D, 16, true>(p, sms, stream)
+                            : launch_shape<D, kMost, true>(p, sms, stream);
+    return rows == 8    ? launch_shape<D, 8, false>(p, sms, stream)
+           : rows == 16 ? launch_shape<D, 16, false>(p, sms, stream)
+                        : launch_shape<D, kMost, false>(p, sms, stream);
+}
+
+template <int D, int Rows>
+size_t workspace_shape(int sms)
+{
+    return attend_grid<D, Rows>(sms) * (sizeof(Split) + 2 * Shape<D, Rows>::kPartial * sizeof(float));
 }
 
 template <int D>
 size_t workspace_dim(int rows, int sms)
 {
-    const int nt = row_tiles<D>(rows);
-    const size_t floats = nt == 1   ? (size_t)attend_grid<D, 1>(sms) * Shape<D, 1>::kPartial
-                          : nt == 2 ? (size_t)attend_grid<D, 2>(sms) * Shape<D, 2>::kPartial
-                                    : (size_t)attend_grid<D, D == 256 ? 2 : 4>(sms) *
-                                          Shape<D, D == 256 ? 2 : 4>::kPartial;
-    return 2 * floats * sizeof(float);
+    constexpr int kMost = D == 256 ? 16 : 32;
+    const int r = unit_rows<D>(rows);
+    return r == 8    ? workspace_shape<D, 8>(sms)
+           : r == 16 ? workspace_shape<D, 16>(sms) : workspace_shape<D, kMost>(sms);
 }
 
 }  // namespace kv4
