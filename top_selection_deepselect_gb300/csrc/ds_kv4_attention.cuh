@@ -80,6 +80,7 @@ struct Shape {
     static constexpr int kPer = kGroups / kStretches;            // groups of a stretch
     static constexpr int kMT = D == 256 ? 1 : 2;                 // 16-token steps of a tile
     static constexpr int kTile = 16 * kMT;
+    static constexpr unsigned kFullMask = ~0u >> (32 - kTile);
     static constexpr int kRecord = record_bytes(D);
     static constexpr int kStageBytes = kTile * kRecord;
     static constexpr int kOutRegs = kGroups * kSubs * kBlocks * 4;
@@ -262,10 +263,10 @@ __device__ __forceinline__ int length_of(const AttendArgs &p, int seq)
 
 // Tiles of every unit of batch entry b: at least one, so that rows that see
 // nothing are written too.
-template <int kTile, bool kListed>
-__device__ __forceinline__ long long tiles_of(const AttendArgs &p, int b)
+template <int kTile>
+__device__ __forceinline__ long long tiles_of(const AttendArgs &p, bool listed, int b)
 {
-    if (kListed)
+    if (listed)
         return p.sel_tiles;
     const int n = length_of(p, sequence_of(p, b));
     return n > kTile ? (n + kTile - 1LL) / kTile : 1;
@@ -318,12 +319,12 @@ struct Line {
     int entry;
 };
 
-template <int kTile, bool kListed>
-__device__ __forceinline__ Line line_of(const AttendArgs &p, long long *scratch)
+template <int kTile>
+__device__ __forceinline__ Line line_of(const AttendArgs &p, bool listed, long long *scratch)
 {
     Line n;
     const int warps = blockDim.x / 32;
-    if (kListed) {
+    if (listed) {
         const long long each = (p.sel_tiles + kUnitCost) * p.units;
         n.all = each * p.a.batch;
         n.per = places_per_cta(n.all, gridDim.x, warps);
@@ -336,7 +337,7 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, long long *scratch)
     n.all = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
-        mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
+        mine = b < p.a.batch ? (tiles_of<kTile>(p, listed, b) + kUnitCost) * p.units : 0;
         n.all += scan_cta(mine, &before, scratch);
     }
     n.per = places_per_cta(n.all, gridDim.x, warps);
@@ -346,7 +347,7 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, long long *scratch)
         const int b = b0 + threadIdx.x;
         long long sum = n.all;
         if (!once) {
-            mine = b < p.a.batch ? (tiles_of<kTile, kListed>(p, b) + kUnitCost) * p.units : 0;
+            mine = b < p.a.batch ? (tiles_of<kTile>(p, listed, b) + kUnitCost) * p.units : 0;
             sum = scan_cta(mine, &before, scratch);
         }
         if (x >= at + before && x < at + before + mine) {
@@ -455,11 +456,15 @@ __device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u,
     }
 }
 
-template <int D, int Rows, bool kListed>
+// kAligned: every token is attended and a page holds whole tiles, so that a tile
+// is one run of bytes; otherwise tokens are looked up one by one, listed or
+// not.
+template <int D, int Rows, bool kAligned>
 __global__ void __launch_bounds__((Shape<D, Rows>::kThreads), (Shape<D, Rows>::kCtas))
 attend_kernel(const __grid_constant__ AttendArgs p)
 {
     using S = Shape<D, Rows>;
+    const bool listed = !kAligned && p.a.indices != nullptr;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     long long *scratch = reinterpret_cast<long long *>(smem + S::kOffScan);
@@ -499,7 +504,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     long long x, per, end, first;
     int entry;
     {
-        const Line line = line_of<S::kTile, kListed>(p, scratch);
+        const Line line = line_of<S::kTile>(p, listed, scratch);
         per = line.per;
         x = per * blockIdx.x;
         end = x + per < line.all ? x + per : line.all;
@@ -512,68 +517,45 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
     while (x < end) {
         // the part of the unit at x that is this CTA's
-        int mine;
-        unsigned e0;
-        {
-            const int seq = sequence_of(p, entry), len = length_of(p, seq);
-            const long long tiles = tiles_of<S::kTile, kListed>(p, entry), each = tiles + kUnitCost;
-            const int u_in = (int)((x - first) / each);
-            const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
-            const long long tile0 = x > zero ? x - zero : 0;
-            const long long stop = zero + tiles < end ? zero + tiles : end;
-            const long long count = stop - zero - tile0;
-            if (count <= 0)
-                break;      // only the unit's first places: its tiles are the next CTA's
-            const Unit u(p, entry, u_in, S::kRows);
-            if (threadIdx.x == 0) {
-                part.list = kListed ? p.a.indices + ((long long)entry * p.a.queries + u.query) * p.a.k
-                                    : nullptr;
-                part.row_table =
-                    p.c.table + ((unsigned)seq < (unsigned)p.c.max_seqs ? seq * p.c.table_stride : 0);
-                part.head_pool = p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
-                const bool last = zero + tiles - first == each * p.units;
-                part.next = zero + tiles;
-                part.next_first = last ? zero + tiles : first;
-                part.next_entry = entry + last;
-                part.seen = kListed ? len - p.a.queries + 1 + u.query : len;
-                part.u.b = u.b, part.u.head = u.head, part.u.query = u.query;
-                part.u.row0 = u.row0, part.u.rows = u.rows;
-                part.whole = count == tiles;
-                part.begins = tile0 == 0;
-                if (tile0 == 0 && count < tiles) {
-                    split->b = entry;
-                    split->unit = u_in;
-                    split->parts = (int)((zero + tiles - 1) / per - blockIdx.x) + 1;
-                }
-            }
-            if (p.a.bf16)
-                load_queries<D, Rows, __nv_bfloat16>(p, u, len, smem);
-            else
-                load_queries<D, Rows, __half>(p, u, len, smem);
-            // the warp's tiles: warp, warp + kWarps, ... of `count`
-            mine = count > warp ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
-            // tokens and list entries are below 2^31; the last tile may end above
-            e0 = (unsigned)((tile0 + warp) * S::kTile) + lane;
-        }
-        __syncthreads();   // query operands and `part` are there
+        const int seq = sequence_of(p, entry), len = length_of(p, seq);
+        const long long tiles = tiles_of<S::kTile>(p, listed, entry), each = tiles + kUnitCost;
+        const int u_in = (int)((x - first) / each);
+        const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
+        const long long tile0 = x > zero ? x - zero : 0;
+        const long long stop = zero + tiles < end ? zero + tiles : end;
+        const long long count = stop - zero - tile0;
+        if (count <= 0)
+            break;      // only the unit's first places: its tiles are the next CTA's
+        const Unit unit(p, entry, u_in, S::kRows);
+        Part now;
+        now.list = listed ? p.a.indices + ((long long)entry * p.a.queries + unit.query) * p.a.k : nullptr;
+        now.row_table =
+            p.c.table + ((unsigned)seq < (unsigned)p.c.max_seqs ? seq * p.c.table_stride : 0);
+        now.head_pool = p.c.pool + (long long)unit.head * p.c.page_size * S::kRecord;
+        now.seen = listed ? len - p.a.queries + 1 + unit.query : len;
+        // the warp's tiles: warp, warp + kWarps, ... of `count`
+        const int mine = count > warp ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
+        // tokens and list entries are below 2^31; the last tile may end above
+        const unsigned e0 = (unsigned)((tile0 + warp) * S::kTile);
 
+        // ---- tokens one by one: a lane each -----------------------------
         // position of this lane's token of the warp's tile i, -1: none
-        auto position = [&](int i) -> int {
+        auto position = [&](const volatile Part &part, int i) -> int {
             if (i >= mine || lane >= S::kTile)
                 return -1;
-            const unsigned e = e0 + i * (S::kWarps * S::kTile);
+            const unsigned e = e0 + lane + i * (S::kWarps * S::kTile);
             int pos = (int)e;
-            if (kListed)
+            if (listed)
                 pos = e < (unsigned)p.a.k ? __ldg(part.list + e) : -1;
             return pos < part.seen ? pos : -1;
         };
-        auto page_of = [&](int pos) -> int {
+        auto page_of = [&](const volatile Part &part, int pos) -> int {
             return pos >= 0 ? __ldg(part.row_table + p.by_page(pos)) : -1;
         };
         // Copies the records of a tile: a lane each, or, where `run` neighbours
         // lie side by side in a page, one lane for all of them.  A run's tokens
         // past the sequence's end are in the page too; the mask leaves them out.
-        auto issue = [&](int pos, int page) {
+        auto issue_tokens = [&](const volatile Part &part, int pos, int page) {
             const uint32_t bar = barriers + fill * 8, dst = shared_address(ring + fill * S::kStageBytes);
             const bool ok = (unsigned)page < (unsigned)p.c.n_pages;   // page is -1 where pos is
             const bool leads = ok && (lane & (p.run - 1)) == 0;
@@ -591,32 +573,99 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
             fill = fill + 1 == S::kStages ? 0 : fill + 1;
         };
+        // ---- whole tiles: a lane looks up one tile in 32 ----------------
+        const unsigned char *tile_src = nullptr;   // of the lane's tile of the 32 under way
+        unsigned tile_mask = 0;
+        int tile_page = -1;                        // page of the lane's tile of the next 32
+        auto tile_pos = [&](int i) { return e0 + i * (S::kWarps * S::kTile); };
+        auto tile_page_of = [&](const volatile Part &part, int i) -> int {
+            return i < mine ? __ldg(part.row_table + p.by_page((int)tile_pos(i))) : -1;
+        };
+        auto next_tiles = [&](const volatile Part &part, int i0) {
+            const int i = i0 + lane, pos = (int)tile_pos(i);
+            const bool ok = i < mine && (unsigned)tile_page < (unsigned)p.c.n_pages;
+            const int in_page = pos - p.by_page(i < mine ? pos : 0) * p.c.page_size;
+            tile_src = ok ? part.head_pool + tile_page * p.c.page_stride + (long long)in_page * S::kRecord
+                          : nullptr;
+            const int left = part.seen - pos;
+            tile_mask = !ok || left <= 0 ? 0u : left >= S::kTile ? S::kFullMask : (1u << left) - 1;
+            tile_page = tile_page_of(part, i + 32);
+        };
+        // tokens past the sequence's end are in the page too
+        auto issue_tile = [&](const volatile Part &part, int i) {
+            if (i > 0 && (i & 31) == 0)
+                next_tiles(part, i);
+            if (lane == (i & 31)) {
+                const uint32_t bar = barriers + fill * 8;
+                masks[fill] = tile_mask;
+                barrier_expect(bar, tile_mask ? S::kStageBytes : 0);
+                if (tile_mask)
+                    copy_bulk(shared_address(ring + fill * S::kStageBytes), tile_src, S::kStageBytes, bar);
+            }
+            fill = fill + 1 == S::kStages ? 0 : fill + 1;
+        };
 
-        // the ring held the last unit's results
+        // first copies and the queries, under way together; the ring held the
+        // last unit's results
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        int pos_next, page_next;
-        {
-            int pos[S::kStages], page[S::kStages];
-#pragma unroll
-            for (int s = 0; s < S::kStages; ++s)
-                pos[s] = position(s);
-#pragma unroll
-            for (int s = 0; s < S::kStages; ++s)
-                page[s] = page_of(pos[s]);
+        int pos_next = -1, page_next = -1, pos_after = -1;
+        if constexpr (kAligned) {
+            tile_page = tile_page_of(now, lane);
+            if (p.a.bf16)
+                load_queries<D, Rows, __nv_bfloat16>(p, unit, len, smem);
+            else
+                load_queries<D, Rows, __half>(p, unit, len, smem);
+            next_tiles(now, 0);
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
                 if (s < mine)
-                    issue(pos[s], page[s]);
+                    issue_tile(now, s);
+            }
+        } else {
+            int pos[S::kStages], page[S::kStages];
+#pragma unroll
+            for (int s = 0; s < S::kStages; ++s)
+                pos[s] = position(now, s);
+#pragma unroll
+            for (int s = 0; s < S::kStages; ++s)
+                page[s] = page_of(now, pos[s]);
+            if (p.a.bf16)
+                load_queries<D, Rows, __nv_bfloat16>(p, unit, len, smem);
+            else
+                load_queries<D, Rows, __half>(p, unit, len, smem);
+#pragma unroll
+            for (int s = 0; s < S::kStages - 1; ++s) {
+                if (s < mine)
+                    issue_tokens(now, pos[s], page[s]);
             }
             pos_next = pos[S::kStages - 1];
             page_next = page[S::kStages - 1];
+            pos_after = position(now, S::kStages);
         }
-        int pos_after = position(S::kStages);
+        if (threadIdx.x == 0) {
+            const bool last = zero + tiles - first == each * p.units;
+            part.list = now.list, part.row_table = now.row_table;
+            part.head_pool = now.head_pool, part.seen = now.seen;
+            part.next = zero + tiles;
+            part.next_first = last ? zero + tiles : first;
+            part.next_entry = entry + last;
+            part.u.b = unit.b, part.u.head = unit.head, part.u.query = unit.query;
+            part.u.row0 = unit.row0, part.u.rows = unit.rows;
+            part.whole = count == tiles;
+            part.begins = tile0 == 0;
+            if (tile0 == 0 && count < tiles) {
+                split->b = entry;
+                split->unit = u_in;
+                split->parts = (int)((zero + tiles - 1) / per - blockIdx.x) + 1;
+            }
+        }
+        __syncthreads();   // query operands and `part` are there
 
         // Output; two rows of the unit for each block of it that this lane
         // shares: row(b, c).
         float o[S::kGroups][S::kSubs][S::kBlocks][4];
         float top[S::kBlocks][2], sum[S::kBlocks][2], fac[S::kBlocks][2];
+        float low[S::kBlocks][2];     // maximum in base-2 units, 0 while there is none
         auto row = [&](int b, int c) { return S::kWide ? b * 16 + g + 8 * c : 2 * t + c; };
         int least = 0x7fffffff;
 #pragma unroll
@@ -624,7 +673,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 top[b][c] = -INFINITY;
-                sum[b][c] = 0.f;
+                sum[b][c] = low[b][c] = 0.f;
                 fac[b][c] = factor[row(b, c)];
                 if (row(b, c) < part.u.rows)
                     least = min(least, limit[row(b, c)]);
@@ -667,6 +716,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     const float m = row_max(fmaxf(best[b][c], top[b][c]));
                     down[c] = top[b][c] == -INFINITY ? 0.f : exp2_fast((top[b][c] - m) * fac[b][c]);
                     top[b][c] = m;
+                    low[b][c] = m == -INFINITY ? 0.f : m * fac[b][c];
                     sum[b][c] *= down[c];
                 }
 #pragma unroll
@@ -678,7 +728,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             o[i][s][b][e] *= down[state(e)];
             }
         };
-        auto low = [&](int b, int c) { return top[b][c] == -INFINITY ? 0.f : top[b][c] * fac[b][c]; };
         // operands of the four codes of each of two tokens in z: codes j of both
         auto value_codes = [](uint32_t z, int j) {
             return j == 0 ? low_codes(z) : j == 1 ? high_codes(z) : j == 2 ? low_codes(z >> 8)
@@ -688,7 +737,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         auto consume = [&](auto masked_tag, const unsigned char *tile, unsigned mask, int base) {
             constexpr bool kMasked = decltype(masked_tag)::value;
             auto seen_by = [&](int token, int r) -> bool {
-                return (mask >> token & 1) && (kListed || base + token < limit[r]);
+                return (mask >> token & 1) && (listed || base + token < limit[r]);
             };
             if constexpr (!S::kWide) {
                 float sc[S::kMT][4];
@@ -736,7 +785,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         best[0][e & 1] = fmaxf(best[0][e & 1], sc[mt][e]);
                     }
                 raise(best);
-                const float low0 = low(0, 0), low1 = low(0, 1);
 #pragma unroll
                 for (int mt = 0; mt < S::kMT; ++mt) {
                     const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kRecord;
@@ -745,7 +793,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     load_scales(sb, ra + S::kNext * S::kRecord + D + 2 * S::kGroups);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        pr[e] = exp2_fast(sc[mt][e] * fac[0][e & 1] - (e & 1 ? low1 : low0));
+                        pr[e] = exp2_fast(sc[mt][e] * fac[0][e & 1] - low[0][e & 1]);
                         if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
                             pr[e] = 0.f;
                         sum[0][e & 1] += pr[e];
@@ -843,12 +891,11 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     raise(best);
 #pragma unroll
                     for (int b = 0; b < S::kBlocks; ++b) {
-                        const float low0 = low(b, 0), low1 = low(b, 1);
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                float pr = exp2_fast(sc[b][half][e] * fac[b][e / 2] - (e / 2 ? low1 : low0));
+                                float pr = exp2_fast(sc[b][half][e] * fac[b][e / 2] - low[b][e / 2]);
                                 if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
                                     pr = 0.f;
                                 sum[b][e / 2] += pr;
@@ -907,11 +954,16 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         for (int i = 0; i < mine; ++i) {
             // every lane is done with the stage that is filled next
             __syncwarp();
-            if (i + S::kStages - 1 < mine)
-                issue(pos_next, page_next);
-            pos_next = pos_after;
-            page_next = page_of(pos_next);
-            pos_after = position(i + S::kStages + 1);
+            if constexpr (kAligned) {
+                if (i + S::kStages - 1 < mine)
+                    issue_tile(part, i + S::kStages - 1);
+            } else {
+                if (i + S::kStages - 1 < mine)
+                    issue_tokens(part, pos_next, page_next);
+                pos_next = pos_after;
+                page_next = page_of(part, pos_next);
+                pos_after = position(part, i + S::kStages + 1);
+            }
 
             const unsigned mask = masks[use];
             const bool came = barrier_wait(barriers + use * 8, phase);
@@ -920,9 +972,9 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 use = 0, phase ^= 1;
             if (!came)
                 lost = true;
-            const int base = kListed ? 0 : (int)(e0 - lane + i * (S::kWarps * S::kTile));
-            if (mask == (S::kTile == 32 ? ~0u : (1u << (S::kTile & 31)) - 1) &&
-                (kListed || base + S::kTile <= least))
+            const int base = listed ? 0 : (int)(e0 + i * (S::kWarps * S::kTile));
+            if (mask == S::kFullMask &&
+                (listed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
             else if (mask)
                 consume(std::true_type{}, data, mask, base);
@@ -940,9 +992,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 for (int step = S::kWide ? 1 : 4; step < (S::kWide ? 4 : 32); step *= 2)
                     s += __shfl_xor_sync(~0u, s, step);
                 if (S::kWide ? t == 0 : g == 0) {
-                    wmax(warp, r) = low(b, c);
-                    if (top[b][c] == -INFINITY)
-                        wmax(warp, r) = -INFINITY;
+                    wmax(warp, r) = top[b][c] == -INFINITY ? -INFINITY : low[b][c];
                     wsum(warp, r) = s;
                 }
                 // narrow: rows of the instruction are channels 4 g + {0, 1} and
@@ -1141,16 +1191,21 @@ int attend_grid(int sms)
     return sms * Shape<D, Rows>::kCtas;
 }
 
-template <int D, int Rows, bool kListed>
+template <int D, int Rows>
 cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
 {
     using S = Shape<D, Rows>;
-    const int ctas = attend_grid<D, Rows>(sms);
     p.blocks = (p.rows + S::kRows - 1) / S::kRows;
-    p.units = p.c.kv_heads * p.blocks * (kListed ? p.a.queries : 1);
+    p.units = p.c.kv_heads * p.blocks * (p.a.indices ? p.a.queries : 1);
     p.sel_tiles = ((long long)p.a.k + S::kTile - 1) / S::kTile;
+    // no more CTAs than the largest possible line has work for
+    const double room = (double)p.c.max_pages * p.c.page_size;
+    const double most = ((p.a.indices ? (double)p.sel_tiles : room / S::kTile + 1) + kUnitCost) * p.units *
+                        p.a.batch / (2 * S::kWarps);
+    int ctas = attend_grid<D, Rows>(sms);
+    ctas = most < ctas ? (int)most + 1 : ctas;
     p.parts = ctas * (long long)(sizeof(Split) / sizeof(float));
-    auto fn = attend_kernel<D, Rows, kListed>;
+    auto fn = p.run == S::kTile ? attend_kernel<D, Rows, true> : attend_kernel<D, Rows, false>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
@@ -1166,6 +1221,8 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, fn, (const AttendArgs)p)) != cudaSuccess)
         return e;
+    if (ctas == 1)
+        return cudaSuccess;    // nothing to join
     cfg.gridDim = dim3((unsigned)(ctas * Rows));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -1186,13 +1243,8 @@ cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t st
         p.run *= 2;
     p.rows = a.indices ? p.group : p.group * a.queries;
     const int rows = unit_rows<D>(p.rows);
-    if (a.indices)
-        return rows == 8    ? launch_shape<D, 8, true>(p, sms, stream)
-               : rows == 16 ? launch_shape<D, 16, true>(p, sms, stream)
-                            : launch_shape<D, kMost, true>(p, sms, stream);
-    return rows == 8    ? launch_shape<D, 8, false>(p, sms, stream)
-           : rows == 16 ? launch_shape<D, 16, false>(p, sms, stream)
-                        : launch_shape<D, kMost, false>(p, sms, stream);
+    return rows == 8    ? launch_shape<D, 8>(p, sms, stream)
+           : rows == 16 ? launch_shape<D, 16>(p, sms, stream) : launch_shape<D, kMost>(p, sms, stream);
 }
 
 template <int D, int Rows>
