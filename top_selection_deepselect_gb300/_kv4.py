@@ -127,38 +127,55 @@ def ds_pages_workspace(n_pages, n):
 
 
 # ---- torch convenience wrappers ------------------------------------------------
-def _torch():
-    import torch
-    return torch
+# These run once a layer and step, around kernels of a few microseconds: what
+# does not change (types, record sizes, workspace sizes) is looked up once.
+_RECORD = {64: 80, 128: 144, 256: 288}
+_torch_names = None
+
+
+def _names():
+    """(torch, int32, uint8, float32, dtype codes, raw stream of a device index)."""
+    global _torch_names
+    if _torch_names is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(index):
+                return torch.cuda.current_stream(index).cuda_stream
+        _torch_names = (torch, torch.int32, torch.uint8, torch.float32,
+                        {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}, raw)
+    return _torch_names
 
 
 def _code(dtype):
-    t = _torch()
-    code = {t.float32: DS_FP32, t.bfloat16: DS_BF16, t.float16: DS_FP16}.get(dtype)
+    code = _names()[4].get(dtype)
     if code is None:
         raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
     return code
 
 
-def _stream(x, stream):
-    return (stream or _torch().cuda.current_stream(x.device)).cuda_stream
+def _stream(device, stream):
+    return _names()[5](device.index) if stream is None else stream.cuda_stream
 
 
-def _int32(name, t, device, shape=None):
-    """Address of a contiguous CUDA int32 tensor."""
-    if t.dtype != _torch().int32 or t.device != device or not t.is_contiguous():
+def _int32(name, t, device, n=None):
+    """Address of a contiguous CUDA int32 tensor, of n entries in one dimension if given."""
+    if t.dtype is not _names()[1] or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if n is not None and (t.dim() != 1 or t.shape[0] != n):
+        raise ValueError("%s must have shape (%d,), got %s" % (name, n, tuple(t.shape)))
     return t.data_ptr()
 
 
-def _check_table(table, device):
-    if (table.dtype != _torch().int32 or table.device != device or table.dim() != 2
-            or table.stride(1) != 1 and table.shape[1] != 1):
-        raise ValueError("table must be an int32 [max_seqs, max_pages] tensor on %s with unit "
-                         "stride in the last dimension" % (device,))
-    return max(table.stride(0), table.shape[1])
+def _table(table, device):
+    """(address, row stride, rows, columns) of a page table."""
+    if table.dtype is not _names()[1] or table.device != device or table.dim() != 2:
+        raise ValueError("table must be an int32 [max_seqs, max_pages] tensor on %s" % (device,))
+    rows, columns = table.shape
+    stride, unit = table.stride()
+    if unit != 1 and columns != 1:
+        raise ValueError("table must have unit stride in the last dimension")
+    return table.data_ptr(), stride if stride > columns else columns, rows, columns
 
 
 def kv4_record_bytes(head_dim):
@@ -168,19 +185,20 @@ def kv4_record_bytes(head_dim):
 
 def _cache(pool, table, head_dim):
     """Descriptor of a pool [n_pages, kv_heads, page_size, record bytes] (uint8) and its table."""
-    if pool.dtype != _torch().uint8 or not pool.is_cuda or pool.dim() != 4:
+    if pool.dtype is not _names()[2] or not pool.is_cuda or pool.dim() != 4:
         raise ValueError("pool must be a 4-D CUDA uint8 tensor [n_pages, kv_heads, page_size, "
                          "record bytes]")
     n_pages, kv_heads, page_size, rec = pool.shape
-    if rec != ds_kv4_record_bytes(head_dim):
+    if rec != _RECORD.get(head_dim):
         raise ValueError("head_dim %d has records of %d bytes, the pool has %d"
                          % (head_dim, ds_kv4_record_bytes(head_dim), rec))
-    if not pool[:1].is_contiguous():
+    stride = pool.stride()
+    page = kv_heads * page_size * rec
+    if stride[1:] != (page_size * rec, rec, 1) and not pool[:1].is_contiguous():
         raise ValueError("each page of pool must be contiguous")
-    stride = max(pool.stride(0), kv_heads * page_size * rec)
-    return ds_kv4_cache_t(pool.data_ptr(), stride, table.data_ptr(),
-                          _check_table(table, pool.device), n_pages, page_size, kv_heads, head_dim,
-                          *table.shape)
+    at, row, rows, columns = _table(table, pool.device)
+    return ds_kv4_cache_t(pool.data_ptr(), stride[0] if stride[0] > page else page, at, row, n_pages,
+                          page_size, kv_heads, head_dim, rows, columns)
 
 
 def kv4_append(pool, table, seq, pos, k, v, stream=None):
@@ -194,15 +212,16 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
     tokens, heads, dim = k.shape
     cache = _cache(pool, table, dim)
-    if heads != cache.kv_heads:
-        raise ValueError("k has %d heads, the pool %d" % (heads, cache.kv_heads))
-    if k.device != pool.device or v.device != pool.device or k.stride(2) != 1 or v.stride(2) != 1:
+    if heads != pool.shape[1]:
+        raise ValueError("k has %d heads, the pool %d" % (heads, pool.shape[1]))
+    device = pool.device
+    ks, vs = k.stride(), v.stride()
+    if k.device != device or v.device != device or ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must be on the pool's device with unit stride in the last "
                          "dimension")
-    ds_kv4_append(cache, _int32("seq", seq, pool.device, (tokens,)),
-                  _int32("pos", pos, pool.device, (tokens,)), tokens, _code(k.dtype),
-                  k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2],
-                  _stream(pool, stream))
+    ds_kv4_append(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
+                  tokens, _code(k.dtype), k.data_ptr(), ks[:2], v.data_ptr(), vs[:2],
+                  _stream(device, stream))
 
 
 def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None):
@@ -211,21 +230,36 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
     Returns (k, v), each [tokens, kv_heads, head_dim] of `dtype`; a token that
     is not there reads as zeros.
     """
-    torch = _torch()
     cache = _cache(pool, table, head_dim)
-    shape = (seq.numel(), cache.kv_heads, head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=pool.device)
-    if v is None:
-        v = torch.empty(shape, dtype=dtype, device=pool.device)
-    for t in (k, v):
-        if (tuple(t.shape) != shape or t.dtype != dtype or t.device != pool.device
+    tokens, device = seq.numel(), pool.device
+    shape = (tokens, pool.shape[1], head_dim)
+    code = _code(dtype)
+    given = [t for t in (k, v) if t is not None]
+    for t in given:
+        if (tuple(t.shape) != shape or t.dtype != dtype or t.device != device
                 or not t.is_contiguous()):
             raise ValueError("k and v must be contiguous %s tensors of %s" % (shape, dtype))
-    ds_kv4_read(cache, _int32("seq", seq, pool.device, shape[:1]),
-                _int32("pos", pos, pool.device, shape[:1]), shape[0], _code(dtype), k.data_ptr(),
-                v.data_ptr(), _stream(pool, stream))
+    if k is None:
+        k = _names()[0].empty(shape, dtype=dtype, device=device)
+    if v is None:
+        v = _names()[0].empty(shape, dtype=dtype, device=device)
+    ds_kv4_read(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
+                tokens, code, k.data_ptr(), v.data_ptr(), _stream(device, stream))
     return k, v
+
+
+_attention_bytes = {}
+
+
+def _attention_workspace(cache, batch, queries, heads, k, device):
+    """Workspace bytes, which depend on these sizes and the device alone."""
+    key = (cache.head_dim, cache.kv_heads, queries, heads, k > 0, device.index)
+    need = _attention_bytes.get(key)
+    if need is None:
+        if len(_attention_bytes) > 1000:
+            _attention_bytes.clear()
+        need = _attention_bytes[key] = ds_kv4_attention_workspace(cache, batch, queries, heads, k)
+    return need
 
 
 def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, out=None, lse=None,
@@ -242,94 +276,103 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     like q, lse float32 [batch, queries, heads]; a query that sees nothing gives
     0 and -inf.
     """
-    torch = _torch()
-    if q.dim() != 4 or q.device != pool.device or q.stride(3) != 1 and q.shape[3] != 1:
-        raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device with "
-                         "unit stride in the last dimension")
-    batch, queries, heads, dim = q.shape
-    cache = _cache(pool, table, dim)
-    code = _code(q.dtype)
+    torch, _, _, float32, codes, _ = _names()
     device = pool.device
-    at = _int32("lengths", lengths, device, (cache.max_seqs,))
-    if seqs is None:
-        if batch > cache.max_seqs:
-            raise ValueError("batch = %d is above the table's %d sequences" % (batch, cache.max_seqs))
-        seqs_at = None
-    else:
-        seqs_at = _int32("seqs", seqs, device, (batch,))
-    k, list_at = 0, None
+    if q.dim() != 4 or q.device != device:
+        raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device")
+    shape, qs, dtype = q.shape, q.stride(), q.dtype
+    batch, queries, heads, dim = shape
+    if qs[3] != 1:
+        raise ValueError("q must have unit stride in the last dimension")
+    cache = _cache(pool, table, dim)
+    code = codes.get(dtype)
+    if code is None:
+        raise TypeError("q must be bfloat16 or float16, got %s" % dtype)
+    rows = table.shape[0]
+    at = _int32("lengths", lengths, device, rows)
+    seqs_at = list_at = None
+    if seqs is not None:
+        seqs_at = _int32("seqs", seqs, device, batch)
+    elif batch > rows:
+        raise ValueError("batch = %d is above the table's %d sequences" % (batch, rows))
+    k = 0
     if indices is not None:
         if indices.dim() != 3 or indices.shape[0] != batch or indices.shape[1] != queries:
             raise ValueError("indices must be [batch, queries, k]")
         k = indices.shape[2]
         list_at = _int32("indices", indices, device)
     if out is None:
-        out = torch.empty((batch, queries, heads, dim), dtype=q.dtype, device=device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != device or not out.is_contiguous():
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if lse is None:
-        lse = torch.empty((batch, queries, heads), dtype=torch.float32, device=device)
-    elif (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != device
+        lse = torch.empty(shape[:3], dtype=float32, device=device)
+    elif (lse.shape != shape[:3] or lse.dtype != float32 or lse.device != device
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [batch, queries, heads] tensor")
     if indices is not None and k == 0:
         out.zero_()
         lse.fill_(-math.inf)
         return out, lse
-    need = ds_kv4_attention_workspace(cache, batch, queries, heads, k)
+    need = _attention_workspace(cache, batch, queries, heads, k, device)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace has %d bytes, %d needed"
-                         % (workspace.numel() * workspace.element_size(), need))
-    ds_kv4_attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(), q.stride()[:3],
-                     list_at, k, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(),
-                     lse.data_ptr(), workspace.data_ptr(),
-                     workspace.numel() * workspace.element_size(), _stream(pool, stream))
+        workspace, size = torch.empty(need, dtype=torch.uint8, device=device), need
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if size < need or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on %s with %d bytes, got %d"
+                             % (device, need, size))
+    ds_kv4_attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(), qs[:3], list_at,
+                     k, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(),
+                     lse.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
     return out, lse
 
 
 def _pool(pool):
     """Descriptor of a pool [layers, n_pages, ...] of pages of any content."""
-    if not pool.is_cuda or pool.dim() < 3:
+    shape = pool.shape
+    if not pool.is_cuda or len(shape) < 3:
         raise ValueError("pool must be a CUDA tensor [layers, n_pages, ...]")
-    layers, n_pages = pool.shape[:2]
-    if not pool[:1, :1].is_contiguous():
+    if not (pool.is_contiguous() or pool[:1, :1].is_contiguous()):
         raise ValueError("each page of pool must be contiguous")
     size = pool.element_size()
-    page = pool[0, 0].numel() * size
-    return ds_page_pool_t(pool.data_ptr(), pool.stride(0) * size, max(pool.stride(1) * size, page),
-                          page, layers, n_pages)
+    page = math.prod(shape[2:]) * size
+    layer, each = pool.stride()[:2]
+    return ds_page_pool_t(pool.data_ptr(), layer * size, max(each * size, page), page, *shape[:2])
 
 
 def _book(table, lengths, refs, page_size):
     device = table.device
     if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor")
-    stride = _check_table(table, device)
-    return ds_page_book_t(
-        table.data_ptr(), stride,
-        None if lengths is None else _int32("lengths", lengths, device, (table.shape[0],)),
-        _int32("refs", refs, device), *table.shape, page_size, refs.numel())
+    at, stride, rows, columns = _table(table, device)
+    return ds_page_book_t(at, stride,
+                          None if lengths is None else _int32("lengths", lengths, device, rows),
+                          _int32("refs", refs, device), rows, columns, page_size, refs.numel())
 
 
 def _work(device, n_pages, n, workspace, status):
-    torch = _torch()
+    """(workspace address, its bytes, status); ones that are not given are made."""
+    torch = _names()[0]
     need = ds_pages_workspace(n_pages, n)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace, size = torch.empty(need, dtype=torch.uint8, device=device), need
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on %s" % (device,))
     if status is None:
         status = torch.empty(2, dtype=torch.int32, device=device)
     else:
-        _int32("status", status, device, (2,))
-    return workspace, workspace.numel() * workspace.element_size(), status
+        _int32("status", status, device, 2)
+    return workspace, size, status
 
 
 def pages_copy(pool, src, dst, stream=None):
     """Page dst[i] of pool [layers, n_pages, ...] := page src[i], in every layer (int32 lists)."""
-    n = src.numel()
-    ds_pages_copy(_pool(pool), _int32("src", src, pool.device, (n,)),
-                  _int32("dst", dst, pool.device, (n,)), n, _stream(pool, stream))
+    n, device = src.numel(), pool.device
+    ds_pages_copy(_pool(pool), _int32("src", src, device, n), _int32("dst", dst, device, n), n,
+                  _stream(device, stream))
 
 
 def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None, status=None,
@@ -339,12 +382,11 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     All or nothing.  Returns status, int32 [2]: pages short (nothing changed
     when above 0), pages taken.
     """
-    n = seqs.numel()
+    n, device = seqs.numel(), table.device
     book = _book(table, lengths, refs, page_size)
-    workspace, size, status = _work(table.device, book.n_pages, n, workspace, status)
-    ds_pages_reserve(book, _int32("seqs", seqs, table.device, (n,)),
-                     _int32("tokens", tokens, table.device, (n,)), n, status.data_ptr(),
-                     workspace.data_ptr(), size, _stream(table, stream))
+    workspace, size, status = _work(device, book.n_pages, n, workspace, status)
+    ds_pages_reserve(book, _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n), n,
+                     status.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
     return status
 
 
@@ -354,22 +396,22 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     pool: [layers, n_pages, kv_heads, page_size, record bytes].  All or nothing;
     returns status as pages_reserve does.
     """
-    n = src.numel()
-    if pool.dim() != 5:
-        raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes]")
+    if pool.dim() != 5 or pool.device != table.device:
+        raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes] on the "
+                         "table's device")
+    n, device = src.numel(), table.device
     book = _book(table, lengths, refs, pool.shape[3])
-    workspace, size, status = _work(table.device, book.n_pages, n, workspace, status)
-    ds_pages_fork(_pool(pool), book, _int32("src", src, table.device, (n,)),
-                  _int32("dst", dst, table.device, (n,)), n, status.data_ptr(),
-                  workspace.data_ptr(), size, _stream(pool, stream))
+    workspace, size, status = _work(device, book.n_pages, n, workspace, status)
+    ds_pages_fork(_pool(pool), book, _int32("src", src, device, n), _int32("dst", dst, device, n), n,
+                  status.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
     return status
 
 
 def pages_free(table, lengths, refs, seqs, page_size, stream=None):
     """The sequences seqs[i] end: their pages' refs go down, their rows become -1."""
-    n = seqs.numel()
-    ds_pages_free(_book(table, lengths, refs, page_size),
-                  _int32("seqs", seqs, table.device, (n,)), n, _stream(table, stream))
+    n, device = seqs.numel(), table.device
+    ds_pages_free(_book(table, lengths, refs, page_size), _int32("seqs", seqs, device, n), n,
+                  _stream(device, stream))
 
 
 def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, stream=None):
@@ -378,11 +420,14 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
     Returns (remap int32 [n_pages]: new number of each page or -1, status int32
     [2]: live pages, pages moved).
     """
-    torch = _torch()
+    device = table.device
+    if pool.device != device:
+        raise ValueError("pool and table must be on one device")
     book = _book(table, None, refs, 1)
+    n_pages = book.n_pages
     if remap is None:
-        remap = torch.empty(book.n_pages, dtype=torch.int32, device=table.device)
-    workspace, size, status = _work(table.device, book.n_pages, 0, workspace, status)
-    ds_pages_compact(_pool(pool), book, _int32("remap", remap, table.device, (book.n_pages,)),
-                     status.data_ptr(), workspace.data_ptr(), size, _stream(pool, stream))
+        remap = _names()[0].empty(n_pages, dtype=_names()[1], device=device)
+    workspace, size, status = _work(device, n_pages, 0, workspace, status)
+    ds_pages_compact(_pool(pool), book, _int32("remap", remap, device, n_pages), status.data_ptr(),
+                     workspace.data_ptr(), size, _stream(device, stream))
     return remap, status
