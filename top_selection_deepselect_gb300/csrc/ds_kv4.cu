@@ -48,6 +48,7 @@ int check_cache(const ds_kv4_cache_t *c, Cache *out)
     out->kv_heads = c->kv_heads;
     out->max_seqs = c->max_seqs;
     out->max_pages = c->max_pages;
+    out->by_page.set(c->page_size);
     return DS_OK;
 }
 
@@ -58,12 +59,12 @@ int check_dtype(int dtype)
     return DS_OK;
 }
 
-int check_tokens(const Cache &c, int head_dim, const int32_t *seq, const int32_t *pos,
-                 int64_t tokens, const void *k, const void *v)
+int check_tokens(const Cache &c, const int32_t *seq, const int32_t *pos, int64_t tokens,
+                 const void *k, const void *v)
 {
     if (tokens < 0)
         return fail(DS_EINVAL, "tokens = %lld is negative", (long long)tokens);
-    if (tokens >= 1LL << 31 || ds::kv4::store_blocks(c, head_dim, tokens) >= 1LL << 31)
+    if (!ds::kv4::store_fits(c, tokens))
         return fail(DS_EUNSUPPORTED, "tokens = %lld are too many for one call", (long long)tokens);
     if (tokens > 0 && (!seq || !pos || !k || !v))
         return fail(DS_EINVAL, "seq, pos, k and v must be non-NULL when tokens > 0");
@@ -115,7 +116,7 @@ int ds_kv4_append(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t
     if (rc == DS_OK)
         rc = check_dtype(dtype);
     if (rc == DS_OK)
-        rc = check_tokens(c, cache->head_dim, seq, pos, tokens, k, v);
+        rc = check_tokens(c, seq, pos, tokens, k, v);
     if (rc != DS_OK)
         return rc;
     if (!k_stride || !v_stride)
@@ -139,7 +140,7 @@ int ds_kv4_read(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t *
     if (rc == DS_OK)
         rc = check_dtype(dtype);
     if (rc == DS_OK)
-        rc = check_tokens(c, cache->head_dim, seq, pos, tokens, k, v);
+        rc = check_tokens(c, seq, pos, tokens, k, v);
     if (rc != DS_OK)
         return rc;
     if (tokens == 0)

@@ -17,12 +17,32 @@ constexpr int kGroup = 32;  // channels that share a scale
 __host__ __device__ constexpr int data_bytes(int d) { return d + 4 * (d / kGroup); }
 __host__ __device__ constexpr int record_bytes(int d) { return (data_bytes(d) + 15) / 16 * 16; }
 
+// Quotient by a fixed divisor of numbers below 2^31: n d' / 2^shift with
+// d' = 2^shift / d rounded up, shift = 31 + ceil(log2 d), which is exact there.
+struct Divider {
+    unsigned mul;
+    int shift;
+    void set(int d)
+    {
+        int l = 0;
+        while ((1LL << l) < d)
+            ++l;
+        mul = (unsigned)(((1ULL << (31 + l)) + d - 1) / d);
+        shift = 31 + l;
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return (int)((unsigned long long)(unsigned)n * mul >> shift);
+    }
+};
+
 struct Cache {
     unsigned char *pool;
     long long page_stride;
     const int32_t *table;
     long long table_stride;
     int n_pages, page_size, kv_heads, max_seqs, max_pages;
+    Divider by_page;
 };
 
 // Token slot (page * page_size + offset) of position `pos` of sequence `seq`,
@@ -31,7 +51,7 @@ __device__ __forceinline__ int token_slot(const Cache &c, int seq, int pos)
 {
     if ((unsigned)seq >= (unsigned)c.max_seqs || pos < 0)
         return -1;
-    const int col = pos / c.page_size;
+    const int col = c.by_page(pos);
     if (col >= c.max_pages)
         return -1;
     const int page = __ldg(c.table + seq * c.table_stride + col);
@@ -45,7 +65,7 @@ __device__ __forceinline__ int token_slot(const Cache &c, int seq, int pos)
 template <int D>
 __device__ __forceinline__ long long record_offset(const Cache &c, int slot, int head)
 {
-    const int page = slot / c.page_size;
+    const int page = c.by_page(slot);
     return page * c.page_stride +
            ((long long)head * c.page_size + (slot - page * c.page_size)) * record_bytes(D);
 }

@@ -50,24 +50,6 @@
 namespace ds {
 namespace kv4 {
 
-// Quotient by a fixed divisor of numbers below 2^31.
-struct Divider {
-    unsigned mul;
-    int shift;
-    void set(int d)
-    {
-        int l = 0;
-        while ((1LL << l) < d)
-            ++l;
-        mul = (unsigned)(((1ULL << (31 + l)) + d - 1) / d);
-        shift = 31 + l;
-    }
-    __device__ __forceinline__ int operator()(int n) const
-    {
-        return (int)((unsigned long long)(unsigned)n * mul >> shift);
-    }
-};
-
 // Shape of one instantiation: head dimension, query rows of a unit (8, 16, 32).
 template <int D, int Rows>
 struct Shape {
@@ -122,7 +104,6 @@ struct Shape {
 struct AttendArgs {
     Cache c;
     Attend a;
-    Divider by_page;
     long long sel_tiles;  // tiles of a unit when tokens are listed
     long long parts;      // floats of the workspace before the partial results
     int run;              // tokens of a tile that lie side by side in a page, a power of two
@@ -405,66 +386,93 @@ struct alignas(16) Split {
 // Query operands of a unit, the rows' factors and limits.  A row is scaled by a
 // power of two to magnitudes of 2^14 to 2^15, so that fp16 holds every bf16 and
 // fp16 value of it (down to 2^-39 of the largest, below which it adds nothing).
-template <int D, int Rows, typename T>
-__device__ __forceinline__ void load_queries(const AttendArgs &p, const Unit &u, int len,
-                                             unsigned char *smem)
-{
+template <int D, int Rows>
+struct Queries {
     using S = Shape<D, Rows>;
-    constexpr int kMine = D / 32;                  // channels of a lane
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    __half *frag = reinterpret_cast<__half *>(smem + S::kOffQ);
-    float *factor = reinterpret_cast<float *>(smem + S::kOffFactor);
-    int *limit = reinterpret_cast<int *>(smem + S::kOffLimit);
-    for (int r = warp; r < S::kRows; r += S::kWarps) {
-        float x[kMine];
-        int j = 0, h = 0;
-        const bool in = r < u.rows;
-        u.row(p, in ? r : 0, &j, &h);
-        const T *q = (const T *)p.a.q + u.b * p.a.q_batch + j * p.a.q_query + h * p.a.q_head;
-        float most = 0.f;
-        bool odd = false;
+    static constexpr int kMine = D / 32;                                    // channels of a lane
+    static constexpr int kTurns = (Rows + S::kWarps - 1) / S::kWarps;       // rows of a warp
+    float x[kTurns][kMine];
+
+    template <typename T>
+    __device__ __forceinline__ void load(const AttendArgs &p, const Unit &u)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
 #pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-            x[e] = in ? to_float(q[lane * kMine + e]) : 0.f;
-            odd |= !(fabsf(x[e]) <= 3.402823466e38f);
-            most = fmaxf(most, fabsf(x[e]));
-        }
+        for (int i = 0; i < kTurns; ++i) {
+            const int r = warp + i * S::kWarps;
+            const bool in = r < u.rows;
+            int j = 0, h = 0;
+            u.row(p, in ? r : 0, &j, &h);
+            const T *q = (const T *)p.a.q + u.b * p.a.q_batch + j * p.a.q_query + h * p.a.q_head;
 #pragma unroll
-        for (int step = 16; step; step /= 2)
-            most = fmaxf(most, __shfl_xor_sync(~0u, most, step));
-        odd = __any_sync(~0u, odd);
-        int up = most > 0.f && !odd ? 14 - ((int)(__float_as_uint(most) >> 23) - 127) : 0;
-        up = up > 100 ? 100 : up;
-        const float lift = copysignf(__uint_as_float((unsigned)(up + 127) << 23), p.a.scale);
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-            const int d = lane * kMine + e, w = d / 8, n = d % 8;
-            const int group = d / kGroup, t = w % 4, half = n / 4, reg = n % 2, second = n % 4 / 2;
-            // operand register of the lane that holds row r % 8, place 2 t:
-            // narrow {reg}, wide {reg, row / 8 % 2}
-            const int at = S::kWide ? (((group * 2 + second) * S::kBlocks + r / 16) * 32 + r % 8 * 4 + t) * 4 +
-                                          reg * 2 + r / 8 % 2
-                                    : ((group * 2 + second) * 32 + r * 4 + t) * 2 + reg;
-            frag[at * 2 + half] = __float2half_rn(x[e] * lift * (reg ? 0.0625f : 1.f));
-        }
-        if (lane == 0) {
-            // score in base-2 units = sum * factor, which is not negative
-            factor[r] = ldexpf(fabsf(p.a.scale) * 1.4426950408889634f, -up);
-            const int see = len - p.a.queries + 1 + j;
-            limit[r] = in && see > 0 ? see : 0;
+            for (int e = 0; e < kMine; ++e)
+                x[i][e] = in ? to_float(q[lane * kMine + e]) : 0.f;
         }
     }
-}
 
-// kAligned: every token is attended and a page holds whole tiles, so that a tile
-// is one run of bytes; otherwise tokens are looked up one by one, listed or
-// not.
-template <int D, int Rows, bool kAligned>
+    __device__ __forceinline__ void load(const AttendArgs &p, const Unit &u)
+    {
+        if (p.a.bf16)
+            load<__nv_bfloat16>(p, u);
+        else
+            load<__half>(p, u);
+    }
+
+    __device__ __forceinline__ void store(const AttendArgs &p, const Unit &u, int len, unsigned char *smem)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        __half *frag = reinterpret_cast<__half *>(smem + S::kOffQ);
+        float *factor = reinterpret_cast<float *>(smem + S::kOffFactor);
+        int *limit = reinterpret_cast<int *>(smem + S::kOffLimit);
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int r = warp + i * S::kWarps;
+            if (r >= Rows)
+                break;
+            // the bits of magnitudes are in the magnitudes' order, those that
+            // are not finite above all others
+            unsigned most = 0;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e)
+                most = max(most, __float_as_uint(x[i][e]) & 0x7fffffffu);
+            most = __reduce_max_sync(~0u, most);
+            int up = most > 0 && most < 0x7f800000u ? 14 + 127 - (int)(most >> 23) : 0;
+            up = up > 100 ? 100 : up;
+            const float lift = copysignf(__uint_as_float((unsigned)(up + 127) << 23), p.a.scale);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int d = lane * kMine + e, w = d / 8, n = d % 8;
+                const int group = d / kGroup, t = w % 4, half = n / 4, reg = n % 2, second = n % 4 / 2;
+                // operand register of the lane that holds row r % 8, place 2 t:
+                // narrow {reg}, wide {reg, row / 8 % 2}
+                const int at = S::kWide ? (((group * 2 + second) * S::kBlocks + r / 16) * 32 + r % 8 * 4 + t) * 4 +
+                                              reg * 2 + r / 8 % 2
+                                        : ((group * 2 + second) * 32 + r * 4 + t) * 2 + reg;
+                frag[at * 2 + half] = __float2half_rn(x[i][e] * lift * (reg ? 0.0625f : 1.f));
+            }
+            if (lane == 0) {
+                // score in base-2 units = sum * factor, which is not negative;
+                // 2^-up in two steps, each of them a normal number
+                const float down = __uint_as_float((unsigned)(127 - up / 2) << 23) *
+                                   (fabsf(p.a.scale) * 1.4426950408889634f);
+                factor[r] = down * __uint_as_float((unsigned)(127 - (up - up / 2)) << 23);
+                int j, h;
+                u.row(p, r < u.rows ? r : 0, &j, &h);
+                const int see = len - p.a.queries + 1 + j;
+                limit[r] = r < u.rows && see > 0 ? see : 0;
+            }
+        }
+    }
+};
+
+// kRun: every token is attended and pages hold whole runs of this many tokens,
+// a tile or half of one; 0: tokens are looked up one by one, listed or not.
+template <int D, int Rows, int kRun>
 __global__ void __launch_bounds__((Shape<D, Rows>::kThreads), (Shape<D, Rows>::kCtas))
 attend_kernel(const __grid_constant__ AttendArgs p)
 {
     using S = Shape<D, Rows>;
-    const bool listed = !kAligned && p.a.indices != nullptr;
+    const bool listed = kRun == 0 && p.a.indices != nullptr;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
     long long *scratch = reinterpret_cast<long long *>(smem + S::kOffScan);
@@ -550,7 +558,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             return pos < part.seen ? pos : -1;
         };
         auto page_of = [&](const volatile Part &part, int pos) -> int {
-            return pos >= 0 ? __ldg(part.row_table + p.by_page(pos)) : -1;
+            return pos >= 0 ? __ldg(part.row_table + p.c.by_page(pos)) : -1;
         };
         // Copies the records of a tile: a lane each, or, where `run` neighbours
         // lie side by side in a page, one lane for all of them.  A run's tokens
@@ -566,42 +574,57 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
             __syncwarp();
             if (leads) {
-                const int in_page = pos - p.by_page(pos) * p.c.page_size;
+                const int in_page = pos - p.c.by_page(pos) * p.c.page_size;
                 copy_bulk(dst + lane * S::kRecord,
                           part.head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
                           p.run * S::kRecord, bar);
             }
             fill = fill + 1 == S::kStages ? 0 : fill + 1;
         };
-        // ---- whole tiles: a lane looks up one tile in 32 ----------------
-        const unsigned char *tile_src = nullptr;   // of the lane's tile of the 32 under way
-        unsigned tile_mask = 0;
-        int tile_page = -1;                        // page of the lane's tile of the next 32
-        auto tile_pos = [&](int i) { return e0 + i * (S::kWarps * S::kTile); };
-        auto tile_page_of = [&](const volatile Part &part, int i) -> int {
-            return i < mine ? __ldg(part.row_table + p.by_page((int)tile_pos(i))) : -1;
+        // ---- runs: a lane looks up one of 32 whole runs ------------------
+        // Tile i is run(s) i << halves and the next; 32 runs are looked up at once.
+        constexpr int halves = kRun > 0 && kRun < S::kTile ? 1 : 0, per_look = 32 >> halves;
+        const unsigned char *run_src = nullptr;    // of the lane's run of those under way
+        unsigned tile_mask = 0;                    // of the run's tile
+        int run_page = -1;                         // of the lane's run of the next ones
+        auto run_pos = [&](int i0) {
+            return (int)(e0 + (i0 + (lane >> halves)) * (S::kWarps * S::kTile) + (lane & halves) * kRun);
         };
-        auto next_tiles = [&](const volatile Part &part, int i0) {
-            const int i = i0 + lane, pos = (int)tile_pos(i);
-            const bool ok = i < mine && (unsigned)tile_page < (unsigned)p.c.n_pages;
-            const int in_page = pos - p.by_page(i < mine ? pos : 0) * p.c.page_size;
-            tile_src = ok ? part.head_pool + tile_page * p.c.page_stride + (long long)in_page * S::kRecord
-                          : nullptr;
-            const int left = part.seen - pos;
-            tile_mask = !ok || left <= 0 ? 0u : left >= S::kTile ? S::kFullMask : (1u << left) - 1;
-            tile_page = tile_page_of(part, i + 32);
+        auto run_page_of = [&](const volatile Part &part, int i0) -> int {
+            const int pos = run_pos(i0);
+            return i0 + (lane >> halves) < mine && (unsigned)pos < (unsigned)part.seen
+                       ? __ldg(part.row_table + p.c.by_page(pos)) : -1;
+        };
+        auto next_runs = [&](const volatile Part &part, int i0) {
+            const int pos = run_pos(i0);
+            const bool ok = (unsigned)run_page < (unsigned)p.c.n_pages;
+            const int in_page = ok ? pos - p.c.by_page(pos) * p.c.page_size : 0;
+            run_src = ok ? part.head_pool + run_page * p.c.page_stride + (long long)in_page * S::kRecord
+                         : nullptr;
+            const int left = part.seen - pos;      // > 0 where there is a page
+            tile_mask = !ok ? 0u : ~0u >> (32 - (left < kRun ? left : kRun));
+            if (halves) {
+                tile_mask <<= (lane & 1) * 16;
+                tile_mask |= __shfl_xor_sync(~0u, tile_mask, 1);
+            }
+            run_page = run_page_of(part, i0 + per_look);
         };
         // tokens past the sequence's end are in the page too
-        auto issue_tile = [&](const volatile Part &part, int i) {
-            if (i > 0 && (i & 31) == 0)
-                next_tiles(part, i);
-            if (lane == (i & 31)) {
-                const uint32_t bar = barriers + fill * 8;
+        auto issue_runs = [&](const volatile Part &part, int i) {
+            const int turn = i & (per_look - 1);
+            if (i > 0 && turn == 0)
+                next_runs(part, i);
+            const uint32_t bar = barriers + fill * 8;
+            if (lane == turn << halves) {
                 masks[fill] = tile_mask;
-                barrier_expect(bar, tile_mask ? S::kStageBytes : 0);
-                if (tile_mask)
-                    copy_bulk(shared_address(ring + fill * S::kStageBytes), tile_src, S::kStageBytes, bar);
+                const int runs = !halves ? tile_mask != 0 : ((tile_mask & 0xffffu) != 0) + (tile_mask > 0xffffu);
+                barrier_expect(bar, runs * kRun * S::kRecord);
             }
+            if (halves)
+                __syncwarp();
+            if (lane >> halves == turn && run_src)
+                copy_bulk(shared_address(ring + fill * S::kStageBytes) + (lane & halves) * kRun * S::kRecord,
+                          run_src, kRun * S::kRecord, bar);
             fill = fill + 1 == S::kStages ? 0 : fill + 1;
         };
 
@@ -609,17 +632,15 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         // last unit's results
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         int pos_next = -1, page_next = -1, pos_after = -1;
-        if constexpr (kAligned) {
-            tile_page = tile_page_of(now, lane);
-            if (p.a.bf16)
-                load_queries<D, Rows, __nv_bfloat16>(p, unit, len, smem);
-            else
-                load_queries<D, Rows, __half>(p, unit, len, smem);
-            next_tiles(now, 0);
+        Queries<D, Rows> queries;
+        if constexpr (kRun > 0) {
+            run_page = run_page_of(now, 0);
+            queries.load(p, unit);
+            next_runs(now, 0);
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
                 if (s < mine)
-                    issue_tile(now, s);
+                    issue_runs(now, s);
             }
         } else {
             int pos[S::kStages], page[S::kStages];
@@ -629,10 +650,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
             for (int s = 0; s < S::kStages; ++s)
                 page[s] = page_of(now, pos[s]);
-            if (p.a.bf16)
-                load_queries<D, Rows, __nv_bfloat16>(p, unit, len, smem);
-            else
-                load_queries<D, Rows, __half>(p, unit, len, smem);
+            queries.load(p, unit);
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
                 if (s < mine)
@@ -642,6 +660,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             page_next = page[S::kStages - 1];
             pos_after = position(now, S::kStages);
         }
+        queries.store(p, unit, len, smem);
         if (threadIdx.x == 0) {
             const bool last = zero + tiles - first == each * p.units;
             part.list = now.list, part.row_table = now.row_table;
@@ -954,9 +973,9 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         for (int i = 0; i < mine; ++i) {
             // every lane is done with the stage that is filled next
             __syncwarp();
-            if constexpr (kAligned) {
+            if constexpr (kRun > 0) {
                 if (i + S::kStages - 1 < mine)
-                    issue_tile(part, i + S::kStages - 1);
+                    issue_runs(part, i + S::kStages - 1);
             } else {
                 if (i + S::kStages - 1 < mine)
                     issue_tokens(part, pos_next, page_next);
@@ -1092,21 +1111,20 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     }
 }
 
-// Joins the partial results of units that several CTAs worked on, a CTA for
-// each query row of the unit that began in attending CTA blockIdx.x / Rows: the
-// weights of the parts first, then D/4 threads for a part's row, the parts
-// dealt out to the rest and their sums added in order.
-constexpr int kJoinThreads = 128;
+// Joins the partial results of units that several CTAs worked on: for the unit
+// that began in attending CTA blockIdx.x / (Rows / 8), a warp a query row, parts
+// in order.  All CTAs together have at most two parts each, so that many parts
+// of one unit mean few units.
+constexpr int kJoinThreads = 256;
 
 template <int D, int Rows>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const __grid_constant__ AttendArgs p)
 {
     using S = Shape<D, Rows>;
-    constexpr int kLanes = D / 4, kTeams = kJoinThreads / kLanes;
-    __shared__ float weight[kJoinThreads], red[kJoinThreads / 32], teams[kTeams][D + 4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int cta = blockIdx.x / Rows, r = blockIdx.x % Rows;
+    constexpr int kMine = D / 32, kAhead = 32 / kMine;      // channels of a lane; parts under way
+    const int lane = threadIdx.x & 31;
+    const int cta = blockIdx.x / (Rows / 8), r = blockIdx.x % (Rows / 8) * 8 + threadIdx.x / 32;
     dependent_grid_wait();
     const int4 split = reinterpret_cast<const int4 *>(p.a.partial)[cta];
     const int parts = split.z;
@@ -1115,64 +1133,53 @@ join_kernel(const __grid_constant__ AttendArgs p)
     const Unit u(p, split.x, split.y, Rows);
     if (r >= u.rows)
         return;
+    // a CTA's second place holds the unit that begins in it
     const float *base = p.a.partial + p.parts + 2LL * cta * S::kPartial;
     auto place = [&](int i) { return base + (i == 0 ? 1 : 2 * i) * (long long)S::kPartial; };
-    auto joined = [&](float v, auto add) {
-#pragma unroll
-        for (int step = 16; step; step /= 2)
-            v = add(v, __shfl_xor_sync(~0u, v, step));
-        __syncthreads();
-        if (lane == 0)
-            red[warp] = v;
-        __syncthreads();
-        v = red[0];
-#pragma unroll
-        for (int w = 1; w < kJoinThreads / 32; ++w)
-            v = add(v, red[w]);
-        return v;
-    };
-    const int team = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
-    float m = -INFINITY, l = 0.f;
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads)
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
         m = fmaxf(m, place(i)[r]);
-    m = joined(m, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+    for (int step = 16; step; step /= 2)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, step));
     const float low = m == -INFINITY ? 0.f : m;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += kJoinThreads) {
-        __syncthreads();
-        const int i = i0 + threadIdx.x;
-        if (i < parts) {
-            const float s = place(i)[S::kRows + r];
-            weight[threadIdx.x] = s != s ? 1.f : exp2_fast(place(i)[r] - low);
-            l += s * weight[threadIdx.x];
+    float l = 0.f, v[kMine];
+#pragma unroll
+    for (int c = 0; c < kMine; ++c)
+        v[c] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+        float f[kAhead][kMine], weight[kAhead], s[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const bool in = i0 + k < parts;
+            const float *q = place(in ? i0 + k : 0);
+            s[k] = in ? q[S::kRows + r] : 0.f;
+            weight[k] = in ? q[r] : -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kMine; ++c)
+                f[k][c] = in ? q[2 * S::kRows + r * D + c * 32 + lane] : 0.f;
         }
-        __syncthreads();
-        const int n = parts - i0 < kJoinThreads ? parts - i0 : kJoinThreads;
-#pragma unroll 4
-        for (int i = team; i < n; i += kTeams) {
-            const float4 f =
-                *reinterpret_cast<const float4 *>(place(i0 + i) + 2 * S::kRows + r * D + d);
-            v.x += f.x * weight[i], v.y += f.y * weight[i];
-            v.z += f.z * weight[i], v.w += f.w * weight[i];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float w = s[k] != s[k] ? 1.f : exp2_fast(weight[k] - low);
+            l += s[k] * w;
+#pragma unroll
+            for (int c = 0; c < kMine; ++c)
+                v[c] += f[k][c] * w;
         }
     }
-    *reinterpret_cast<float4 *>(&teams[team][d]) = v;
-    l = joined(l, [](float a, float b) { return a + b; });
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     int j, h;
     u.row(p, r, &j, &h);
     const long long row = ((long long)u.b * p.a.queries + j) * p.a.heads + h;
-    for (int c = threadIdx.x; c < D; c += kJoinThreads) {
-        float x = 0.f;
 #pragma unroll
-        for (int k = 0; k < kTeams; ++k)
-            x += teams[k][c];
-        x = l == 0.f ? 0.f : x / l;
+    for (int c = 0; c < kMine; ++c) {
         if (p.a.bf16)
-            from_float(((__nv_bfloat16 *)p.a.out)[row * D + c], x);
+            from_float(((__nv_bfloat16 *)p.a.out)[row * D + c * 32 + lane], v[c] * inv);
         else
-            from_float(((__half *)p.a.out)[row * D + c], x);
+            from_float(((__half *)p.a.out)[row * D + c * 32 + lane], v[c] * inv);
     }
-    if (p.a.lse && threadIdx.x == 0)
+    if (p.a.lse && lane == 0)
         p.a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1205,7 +1212,8 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
     int ctas = attend_grid<D, Rows>(sms);
     ctas = most < ctas ? (int)most + 1 : ctas;
     p.parts = ctas * (long long)(sizeof(Split) / sizeof(float));
-    auto fn = p.run == S::kTile ? attend_kernel<D, Rows, true> : attend_kernel<D, Rows, false>;
+    auto fn = p.a.indices || p.run < 16 ? attend_kernel<D, Rows, 0>
+              : p.run == S::kTile       ? attend_kernel<D, Rows, S::kTile> : attend_kernel<D, Rows, 16>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
@@ -1223,7 +1231,7 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
         return e;
     if (ctas == 1)
         return cudaSuccess;    // nothing to join
-    cfg.gridDim = dim3((unsigned)(ctas * Rows));
+    cfg.gridDim = dim3((unsigned)(ctas * (Rows / 8)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<D, Rows>, (const AttendArgs)p);
@@ -1236,7 +1244,6 @@ cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t st
     AttendArgs p;
     p.c = c;
     p.a = a;
-    p.by_page.set(c.page_size);
     p.group = a.heads / c.kv_heads;
     p.run = 1;
     while (!a.indices && p.run < Shape<D, 8>::kTile && c.page_size % (2 * p.run) == 0)

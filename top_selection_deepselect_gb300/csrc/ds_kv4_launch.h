@@ -11,7 +11,8 @@ namespace kv4 {
 
 struct Cache;
 
-long long store_blocks(const Cache &c, int head_dim, long long tokens);
+// Whether append and read can number the rows of so many tokens.
+bool store_fits(const Cache &c, long long tokens);
 cudaError_t launch_append(const Cache &c, int head_dim, int dtype, const int32_t *seq,
                           const int32_t *pos, long long tokens, const void *k, const int64_t *ks,
                           const void *v, const int64_t *vs, cudaStream_t stream);

@@ -4,7 +4,10 @@
 // 16-bit type), so a vector of D channels takes D/8 neighbouring lanes and a
 // group of 32 channels four of them: the group's largest magnitude is two
 // shuffles away, and the reordering inside the record is a shuffle too, so that
-// codes leave and arrive as whole words.  Both kernels move each byte once.
+// codes leave and arrive as whole words.  Both kernels move each byte once and
+// are bound by the bytes only while a lane's eight channels cost few
+// instructions, so that magnitudes are compared as bits, quotients and integers
+// come from multiply-adds, and nothing is divided per lane but by constants.
 #include "ds_kv4.cuh"
 #include "ds_kv4_launch.h"
 
@@ -19,20 +22,23 @@ struct alignas(sizeof(T) * 8 < 16 ? sizeof(T) * 8 : 16) Eight {
     T x[8];
 };
 
-// What a lane works on: token, head, key or value, and word w of the vector.
+// What a lane works on: rows of D/8 lanes are (token, head, key or value), the
+// last fastest.
 template <int D>
 struct Place {
-    long long token;
-    int head, which, w, slot;
+    int token, head, which, w, slot;
     bool in;
-    __device__ Place(const Cache &c, const int32_t *seq, const int32_t *pos, long long tokens)
+    __device__ __forceinline__ Place(const Cache &c, const Divider &by_heads,
+                                     const int32_t *__restrict__ seq, const int32_t *__restrict__ pos,
+                                     int tokens)
     {
-        const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-        w = (int)(i % (D / 8));
-        const long long r = i / (D / 8);
-        which = (int)(r & 1);
-        head = (int)((r >> 1) % c.kv_heads);
-        token = (r >> 1) / c.kv_heads;
+        w = threadIdx.x % (D / 8);
+        // rows / 2 is below 2^31: the callers refuse more
+        const long long row = (long long)blockIdx.x * (kThreads / (D / 8)) + threadIdx.x / (D / 8);
+        which = (int)(row & 1);
+        const int r = (int)(row >> 1);
+        token = by_heads(r);
+        head = r - token * c.kv_heads;
         in = token < tokens;
         slot = in ? token_slot(c, __ldg(seq + token), __ldg(pos + token)) : -1;
     }
@@ -54,17 +60,28 @@ __device__ __forceinline__ int key_place(int w)
     return (w & ~(4 * n - 1)) | n * (w % 4) | (w / 4 % n);
 }
 
+// x / step rounded to the nearest float, step normal or subnormal fp16 and inv
+// the nearest float to 1 / step: the quotient's first value is within one unit
+// in the last place, and one correction by the exact remainder makes it the
+// nearest (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990).  A rounded quotient is
+// what the format asks for: ties of x / scale go to even.
+__device__ __forceinline__ float quotient(float x, float step, float inv)
+{
+    const float q = x * inv;
+    return fmaf(fmaf(-q, step, x), inv, q);
+}
+
 template <typename T, int D, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-append_kernel(Cache c, const int32_t *__restrict__ seq, const int32_t *__restrict__ pos,
-              long long tokens, const T *__restrict__ k, long long k_token, long long k_head,
-              const T *__restrict__ v, long long v_token, long long v_head)
+append_kernel(Cache c, Divider by_heads, const int32_t *__restrict__ seq,
+              const int32_t *__restrict__ pos, int tokens, const T *__restrict__ k, long long k_token,
+              long long k_head, const T *__restrict__ v, long long v_token, long long v_head)
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
-    const Place<D> at(c, seq, pos, tokens);
     const int lane = threadIdx.x & 31, first = lane & ~(kWords - 1);
-
+    const Place<D> at(c, by_heads, seq, pos, tokens);
     float x[8];
     if (at.slot >= 0) {
         const T *src = at.which ? v + at.token * v_token + at.head * v_head
@@ -85,33 +102,40 @@ append_kernel(Cache c, const int32_t *__restrict__ seq, const int32_t *__restric
             x[j] = 0.f;
     }
 
-    // scale of the group; a NaN or an infinity poisons it
-    float most = 0.f;
-    int bad = 0;
+    // largest magnitude of the group: bits of magnitudes are in their order,
+    // those that are not finite above all others
+    unsigned most = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float a = fabsf(x[j]);
-        bad |= !(a <= 3.402823466e38f);
-        most = fmaxf(most, a);
-    }
-    most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-    bad |= __shfl_xor_sync(~0u, bad, 1);
-    bad |= __shfl_xor_sync(~0u, bad, 2);
-    __half scale = __float2half_rn(most / 7.f);
+    for (int j = 0; j < 8; ++j)
+        most = max(most, __float_as_uint(x[j]) & 0x7fffffffu);
+    most = max(most, __shfl_xor_sync(~0u, most, 1));
+    most = max(most, __shfl_xor_sync(~0u, most, 2));
+    const bool bad = most >= 0x7f800000u;      // a NaN or an infinity poisons the group
+    __half scale = __float2half_rn(__uint_as_float(most) / 7.f);
     if (__hisinf(scale))
         scale = __ushort_as_half(0x7bff);
     const float step = __half2float(scale);
+    // zero, subnormal and largest scales: codes may be anything or beyond 7
+    const bool edge = step < 6.103515625e-05f || step == 65504.f;
+    const float inv = step > 0.f ? 1.f / step : 0.f;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        q[j] = quotient(x[j], step, inv);
+    if (edge) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            q[j] = fminf(fmaxf(q[j], -7.f), 7.f);
+    }
+    // the float q + 12582920 (1.5 2^23 + 8) holds rint(q) + 8 in its low
+    // bits, above a constant that the sum takes away once for all eight
     unsigned word = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float q = step > 0.f && !bad ? rintf(x[j] / step) : 0.f;
-        q = fminf(fmaxf(q, -7.f), 7.f);
-        word |= (unsigned)((int)q + 8) << (4 * j);
-    }
-    unsigned bits = __half_as_ushort(scale);
-    if (bad)
-        bits = 0x7fffu;
+    for (int j = 0; j < 8; ++j)
+        word += __float_as_uint(q[j] + 12582920.f) << (4 * j);
+    word -= 0x3f400000u;
+    word = bad || step == 0.f ? 0x88888888u : word;
+    const unsigned bits = bad ? 0x7fffu : __half_as_ushort(scale);
 
     // stored order
     const unsigned kw = __shfl_sync(~0u, word, first + key_source<D>(at.w));
@@ -124,25 +148,33 @@ append_kernel(Cache c, const int32_t *__restrict__ seq, const int32_t *__restric
     // scales: four lanes of a group hold it; neighbours (4 i, 4 i + 4) pair up
     const unsigned next = __shfl_down_sync(~0u, bits, 4);
 
-    if (at.slot < 0)
-        return;
-    unsigned char *rec = c.pool + record_offset<D>(c, at.slot, at.head);
-    reinterpret_cast<unsigned *>(rec + (at.which ? D / 2 : 0))[at.w] = at.which ? vw : kw;
-    if (at.w % 8 == 0)
-        reinterpret_cast<unsigned *>(rec + D + (at.which ? D / 16 : 0))[at.w / 8] = bits | next << 16;
-    if (record_bytes(D) > data_bytes(D) && at.w * 4 < record_bytes(D) - data_bytes(D) && at.which)
-        reinterpret_cast<unsigned *>(rec + data_bytes(D))[at.w] = 0;
+    if (at.slot >= 0) {
+        unsigned char *rec = c.pool + record_offset<D>(c, at.slot, at.head);
+        reinterpret_cast<unsigned *>(rec + (at.which ? D / 2 : 0))[at.w] = at.which ? vw : kw;
+        if (at.w % 8 == 0)
+            reinterpret_cast<unsigned *>(rec + D + (at.which ? D / 16 : 0))[at.w / 8] = bits | next << 16;
+        if (record_bytes(D) > data_bytes(D) && at.w * 4 < record_bytes(D) - data_bytes(D) && at.which)
+            reinterpret_cast<unsigned *>(rec + data_bytes(D))[at.w] = 0;
+    }
+}
+
+// Codes n and n + 4 of a word, as floats: (code | 1024 in fp16) - 1032 is exact.
+__device__ __forceinline__ float2 two_codes(unsigned word, int n)
+{
+    const unsigned x = (word >> (4 * n) & 0x000f000fu) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6408)));
+    return __half22float2(h);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(Cache c, const int32_t *__restrict__ seq, const int32_t *__restrict__ pos,
-            long long tokens, T *__restrict__ k, T *__restrict__ v)
+read_kernel(Cache c, Divider by_heads, const int32_t *__restrict__ seq,
+            const int32_t *__restrict__ pos, int tokens, T *__restrict__ k, T *__restrict__ v)
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
-    const Place<D> at(c, seq, pos, tokens);
     const int lane = threadIdx.x & 31, first = lane & ~(kWords - 1);
+    const Place<D> at(c, by_heads, seq, pos, tokens);
     unsigned stored = 0x88888888u;
     float scale = 0.f;
     if (at.slot >= 0) {
@@ -164,15 +196,19 @@ read_kernel(Cache c, const int32_t *__restrict__ seq, const int32_t *__restrict_
     const unsigned word = at.which ? vw : kw;
     Eight<T> e;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        from_float(e.x[j], (float)((int)(word >> (4 * j) & 15) - 8) * scale);
-    T *dst = (at.which ? v : k) + (at.token * c.kv_heads + at.head) * D;
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = two_codes(word, j);
+        from_float(e.x[j], f.x * scale);
+        from_float(e.x[j + 4], f.y * scale);
+    }
+    T *dst = (at.which ? v : k) + ((long long)at.token * c.kv_heads + at.head) * D;
     *reinterpret_cast<Eight<T> *>(dst + at.w * 8) = e;
 }
 
 long long blocks_for(const Cache &c, int d, long long tokens)
 {
-    return (tokens * c.kv_heads * 2 * (d / 8) + kThreads - 1) / kThreads;
+    const long long rows = tokens * c.kv_heads * 2, each = kThreads / (d / 8);
+    return (rows + each - 1) / each;
 }
 
 template <typename T, int D>
@@ -186,8 +222,10 @@ cudaError_t append_one(const Cache &c, const int32_t *seq, const int32_t *pos, l
     for (int j = 0; j < 2; ++j)
         vec = vec && ks[j] * (long long)sizeof(T) % 16 == 0 && vs[j] * (long long)sizeof(T) % 16 == 0;
     const unsigned grid = (unsigned)blocks_for(c, D, tokens);
+    Divider by_heads;
+    by_heads.set(c.kv_heads);
     auto fn = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
-    fn<<<grid, kThreads, 0, stream>>>(c, seq, pos, tokens, (const T *)k, ks[0], ks[1],
+    fn<<<grid, kThreads, 0, stream>>>(c, by_heads, seq, pos, (int)tokens, (const T *)k, ks[0], ks[1],
                                       (const T *)v, vs[0], vs[1]);
     return cudaGetLastError();
 }
@@ -197,7 +235,9 @@ cudaError_t read_one(const Cache &c, const int32_t *seq, const int32_t *pos, lon
                      void *k, void *v, cudaStream_t stream)
 {
     const unsigned grid = (unsigned)blocks_for(c, D, tokens);
-    read_kernel<T, D><<<grid, kThreads, 0, stream>>>(c, seq, pos, tokens, (T *)k, (T *)v);
+    Divider by_heads;
+    by_heads.set(c.kv_heads);
+    read_kernel<T, D><<<grid, kThreads, 0, stream>>>(c, by_heads, seq, pos, (int)tokens, (T *)k, (T *)v);
     return cudaGetLastError();
 }
 
@@ -222,9 +262,10 @@ cudaError_t read_dim(const Cache &c, int d, const int32_t *seq, const int32_t *p
 
 }  // namespace
 
-long long store_blocks(const Cache &c, int head_dim, long long tokens)
+bool store_fits(const Cache &c, long long tokens)
 {
-    return blocks_for(c, head_dim, tokens);
+    // (token, head) rows are numbered below 2^31, those of the last CTA too
+    return tokens < 1LL << 31 && tokens * c.kv_heads < (1LL << 31) - kThreads;
 }
 
 cudaError_t launch_append(const Cache &c, int head_dim, int dtype, const int32_t *seq,
