@@ -45,29 +45,29 @@ struct Cache {
     Divider by_page;
 };
 
-// Token slot (page * page_size + offset) of position `pos` of sequence `seq`,
-// or -1 where the sequence, the position or the page is out of range.
-__device__ __forceinline__ int token_slot(const Cache &c, int seq, int pos)
+// Page and offset in it of position `pos` of sequence `seq`; page -1 where the
+// sequence, the position or the page is out of range.
+struct Slot {
+    int page, offset;
+};
+
+__device__ __forceinline__ Slot token_slot(const Cache &c, int seq, int pos)
 {
     if ((unsigned)seq >= (unsigned)c.max_seqs || pos < 0)
-        return -1;
+        return {-1, 0};
     const int col = c.by_page(pos);
     if (col >= c.max_pages)
-        return -1;
+        return {-1, 0};
     const int page = __ldg(c.table + seq * c.table_stride + col);
-    if ((unsigned)page >= (unsigned)c.n_pages)
-        return -1;
-    return page * c.page_size + (pos - col * c.page_size);
+    return {(unsigned)page < (unsigned)c.n_pages ? page : -1, pos - col * c.page_size};
 }
 
 // Byte offset of the record of (slot, head) in the pool: 64 bits, a pool may
 // be hundreds of gigabytes.
 template <int D>
-__device__ __forceinline__ long long record_offset(const Cache &c, int slot, int head)
+__device__ __forceinline__ long long record_offset(const Cache &c, const Slot &s, int head)
 {
-    const int page = c.by_page(slot);
-    return page * c.page_stride +
-           ((long long)head * c.page_size + (slot - page * c.page_size)) * record_bytes(D);
+    return s.page * c.page_stride + ((long long)head * c.page_size + s.offset) * record_bytes(D);
 }
 
 __device__ __forceinline__ float to_float(float x) { return x; }
