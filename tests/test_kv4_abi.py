@@ -51,6 +51,15 @@ def cache(**kw):
     return ds.ds_kv4_cache_t(*[a[name] for name, _ in ds.ds_kv4_cache_t._fields_])
 
 
+def test_packed_descriptors_are_the_structures():
+    """The byte strings that the torch wrappers pass have the structures' layout."""
+    from top_selection_deepselect_gb300 import _kv4
+    for pack, kind in [(_kv4._pack_cache, ds.ds_kv4_cache_t), (_kv4._pack_pool, ds.ds_page_pool_t),
+                       (_kv4._pack_book, ds.ds_page_book_t)]:
+        values = [1000 + i for i in range(len(kind._fields_))]
+        assert pack(*values) == bytes(kind(*values))
+
+
 BAD_CACHES = [
     (dict(pool=None), EINVAL), (dict(pool=FAKE + 8), EINVAL), (dict(table=None), EINVAL),
     (dict(page_stride=2 * 16 * 144 - 16), EINVAL), (dict(page_stride=2 * 16 * 144 + 8), EINVAL),

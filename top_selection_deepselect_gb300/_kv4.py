@@ -7,6 +7,7 @@ torch and enqueue on the current stream.
 """
 import ctypes
 import math
+import struct
 
 from ._binding import DS_BF16, DS_FP16, DS_FP32, _check, load_library
 
@@ -127,49 +128,66 @@ def ds_pages_workspace(n_pages, n):
 
 
 # ---- torch convenience wrappers ------------------------------------------------
-# These run once a layer and step, around kernels of a few microseconds: what
-# does not change (types, record sizes, workspace sizes) is looked up once.
+# These run once a layer and step, around kernels of a few microseconds, so that
+# their own time counts: types and sizes are looked up once, and descriptors are
+# packed as bytes, which costs a quarter of filling a ctypes structure.
 _RECORD = {64: 80, 128: 144, 256: 288}
-_torch_names = None
+_pack_cache = struct.Struct("@PqPq6i").pack     # ds_kv4_cache_t
+_pack_pool = struct.Struct("@P3q2i").pack       # ds_page_pool_t
+_pack_book = struct.Struct("@PqPP4i").pack      # ds_page_book_t
+_pack_2 = struct.Struct("@2q").pack
+_pack_3 = struct.Struct("@3q").pack
 
 
-def _names():
-    """(torch, int32, uint8, float32, dtype codes, raw stream of a device index)."""
-    global _torch_names
-    if _torch_names is None:
+class _Torch:
+    """What the wrappers need of torch and of the library, found at the first call."""
+    ready = False
+
+    def find(self):
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            def raw(index):
-                return torch.cuda.current_stream(index).cuda_stream
-        _torch_names = (torch, torch.int32, torch.uint8, torch.float32,
-                        {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}, raw)
-    return _torch_names
+        self.torch, self.empty = torch, torch.empty
+        self.int32, self.uint8, self.float32 = torch.int32, torch.uint8, torch.float32
+        self.codes = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        lib = _lib()
+
+        def bytes_for(name, at):
+            """The function with byte strings in the places `at` of its structures."""
+            f = lib[name]
+            f.argtypes = [ctypes.c_char_p if i in at else a
+                          for i, a in enumerate(getattr(lib, name).argtypes)]
+            f.restype = getattr(lib, name).restype
+            return f
+
+        self.append = bytes_for("ds_kv4_append", (0, 6, 8))
+        self.read = bytes_for("ds_kv4_read", (0,))
+        self.attention = bytes_for("ds_kv4_attention", (0, 8))
+        self.workspace = bytes_for("ds_kv4_attention_workspace", (0,))
+        self.copy = bytes_for("ds_pages_copy", (0,))
+        self.reserve = bytes_for("ds_pages_reserve", (0,))
+        self.fork = bytes_for("ds_pages_fork", (0, 1))
+        self.free = bytes_for("ds_pages_free", (0,))
+        self.compact = bytes_for("ds_pages_compact", (0, 1))
+        self.ready = True
+        return self
 
 
-def _code(dtype):
-    code = _names()[4].get(dtype)
-    if code is None:
-        raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
-    return code
-
-
-def _stream(device, stream):
-    return _names()[5](device.index) if stream is None else stream.cuda_stream
+_t = _Torch()
 
 
 def _int32(name, t, device, n=None):
-    """Address of a contiguous CUDA int32 tensor, of n entries in one dimension if given."""
-    if t.dtype is not _names()[1] or t.device != device or not t.is_contiguous():
+    """Address of a contiguous int32 tensor on `device`, of n entries in one dimension if given."""
+    if t.dtype is not _t.int32 or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
-    if n is not None and (t.dim() != 1 or t.shape[0] != n):
+    if n is not None and t.shape != (n,):
         raise ValueError("%s must have shape (%d,), got %s" % (name, n, tuple(t.shape)))
     return t.data_ptr()
 
 
 def _table(table, device):
     """(address, row stride, rows, columns) of a page table."""
-    if table.dtype is not _names()[1] or table.device != device or table.dim() != 2:
+    if table.dtype is not _t.int32 or table.device != device or table.dim() != 2:
         raise ValueError("table must be an int32 [max_seqs, max_pages] tensor on %s" % (device,))
     rows, columns = table.shape
     stride, unit = table.stride()
@@ -178,27 +196,34 @@ def _table(table, device):
     return table.data_ptr(), stride if stride > columns else columns, rows, columns
 
 
+def _space(name, t, device):
+    """Bytes of a workspace that was passed in."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be contiguous on %s" % (name, device))
+    return t.numel() * t.element_size()
+
+
 def kv4_record_bytes(head_dim):
     """Bytes of one token's record of one key/value head (head_dim 64, 128 or 256)."""
     return ds_kv4_record_bytes(head_dim)
 
 
-def _cache(pool, table, head_dim):
+def _cache(pool, table, head_dim, device):
     """Descriptor of a pool [n_pages, kv_heads, page_size, record bytes] (uint8) and its table."""
-    if pool.dtype is not _names()[2] or not pool.is_cuda or pool.dim() != 4:
+    if pool.dtype is not _t.uint8 or not pool.is_cuda or pool.dim() != 4:
         raise ValueError("pool must be a 4-D CUDA uint8 tensor [n_pages, kv_heads, page_size, "
                          "record bytes]")
     n_pages, kv_heads, page_size, rec = pool.shape
     if rec != _RECORD.get(head_dim):
         raise ValueError("head_dim %d has records of %d bytes, the pool has %d"
                          % (head_dim, ds_kv4_record_bytes(head_dim), rec))
-    stride = pool.stride()
+    each, head, token, unit = pool.stride()
     page = kv_heads * page_size * rec
-    if stride[1:] != (page_size * rec, rec, 1) and not pool[:1].is_contiguous():
+    if (unit != 1 or token != rec or head != page_size * rec) and not pool[:1].is_contiguous():
         raise ValueError("each page of pool must be contiguous")
-    at, row, rows, columns = _table(table, pool.device)
-    return ds_kv4_cache_t(pool.data_ptr(), stride[0] if stride[0] > page else page, at, row, n_pages,
-                          page_size, kv_heads, head_dim, rows, columns)
+    at, row, rows, columns = _table(table, device)
+    return _pack_cache(pool.data_ptr(), each if each > page else page, at, row, n_pages, page_size,
+                       kv_heads, head_dim, rows, columns)
 
 
 def kv4_append(pool, table, seq, pos, k, v, stream=None):
@@ -208,20 +233,27 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
     stride in the last dimension; seq and pos: int32 [tokens].  The pages must
     be in the table (pages_reserve); tokens without one are skipped.
     """
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+    t = _t if _t.ready else _t.find()
+    shape, dtype, device = k.shape, k.dtype, pool.device
+    if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
-    tokens, heads, dim = k.shape
-    cache = _cache(pool, table, dim)
+    tokens, heads, dim = shape
+    cache = _cache(pool, table, dim, device)
     if heads != pool.shape[1]:
         raise ValueError("k has %d heads, the pool %d" % (heads, pool.shape[1]))
-    device = pool.device
-    ks, vs = k.stride(), v.stride()
-    if k.device != device or v.device != device or ks[2] != 1 or vs[2] != 1:
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError("k and v must be float32, bfloat16 or float16, got %s" % dtype)
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if k.device != device or v.device != device or k2 != 1 or v2 != 1:
         raise ValueError("k and v must be on the pool's device with unit stride in the last "
                          "dimension")
-    ds_kv4_append(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
-                  tokens, _code(k.dtype), k.data_ptr(), ks[:2], v.data_ptr(), vs[:2],
-                  _stream(device, stream))
+    status = t.append(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
+                      tokens, code, k.data_ptr(), _pack_2(k0, k1), v.data_ptr(), _pack_2(v0, v1),
+                      t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "ds_kv4_append")
 
 
 def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None):
@@ -230,35 +262,43 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
     Returns (k, v), each [tokens, kv_heads, head_dim] of `dtype`; a token that
     is not there reads as zeros.
     """
-    cache = _cache(pool, table, head_dim)
+    t = _t if _t.ready else _t.find()
     tokens, device = seq.numel(), pool.device
+    cache = _cache(pool, table, head_dim, device)
     shape = (tokens, pool.shape[1], head_dim)
-    code = _code(dtype)
-    given = [t for t in (k, v) if t is not None]
-    for t in given:
-        if (tuple(t.shape) != shape or t.dtype != dtype or t.device != device
-                or not t.is_contiguous()):
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
+    for x in (k, v):
+        if x is not None and (x.shape != shape or x.dtype != dtype or x.device != device
+                              or not x.is_contiguous()):
             raise ValueError("k and v must be contiguous %s tensors of %s" % (shape, dtype))
     if k is None:
-        k = _names()[0].empty(shape, dtype=dtype, device=device)
+        k = t.empty(shape, dtype=dtype, device=device)
     if v is None:
-        v = _names()[0].empty(shape, dtype=dtype, device=device)
-    ds_kv4_read(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
-                tokens, code, k.data_ptr(), v.data_ptr(), _stream(device, stream))
+        v = t.empty(shape, dtype=dtype, device=device)
+    status = t.read(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
+                    tokens, code, k.data_ptr(), v.data_ptr(),
+                    t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "ds_kv4_read")
     return k, v
 
 
 _attention_bytes = {}
 
 
-def _attention_workspace(cache, batch, queries, heads, k, device):
+def _attention_workspace(cache, batch, queries, heads, k, dim, kv_heads, index):
     """Workspace bytes, which depend on these sizes and the device alone."""
-    key = (cache.head_dim, cache.kv_heads, queries, heads, k > 0, device.index)
+    key = (dim, kv_heads, queries, heads, k > 0, index)
     need = _attention_bytes.get(key)
     if need is None:
+        n = ctypes.c_size_t(0)
+        _check(_t.workspace(cache, batch, queries, heads, k, ctypes.byref(n)),
+               "ds_kv4_attention_workspace")
         if len(_attention_bytes) > 1000:
             _attention_bytes.clear()
-        need = _attention_bytes[key] = ds_kv4_attention_workspace(cache, batch, queries, heads, k)
+        need = _attention_bytes[key] = n.value
     return need
 
 
@@ -276,16 +316,16 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     like q, lse float32 [batch, queries, heads]; a query that sees nothing gives
     0 and -inf.
     """
-    torch, _, _, float32, codes, _ = _names()
-    device = pool.device
-    if q.dim() != 4 or q.device != device:
+    t = _t if _t.ready else _t.find()
+    device, shape, dtype = pool.device, q.shape, q.dtype
+    if len(shape) != 4 or q.device != device:
         raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device")
-    shape, qs, dtype = q.shape, q.stride(), q.dtype
     batch, queries, heads, dim = shape
-    if qs[3] != 1:
+    q0, q1, q2, q3 = q.stride()
+    if q3 != 1:
         raise ValueError("q must have unit stride in the last dimension")
-    cache = _cache(pool, table, dim)
-    code = codes.get(dtype)
+    cache = _cache(pool, table, dim, device)
+    code = t.codes.get(dtype)
     if code is None:
         raise TypeError("q must be bfloat16 or float16, got %s" % dtype)
     rows = table.shape[0]
@@ -302,67 +342,68 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
         k = indices.shape[2]
         list_at = _int32("indices", indices, device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = t.empty(shape, dtype=dtype, device=device)
     elif out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=float32, device=device)
-    elif (lse.shape != shape[:3] or lse.dtype != float32 or lse.device != device
+        lse = t.empty((batch, queries, heads), dtype=t.float32, device=device)
+    elif (lse.shape != shape[:3] or lse.dtype != t.float32 or lse.device != device
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [batch, queries, heads] tensor")
     if indices is not None and k == 0:
         out.zero_()
         lse.fill_(-math.inf)
         return out, lse
-    need = _attention_workspace(cache, batch, queries, heads, k, device)
+    index = device.index
+    size = _attention_workspace(cache, batch, queries, heads, k, dim, pool.shape[1], index)
     if workspace is None:
-        workspace, size = torch.empty(need, dtype=torch.uint8, device=device), need
+        workspace = t.empty(size, dtype=t.uint8, device=device)
     else:
-        size = workspace.numel() * workspace.element_size()
-        if size < need or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous on %s with %d bytes, got %d"
-                             % (device, need, size))
-    ds_kv4_attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(), qs[:3], list_at,
-                     k, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(),
-                     lse.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
+        given = _space("workspace", workspace, device)
+        if given < size:
+            raise ValueError("workspace has %d bytes, %d needed" % (given, size))
+    status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
+                         _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
+                         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                         t.raw_stream(index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "ds_kv4_attention")
     return out, lse
 
 
-def _pool(pool):
+def _pool(pool, device):
     """Descriptor of a pool [layers, n_pages, ...] of pages of any content."""
     shape = pool.shape
-    if not pool.is_cuda or len(shape) < 3:
-        raise ValueError("pool must be a CUDA tensor [layers, n_pages, ...]")
+    if not pool.is_cuda or len(shape) < 3 or pool.device != device:
+        raise ValueError("pool must be a CUDA tensor [layers, n_pages, ...] on %s" % (device,))
     if not (pool.is_contiguous() or pool[:1, :1].is_contiguous()):
         raise ValueError("each page of pool must be contiguous")
     size = pool.element_size()
     page = math.prod(shape[2:]) * size
     layer, each = pool.stride()[:2]
-    return ds_page_pool_t(pool.data_ptr(), layer * size, max(each * size, page), page, *shape[:2])
+    each *= size
+    return _pack_pool(pool.data_ptr(), layer * size, each if each > page else page, page, shape[0],
+                      shape[1])
 
 
-def _book(table, lengths, refs, page_size):
-    device = table.device
+def _book(table, lengths, refs, page_size, device):
+    """Descriptor of the pages' bookkeeping."""
     if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor")
     at, stride, rows, columns = _table(table, device)
-    return ds_page_book_t(at, stride,
-                          None if lengths is None else _int32("lengths", lengths, device, rows),
-                          _int32("refs", refs, device), rows, columns, page_size, refs.numel())
+    return _pack_book(at, stride,
+                      0 if lengths is None else _int32("lengths", lengths, device, rows),
+                      _int32("refs", refs, device), rows, columns, page_size, refs.numel())
 
 
-def _work(device, n_pages, n, workspace, status):
-    """(workspace address, its bytes, status); ones that are not given are made."""
-    torch = _names()[0]
-    need = ds_pages_workspace(n_pages, n)
+def _work(t, device, need, workspace, status):
+    """(workspace, its bytes, status); ones that are not given are made."""
     if workspace is None:
-        workspace, size = torch.empty(need, dtype=torch.uint8, device=device), need
+        workspace, size = t.empty(need, dtype=t.uint8, device=device), need
     else:
-        size = workspace.numel() * workspace.element_size()
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous on %s" % (device,))
+        size = _space("workspace", workspace, device)
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=device)
+        status = t.empty(2, dtype=t.int32, device=device)
     else:
         _int32("status", status, device, 2)
     return workspace, size, status
@@ -370,9 +411,12 @@ def _work(device, n_pages, n, workspace, status):
 
 def pages_copy(pool, src, dst, stream=None):
     """Page dst[i] of pool [layers, n_pages, ...] := page src[i], in every layer (int32 lists)."""
+    t = _t if _t.ready else _t.find()
     n, device = src.numel(), pool.device
-    ds_pages_copy(_pool(pool), _int32("src", src, device, n), _int32("dst", dst, device, n), n,
-                  _stream(device, stream))
+    status = t.copy(_pool(pool, device), _int32("src", src, device, n), _int32("dst", dst, device, n),
+                    n, t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "ds_pages_copy")
 
 
 def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None, status=None,
@@ -382,11 +426,15 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     All or nothing.  Returns status, int32 [2]: pages short (nothing changed
     when above 0), pages taken.
     """
+    t = _t if _t.ready else _t.find()
     n, device = seqs.numel(), table.device
-    book = _book(table, lengths, refs, page_size)
-    workspace, size, status = _work(device, book.n_pages, n, workspace, status)
-    ds_pages_reserve(book, _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n), n,
-                     status.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
+    book = _book(table, lengths, refs, page_size, device)
+    workspace, size, status = _work(t, device, ds_pages_workspace(refs.numel(), n), workspace, status)
+    rc = t.reserve(book, _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n), n,
+                   status.data_ptr(), workspace.data_ptr(), size,
+                   t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "ds_pages_reserve")
     return status
 
 
@@ -396,22 +444,28 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     pool: [layers, n_pages, kv_heads, page_size, record bytes].  All or nothing;
     returns status as pages_reserve does.
     """
-    if pool.dim() != 5 or pool.device != table.device:
-        raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes] on the "
-                         "table's device")
+    t = _t if _t.ready else _t.find()
+    if pool.dim() != 5:
+        raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes]")
     n, device = src.numel(), table.device
-    book = _book(table, lengths, refs, pool.shape[3])
-    workspace, size, status = _work(device, book.n_pages, n, workspace, status)
-    ds_pages_fork(_pool(pool), book, _int32("src", src, device, n), _int32("dst", dst, device, n), n,
-                  status.data_ptr(), workspace.data_ptr(), size, _stream(device, stream))
+    book = _book(table, lengths, refs, pool.shape[3], device)
+    workspace, size, status = _work(t, device, ds_pages_workspace(refs.numel(), n), workspace, status)
+    rc = t.fork(_pool(pool, device), book, _int32("src", src, device, n),
+                _int32("dst", dst, device, n), n, status.data_ptr(), workspace.data_ptr(), size,
+                t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "ds_pages_fork")
     return status
 
 
 def pages_free(table, lengths, refs, seqs, page_size, stream=None):
     """The sequences seqs[i] end: their pages' refs go down, their rows become -1."""
+    t = _t if _t.ready else _t.find()
     n, device = seqs.numel(), table.device
-    ds_pages_free(_book(table, lengths, refs, page_size), _int32("seqs", seqs, device, n), n,
-                  _stream(device, stream))
+    rc = t.free(_book(table, lengths, refs, page_size, device), _int32("seqs", seqs, device, n), n,
+                t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "ds_pages_free")
 
 
 def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, stream=None):
@@ -420,14 +474,15 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
     Returns (remap int32 [n_pages]: new number of each page or -1, status int32
     [2]: live pages, pages moved).
     """
-    device = table.device
-    if pool.device != device:
-        raise ValueError("pool and table must be on one device")
-    book = _book(table, None, refs, 1)
-    n_pages = book.n_pages
+    t = _t if _t.ready else _t.find()
+    device, n_pages = table.device, refs.numel()
+    book = _book(table, None, refs, 1, device)
     if remap is None:
-        remap = _names()[0].empty(n_pages, dtype=_names()[1], device=device)
-    workspace, size, status = _work(device, n_pages, 0, workspace, status)
-    ds_pages_compact(_pool(pool), book, _int32("remap", remap, device, n_pages), status.data_ptr(),
-                     workspace.data_ptr(), size, _stream(device, stream))
+        remap = t.empty(n_pages, dtype=t.int32, device=device)
+    workspace, size, status = _work(t, device, ds_pages_workspace(n_pages, 0), workspace, status)
+    rc = t.compact(_pool(pool, device), book, _int32("remap", remap, device, n_pages),
+                   status.data_ptr(), workspace.data_ptr(), size,
+                   t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "ds_pages_compact")
     return remap, status

@@ -12,4 +12,7 @@ extern thread_local char g_detail[512];
 int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail_cuda(cudaError_t e, const char *what);
 
+// The current device's ordinal and its SM count, asked of CUDA once a device.
+int current_device(int *dev, int *sms);
+
 }  // namespace ds

@@ -86,15 +86,6 @@ int check_attention(const Cache &c, int batch, int queries, int heads, int k)
     return DS_OK;
 }
 
-int sm_count(int *sms)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return e == cudaSuccess ? DS_OK : fail_cuda(e, "SM count");
-}
-
 }  // namespace
 
 extern "C" {
@@ -157,14 +148,14 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
 {
     ds::g_detail[0] = '\0';
     Cache c;
-    int rc = check_cache(cache, &c), sms = 0;
+    int rc = check_cache(cache, &c), dev = 0, sms = 0;
     if (rc == DS_OK)
         rc = check_attention(c, batch, queries, heads, k);
     if (rc != DS_OK)
         return rc;
     if (!bytes)
         return fail(DS_EINVAL, "bytes must be non-NULL");
-    if ((rc = sm_count(&sms)) != DS_OK)
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
         return rc;
     *bytes = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
     return DS_OK;
@@ -177,7 +168,7 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
 {
     ds::g_detail[0] = '\0';
     Cache c;
-    int rc = check_cache(cache, &c), sms = 0;
+    int rc = check_cache(cache, &c), dev = 0, sms = 0;
     if (rc == DS_OK)
         rc = check_attention(c, batch, queries, heads, k);
     if (rc != DS_OK)
@@ -194,7 +185,7 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
         return fail(DS_EINVAL, "lengths, q and out must be non-NULL when batch and queries are > 0");
     if ((uintptr_t)q % 2 != 0 || (uintptr_t)out % 16 != 0)
         return fail(DS_EINVAL, "q must be aligned to its elements and out to 16 bytes");
-    if ((rc = sm_count(&sms)) != DS_OK)
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
         return rc;
     const size_t need = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
     if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
@@ -217,7 +208,8 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
     a.heads = heads;
     a.k = k;
     a.bf16 = dtype == DS_BF16;
-    const cudaError_t e = ds::kv4::launch_attention(c, cache->head_dim, a, sms, (cudaStream_t)stream);
+    const cudaError_t e = ds::kv4::launch_attention(c, cache->head_dim, a, dev, sms,
+                                                    (cudaStream_t)stream);
     return e == cudaSuccess ? DS_OK : fail_cuda(e, "ds_kv4_attention");
 }
 

@@ -5,9 +5,9 @@
 namespace ds {
 namespace kv4 {
 
-cudaError_t launch_attention_64(const Cache &c, const Attend &a, int sms, cudaStream_t stream);
-cudaError_t launch_attention_128(const Cache &c, const Attend &a, int sms, cudaStream_t stream);
-cudaError_t launch_attention_256(const Cache &c, const Attend &a, int sms, cudaStream_t stream);
+cudaError_t launch_attention_64(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream);
+cudaError_t launch_attention_128(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream);
+cudaError_t launch_attention_256(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream);
 
 size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads, int k, int sms)
 {
@@ -16,12 +16,12 @@ size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads,
            : head_dim == 128 ? workspace_dim<128>(rows, sms) : workspace_dim<256>(rows, sms);
 }
 
-cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int sms,
+cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int dev, int sms,
                              cudaStream_t stream)
 {
-    return head_dim == 64    ? launch_attention_64(c, a, sms, stream)
-           : head_dim == 128 ? launch_attention_128(c, a, sms, stream)
-                             : launch_attention_256(c, a, sms, stream);
+    return head_dim == 64    ? launch_attention_64(c, a, dev, sms, stream)
+           : head_dim == 128 ? launch_attention_128(c, a, dev, sms, stream)
+                             : launch_attention_256(c, a, dev, sms, stream);
 }
 
 }  // namespace kv4

@@ -41,6 +41,7 @@
 // workspace; a second launch joins them in a fixed order.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "ds_device.cuh"
@@ -1199,7 +1200,7 @@ int attend_grid(int sms)
 }
 
 template <int D, int Rows>
-cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
+cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
 {
     using S = Shape<D, Rows>;
     p.blocks = (p.rows + S::kRows - 1) / S::kRows;
@@ -1212,11 +1213,18 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
     int ctas = attend_grid<D, Rows>(sms);
     ctas = most < ctas ? (int)most + 1 : ctas;
     p.parts = ctas * (long long)(sizeof(Split) / sizeof(float));
-    auto fn = p.a.indices || p.run < 16 ? attend_kernel<D, Rows, 0>
-              : p.run == S::kTile       ? attend_kernel<D, Rows, S::kTile> : attend_kernel<D, Rows, 16>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess)
-        return e;
+    const int which = p.a.indices || p.run < 16 ? 0 : p.run == S::kTile ? 1 : 2;
+    auto fn = which == 0   ? attend_kernel<D, Rows, 0>
+              : which == 1 ? attend_kernel<D, Rows, S::kTile> : attend_kernel<D, Rows, 16>;
+    // the kernels' shared memory is raised once a device
+    static std::atomic<unsigned long long> raised[3];
+    cudaError_t e = cudaSuccess;
+    if (!(raised[which].load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess)
+            return e;
+        raised[which].fetch_or(1ULL << dev, std::memory_order_relaxed);
+    }
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1238,7 +1246,7 @@ cudaError_t launch_shape(AttendArgs &p, int sms, cudaStream_t stream)
 }
 
 template <int D>
-cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t stream)
+cudaError_t launch_dim(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream)
 {
     constexpr int kMost = D == 256 ? 16 : 32;
     AttendArgs p;
@@ -1250,8 +1258,8 @@ cudaError_t launch_dim(const Cache &c, const Attend &a, int sms, cudaStream_t st
         p.run *= 2;
     p.rows = a.indices ? p.group : p.group * a.queries;
     const int rows = unit_rows<D>(p.rows);
-    return rows == 8    ? launch_shape<D, 8>(p, sms, stream)
-           : rows == 16 ? launch_shape<D, 16>(p, sms, stream) : launch_shape<D, kMost>(p, sms, stream);
+    return rows == 8    ? launch_shape<D, 8>(p, dev, sms, stream)
+           : rows == 16 ? launch_shape<D, 16>(p, dev, sms, stream) : launch_shape<D, kMost>(p, dev, sms, stream);
 }
 
 template <int D, int Rows>

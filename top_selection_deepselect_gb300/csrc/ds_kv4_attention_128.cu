@@ -4,9 +4,9 @@
 namespace ds {
 namespace kv4 {
 
-cudaError_t launch_attention_128(const Cache &c, const Attend &a, int sms, cudaStream_t stream)
+cudaError_t launch_attention_128(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream)
 {
-    return launch_dim<128>(c, a, sms, stream);
+    return launch_dim<128>(c, a, dev, sms, stream);
 }
 
 }  // namespace kv4

@@ -34,7 +34,7 @@ struct Attend {
 };
 
 size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads, int k, int sms);
-cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int sms,
+cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int dev, int sms,
                              cudaStream_t stream);
 
 }  // namespace kv4

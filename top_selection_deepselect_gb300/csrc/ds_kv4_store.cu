@@ -74,12 +74,14 @@ __device__ __forceinline__ float quotient(float x, float step, float inv)
 template <typename T, bool kVec>
 __device__ __forceinline__ Eight<T> load_eight(const T *src)
 {
-    if (kVec)
-        return *reinterpret_cast<const Eight<T> *>(src);
     Eight<T> e;
+    if constexpr (kVec) {
+        e = *reinterpret_cast<const Eight<T> *>(src);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        e.x[j] = src[j];
+        for (int j = 0; j < 8; ++j)
+            e.x[j] = src[j];
+    }
     return e;
 }
 

@@ -465,11 +465,9 @@ int check_work(const void *ws, size_t bytes, size_t need)
 int move_grid(long long items, unsigned *grid)
 {
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess)
-        return fail_cuda(e, "SM count");
+    const int rc = ds::current_device(&dev, &sms);
+    if (rc != DS_OK)
+        return rc;
     const long long most = 8LL * sms;
     *grid = (unsigned)(items < 1 ? 1 : items < most ? items : most);
     return DS_OK;

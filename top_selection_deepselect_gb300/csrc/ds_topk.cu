@@ -9,6 +9,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 #include <stdarg.h>
 #include <stdio.h>
@@ -36,6 +37,25 @@ int fail(int status, const char *fmt, ...)
 int fail_cuda(cudaError_t e, const char *what)
 {
     return fail(DS_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+int current_device(int *dev, int *sms)
+{
+    static std::atomic<int> known[64];
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess)
+        return fail_cuda(e, "cudaGetDevice");
+    if (*dev < 0 || *dev >= 64)
+        return fail(DS_EUNSUPPORTED, "device ordinal %d out of range", *dev);
+    int n = known[*dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (e != cudaSuccess)
+            return fail_cuda(e, "cudaDeviceGetAttribute(SM count)");
+        known[*dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return DS_OK;
 }
 
 }  // namespace ds
