@@ -112,6 +112,7 @@ struct AttendArgs {
     int rows;             // query rows of a unit before it is cut into blocks
     int blocks;           // blocks of kRows rows, a unit each
     int units;            // units of a batch entry
+    Divider by_group, by_blocks, by_heads;
 };
 
 __device__ __forceinline__ uint32_t shared_address(const void *p)
@@ -214,6 +215,15 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const unsigned char
         const uint4 v = *reinterpret_cast<const uint4 *>(p);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_four(T *dst, const float4 &v, float factor)
+{
+    T y[4];
+    from_float(y[0], v.x * factor), from_float(y[1], v.y * factor);
+    from_float(y[2], v.z * factor), from_float(y[3], v.w * factor);
+    *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
 }
 
 // Scales of G groups as floats.
@@ -351,17 +361,16 @@ struct Unit {
     __device__ __forceinline__ Unit(const AttendArgs &p, int entry, int u, int block_rows)
     {
         b = entry;
-        const int block = u % p.blocks;
-        u /= p.blocks;
-        head = u % p.c.kv_heads;
-        query = p.a.indices ? u / p.c.kv_heads : 0;
+        const int v = p.by_blocks(u), block = u - v * p.blocks, q = p.by_heads(v);
+        head = v - q * p.c.kv_heads;
+        query = q;    // 0 unless tokens are listed: then each query is a unit of its own
         row0 = block * block_rows;
         rows = p.rows - row0 < block_rows ? p.rows - row0 : block_rows;
     }
     // row r of the block -> (query, query head)
     __device__ __forceinline__ void row(const AttendArgs &p, int r, int *j, int *h) const
     {
-        const int e = row0 + r, q = e / p.group;
+        const int e = row0 + r, q = p.by_group(e);
         *j = query + q;
         *h = head * p.group + (e - q * p.group);
     }
@@ -372,10 +381,12 @@ struct Unit {
 struct Part {
     const int32_t *list, *row_table;     // listed positions; the sequence's row of the table
     const unsigned char *head_pool;      // records of the head in page 0
-    long long next, next_first;          // place of the line to go on at, its entry's first place
+    long long next;                      // place of the line where the next unit begins
     Unit u;
-    int next_entry, seen;                // positions attended are below `seen`
-    int whole, begins;                   // all of the unit's tiles are this CTA's; its first one is
+    int next_entry, next_unit;           // and which one it is
+    int seen;                            // positions attended are below `seen`
+    int whole, begins, active;           // all of the unit's tiles are this CTA's; its first one is;
+                                         // warps that have tiles
 };
 static_assert(sizeof(Part) <= 128, "room in Shape");
 
@@ -510,26 +521,30 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     if (threadIdx.x == 0)
         split->parts = 0;
 
-    long long x, per, end, first;
-    int entry;
+    // place to go on at, the unit there (number u_in of its entry) and where it begins
+    long long x, per, end, start;
+    int entry, u_in;
     {
         const Line line = line_of<S::kTile>(p, listed, scratch);
         per = line.per;
         x = per * blockIdx.x;
         end = x + per < line.all ? x + per : line.all;
-        first = line.first;
+        if (x >= end)
+            return;
         entry = line.entry;
+        const long long each = tiles_of<S::kTile>(p, listed, entry) + kUnitCost;
+        u_in = (int)((x - line.first) / each);
+        start = line.first + u_in * each;
     }
 
     const int tok_row = g & 1 ? S::odd(g / 2) : S::even(g / 2);   // token at place g
     const int tok_a = S::even(t), tok_b = S::odd(t);              // at places 2 t and 2 t + 1
 
-    while (x < end) {
+    while (true) {
         // the part of the unit at x that is this CTA's
         const int seq = sequence_of(p, entry), len = length_of(p, seq);
-        const long long tiles = tiles_of<S::kTile>(p, listed, entry), each = tiles + kUnitCost;
-        const int u_in = (int)((x - first) / each);
-        const long long zero = first + u_in * each + kUnitCost;    // place of the unit's tile 0
+        const long long tiles = tiles_of<S::kTile>(p, listed, entry);
+        const long long zero = start + kUnitCost;     // place of the unit's tile 0
         const long long tile0 = x > zero ? x - zero : 0;
         const long long stop = zero + tiles < end ? zero + tiles : end;
         const long long count = stop - zero - tile0;
@@ -630,13 +645,17 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         };
 
         // first copies and the queries, under way together; the ring held the
-        // last unit's results
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        // last unit's results, which everybody has read by now
+        auto ring_is_free = [&] {
+            __syncthreads();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        };
         int pos_next = -1, page_next = -1, pos_after = -1;
         Queries<D, Rows> queries;
         if constexpr (kRun > 0) {
             run_page = run_page_of(now, 0);
             queries.load(p, unit);
+            ring_is_free();
             next_runs(now, 0);
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
@@ -652,6 +671,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             for (int s = 0; s < S::kStages; ++s)
                 page[s] = page_of(now, pos[s]);
             queries.load(p, unit);
+            ring_is_free();
 #pragma unroll
             for (int s = 0; s < S::kStages - 1; ++s) {
                 if (s < mine)
@@ -663,12 +683,13 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         }
         queries.store(p, unit, len, smem);
         if (threadIdx.x == 0) {
-            const bool last = zero + tiles - first == each * p.units;
+            const bool last = u_in + 1 == p.units;
             part.list = now.list, part.row_table = now.row_table;
             part.head_pool = now.head_pool, part.seen = now.seen;
             part.next = zero + tiles;
-            part.next_first = last ? zero + tiles : first;
             part.next_entry = entry + last;
+            part.next_unit = last ? 0 : u_in + 1;
+            part.active = count < S::kWarps ? (int)count : S::kWarps;
             part.u.b = unit.b, part.u.head = unit.head, part.u.query = unit.query;
             part.u.row0 = unit.row0, part.u.rows = unit.rows;
             part.whole = count == tiles;
@@ -1002,10 +1023,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         __syncwarp();
 
         // ---- the warps' results, side by side in the rings' place ----------
+        // (a warp without tiles has none)
+        const int active = part.active;
 #pragma unroll
         for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                if (warp >= active)
+                    break;
                 const int r = row(b, c);
                 float s = lost ? __int_as_float(0x7fffffff) : sum[b][c];
 #pragma unroll
@@ -1042,73 +1067,48 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         const bool whole = part.whole;
         // a CTA's second place is for the unit that begins in it
         float *to_join = p.a.partial + p.parts + (blockIdx.x * 2LL + part.begins) * S::kPartial;
-        // weights of the warps' results: 2^(max - largest max)
-        if (threadIdx.x < S::kRows) {
-            const int r = threadIdx.x;
-            float m = -INFINITY, l = 0.f;
-            for (int w = 0; w < S::kWarps; ++w)
-                m = fmaxf(m, wmax(w, r));
-            for (int w = 0; w < S::kWarps; ++w) {
-                const float f = wmax(w, r);
-                // a warp that saw nothing has sum 0; one whose scores are NaN
-                // has a maximum of -inf, and its NaN goes on
-                const float weight = m == -INFINITY ? 1.f : exp2_fast(f - m);
-                const float s = wsum(w, r);
-                l += s == 0.f ? 0.f : s * weight;
-                wmax(w, r) = s != s ? 1.f : weight;
-            }
-            if (whole) {
-                wsum(0, r) = l == 0.f ? 0.f : 1.f / l;
-                if (r < u.rows && p.a.lse) {
-                    int j, h;
-                    u.row(p, r, &j, &h);
-                    p.a.lse[((long long)u.b * p.a.queries + j) * p.a.heads + h] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                }
-            } else {
-                to_join[r] = m;
-                to_join[S::kRows + r] = l;
-            }
-        }
-        __syncthreads();
         for (int e = threadIdx.x; e < S::kRows * D / 4; e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             if (r >= u.rows)
                 break;
+            float m = -INFINITY, l = 0.f;
+            for (int w = 0; w < active; ++w)
+                m = fmaxf(m, wmax(w, r));
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) {
+            for (int w = 0; w < active; ++w) {
+                // a warp that saw nothing has maximum -inf and sum 0; one whose
+                // scores are NaN has maximum -inf, and its NaN goes on
+                const float s = wsum(w, r);
+                const float weight = s == 0.f ? 0.f : s != s ? 1.f : exp2_fast(wmax(w, r) - m);
                 const float4 f = *reinterpret_cast<const float4 *>(
                     smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
-                const float weight = wmax(w, r);
+                l += s * weight;
                 v.x += f.x * weight, v.y += f.y * weight, v.z += f.z * weight, v.w += f.w * weight;
             }
+            int j, h;
+            u.row(p, r, &j, &h);
+            const long long at = ((long long)u.b * p.a.queries + j) * p.a.heads + h;
             if (whole) {
-                const float inv = wsum(0, r);
-                int j, h;
-                u.row(p, r, &j, &h);
-                const long long to = (((long long)u.b * p.a.queries + j) * p.a.heads + h) * D + d;
-                if (p.a.bf16) {
-                    __nv_bfloat16 y[4];
-                    from_float(y[0], v.x * inv), from_float(y[1], v.y * inv);
-                    from_float(y[2], v.z * inv), from_float(y[3], v.w * inv);
-                    *reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + to) =
-                        *reinterpret_cast<const uint2 *>(y);
-                } else {
-                    __half y[4];
-                    from_float(y[0], v.x * inv), from_float(y[1], v.y * inv);
-                    from_float(y[2], v.z * inv), from_float(y[3], v.w * inv);
-                    *reinterpret_cast<uint2 *>((__half *)p.a.out + to) =
-                        *reinterpret_cast<const uint2 *>(y);
-                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                if (p.a.bf16)
+                    store_four((__nv_bfloat16 *)p.a.out + at * D + d, v, inv);
+                else
+                    store_four((__half *)p.a.out + at * D + d, v, inv);
+                if (d == 0 && p.a.lse)
+                    p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
                 *reinterpret_cast<float4 *>(to_join + 2 * S::kRows + r * D + d) = v;
+                if (d == 0) {
+                    to_join[r] = m;
+                    to_join[S::kRows + r] = l;
+                }
             }
         }
-        x = part.next;
-        first = part.next_first;
+        x = start = part.next;
         entry = part.next_entry;
-        __syncthreads();
+        u_in = part.next_unit;
+        if (x >= end)
+            break;
     }
 }
 
@@ -1205,6 +1205,9 @@ cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
     using S = Shape<D, Rows>;
     p.blocks = (p.rows + S::kRows - 1) / S::kRows;
     p.units = p.c.kv_heads * p.blocks * (p.a.indices ? p.a.queries : 1);
+    p.by_group.set(p.group);
+    p.by_blocks.set(p.blocks);
+    p.by_heads.set(p.c.kv_heads);
     p.sel_tiles = ((long long)p.a.k + S::kTile - 1) / S::kTile;
     // no more CTAs than the largest possible line has work for
     const double room = (double)p.c.max_pages * p.c.page_size;
