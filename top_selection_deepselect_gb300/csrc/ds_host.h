@@ -1,4 +1,4 @@
-// ds_host.h -- error reporting shared by the library's host code.
+// ds_host.h -- error reporting and launches shared by the library's host code.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,6 +11,26 @@ extern thread_local char g_detail[512];
 // Records a message and returns `status`.
 int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail_cuda(cudaError_t e, const char *what);
+
+// Launches with programmatic dependent launch: the grid may be scheduled while
+// the previous kernel on the stream drains.  The kernel calls
+// dependent_grid_wait() before it touches memory and allow_dependent_grid().
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem,
+                              cudaStream_t stream, Args &&...args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // The current device's ordinal and its SM count, asked of CUDA once a device.
 int current_device(int *dev, int *sms);

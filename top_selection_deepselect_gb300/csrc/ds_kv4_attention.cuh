@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "ds_device.cuh"
+#include "ds_host.h"
 #include "ds_kv4.cuh"
 #include "ds_kv4_launch.h"
 
@@ -1127,6 +1128,7 @@ join_kernel(const __grid_constant__ AttendArgs p)
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x / (Rows / 8), r = blockIdx.x % (Rows / 8) * 8 + threadIdx.x / 32;
     dependent_grid_wait();
+    allow_dependent_grid();
     const int4 split = reinterpret_cast<const int4 *>(p.a.partial)[cta];
     const int parts = split.z;
     if (parts == 0)
@@ -1228,24 +1230,10 @@ cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
             return e;
         raised[which].fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, fn, (const AttendArgs)p)) != cudaSuccess)
+    e = launch_overlapped(fn, ctas, S::kThreads, S::kSmem, stream, p);
+    if (e != cudaSuccess || ctas == 1)    // one CTA leaves nothing to join
         return e;
-    if (ctas == 1)
-        return cudaSuccess;    // nothing to join
-    cfg.gridDim = dim3((unsigned)(ctas * (Rows / 8)));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, Rows>, (const AttendArgs)p);
+    return launch_overlapped(join_kernel<D, Rows>, ctas * (Rows / 8), kJoinThreads, 0, stream, p);
 }
 
 template <int D>

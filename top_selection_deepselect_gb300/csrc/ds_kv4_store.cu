@@ -9,6 +9,8 @@
 // instructions: magnitudes are compared as bits, quotients and integers come
 // from multiply-adds, and a token's place is looked up once for several heads
 // where there are tokens enough.
+#include "ds_device.cuh"
+#include "ds_host.h"
 #include "ds_kv4.cuh"
 #include "ds_kv4_launch.h"
 
@@ -151,6 +153,8 @@ append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__res
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
+    dependent_grid_wait();
+    allow_dependent_grid();
     const int lane = threadIdx.x & 31, first = lane & ~(kWords - 1);
     const Place<D> at(c, by_runs, each, runs, seq, pos, tokens);
     const bool there = at.slot.page >= 0;
@@ -220,6 +224,8 @@ read_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__restr
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
+    dependent_grid_wait();
+    allow_dependent_grid();
     const int lane = threadIdx.x & 31, first = lane & ~(kWords - 1);
     const Place<D> at(c, by_runs, each, runs, seq, pos, tokens);
     const bool there = at.slot.page >= 0;
@@ -288,9 +294,8 @@ cudaError_t append_one(const Cache &c, const int32_t *seq, const int32_t *pos, l
         vec = vec && ks[j] * (long long)sizeof(T) % 16 == 0 && vs[j] * (long long)sizeof(T) % 16 == 0;
     const Launch l(c, D, tokens);
     auto fn = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
-    fn<<<l.grid, kThreads, 0, stream>>>(c, l.by_runs, l.each, l.runs, seq, pos, (int)tokens,
-                                        (const T *)k, ks[0], ks[1], (const T *)v, vs[0], vs[1]);
-    return cudaGetLastError();
+    return launch_overlapped(fn, l.grid, kThreads, 0, stream, c, l.by_runs, l.each, l.runs, seq, pos,
+                             (int)tokens, (const T *)k, ks[0], ks[1], (const T *)v, vs[0], vs[1]);
 }
 
 template <typename T, int D>
@@ -298,9 +303,8 @@ cudaError_t read_one(const Cache &c, const int32_t *seq, const int32_t *pos, lon
                      void *k, void *v, cudaStream_t stream)
 {
     const Launch l(c, D, tokens);
-    read_kernel<T, D><<<l.grid, kThreads, 0, stream>>>(c, l.by_runs, l.each, l.runs, seq, pos,
-                                                       (int)tokens, (T *)k, (T *)v);
-    return cudaGetLastError();
+    return launch_overlapped(read_kernel<T, D>, l.grid, kThreads, 0, stream, c, l.by_runs, l.each, l.runs,
+                             seq, pos, (int)tokens, (T *)k, (T *)v);
 }
 
 template <typename T>

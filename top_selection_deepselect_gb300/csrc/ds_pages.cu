@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 
+#include "ds_device.cuh"
 #include "ds_host.h"
 #include "ds_topk.h"
 
@@ -119,6 +120,8 @@ __global__ void __launch_bounds__(kThreads)
 reserve_kernel(Book book, const int32_t *seqs, const int32_t *tokens, int n, int32_t *status,
                int32_t *ws)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     const Work w = work_of(ws, book.n_pages, n);
     // lengths before the call, then the claims
     for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -187,6 +190,8 @@ __global__ void __launch_bounds__(kThreads)
 fork_plan_kernel(Book book, const int32_t *src, const int32_t *dst, int n, int32_t *status,
                  int32_t *ws)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     const Work w = work_of(ws, book.n_pages, n);
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const int s = src[i], d = dst[i];
@@ -274,6 +279,8 @@ __device__ void move_pages(const Pool &pool, long long moves, From from, To to)
 __global__ void __launch_bounds__(kMoveThreads)
 copy_kernel(Pool pool, const int32_t *src, const int32_t *dst, int n)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     move_pages(pool, n, [&](long long m) { return src[m]; }, [&](long long m) { return dst[m]; });
 }
 
@@ -281,6 +288,8 @@ copy_kernel(Pool pool, const int32_t *src, const int32_t *dst, int n)
 __global__ void __launch_bounds__(kMoveThreads)
 fork_kernel(Pool pool, Book book, const int32_t *src, const int32_t *dst, int n, int32_t *ws)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     const Work w = work_of(ws, book.n_pages, n);
     const int pieces = (book.max_pages + kMoveThreads - 1) / kMoveThreads;
     for (long long it = blockIdx.x; it < (long long)n * pieces; it += gridDim.x) {
@@ -311,6 +320,8 @@ fork_kernel(Pool pool, Book book, const int32_t *src, const int32_t *dst, int n,
 __global__ void __launch_bounds__(kMoveThreads)
 free_kernel(Book book, const int32_t *seqs)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     __shared__ int length;
     const int s = seqs[blockIdx.x];
     if ((unsigned)s >= (unsigned)book.max_seqs)
@@ -333,6 +344,8 @@ free_kernel(Book book, const int32_t *seqs)
 __global__ void __launch_bounds__(kThreads)
 compact_plan_kernel(Book book, int32_t *remap, int32_t *status, int32_t *holes, int32_t *movers)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     __shared__ int live_below;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     int lo, hi, before;
@@ -377,6 +390,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 compact_kernel(Pool pool, Book book, const int32_t *remap, const int32_t *status,
                const int32_t *holes, const int32_t *movers)
 {
+    ds::dependent_grid_wait();
+    ds::allow_dependent_grid();
     const int moves = status[1];
     const long long threads = (long long)gridDim.x * kMoveThreads;
     const long long me = (long long)blockIdx.x * kMoveThreads + threadIdx.x;
@@ -475,9 +490,8 @@ int move_grid(long long items, unsigned *grid)
 
 long long chunks_of(const Pool &p) { return p.layers * ((p.page_bytes + kChunk - 1) / kChunk); }
 
-int finish(const char *what)
+int finish(const char *what, cudaError_t e)
 {
-    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DS_OK : fail_cuda(e, what);
 }
 
@@ -503,8 +517,8 @@ int ds_pages_copy(const ds_page_pool_t *pool, const int32_t *src, const int32_t 
         return rc;
     if ((rc = move_grid(n * chunks_of(*pool), &grid)) != DS_OK)
         return rc;
-    copy_kernel<<<grid, kMoveThreads, 0, (cudaStream_t)stream>>>(*pool, src, dst, n);
-    return finish("ds_pages_copy");
+    return finish("ds_pages_copy", ds::launch_overlapped(copy_kernel, grid, kMoveThreads, 0,
+                                                         (cudaStream_t)stream, *pool, src, dst, n));
 }
 
 int ds_pages_reserve(const ds_page_book_t *book, const int32_t *seqs, const int32_t *tokens, int n,
@@ -520,9 +534,9 @@ int ds_pages_reserve(const ds_page_book_t *book, const int32_t *seqs, const int3
         rc = check_work(workspace, workspace_bytes, ds_pages_workspace(book->n_pages, n));
     if (rc != DS_OK)
         return rc;
-    reserve_kernel<<<1, kThreads, 0, (cudaStream_t)stream>>>(*book, seqs, tokens, n, status,
-                                                            (int32_t *)workspace);
-    return finish("ds_pages_reserve");
+    return finish("ds_pages_reserve",
+                  ds::launch_overlapped(reserve_kernel, 1, kThreads, 0, (cudaStream_t)stream, *book, seqs,
+                                        tokens, n, status, (int32_t *)workspace));
 }
 
 int ds_pages_fork(const ds_page_pool_t *pool, const ds_page_book_t *book, const int32_t *src,
@@ -547,10 +561,12 @@ int ds_pages_fork(const ds_page_pool_t *pool, const ds_page_book_t *book, const 
     if (rc != DS_OK)
         return rc;
     int32_t *ws = (int32_t *)workspace;
-    fork_plan_kernel<<<1, kThreads, 0, (cudaStream_t)stream>>>(*book, src, dst, n, status, ws);
-    if (n > 0)
-        fork_kernel<<<grid, kMoveThreads, 0, (cudaStream_t)stream>>>(*pool, *book, src, dst, n, ws);
-    return finish("ds_pages_fork");
+    cudaError_t e = ds::launch_overlapped(fork_plan_kernel, 1, kThreads, 0, (cudaStream_t)stream, *book,
+                                          src, dst, n, status, ws);
+    if (e == cudaSuccess && n > 0)
+        e = ds::launch_overlapped(fork_kernel, grid, kMoveThreads, 0, (cudaStream_t)stream, *pool, *book,
+                                  src, dst, n, ws);
+    return finish("ds_pages_fork", e);
 }
 
 int ds_pages_free(const ds_page_book_t *book, const int32_t *seqs, int n, void *stream)
@@ -561,8 +577,8 @@ int ds_pages_free(const ds_page_book_t *book, const int32_t *seqs, int n, void *
         rc = check_list(n, seqs != nullptr);
     if (rc != DS_OK || n == 0)
         return rc;
-    free_kernel<<<(unsigned)n, kMoveThreads, 0, (cudaStream_t)stream>>>(*book, seqs);
-    return finish("ds_pages_free");
+    return finish("ds_pages_free", ds::launch_overlapped(free_kernel, (unsigned)n, kMoveThreads, 0,
+                                                         (cudaStream_t)stream, *book, seqs));
 }
 
 int ds_pages_compact(const ds_page_pool_t *pool, const ds_page_book_t *book, int32_t *remap,
@@ -584,10 +600,12 @@ int ds_pages_compact(const ds_page_pool_t *pool, const ds_page_book_t *book, int
     if (rc != DS_OK)
         return rc;
     int32_t *holes = (int32_t *)workspace, *movers = holes + book->n_pages;
-    compact_plan_kernel<<<1, kThreads, 0, (cudaStream_t)stream>>>(*book, remap, status, holes, movers);
-    compact_kernel<<<grid, kMoveThreads, 0, (cudaStream_t)stream>>>(*pool, *book, remap, status,
-                                                                   holes, movers);
-    return finish("ds_pages_compact");
+    cudaError_t e = ds::launch_overlapped(compact_plan_kernel, 1, kThreads, 0, (cudaStream_t)stream,
+                                          *book, remap, status, holes, movers);
+    if (e == cudaSuccess)
+        e = ds::launch_overlapped(compact_kernel, grid, kMoveThreads, 0, (cudaStream_t)stream, *pool,
+                                  *book, remap, status, holes, movers);
+    return finish("ds_pages_compact", e);
 }
 
 }  // extern "C"
