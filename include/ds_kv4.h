@@ -12,10 +12,11 @@
  *     D/32 fp16   value scales
  *     zeros up to a multiple of 16 bytes
  * so 80 (72 used), 144 and 288 bytes.  A code u in 0..15 stands for
- * (u - 8) * scale.  Quantisation of a group x: scale = fp16(max|x| / 7),
- * u = 8 + clamp(rint(x / scale), -7, 7), u = 8 where the scale is 0; a scale
- * beyond fp16 is 65504 (the codes clamp), and a group with a NaN or an
- * infinity gets the scale NaN, so that it reads back as NaN.
+ * (u - 8) * scale.  Quantisation of a group x: scale = fp16(max|x| * r) with r
+ * the fp32 number nearest to 1/7 and the product rounded to fp32 first, u = 8 +
+ * clamp(rint(fp32(x / scale)), -7, 7), u = 8 where the scale is 0; a scale beyond
+ * fp16 is 65504 (the codes clamp), and a group with a NaN or an infinity gets the
+ * scale NaN, so that it reads back as NaN.
  * Order inside a record, for each stretch of W = min(D, 128) channels, with
  * n = W / 32 groups: the key's 32-bit words (eight channels, lowest channel
  * in the lowest bits) stand with word 4 i + t of the stretch at place

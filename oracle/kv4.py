@@ -37,7 +37,7 @@ def quantise(x):
     bad = ~np.isfinite(g).all(-1)
     with np.errstate(all="ignore"):
         top = np.where(bad, np.float32(0), np.abs(g).max(-1).astype(np.float32))
-        scale = (top / np.float32(7)).astype(np.float16)
+        scale = (top * (np.float32(1) / np.float32(7))).astype(np.float16)
         scale = np.where(np.isinf(scale), np.float16(65504), scale)
         step = scale.astype(np.float32)[..., None]
         code = np.where((step > 0) & ~bad[..., None], np.rint(g / step), 0)

@@ -367,6 +367,39 @@ def test_another_stream_and_a_graph(ds):
     assert torch.equal(out, now[0]) and torch.equal(lse, now[1])
 
 
+def test_streams_and_threads_do_not_share_a_workspace_at_a_time(ds):
+    """Calls without a workspace, from several streams and from several host threads on one."""
+    import threading
+    rng = np.random.default_rng(12)
+    jobs = []
+    for i, n in enumerate([9000, 4000, 7000, 12000]):
+        lengths = np.array([n], dtype=np.int32)
+        table, n_pages = make_table(rng, lengths, 16, wide=-(-n // 16))
+        pool, t, size = dev(random_pool(rng, n_pages, 1, 16, 64)), dev(table), dev(lengths)
+        q = dev(rng.standard_normal((1, 1, 8, 64)).astype(np.float32)).bfloat16()
+        space = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+        jobs.append(((q, pool, t, size), ds.kv4_attention(q, pool, t, size, workspace=space)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+
+    def work(job, stream, got):
+        with torch.cuda.stream(stream):
+            got += [ds.kv4_attention(*job[0]) for _ in range(40)]
+
+    for one in (False, True):
+        got = [[] for _ in jobs]
+        threads = [threading.Thread(target=work, args=(j, streams[0] if one else s, g))
+                   for j, s, g in zip(jobs, streams, got)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for (_, want), results in zip(jobs, got):
+            assert len(results) == 40
+            assert all(torch.equal(want[0], r[0]) and torch.equal(want[1], r[1]) for r in results)
+
+
 def test_refusals(ds):
     pool = torch.zeros((4, 2, 16, 144), dtype=torch.uint8, device=DEV)
     table = torch.zeros((3, 4), dtype=torch.int32, device=DEV)

@@ -8,6 +8,7 @@ torch and enqueue on the current stream.
 import ctypes
 import math
 import struct
+import threading
 
 from ._binding import DS_BF16, DS_FP16, DS_FP32, _check, load_library
 
@@ -150,6 +151,8 @@ class _Torch:
         self.codes = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.capturing = torch.cuda.is_current_stream_capturing
+        self.on_stream = torch.cuda.stream
         lib = _lib()
 
         def bytes_for(name, at):
@@ -174,6 +177,32 @@ class _Torch:
 
 
 _t = _Torch()
+
+# Workspaces of calls that are given none: one for each device and stream, grown
+# as needed and kept.  Calls on one stream follow each other, so that they can
+# share it; _order keeps the launches of one call together where several host
+# threads use a stream.  A call that is being captured into a graph gets memory of
+# its own, since the graph may run on any stream.
+_kept = {}
+_order = threading.Lock()
+_KEPT_BYTES = 1 << 20     # at least this much, so that few calls grow it
+
+
+def _grow(t, device, need, key):
+    size = max(need, _KEPT_BYTES)
+    # the old one, if any, goes back to its stream's memory in order
+    space = t.empty(size, dtype=t.uint8, device=device)
+    _kept[key] = (space, size)
+    return space, size
+
+
+def _workspace(t, device, raw, need):
+    """(workspace, its bytes) for a call on the device's current stream, whose handle is raw."""
+    if t.capturing():
+        return t.empty(need, dtype=t.uint8, device=device), need
+    key = (device.index, raw)
+    space = _kept.get(key)
+    return space if space is not None and space[1] >= need else _grow(t, device, need, key)
 
 
 def _int32(name, t, device, n=None):
@@ -234,6 +263,9 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
     be in the table (pages_reserve); tokens without one are skipped.
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return kv4_append(pool, table, seq, pos, k, v)
     shape, dtype, device = k.shape, k.dtype, pool.device
     if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
@@ -251,7 +283,7 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
                          "dimension")
     status = t.append(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
                       tokens, code, k.data_ptr(), _pack_2(k0, k1), v.data_ptr(), _pack_2(v0, v1),
-                      t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+                      t.raw_stream(device.index))
     if status:
         _check(status, "ds_kv4_append")
 
@@ -263,6 +295,9 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
     is not there reads as zeros.
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return kv4_read(pool, table, seq, pos, head_dim, dtype, k, v)
     tokens, device = seq.numel(), pool.device
     cache = _cache(pool, table, head_dim, device)
     shape = (tokens, pool.shape[1], head_dim)
@@ -279,7 +314,7 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
         v = t.empty(shape, dtype=dtype, device=device)
     status = t.read(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
                     tokens, code, k.data_ptr(), v.data_ptr(),
-                    t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+                    t.raw_stream(device.index))
     if status:
         _check(status, "ds_kv4_read")
     return k, v
@@ -317,6 +352,9 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     0 and -inf.
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return kv4_attention(q, pool, table, lengths, indices, scale, seqs, out, lse, workspace)
     device, shape, dtype = pool.device, q.shape, q.dtype
     if len(shape) != 4 or q.device != device:
         raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device")
@@ -356,16 +394,17 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
         return out, lse
     index = device.index
     size = _attention_workspace(cache, batch, queries, heads, k, dim, pool.shape[1], index)
-    if workspace is None:
-        workspace = t.empty(size, dtype=t.uint8, device=device)
-    else:
-        given = _space("workspace", workspace, device)
-        if given < size:
-            raise ValueError("workspace has %d bytes, %d needed" % (given, size))
-    status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
-                         _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
-                         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
-                         t.raw_stream(index) if stream is None else stream.cuda_stream)
+    raw = t.raw_stream(index)
+    with _order:
+        if workspace is None:
+            workspace, size = _workspace(t, device, raw, size)
+        else:
+            given = _space("workspace", workspace, device)
+            if given < size:
+                raise ValueError("workspace has %d bytes, %d needed" % (given, size))
+        status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
+                             _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, raw)
     if status:
         _check(status, "ds_kv4_attention")
     return out, lse
@@ -396,25 +435,29 @@ def _book(table, lengths, refs, page_size, device):
                       _int32("refs", refs, device), rows, columns, page_size, refs.numel())
 
 
-def _work(t, device, need, workspace, status):
-    """(workspace, its bytes, status); ones that are not given are made."""
-    if workspace is None:
-        workspace, size = t.empty(need, dtype=t.uint8, device=device), need
-    else:
-        size = _space("workspace", workspace, device)
+def _status(t, device, status):
     if status is None:
-        status = t.empty(2, dtype=t.int32, device=device)
-    else:
-        _int32("status", status, device, 2)
-    return workspace, size, status
+        return t.empty(2, dtype=t.int32, device=device)
+    _int32("status", status, device, 2)
+    return status
+
+
+def _work(t, device, raw, need, workspace):
+    """(workspace, its bytes); called under _order."""
+    if workspace is None:
+        return _workspace(t, device, raw, need)
+    return workspace, _space("workspace", workspace, device)
 
 
 def pages_copy(pool, src, dst, stream=None):
     """Page dst[i] of pool [layers, n_pages, ...] := page src[i], in every layer (int32 lists)."""
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return pages_copy(pool, src, dst)
     n, device = src.numel(), pool.device
     status = t.copy(_pool(pool, device), _int32("src", src, device, n), _int32("dst", dst, device, n),
-                    n, t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+                    n, t.raw_stream(device.index))
     if status:
         _check(status, "ds_pages_copy")
 
@@ -427,12 +470,17 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     when above 0), pages taken.
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace, status)
     n, device = seqs.numel(), table.device
     book = _book(table, lengths, refs, page_size, device)
-    workspace, size, status = _work(t, device, ds_pages_workspace(refs.numel(), n), workspace, status)
-    rc = t.reserve(book, _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n), n,
-                   status.data_ptr(), workspace.data_ptr(), size,
-                   t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    status = _status(t, device, status)
+    seqs_at, tokens_at = _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n)
+    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(device.index)
+    with _order:
+        workspace, size = _work(t, device, raw, need, workspace)
+        rc = t.reserve(book, seqs_at, tokens_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_reserve")
     return status
@@ -445,14 +493,19 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     returns status as pages_reserve does.
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return pages_fork(pool, table, lengths, refs, src, dst, workspace, status)
     if pool.dim() != 5:
         raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes]")
     n, device = src.numel(), table.device
     book = _book(table, lengths, refs, pool.shape[3], device)
-    workspace, size, status = _work(t, device, ds_pages_workspace(refs.numel(), n), workspace, status)
-    rc = t.fork(_pool(pool, device), book, _int32("src", src, device, n),
-                _int32("dst", dst, device, n), n, status.data_ptr(), workspace.data_ptr(), size,
-                t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    at, status = _pool(pool, device), _status(t, device, status)
+    src_at, dst_at = _int32("src", src, device, n), _int32("dst", dst, device, n)
+    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(device.index)
+    with _order:
+        workspace, size = _work(t, device, raw, need, workspace)
+        rc = t.fork(at, book, src_at, dst_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_fork")
     return status
@@ -461,9 +514,12 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
 def pages_free(table, lengths, refs, seqs, page_size, stream=None):
     """The sequences seqs[i] end: their pages' refs go down, their rows become -1."""
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return pages_free(table, lengths, refs, seqs, page_size)
     n, device = seqs.numel(), table.device
     rc = t.free(_book(table, lengths, refs, page_size, device), _int32("seqs", seqs, device, n), n,
-                t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+                t.raw_stream(device.index))
     if rc:
         _check(rc, "ds_pages_free")
 
@@ -475,14 +531,19 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
     [2]: live pages, pages moved).
     """
     t = _t if _t.ready else _t.find()
+    if stream is not None:
+        with t.on_stream(stream):      # what is allocated belongs to that stream
+            return pages_compact(pool, table, refs, workspace, remap, status)
     device, n_pages = table.device, refs.numel()
     book = _book(table, None, refs, 1, device)
     if remap is None:
         remap = t.empty(n_pages, dtype=t.int32, device=device)
-    workspace, size, status = _work(t, device, ds_pages_workspace(n_pages, 0), workspace, status)
-    rc = t.compact(_pool(pool, device), book, _int32("remap", remap, device, n_pages),
-                   status.data_ptr(), workspace.data_ptr(), size,
-                   t.raw_stream(device.index) if stream is None else stream.cuda_stream)
+    at, status = _pool(pool, device), _status(t, device, status)
+    remap_at = _int32("remap", remap, device, n_pages)
+    need, raw = ds_pages_workspace(n_pages, 0), t.raw_stream(device.index)
+    with _order:
+        workspace, size = _work(t, device, raw, need, workspace)
+        rc = t.compact(at, book, remap_at, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_compact")
     return remap, status

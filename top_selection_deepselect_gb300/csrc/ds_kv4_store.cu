@@ -120,7 +120,7 @@ __device__ __forceinline__ unsigned encode(const Eight<T> &e, unsigned *bits)
 {
     const unsigned most = largest(e);
     const bool bad = most >= 0x7f800000u;      // a NaN or an infinity poisons the group
-    __half scale = __float2half_rn(quotient(__uint_as_float(most), 7.f, 1.f / 7.f));
+    __half scale = __float2half_rn(__uint_as_float(most) * (1.f / 7.f));
     if (__hisinf(scale))
         scale = __ushort_as_half(0x7bff);
     const float step = __half2float(scale);
