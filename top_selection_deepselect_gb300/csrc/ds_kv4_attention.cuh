@@ -72,6 +72,8 @@ struct Shape {
     // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.
     static constexpr int kWarps = kOutRegs == 64 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
+    // 16-token steps whose scores are made before their values are used (wide)
+    static constexpr int kJoint = kMT == 2 && kBlocks == 1 ? 2 : 1;
     static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
     static constexpr int kStages = D == 64 ? (kCtas == 2 ? 4 : 6) : kCtas == 2 ? 3 : kWarps == 12 ? 4 : 5;
     static constexpr int kOutStride = D + 4;                     // floats of an output row in shared memory
@@ -874,118 +876,128 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 }
             } else {
 #pragma unroll 1
-                for (int mt = 0; mt < S::kMT; ++mt) {
-                    // scores of the step's places 2 t, 2 t + 1 (half 0) and those + 8
-                    float sc[S::kBlocks][2][4];
-                    const unsigned char *step = tile + mt * 16 * S::kRecord;
-                    const unsigned char *ra = step + tok_a * S::kRecord, *rb = step + tok_b * S::kRecord;
+                for (int m0 = 0; m0 < S::kMT; m0 += S::kJoint) {
+                    // scores of a step's places 2 t, 2 t + 1 (half 0) and those + 8
+                    float sc[S::kJoint][S::kBlocks][2][4];
+                    const int next = S::kNext * S::kRecord;
+                    auto record = [&](int m, int token) {
+                        return tile + ((m0 + m) * 16 + token) * S::kRecord;
+                    };
 #pragma unroll
-                    for (int b = 0; b < S::kBlocks; ++b)
+                    for (int m = 0; m < S::kJoint; ++m) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[b][0][e] = sc[b][1][e] = 0.f;
+                        for (int half = 0; half < 2; ++half) {
+                            const unsigned char *rk = record(m, tok_row) + half * next;
+                            float sa[S::kGroups], sb[S::kGroups];
+                            load_scales(sa, record(m, tok_a) + half * next + D);
+                            load_scales(sb, record(m, tok_b) + half * next + D);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const unsigned char *rk = step + (tok_row + half * S::kNext) * S::kRecord;
-                        float sa[S::kGroups], sb[S::kGroups];
-                        load_scales(sa, ra + half * S::kNext * S::kRecord + D);
-                        load_scales(sb, rb + half * S::kNext * S::kRecord + D);
+                            for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
-                        for (int st = 0; st < S::kStretches; ++st) {
-                            uint32_t wk[S::kPer];
-                            load_words(wk, rk + st * 64 + t * S::kPer * 4);
+                                for (int e = 0; e < 4; ++e)
+                                    sc[m][b][half][e] = 0.f;
 #pragma unroll
-                            for (int i = 0; i < S::kPer; ++i) {
-                                const int group = st * S::kPer + i;
-                                const uint32_t k0 = low_codes(wk[i]), k1 = high_codes(wk[i]);
-                                const uint32_t k2 = low_codes(wk[i] >> 8), k3 = high_codes(wk[i] >> 8);
+                            for (int st = 0; st < S::kStretches; ++st) {
+                                uint32_t wk[S::kPer];
+                                load_words(wk, rk + st * 64 + t * S::kPer * 4);
 #pragma unroll
-                                for (int b = 0; b < S::kBlocks; ++b) {
-                                    const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kOffQ) +
-                                                      (group * 2 * S::kBlocks + b) * 32 + lane;
-                                    const uint4 q0 = qf[0], q1 = qf[S::kBlocks * 32];
-                                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma16816(acc, q0.x, q0.y, q0.z, q0.w, k0, k1);
-                                    mma16816(acc, q1.x, q1.y, q1.z, q1.w, k2, k3);
+                                for (int i = 0; i < S::kPer; ++i) {
+                                    const int group = st * S::kPer + i;
+                                    const uint32_t k0 = low_codes(wk[i]), k1 = high_codes(wk[i]);
+                                    const uint32_t k2 = low_codes(wk[i] >> 8), k3 = high_codes(wk[i] >> 8);
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        sc[b][half][e] += (e & 1 ? sb[group] : sa[group]) * acc[e];
+                                    for (int b = 0; b < S::kBlocks; ++b) {
+                                        const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kOffQ) +
+                                                          (group * 2 * S::kBlocks + b) * 32 + lane;
+                                        const uint4 q0 = qf[0], q1 = qf[S::kBlocks * 32];
+                                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma16816(acc, q0.x, q0.y, q0.z, q0.w, k0, k1);
+                                        mma16816(acc, q1.x, q1.y, q1.z, q1.w, k2, k3);
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            sc[m][b][half][e] += (e & 1 ? sb[group] : sa[group]) * acc[e];
+                                    }
                                 }
                             }
                         }
                     }
-                    auto token = [&](int half, int e) {
-                        return mt * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
+                    auto token = [&](int m, int half, int e) {
+                        return (m0 + m) * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
                     };
                     float best[S::kBlocks][2];
 #pragma unroll
                     for (int b = 0; b < S::kBlocks; ++b) {
                         best[b][0] = best[b][1] = -INFINITY;
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
+                        for (int m = 0; m < S::kJoint; ++m)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
-                                    sc[b][half][e] = -INFINITY;
-                                best[b][e / 2] = fmaxf(best[b][e / 2], sc[b][half][e]);
-                            }
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
+                                        sc[m][b][half][e] = -INFINITY;
+                                    best[b][e / 2] = fmaxf(best[b][e / 2], sc[m][b][half][e]);
+                                }
                     }
                     raise(best);
 #pragma unroll
-                    for (int b = 0; b < S::kBlocks; ++b) {
+                    for (int m = 0; m < S::kJoint; ++m) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half)
+                        for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float pr = exp2_fast(sc[b][half][e] * fac[b][e / 2] - low[b][e / 2]);
-                                if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
-                                    pr = 0.f;
-                                sum[b][e / 2] += pr;
-                                sc[b][half][e] = pr;
-                            }
-                    }
+                            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int st = 0; st < S::kStretches; ++st) {
-                        constexpr int kW = S::kPer / 2;
-                        const int at = D / 2 + st * 64 + g * kW * 4, next = S::kNext * S::kRecord;
-                        uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
-                        load_words(wa, ra + at);
-                        load_words(wb, rb + at);
-                        load_words(xa, ra + next + at);
-                        load_words(xb, rb + next + at);
+                                for (int e = 0; e < 4; ++e) {
+                                    float pr = exp2_fast(sc[m][b][half][e] * fac[b][e / 2] - low[b][e / 2]);
+                                    if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
+                                        pr = 0.f;
+                                    sum[b][e / 2] += pr;
+                                    sc[m][b][half][e] = pr;
+                                }
+                        const unsigned char *ra = record(m, tok_a), *rb = record(m, tok_b);
+                        float vs[4][S::kGroups];     // value scales of the lane's four tokens
+                        load_scales(vs[0], ra + D + 2 * S::kGroups);
+                        load_scales(vs[1], rb + D + 2 * S::kGroups);
+                        load_scales(vs[2], ra + next + D + 2 * S::kGroups);
+                        load_scales(vs[3], rb + next + D + 2 * S::kGroups);
 #pragma unroll
-                        for (int i = 0; i < S::kPer; ++i) {
-                            const int group = st * S::kPer + i;
-                            const int vs = D + 2 * S::kGroups + 2 * group;
-                            const float s0 = __half2float(*reinterpret_cast<const __half *>(ra + vs));
-                            const float s1 = __half2float(*reinterpret_cast<const __half *>(rb + vs));
-                            const float s2 = __half2float(*reinterpret_cast<const __half *>(ra + next + vs));
-                            const float s3 = __half2float(*reinterpret_cast<const __half *>(rb + next + vs));
-                            const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
-                            const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
-                            uint32_t pa[S::kBlocks][4];
+                        for (int st = 0; st < S::kStretches; ++st) {
+                            constexpr int kW = S::kPer / 2;
+                            const int at = D / 2 + st * 64 + g * kW * 4;
+                            uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
+                            load_words(wa, ra + at);
+                            load_words(wb, rb + at);
+                            load_words(xa, ra + next + at);
+                            load_words(xb, rb + next + at);
 #pragma unroll
-                            for (int b = 0; b < S::kBlocks; ++b) {
-                                float w[2][4];
+                            for (int i = 0; i < S::kPer; ++i) {
+                                const int group = st * S::kPer + i;
+                                const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                                const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                                uint32_t pa[S::kBlocks][4];
 #pragma unroll
-                                for (int half = 0; half < 2; ++half)
+                                for (int b = 0; b < S::kBlocks; ++b) {
+                                    float w[2][4];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        w[half][e] = sc[b][half][e] * (half ? (e & 1 ? s3 : s2) : (e & 1 ? s1 : s0));
-                                        if (kMasked && !seen_by(token(half, e), row(b, e / 2)))
-                                            w[half][e] = 0.f;
-                                    }
-                                pa[b][0] = pack_half2(w[0][0], w[0][1]);
-                                pa[b][1] = pack_half2(w[0][2], w[0][3]);
-                                pa[b][2] = pack_half2(w[1][0], w[1][1]);
-                                pa[b][3] = pack_half2(w[1][2], w[1][3]);
-                            }
+                                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t b0 = value_codes(z, j), b1 = value_codes(y, j);
+                                        for (int e = 0; e < 4; ++e) {
+                                            w[half][e] = sc[m][b][half][e] * vs[half * 2 + (e & 1)][group];
+                                            if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
+                                                w[half][e] = 0.f;
+                                        }
+                                    pa[b][0] = pack_half2(w[0][0], w[0][1]);
+                                    pa[b][1] = pack_half2(w[0][2], w[0][3]);
+                                    pa[b][2] = pack_half2(w[1][0], w[1][1]);
+                                    pa[b][3] = pack_half2(w[1][2], w[1][3]);
+                                }
 #pragma unroll
-                                for (int b = 0; b < S::kBlocks; ++b)
-                                    mma16816(o[group][j][b], pa[b][0], pa[b][1], pa[b][2], pa[b][3], b0, b1);
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t b0 = value_codes(z, j), b1 = value_codes(y, j);
+#pragma unroll
+                                    for (int b = 0; b < S::kBlocks; ++b)
+                                        mma16816(o[group][j][b], pa[b][0], pa[b][1], pa[b][2], pa[b][3], b0, b1);
+                                }
                             }
                         }
                     }
