@@ -784,38 +784,43 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 return (mask >> token & 1) && (listed || base + token < limit[r]);
             };
             if constexpr (!S::kWide) {
-                float sc[S::kMT][4];
+                float sc[S::kMT][4], sa[S::kMT][S::kGroups], sb[S::kMT][S::kGroups];
 #pragma unroll
                 for (int mt = 0; mt < S::kMT; ++mt) {
                     const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kRecord;
-                    const unsigned char *rb = ra + S::kNext * S::kRecord;
-                    float sa[S::kGroups], sb[S::kGroups];
-                    load_scales(sa, ra + D);
-                    load_scales(sb, rb + D);
+                    load_scales(sa[mt], ra + D);
+                    load_scales(sb[mt], ra + S::kNext * S::kRecord + D);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sc[mt][e] = 0.f;
+                }
 #pragma unroll
-                    for (int st = 0; st < S::kStretches; ++st) {
-                        uint32_t wa[S::kPer], wb[S::kPer];
-                        load_words(wa, ra + st * 64 + t * S::kPer * 4);
-                        load_words(wb, rb + st * 64 + t * S::kPer * 4);
+                for (int st = 0; st < S::kStretches; ++st) {
+                    uint32_t wa[S::kMT][S::kPer], wb[S::kMT][S::kPer];
 #pragma unroll
-                        for (int i = 0; i < S::kPer; ++i) {
-                            const int group = st * S::kPer + i;
-                            const uint2 *qf = reinterpret_cast<const uint2 *>(smem + S::kOffQ) +
-                                              group * 2 * 32 + lane;
-                            const uint2 q0 = qf[0], q1 = qf[32];
-                            const uint32_t ha = wa[i] >> 8, hb = wb[i] >> 8;
+                    for (int mt = 0; mt < S::kMT; ++mt) {
+                        const unsigned char *ra =
+                            tile + (mt * 16 + tok_row) * S::kRecord + st * 64 + t * S::kPer * 4;
+                        load_words(wa[mt], ra);
+                        load_words(wb[mt], ra + S::kNext * S::kRecord);
+                    }
+#pragma unroll
+                    for (int i = 0; i < S::kPer; ++i) {
+                        const int group = st * S::kPer + i;
+                        const uint2 *qf = reinterpret_cast<const uint2 *>(smem + S::kOffQ) + group * 2 * 32 + lane;
+                        const uint2 q0 = qf[0], q1 = qf[32];
+#pragma unroll
+                        for (int mt = 0; mt < S::kMT; ++mt) {
+                            const uint32_t la = wa[mt][i], lb = wb[mt][i], ha = la >> 8, hb = lb >> 8;
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(acc, low_codes(wa[i]), low_codes(wb[i]), high_codes(wa[i]),
-                                     high_codes(wb[i]), q0.x, q0.y);
-                            mma16816(acc, low_codes(ha), low_codes(hb), high_codes(ha), high_codes(hb),
-                                     q1.x, q1.y);
-                            sc[mt][0] += sa[group] * acc[0];
-                            sc[mt][1] += sa[group] * acc[1];
-                            sc[mt][2] += sb[group] * acc[2];
-                            sc[mt][3] += sb[group] * acc[3];
+                            mma16816(acc, low_codes(la), low_codes(lb), high_codes(la), high_codes(lb), q0.x,
+                                     q0.y);
+                            mma16816(acc, low_codes(ha), low_codes(hb), high_codes(ha), high_codes(hb), q1.x,
+                                     q1.y);
+                            sc[mt][0] += sa[mt][group] * acc[0];
+                            sc[mt][1] += sa[mt][group] * acc[1];
+                            sc[mt][2] += sb[mt][group] * acc[2];
+                            sc[mt][3] += sb[mt][group] * acc[3];
                         }
                     }
                 }
