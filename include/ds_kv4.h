@@ -111,6 +111,7 @@ int ds_kv4_read(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t *
  *   lse       device float[batch][queries][heads], log of the sum of
  *             exp(scale * q k), or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_attention_workspace bytes
+ *             (NULL when that is 0)
  * A query that sees no token gives out = 0 and lse = -inf.
  */
 int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const int32_t *seqs,
@@ -118,8 +119,8 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
                      const int64_t *q_stride, const int32_t *indices, int k, float scale, void *out,
                      float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of ds_kv4_attention on the current device; k = 0 when every
- * token is attended. */
+/* Workspace bytes of ds_kv4_attention on the current device for these sizes, 0
+ * where no sequence is shared by CTAs; k = 0 when every token is attended. */
 int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queries, int heads,
                                int k, size_t *bytes);
 

@@ -323,18 +323,15 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
 _attention_bytes = {}
 
 
-def _attention_workspace(cache, batch, queries, heads, k, dim, kv_heads, index):
-    """Workspace bytes, which depend on these sizes and the device alone."""
-    key = (dim, kv_heads, queries, heads, k > 0, index)
-    need = _attention_bytes.get(key)
-    if need is None:
-        n = ctypes.c_size_t(0)
-        _check(_t.workspace(cache, batch, queries, heads, k, ctypes.byref(n)),
-               "ds_kv4_attention_workspace")
-        if len(_attention_bytes) > 1000:
-            _attention_bytes.clear()
-        need = _attention_bytes[key] = n.value
-    return need
+def _attention_workspace(cache, batch, queries, heads, k, key):
+    """Workspace bytes, which depend on the sizes in `key` and the device alone."""
+    n = ctypes.c_size_t(0)
+    _check(_t.workspace(cache, batch, queries, heads, k, ctypes.byref(n)),
+           "ds_kv4_attention_workspace")
+    if len(_attention_bytes) > 10000:
+        _attention_bytes.clear()
+    _attention_bytes[key] = n.value
+    return n.value
 
 
 def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, out=None, lse=None,
@@ -393,18 +390,23 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
         lse.fill_(-math.inf)
         return out, lse
     index = device.index
-    size = _attention_workspace(cache, batch, queries, heads, k, dim, pool.shape[1], index)
+    key = (index, shape, k, pool.shape, table.shape)
+    size = _attention_bytes.get(key)
+    if size is None:
+        size = _attention_workspace(cache, batch, queries, heads, k, key)
     raw = t.raw_stream(index)
     with _order:
         if workspace is None:
-            workspace, size = _workspace(t, device, raw, size)
+            if size:
+                workspace, size = _workspace(t, device, raw, size)
         else:
             given = _space("workspace", workspace, device)
             if given < size:
                 raise ValueError("workspace has %d bytes, %d needed" % (given, size))
         status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
                              _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
-                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, raw)
+                             out.data_ptr(), lse.data_ptr(),
+                             None if workspace is None else workspace.data_ptr(), size, raw)
     if status:
         _check(status, "ds_kv4_attention")
     return out, lse

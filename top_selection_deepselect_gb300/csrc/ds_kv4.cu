@@ -157,7 +157,12 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
         return fail(DS_EINVAL, "bytes must be non-NULL");
     if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
         return rc;
-    *bytes = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
+    ds::kv4::Attend a = {};
+    a.batch = batch;
+    a.queries = queries;
+    a.heads = heads;
+    a.k = k;
+    *bytes = batch == 0 || queries == 0 ? 0 : ds::kv4::attention_workspace(c, cache->head_dim, a, sms);
     return DS_OK;
 }
 
@@ -187,10 +192,6 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
         return fail(DS_EINVAL, "q must be aligned to its elements and out to 16 bytes");
     if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
         return rc;
-    const size_t need = ds::kv4::attention_workspace(c, cache->head_dim, queries, heads, k, sms);
-    if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
-        return fail(DS_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)",
-                    need, workspace_bytes);
     ds::kv4::Attend a;
     a.lengths = lengths;
     a.seqs = seqs;
@@ -208,6 +209,10 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
     a.heads = heads;
     a.k = k;
     a.bf16 = dtype == DS_BF16;
+    const size_t need = ds::kv4::attention_workspace(c, cache->head_dim, a, sms);
+    if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
+        return fail(DS_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)",
+                    need, workspace_bytes);
     const cudaError_t e = ds::kv4::launch_attention(c, cache->head_dim, a, dev, sms,
                                                     (cudaStream_t)stream);
     return e == cudaSuccess ? DS_OK : fail_cuda(e, "ds_kv4_attention");

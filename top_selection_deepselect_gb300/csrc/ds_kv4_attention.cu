@@ -9,11 +9,10 @@ cudaError_t launch_attention_64(const Cache &c, const Attend &a, int dev, int sm
 cudaError_t launch_attention_128(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream);
 cudaError_t launch_attention_256(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream);
 
-size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads, int k, int sms)
+size_t attention_workspace(const Cache &c, int head_dim, const Attend &a, int sms)
 {
-    const int rows = heads / c.kv_heads * (k > 0 ? 1 : queries);
-    return head_dim == 64    ? workspace_dim<64>(rows, sms)
-           : head_dim == 128 ? workspace_dim<128>(rows, sms) : workspace_dim<256>(rows, sms);
+    return head_dim == 64    ? workspace_dim<64>(c, a, sms)
+           : head_dim == 128 ? workspace_dim<128>(c, a, sms) : workspace_dim<256>(c, a, sms);
 }
 
 cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int dev, int sms,

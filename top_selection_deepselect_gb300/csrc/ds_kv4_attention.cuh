@@ -115,6 +115,7 @@ struct AttendArgs {
     int rows;             // query rows of a unit before it is cut into blocks
     int blocks;           // blocks of kRows rows, a unit each
     int units;            // units of a batch entry
+    int whole;            // units are not cut: each is its first place's CTA's
     Divider by_group, by_blocks, by_heads;
 };
 
@@ -299,12 +300,13 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
 // as the others.
 constexpr int kUnitCost = 12;
 
-// Places of the line for each of `ctas` CTAs: two tiles a warp at least, so
-// that there are not more parts to join than the work is worth.
-__device__ __forceinline__ long long places_per_cta(long long all, int ctas, int warps)
+// Places of the line for each CTA: two tiles a warp at least where units are
+// cut, so that there are not more parts to join than the work is worth.
+__device__ __forceinline__ long long places_per_cta(const AttendArgs &p, long long all)
 {
-    const long long even = (all + ctas - 1) / ctas;
-    return even > 2 * warps ? even : 2 * warps;
+    const long long even = (all + gridDim.x - 1) / gridDim.x;
+    const int least = p.whole ? 1 : 2 * (blockDim.x / 32);
+    return even > least ? even : least;
 }
 
 // The line's length, places for each CTA, and the batch entry that this CTA's
@@ -318,11 +320,10 @@ template <int kTile>
 __device__ __forceinline__ Line line_of(const AttendArgs &p, bool listed, long long *scratch)
 {
     Line n;
-    const int warps = blockDim.x / 32;
     if (listed) {
         const long long each = (p.sel_tiles + kUnitCost) * p.units;
         n.all = each * p.a.batch;
-        n.per = places_per_cta(n.all, gridDim.x, warps);
+        n.per = places_per_cta(p, n.all);
         n.entry = (int)(n.per * blockIdx.x / each);
         n.first = n.entry * each;
         return n;
@@ -335,7 +336,7 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, bool listed, long l
         mine = b < p.a.batch ? (tiles_of<kTile>(p, listed, b) + kUnitCost) * p.units : 0;
         n.all += scan_cta(mine, &before, scratch);
     }
-    n.per = places_per_cta(n.all, gridDim.x, warps);
+    n.per = places_per_cta(p, n.all);
     const long long x = n.per * blockIdx.x;
     long long at = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += blockDim.x) {
@@ -521,7 +522,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
     volatile Part &part = *reinterpret_cast<Part *>(smem + S::kOffPart);
     Split *split = reinterpret_cast<Split *>(p.a.partial) + blockIdx.x;
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && !p.whole)
         split->parts = 0;
 
     // place to go on at, the unit there (number u_in of its entry) and where it begins
@@ -538,6 +539,13 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         const long long each = tiles_of<S::kTile>(p, listed, entry) + kUnitCost;
         u_in = (int)((x - line.first) / each);
         start = line.first + u_in * each;
+        if (p.whole && x > start) {
+            x = start = start + each;
+            if (++u_in == p.units)
+                u_in = 0, ++entry;
+            if (x >= end)
+                return;
+        }
     }
 
     const int tok_row = g & 1 ? S::odd(g / 2) : S::even(g / 2);   // token at place g
@@ -549,7 +557,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         const long long tiles = tiles_of<S::kTile>(p, listed, entry);
         const long long zero = start + kUnitCost;     // place of the unit's tile 0
         const long long tile0 = x > zero ? x - zero : 0;
-        const long long stop = zero + tiles < end ? zero + tiles : end;
+        const long long stop = p.whole || zero + tiles < end ? zero + tiles : end;
         const long long count = stop - zero - tile0;
         if (count <= 0)
             break;      // only the unit's first places: its tiles are the next CTA's
@@ -1212,30 +1220,40 @@ int unit_rows(int rows)
     return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
 }
 
+// How a call is laid out: sizes of its units, its CTAs, and whether units are
+// cut between CTAs.  They are not, and the join is saved, where a unit is at
+// most two tiles a warp, and where tokens are listed, so that all units are of
+// one known size, and whole ones keep at least half of one wave of CTAs or four
+// fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 20.5
+// instead of 26.6 us; 64 units of 2048 tokens for 304 CTAs: 22.5 cut, 30.7 whole).
 template <int D, int Rows>
-int attend_grid(int sms)
+int lay_out(AttendArgs &p, int sms)
 {
-    return sms * Shape<D, Rows>::kCtas;
+    using S = Shape<D, Rows>;
+    p.blocks = (p.rows + S::kRows - 1) / S::kRows;
+    p.units = p.c.kv_heads * p.blocks * (p.a.k > 0 ? p.a.queries : 1);
+    p.sel_tiles = ((long long)p.a.k + S::kTile - 1) / S::kTile;
+    const double room = (double)p.c.max_pages * p.c.page_size;
+    const double tiles = p.a.k > 0 ? (double)p.sel_tiles : room / S::kTile + 1;   // of a unit, at most
+    const double units = (double)p.units * p.a.batch, ctas = (double)sms * S::kCtas;
+    const double waves = (double)(long long)((units + ctas - 1) / ctas);
+    p.whole = tiles <= 2 * S::kWarps ||
+              (p.a.k > 0 && units >= (units <= ctas ? 0.5 * ctas : 0.8 * ctas * waves));
+    // no more CTAs than the largest possible line has work for
+    const double most = p.whole ? units : (tiles + kUnitCost) * units / (2 * S::kWarps) + 1;
+    return (int)(most < ctas ? most : ctas);
 }
 
 template <int D, int Rows>
 cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
 {
     using S = Shape<D, Rows>;
-    p.blocks = (p.rows + S::kRows - 1) / S::kRows;
-    p.units = p.c.kv_heads * p.blocks * (p.a.indices ? p.a.queries : 1);
+    const int ctas = lay_out<D, Rows>(p, sms);
     p.by_group.set(p.group);
     p.by_blocks.set(p.blocks);
     p.by_heads.set(p.c.kv_heads);
-    p.sel_tiles = ((long long)p.a.k + S::kTile - 1) / S::kTile;
-    // no more CTAs than the largest possible line has work for
-    const double room = (double)p.c.max_pages * p.c.page_size;
-    const double most = ((p.a.indices ? (double)p.sel_tiles : room / S::kTile + 1) + kUnitCost) * p.units *
-                        p.a.batch / (2 * S::kWarps);
-    int ctas = attend_grid<D, Rows>(sms);
-    ctas = most < ctas ? (int)most + 1 : ctas;
     p.parts = ctas * (long long)(sizeof(Split) / sizeof(float));
-    const int which = p.a.indices || p.run < 16 ? 0 : p.run == S::kTile ? 1 : 2;
+    const int which = p.a.k > 0 || p.run < 16 ? 0 : p.run == S::kTile ? 1 : 2;
     auto fn = which == 0   ? attend_kernel<D, Rows, 0>
               : which == 1 ? attend_kernel<D, Rows, S::kTile> : attend_kernel<D, Rows, 16>;
     // the kernels' shared memory is raised once a device
@@ -1248,41 +1266,51 @@ cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
         raised[which].fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
     e = launch_overlapped(fn, ctas, S::kThreads, S::kSmem, stream, p);
-    if (e != cudaSuccess || ctas == 1)    // one CTA leaves nothing to join
+    if (e != cudaSuccess || p.whole)
         return e;
     return launch_overlapped(join_kernel<D, Rows>, ctas * (Rows / 8), kJoinThreads, 0, stream, p);
+}
+
+// The arguments that the layout goes by.
+template <int D>
+AttendArgs attend_args(const Cache &c, const Attend &a)
+{
+    AttendArgs p;
+    p.c = c;
+    p.a = a;
+    p.group = a.heads / c.kv_heads;
+    p.rows = a.k > 0 ? p.group : p.group * a.queries;
+    p.run = 1;
+    while (a.k == 0 && p.run < Shape<D, 8>::kTile && c.page_size % (2 * p.run) == 0)
+        p.run *= 2;
+    return p;
 }
 
 template <int D>
 cudaError_t launch_dim(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream)
 {
     constexpr int kMost = D == 256 ? 16 : 32;
-    AttendArgs p;
-    p.c = c;
-    p.a = a;
-    p.group = a.heads / c.kv_heads;
-    p.run = 1;
-    while (!a.indices && p.run < Shape<D, 8>::kTile && c.page_size % (2 * p.run) == 0)
-        p.run *= 2;
-    p.rows = a.indices ? p.group : p.group * a.queries;
+    AttendArgs p = attend_args<D>(c, a);
     const int rows = unit_rows<D>(p.rows);
     return rows == 8    ? launch_shape<D, 8>(p, dev, sms, stream)
            : rows == 16 ? launch_shape<D, 16>(p, dev, sms, stream) : launch_shape<D, kMost>(p, dev, sms, stream);
 }
 
 template <int D, int Rows>
-size_t workspace_shape(int sms)
+size_t workspace_shape(AttendArgs &p, int sms)
 {
-    return attend_grid<D, Rows>(sms) * (sizeof(Split) + 2 * Shape<D, Rows>::kPartial * sizeof(float));
+    const int ctas = lay_out<D, Rows>(p, sms);
+    return p.whole ? 0 : ctas * (sizeof(Split) + 2 * Shape<D, Rows>::kPartial * sizeof(float));
 }
 
 template <int D>
-size_t workspace_dim(int rows, int sms)
+size_t workspace_dim(const Cache &c, const Attend &a, int sms)
 {
     constexpr int kMost = D == 256 ? 16 : 32;
-    const int r = unit_rows<D>(rows);
-    return r == 8    ? workspace_shape<D, 8>(sms)
-           : r == 16 ? workspace_shape<D, 16>(sms) : workspace_shape<D, kMost>(sms);
+    AttendArgs p = attend_args<D>(c, a);
+    const int rows = unit_rows<D>(p.rows);
+    return rows == 8    ? workspace_shape<D, 8>(p, sms)
+           : rows == 16 ? workspace_shape<D, 16>(p, sms) : workspace_shape<D, kMost>(p, sms);
 }
 
 }  // namespace kv4

@@ -33,7 +33,8 @@ struct Attend {
     int bf16;        // 1: q and out are bf16, 0: fp16
 };
 
-size_t attention_workspace(const Cache &c, int head_dim, int queries, int heads, int k, int sms);
+// Workspace that a call of these sizes (batch, queries, heads, k) needs.
+size_t attention_workspace(const Cache &c, int head_dim, const Attend &a, int sms);
 cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int dev, int sms,
                              cudaStream_t stream);
 
