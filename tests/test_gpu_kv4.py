@@ -197,6 +197,26 @@ def test_selected_attention(ds, dim, dtype, hk, group, k, page, queries):
     check_attention(ds, q, dtype, pool, table, lengths, indices=idx)
 
 
+@pytest.mark.parametrize("dim,hk,group,k,batch", [
+    (128, 2, 4, 1500, 3), (64, 1, 16, 2048, 2), (256, 1, 3, 1025, 2), (128, 1, 32, 700, 1), (64, 3, 2, 4096, 1),
+    (128, 1, 8, 20000, 2), (256, 1, 16, 555, 2), (64, 8, 4, 600, 40), (128, 1, 40, 513, 2)])
+def test_long_lists(ds, dim, hk, group, k, batch):
+    """Lists that are one CTA's, that a cluster shares, and that a launch joins; parts without any token."""
+    rng = np.random.default_rng(dim + k)
+    page = 16
+    lengths = np.array([3000] * batch, dtype=np.int32)
+    lengths[0] = 40
+    table, n_pages = make_table(rng, lengths, page, wide=-(-3000 // page))
+    pool = random_pool(rng, n_pages, hk, page, dim)
+    idx = rng.integers(0, 3000, (batch, 1, k)).astype(np.int32)
+    idx[-1, 0, k // 5:k // 2] = -1
+    idx[-1, 0, -(k // 4):] = -1
+    q = rng.standard_normal((batch, 1, hk * group, dim)).astype(np.float32)
+    out, lse = check_attention(ds, q, "fp16", pool, table, lengths, indices=idx)
+    again = ds.kv4_attention(dev(q).half(), dev(pool), dev(table), dev(lengths), indices=dev(idx))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("lengths,hk,group,dim", [
     ([20011], 1, 4, 128), ([9000, 3, 0, 5000, 1], 2, 8, 64), ([4099] * 3, 1, 20, 256)])
 def test_long_sequences(ds, lengths, hk, group, dim):

@@ -42,6 +42,7 @@
 #pragma once
 
 #include <atomic>
+#include <cooperative_groups.h>
 #include <type_traits>
 
 #include "ds_device.cuh"
@@ -116,6 +117,7 @@ struct AttendArgs {
     int blocks;           // blocks of kRows rows, a unit each
     int units;            // units of a batch entry
     int whole;            // units are not cut: each is its first place's CTA's
+    int cluster;          // > 1: a unit is a cluster's, cut evenly and joined in it
     Divider by_group, by_blocks, by_heads;
 };
 
@@ -522,13 +524,21 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
     volatile Part &part = *reinterpret_cast<Part *>(smem + S::kOffPart);
     Split *split = reinterpret_cast<Split *>(p.a.partial) + blockIdx.x;
-    if (threadIdx.x == 0 && !p.whole)
+    const bool clustered = kRun == 0 && p.cluster > 1;
+    if (threadIdx.x == 0 && !p.whole && !clustered)
         split->parts = 0;
 
     // place to go on at, the unit there (number u_in of its entry) and where it begins
     long long x, per, end, start;
     int entry, u_in;
-    {
+    if (clustered) {
+        const int n = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+        entry = n / p.units;
+        u_in = n - entry * p.units;
+        start = per = 0;
+        x = kUnitCost + p.sel_tiles * rank / p.cluster;
+        end = kUnitCost + p.sel_tiles * (rank + 1) / p.cluster;
+    } else {
         const Line line = line_of<S::kTile>(p, listed, scratch);
         per = line.per;
         x = per * blockIdx.x;
@@ -705,7 +715,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             part.u.row0 = unit.row0, part.u.rows = unit.rows;
             part.whole = count == tiles;
             part.begins = tile0 == 0;
-            if (tile0 == 0 && count < tiles) {
+            if (tile0 == 0 && count < tiles && !clustered) {
                 split->b = entry;
                 split->unit = u_in;
                 split->parts = (int)((zero + tiles - 1) / per - blockIdx.x) + 1;
@@ -1093,40 +1103,102 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         const bool whole = part.whole;
         // a CTA's second place is for the unit that begins in it
         float *to_join = p.a.partial + p.parts + (blockIdx.x * 2LL + part.begins) * S::kPartial;
-        for (int e = threadIdx.x; e < S::kRows * D / 4; e += S::kThreads) {
-            const int r = e / (D / 4), d = e % (D / 4) * 4;
-            if (r >= u.rows)
-                break;
-            float m = -INFINITY, l = 0.f;
-            for (int w = 0; w < active; ++w)
-                m = fmaxf(m, wmax(w, r));
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < active; ++w) {
-                // a warp that saw nothing has maximum -inf and sum 0; one whose
-                // scores are NaN has maximum -inf, and its NaN goes on
-                const float s = wsum(w, r);
-                const float weight = s == 0.f ? 0.f : s != s ? 1.f : exp2_fast(wmax(w, r) - m);
-                const float4 f = *reinterpret_cast<const float4 *>(
-                    smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
-                l += s * weight;
-                v.x += f.x * weight, v.y += f.y * weight, v.z += f.z * weight, v.w += f.w * weight;
+        // Four channels of a row: maximum, sum and output of all parts i < n, which
+        // weigh 2^(maximum - largest maximum).  A part that saw nothing has maximum
+        // -inf and sum 0; one whose scores are NaN has maximum -inf, and its NaN
+        // goes on.
+        struct Four {
+            float m, l;
+            float4 v;
+        };
+        auto add_up = [&](int n, auto maximum, auto sum_of, auto output) {
+            Four f = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            for (int i = 0; i < n; ++i)
+                f.m = fmaxf(f.m, maximum(i));
+            for (int i = 0; i < n; ++i) {
+                const float s = sum_of(i);
+                const float weight = s == 0.f ? 0.f : s != s ? 1.f : exp2_fast(maximum(i) - f.m);
+                const float4 o4 = output(i);
+                f.l += s * weight;
+                f.v.x += o4.x * weight, f.v.y += o4.y * weight;
+                f.v.z += o4.z * weight, f.v.w += o4.w * weight;
             }
+            return f;
+        };
+        auto of_warps = [&](int r, int d) {
+            return add_up(active, [&](int w) { return wmax(w, r); }, [&](int w) { return wsum(w, r); },
+                          [&](int w) {
+                              return *reinterpret_cast<const float4 *>(
+                                  smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
+                          });
+        };
+        auto finish = [&](int r, int d, const Four &f) {
             int j, h;
             u.row(p, r, &j, &h);
             const long long at = ((long long)u.b * p.a.queries + j) * p.a.heads + h;
+            const float inv = f.l == 0.f ? 0.f : 1.f / f.l;
+            if (p.a.bf16)
+                store_four((__nv_bfloat16 *)p.a.out + at * D + d, f.v, inv);
+            else
+                store_four((__half *)p.a.out + at * D + d, f.v, inv);
+            if (d == 0 && p.a.lse)
+                p.a.lse[at] = f.l == 0.f ? -INFINITY : (f.m + log2f(f.l)) * 0.6931471805599453f;
+        };
+        constexpr int kFours = S::kRows * D / 4;
+        if constexpr (kRun == 0) {
+            if (clustered) {
+                // this CTA's part into its shared memory, then every CTA of the
+                // cluster joins its share of the rows from all of them
+                constexpr int kMine = (kFours + S::kThreads - 1) / S::kThreads;
+                Four f[kMine];
+#pragma unroll
+                for (int n = 0; n < kMine; ++n) {
+                    const int e = threadIdx.x + n * S::kThreads, r = e / (D / 4);
+                    if (r < u.rows)
+                        f[n] = of_warps(r, e % (D / 4) * 4);
+                }
+                __syncthreads();
+                float *mine = reinterpret_cast<float *>(smem);     // maxima, sums, outputs
+#pragma unroll
+                for (int n = 0; n < kMine; ++n) {
+                    const int e = threadIdx.x + n * S::kThreads, r = e / (D / 4), d = e % (D / 4) * 4;
+                    if (r < u.rows) {
+                        *reinterpret_cast<float4 *>(mine + 2 * S::kRows + r * D + d) = f[n].v;
+                        if (d == 0)
+                            mine[r] = f[n].m, mine[S::kRows + r] = f[n].l;
+                    }
+                }
+                cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+                cluster.sync();
+                for (int e = threadIdx.x + cluster.block_rank() * S::kThreads; e < kFours;
+                     e += p.cluster * S::kThreads) {
+                    const int r = e / (D / 4), d = e % (D / 4) * 4;
+                    if (r >= u.rows)
+                        break;
+                    auto of = [&](int i) { return cluster.map_shared_rank(mine, i); };
+                    finish(r, d, add_up(p.cluster, [&](int i) { return of(i)[r]; },
+                                        [&](int i) { return of(i)[S::kRows + r]; },
+                                        [&](int i) {
+                                            return *reinterpret_cast<const float4 *>(
+                                                of(i) + 2 * S::kRows + r * D + d);
+                                        }));
+                }
+                cluster.sync();     // the others have read this CTA's part
+                return;
+            }
+        }
+        for (int e = threadIdx.x; e < kFours; e += S::kThreads) {
+            const int r = e / (D / 4), d = e % (D / 4) * 4;
+            if (r >= u.rows)
+                break;
+            const Four f = of_warps(r, d);
             if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                if (p.a.bf16)
-                    store_four((__nv_bfloat16 *)p.a.out + at * D + d, v, inv);
-                else
-                    store_four((__half *)p.a.out + at * D + d, v, inv);
-                if (d == 0 && p.a.lse)
-                    p.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                finish(r, d, f);
             } else {
-                *reinterpret_cast<float4 *>(to_join + 2 * S::kRows + r * D + d) = v;
+                *reinterpret_cast<float4 *>(to_join + 2 * S::kRows + r * D + d) = f.v;
                 if (d == 0) {
-                    to_join[r] = m;
-                    to_join[S::kRows + r] = l;
+                    to_join[r] = f.m;
+                    to_join[S::kRows + r] = f.l;
                 }
             }
         }
@@ -1239,6 +1311,17 @@ int lay_out(AttendArgs &p, int sms)
     const double waves = (double)(long long)((units + ctas - 1) / ctas);
     p.whole = tiles <= 2 * S::kWarps ||
               (p.a.k > 0 && units >= (units <= ctas ? 0.5 * ctas : 0.8 * ctas * waves));
+    // Few listed units of middling size: a cluster of CTAs each, which joins its
+    // parts in shared memory, while that gives no warp more than four tiles
+    // (64 units of 2048 tokens, four CTAs each: 20.5 us, with a join launch 22.5).
+    p.cluster = 1;
+    if (p.a.k > 0 && !p.whole) {
+        while (p.cluster < 8 && tiles > 2 * S::kWarps * p.cluster && 2 * p.cluster * units <= ctas)
+            p.cluster *= 2;
+        if (tiles <= 4 * S::kWarps * p.cluster)
+            return (int)(units * p.cluster);
+        p.cluster = 1;
+    }
     // no more CTAs than the largest possible line has work for
     const double most = p.whole ? units : (tiles + kUnitCost) * units / (2 * S::kWarps) + 1;
     return (int)(most < ctas ? most : ctas);
@@ -1265,8 +1348,8 @@ cudaError_t launch_shape(AttendArgs &p, int dev, int sms, cudaStream_t stream)
             return e;
         raised[which].fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
-    e = launch_overlapped(fn, ctas, S::kThreads, S::kSmem, stream, p);
-    if (e != cudaSuccess || p.whole)
+    e = launch_clusters(fn, p.cluster, ctas, S::kThreads, S::kSmem, stream, p);
+    if (e != cudaSuccess || p.whole || p.cluster > 1)
         return e;
     return launch_overlapped(join_kernel<D, Rows>, ctas * (Rows / 8), kJoinThreads, 0, stream, p);
 }
@@ -1300,7 +1383,7 @@ template <int D, int Rows>
 size_t workspace_shape(AttendArgs &p, int sms)
 {
     const int ctas = lay_out<D, Rows>(p, sms);
-    return p.whole ? 0 : ctas * (sizeof(Split) + 2 * Shape<D, Rows>::kPartial * sizeof(float));
+    return p.whole || p.cluster > 1 ? 0 : ctas * (sizeof(Split) + 2 * Shape<D, Rows>::kPartial * sizeof(float));
 }
 
 template <int D>
