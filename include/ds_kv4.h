@@ -71,9 +71,9 @@ int ds_kv4_record_bytes(int head_dim);
 /*
  * ds_kv4_append -- quantise `tokens` keys and values into the cache.
  *   seq, pos  device int32[tokens]: the sequence and the position in it of
- *             each token; distinct pairs (of two equal ones either may stay);
- *             a token with seq outside [0, max_seqs) or pos outside its
- *             sequence's pages is skipped
+ *             each token; distinct pairs (one that is given twice may end as a
+ *             mixture of both); a token with seq outside [0, max_seqs) or pos
+ *             outside its sequence's pages is skipped
  *   k, v      device [tokens][kv_heads][head_dim] of `dtype` (DS_FP32,
  *             DS_BF16 or DS_FP16), unit stride in the last dimension,
  *             k_stride / v_stride = {token stride, head stride} in elements
@@ -112,7 +112,9 @@ int ds_kv4_read(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t *
  *             exp(scale * q k), or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_attention_workspace bytes
  *             (NULL when that is 0)
- * A query that sees no token gives out = 0 and lse = -inf.
+ * A query that sees no token gives out = 0 and lse = -inf.  (A copy into shared
+ * memory that does not end within a second, which no working GPU does, is given
+ * up, and what depends on it is NaN.)
  */
 int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const int32_t *seqs,
                      int batch, int queries, int heads, int dtype, const void *q,

@@ -138,21 +138,35 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, unsigned bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// Whether the phase ended; gives up after kPatience tries (far beyond any
-// copy's time), so that a copy that never ends cannot hang the GPU.
-constexpr int kPatience = 1 << 20;
+// Whether the phase ended within kPatience nanoseconds (far beyond any copy's
+// time): a copy that never ends must not hang the GPU.
+constexpr long long kPatience = 1000000000;
+__device__ __forceinline__ bool barrier_done(uint32_t bar, unsigned phase)
+{
+    unsigned done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ long long nanoseconds()
+{
+    long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, unsigned phase)
 {
-    for (int i = 0; i < kPatience; ++i) {
-        unsigned done;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(bar), "r"(phase) : "memory");
-        if (done)
-            return true;
-    }
-    return false;
+    if (barrier_done(bar, phase))
+        return true;
+    const long long from = nanoseconds();
+    while (!barrier_done(bar, phase))
+        if (nanoseconds() - from > kPatience)
+            return false;
+    return true;
 }
 
 // Asynchronous copy of `bytes` (a multiple of 16) from global to shared memory.
@@ -507,7 +521,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     };
 
     // state of the warp's ring: the stage filled and the one used next, the
-    // phase of the latter; lost: a copy did not arrive, the results become NaN
+    // phase of the latter; lost: a copy did not arrive, the ring is not used any
+    // more and all further results are NaN
     const uint32_t barriers = shared_address(smem + S::kOffBarrier) + warp * S::kStages * 8;
     int fill = 0, use = 0;
     unsigned phase = 0;
@@ -579,7 +594,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         now.head_pool = p.c.pool + (long long)unit.head * p.c.page_size * S::kRecord;
         now.seen = listed ? len - p.a.queries + 1 + unit.query : len;
         // the warp's tiles: warp, warp + kWarps, ... of `count`
-        const int mine = count > warp ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
+        const int mine =
+            count > warp && !lost ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
         // tokens and list entries are below 2^31; the last tile may end above
         const unsigned e0 = (unsigned)((tile0 + warp) * S::kTile);
 
@@ -1047,8 +1063,16 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             const unsigned char *data = ring + use * S::kStageBytes;
             if (++use == S::kStages)
                 use = 0, phase ^= 1;
-            if (!came)
+            if (!came) {
+                // the copies after it get as long to end
                 lost = true;
+                for (int left = min(S::kStages - 1, mine - 1 - i); left > 0; --left) {
+                    barrier_wait(barriers + use * 8, phase);
+                    if (++use == S::kStages)
+                        use = 0, phase ^= 1;
+                }
+                break;
+            }
             const int base = listed ? 0 : (int)(e0 + i * (S::kWarps * S::kTile));
             if (mask == S::kFullMask &&
                 (listed || base + S::kTile <= least))
