@@ -316,11 +316,17 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
 // as the others.
 constexpr int kUnitCost = 12;
 
+// Quotient of numbers that are not negative, in 32 bits where that is enough.
+__device__ __forceinline__ long long divided(long long a, long long b)
+{
+    return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // Places of the line for each CTA: two tiles a warp at least where units are
 // cut, so that there are not more parts to join than the work is worth.
 __device__ __forceinline__ long long places_per_cta(const AttendArgs &p, long long all)
 {
-    const long long even = (all + gridDim.x - 1) / gridDim.x;
+    const long long even = divided(all + gridDim.x - 1, gridDim.x);
     const int least = p.whole ? 1 : 2 * (blockDim.x / 32);
     return even > least ? even : least;
 }
@@ -340,7 +346,7 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, bool listed, long l
         const long long each = (p.sel_tiles + kUnitCost) * p.units;
         n.all = each * p.a.batch;
         n.per = places_per_cta(p, n.all);
-        n.entry = (int)(n.per * blockIdx.x / each);
+        n.entry = (int)divided(n.per * blockIdx.x, each);
         n.first = n.entry * each;
         return n;
     }
@@ -562,7 +568,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             return;
         entry = line.entry;
         const long long each = tiles_of<S::kTile>(p, listed, entry) + kUnitCost;
-        u_in = (int)((x - line.first) / each);
+        u_in = (int)divided(x - line.first, each);
         start = line.first + u_in * each;
         if (p.whole && x > start) {
             x = start = start + each;
@@ -734,7 +740,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             if (tile0 == 0 && count < tiles && !clustered) {
                 split->b = entry;
                 split->unit = u_in;
-                split->parts = (int)((zero + tiles - 1) / per - blockIdx.x) + 1;
+                split->parts = (int)(divided(zero + tiles - 1, per) - blockIdx.x) + 1;
             }
         }
         __syncthreads();   // query operands and `part` are there
