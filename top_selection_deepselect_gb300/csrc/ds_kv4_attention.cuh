@@ -313,8 +313,9 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
 // tiles.  A unit's start and end (its queries, the first copies' latency, the
 // meeting of the warps) cost a CTA as much as some tiles do; without these
 // places the CTA that met 24 empty sequences in a row took four times as long
-// as the others.
-constexpr int kUnitCost = 12;
+// as the others (37 ragged sequences of 5 drafts: 119 us; with 12, 18, 24 and 32
+// places 41, 39, 37 and 37; 16 x 16384 tokens 68, 68, 66 and 68).
+constexpr int kUnitCost = 24;
 
 // Quotient of numbers that are not negative, in 32 bits where that is enough.
 __device__ __forceinline__ long long divided(long long a, long long b)
