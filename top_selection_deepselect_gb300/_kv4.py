@@ -146,7 +146,7 @@ class _Torch:
 
     def find(self):
         import torch
-        self.torch, self.empty = torch, torch.empty
+        self.torch, self.empty, self.empty_like = torch, torch.empty, torch.empty_like
         self.int32, self.uint8, self.float32 = torch.int32, torch.uint8, torch.float32
         self.codes = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -188,36 +188,32 @@ _order = threading.Lock()
 _KEPT_BYTES = 1 << 20     # at least this much, so that few calls grow it
 
 
-def _grow(t, device, need, key):
-    size = max(need, _KEPT_BYTES)
-    # the old one, if any, goes back to its stream's memory in order
-    space = t.empty(size, dtype=t.uint8, device=device)
-    _kept[key] = (space, size)
-    return space, size
-
-
-def _workspace(t, device, raw, need):
+def _workspace(t, index, raw, need):
     """(workspace, its bytes) for a call on the device's current stream, whose handle is raw."""
     if t.capturing():
-        return t.empty(need, dtype=t.uint8, device=device), need
-    key = (device.index, raw)
+        return t.empty(need, dtype=t.uint8, device=t.torch.device("cuda", index)), need
+    key = (index, raw)
     space = _kept.get(key)
-    return space if space is not None and space[1] >= need else _grow(t, device, need, key)
+    if space is None or space[1] < need:
+        size = max(need, _KEPT_BYTES)
+        # an old one goes back to its stream's memory, in order
+        space = _kept[key] = (t.empty(size, dtype=t.uint8, device=t.torch.device("cuda", index)), size)
+    return space
 
 
-def _int32(name, t, device, n=None):
-    """Address of a contiguous int32 tensor on `device`, of n entries in one dimension if given."""
-    if t.dtype is not _t.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
-    if n is not None and t.shape != (n,):
-        raise ValueError("%s must have shape (%d,), got %s" % (name, n, tuple(t.shape)))
-    return t.data_ptr()
+def _int32(name, x, index, n=None):
+    """Address of a contiguous int32 tensor on device `index`, of n entries in one dimension if given."""
+    if x.dtype is not _t.int32 or x.get_device() != index or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor on cuda:%d" % (name, index))
+    if n is not None and x.shape != (n,):
+        raise ValueError("%s must have shape (%d,), got %s" % (name, n, tuple(x.shape)))
+    return x.data_ptr()
 
 
-def _table(table, device):
-    """(address, row stride, rows, columns) of a page table."""
-    if table.dtype is not _t.int32 or table.device != device or table.dim() != 2:
-        raise ValueError("table must be an int32 [max_seqs, max_pages] tensor on %s" % (device,))
+def _table(table, index):
+    """(address, row stride, rows, columns) of a page table on device `index`."""
+    if table.dtype is not _t.int32 or table.get_device() != index or table.dim() != 2:
+        raise ValueError("table must be an int32 [max_seqs, max_pages] tensor on cuda:%d" % index)
     rows, columns = table.shape
     stride, unit = table.stride()
     if unit != 1 and columns != 1:
@@ -225,11 +221,19 @@ def _table(table, device):
     return table.data_ptr(), stride if stride > columns else columns, rows, columns
 
 
-def _space(name, t, device):
+def _space(name, x, index):
     """Bytes of a workspace that was passed in."""
-    if t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be contiguous on %s" % (name, device))
-    return t.numel() * t.element_size()
+    if x.get_device() != index or not x.is_contiguous():
+        raise ValueError("%s must be contiguous on cuda:%d" % (name, index))
+    return x.numel() * x.element_size()
+
+
+def _cuda(name, x):
+    """Index of a tensor's CUDA device."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return index
 
 
 def kv4_record_bytes(head_dim):
@@ -237,9 +241,9 @@ def kv4_record_bytes(head_dim):
     return ds_kv4_record_bytes(head_dim)
 
 
-def _cache(pool, table, head_dim, device):
+def _cache(pool, table, head_dim, index):
     """Descriptor of a pool [n_pages, kv_heads, page_size, record bytes] (uint8) and its table."""
-    if pool.dtype is not _t.uint8 or not pool.is_cuda or pool.dim() != 4:
+    if pool.dtype is not _t.uint8 or pool.dim() != 4:
         raise ValueError("pool must be a 4-D CUDA uint8 tensor [n_pages, kv_heads, page_size, "
                          "record bytes]")
     n_pages, kv_heads, page_size, rec = pool.shape
@@ -250,7 +254,7 @@ def _cache(pool, table, head_dim, device):
     page = kv_heads * page_size * rec
     if (unit != 1 or token != rec or head != page_size * rec) and not pool[:1].is_contiguous():
         raise ValueError("each page of pool must be contiguous")
-    at, row, rows, columns = _table(table, device)
+    at, row, rows, columns = _table(table, index)
     return _pack_cache(pool.data_ptr(), each if each > page else page, at, row, n_pages, page_size,
                        kv_heads, head_dim, rows, columns)
 
@@ -266,11 +270,11 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return kv4_append(pool, table, seq, pos, k, v)
-    shape, dtype, device = k.shape, k.dtype, pool.device
+    shape, dtype, index = k.shape, k.dtype, _cuda("pool", pool)
     if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
     tokens, heads, dim = shape
-    cache = _cache(pool, table, dim, device)
+    cache = _cache(pool, table, dim, index)
     if heads != pool.shape[1]:
         raise ValueError("k has %d heads, the pool %d" % (heads, pool.shape[1]))
     code = t.codes.get(dtype)
@@ -278,12 +282,12 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
         raise TypeError("k and v must be float32, bfloat16 or float16, got %s" % dtype)
     k0, k1, k2 = k.stride()
     v0, v1, v2 = v.stride()
-    if k.device != device or v.device != device or k2 != 1 or v2 != 1:
+    if k.get_device() != index or v.get_device() != index or k2 != 1 or v2 != 1:
         raise ValueError("k and v must be on the pool's device with unit stride in the last "
                          "dimension")
-    status = t.append(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
+    status = t.append(cache, _int32("seq", seq, index, tokens), _int32("pos", pos, index, tokens),
                       tokens, code, k.data_ptr(), _pack_2(k0, k1), v.data_ptr(), _pack_2(v0, v1),
-                      t.raw_stream(device.index))
+                      t.raw_stream(index))
     if status:
         _check(status, "ds_kv4_append")
 
@@ -298,23 +302,22 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return kv4_read(pool, table, seq, pos, head_dim, dtype, k, v)
-    tokens, device = seq.numel(), pool.device
-    cache = _cache(pool, table, head_dim, device)
+    tokens, index = seq.numel(), _cuda("pool", pool)
+    cache = _cache(pool, table, head_dim, index)
     shape = (tokens, pool.shape[1], head_dim)
     code = t.codes.get(dtype)
     if code is None:
         raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
     for x in (k, v):
-        if x is not None and (x.shape != shape or x.dtype != dtype or x.device != device
+        if x is not None and (x.shape != shape or x.dtype != dtype or x.get_device() != index
                               or not x.is_contiguous()):
             raise ValueError("k and v must be contiguous %s tensors of %s" % (shape, dtype))
     if k is None:
-        k = t.empty(shape, dtype=dtype, device=device)
+        k = t.empty(shape, dtype=dtype, device=pool.device)
     if v is None:
-        v = t.empty(shape, dtype=dtype, device=device)
-    status = t.read(cache, _int32("seq", seq, device, tokens), _int32("pos", pos, device, tokens),
-                    tokens, code, k.data_ptr(), v.data_ptr(),
-                    t.raw_stream(device.index))
+        v = t.empty_like(k)
+    status = t.read(cache, _int32("seq", seq, index, tokens), _int32("pos", pos, index, tokens),
+                    tokens, code, k.data_ptr(), v.data_ptr(), t.raw_stream(index))
     if status:
         _check(status, "ds_kv4_read")
     return k, v
@@ -352,22 +355,22 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return kv4_attention(q, pool, table, lengths, indices, scale, seqs, out, lse, workspace)
-    device, shape, dtype = pool.device, q.shape, q.dtype
-    if len(shape) != 4 or q.device != device:
+    index, shape, dtype = _cuda("pool", pool), q.shape, q.dtype
+    if len(shape) != 4 or q.get_device() != index:
         raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device")
     batch, queries, heads, dim = shape
     q0, q1, q2, q3 = q.stride()
     if q3 != 1:
         raise ValueError("q must have unit stride in the last dimension")
-    cache = _cache(pool, table, dim, device)
+    cache = _cache(pool, table, dim, index)
     code = t.codes.get(dtype)
     if code is None:
         raise TypeError("q must be bfloat16 or float16, got %s" % dtype)
     rows = table.shape[0]
-    at = _int32("lengths", lengths, device, rows)
+    at = _int32("lengths", lengths, index, rows)
     seqs_at = list_at = None
     if seqs is not None:
-        seqs_at = _int32("seqs", seqs, device, batch)
+        seqs_at = _int32("seqs", seqs, index, batch)
     elif batch > rows:
         raise ValueError("batch = %d is above the table's %d sequences" % (batch, rows))
     k = 0
@@ -375,21 +378,20 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
         if indices.dim() != 3 or indices.shape[0] != batch or indices.shape[1] != queries:
             raise ValueError("indices must be [batch, queries, k]")
         k = indices.shape[2]
-        list_at = _int32("indices", indices, device)
+        list_at = _int32("indices", indices, index)
     if out is None:
-        out = t.empty(shape, dtype=dtype, device=device)
-    elif out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        out = t.empty(shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if lse is None:
-        lse = t.empty((batch, queries, heads), dtype=t.float32, device=device)
-    elif (lse.shape != shape[:3] or lse.dtype != t.float32 or lse.device != device
+        lse = t.empty((batch, queries, heads), dtype=t.float32, device=q.device)
+    elif (lse.shape != shape[:3] or lse.dtype != t.float32 or lse.get_device() != index
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [batch, queries, heads] tensor")
     if indices is not None and k == 0:
         out.zero_()
         lse.fill_(-math.inf)
         return out, lse
-    index = device.index
     key = (index, shape, k, pool.shape, table.shape)
     size = _attention_bytes.get(key)
     if size is None:
@@ -398,9 +400,9 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     with _order:
         if workspace is None:
             if size:
-                workspace, size = _workspace(t, device, raw, size)
+                workspace, size = _workspace(t, index, raw, size)
         else:
-            given = _space("workspace", workspace, device)
+            given = _space("workspace", workspace, index)
             if given < size:
                 raise ValueError("workspace has %d bytes, %d needed" % (given, size))
         status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
@@ -412,11 +414,11 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     return out, lse
 
 
-def _pool(pool, device):
+def _pool(pool, index):
     """Descriptor of a pool [layers, n_pages, ...] of pages of any content."""
     shape = pool.shape
-    if not pool.is_cuda or len(shape) < 3 or pool.device != device:
-        raise ValueError("pool must be a CUDA tensor [layers, n_pages, ...] on %s" % (device,))
+    if len(shape) < 3 or pool.get_device() != index:
+        raise ValueError("pool must be a tensor [layers, n_pages, ...] on cuda:%d" % index)
     if not (pool.is_contiguous() or pool[:1, :1].is_contiguous()):
         raise ValueError("each page of pool must be contiguous")
     size = pool.element_size()
@@ -427,28 +429,26 @@ def _pool(pool, device):
                       shape[1])
 
 
-def _book(table, lengths, refs, page_size, device):
+def _book(table, lengths, refs, page_size, index):
     """Descriptor of the pages' bookkeeping."""
-    if not table.is_cuda:
-        raise ValueError("table must be a CUDA tensor")
-    at, stride, rows, columns = _table(table, device)
+    at, stride, rows, columns = _table(table, index)
     return _pack_book(at, stride,
-                      0 if lengths is None else _int32("lengths", lengths, device, rows),
-                      _int32("refs", refs, device), rows, columns, page_size, refs.numel())
+                      0 if lengths is None else _int32("lengths", lengths, index, rows),
+                      _int32("refs", refs, index), rows, columns, page_size, refs.numel())
 
 
-def _status(t, device, status):
+def _status(status, table, index):
     if status is None:
-        return t.empty(2, dtype=t.int32, device=device)
-    _int32("status", status, device, 2)
+        return _t.empty(2, dtype=_t.int32, device=table.device)
+    _int32("status", status, index, 2)
     return status
 
 
-def _work(t, device, raw, need, workspace):
+def _work(t, index, raw, need, workspace):
     """(workspace, its bytes); called under _order."""
     if workspace is None:
-        return _workspace(t, device, raw, need)
-    return workspace, _space("workspace", workspace, device)
+        return _workspace(t, index, raw, need)
+    return workspace, _space("workspace", workspace, index)
 
 
 def pages_copy(pool, src, dst, stream=None):
@@ -457,9 +457,9 @@ def pages_copy(pool, src, dst, stream=None):
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return pages_copy(pool, src, dst)
-    n, device = src.numel(), pool.device
-    status = t.copy(_pool(pool, device), _int32("src", src, device, n), _int32("dst", dst, device, n),
-                    n, t.raw_stream(device.index))
+    n, index = src.numel(), _cuda("pool", pool)
+    status = t.copy(_pool(pool, index), _int32("src", src, index, n), _int32("dst", dst, index, n), n,
+                    t.raw_stream(index))
     if status:
         _check(status, "ds_pages_copy")
 
@@ -475,13 +475,13 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace, status)
-    n, device = seqs.numel(), table.device
-    book = _book(table, lengths, refs, page_size, device)
-    status = _status(t, device, status)
-    seqs_at, tokens_at = _int32("seqs", seqs, device, n), _int32("tokens", tokens, device, n)
-    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(device.index)
+    n, index = seqs.numel(), _cuda("table", table)
+    book = _book(table, lengths, refs, page_size, index)
+    status = _status(status, table, index)
+    seqs_at, tokens_at = _int32("seqs", seqs, index, n), _int32("tokens", tokens, index, n)
+    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(index)
     with _order:
-        workspace, size = _work(t, device, raw, need, workspace)
+        workspace, size = _work(t, index, raw, need, workspace)
         rc = t.reserve(book, seqs_at, tokens_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_reserve")
@@ -500,13 +500,13 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
             return pages_fork(pool, table, lengths, refs, src, dst, workspace, status)
     if pool.dim() != 5:
         raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes]")
-    n, device = src.numel(), table.device
-    book = _book(table, lengths, refs, pool.shape[3], device)
-    at, status = _pool(pool, device), _status(t, device, status)
-    src_at, dst_at = _int32("src", src, device, n), _int32("dst", dst, device, n)
-    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(device.index)
+    n, index = src.numel(), _cuda("table", table)
+    book = _book(table, lengths, refs, pool.shape[3], index)
+    at, status = _pool(pool, index), _status(status, table, index)
+    src_at, dst_at = _int32("src", src, index, n), _int32("dst", dst, index, n)
+    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(index)
     with _order:
-        workspace, size = _work(t, device, raw, need, workspace)
+        workspace, size = _work(t, index, raw, need, workspace)
         rc = t.fork(at, book, src_at, dst_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_fork")
@@ -519,9 +519,9 @@ def pages_free(table, lengths, refs, seqs, page_size, stream=None):
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return pages_free(table, lengths, refs, seqs, page_size)
-    n, device = seqs.numel(), table.device
-    rc = t.free(_book(table, lengths, refs, page_size, device), _int32("seqs", seqs, device, n), n,
-                t.raw_stream(device.index))
+    n, index = seqs.numel(), _cuda("table", table)
+    rc = t.free(_book(table, lengths, refs, page_size, index), _int32("seqs", seqs, index, n), n,
+                t.raw_stream(index))
     if rc:
         _check(rc, "ds_pages_free")
 
@@ -536,15 +536,15 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
     if stream is not None:
         with t.on_stream(stream):      # what is allocated belongs to that stream
             return pages_compact(pool, table, refs, workspace, remap, status)
-    device, n_pages = table.device, refs.numel()
-    book = _book(table, None, refs, 1, device)
+    index, n_pages = _cuda("table", table), refs.numel()
+    book = _book(table, None, refs, 1, index)
     if remap is None:
-        remap = t.empty(n_pages, dtype=t.int32, device=device)
-    at, status = _pool(pool, device), _status(t, device, status)
-    remap_at = _int32("remap", remap, device, n_pages)
-    need, raw = ds_pages_workspace(n_pages, 0), t.raw_stream(device.index)
+        remap = t.empty_like(refs)
+    at, status = _pool(pool, index), _status(status, table, index)
+    remap_at = _int32("remap", remap, index, n_pages)
+    need, raw = ds_pages_workspace(n_pages, 0), t.raw_stream(index)
     with _order:
-        workspace, size = _work(t, device, raw, need, workspace)
+        workspace, size = _work(t, index, raw, need, workspace)
         rc = t.compact(at, book, remap_at, status.data_ptr(), workspace.data_ptr(), size, raw)
     if rc:
         _check(rc, "ds_pages_compact")

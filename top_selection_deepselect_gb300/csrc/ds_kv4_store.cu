@@ -145,8 +145,10 @@ __device__ __forceinline__ unsigned encode(const Eight<T> &e, unsigned *bits)
     return bad || step == 0.f ? 0x88888888u : word - 0x3f400000u;
 }
 
+// Six CTAs an SM: 63.5 -> 61.4 us for the prefill below (five, the registers'
+// own choice; seven and eight spill).
 template <typename T, int D, bool kVec>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
 append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__restrict__ seq,
               const int32_t *__restrict__ pos, int tokens, const T *__restrict__ k, long long k_token,
               long long k_head, const T *__restrict__ v, long long v_token, long long v_head)
@@ -261,8 +263,8 @@ read_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__restr
 // Launch shape: heads that a lane takes one after another (1, 2 or 4, a divisor
 // of kv_heads).  More than one saves looking the token up again, but only where
 // the rest still fills the GPU (kFill threads): 28693 tokens of 8 heads of 128
-// are appended and read in 66 us with four heads and in 86 us with one, 64
-// tokens in 16 us and in 10 us.
+// are appended and read in 61 us with four heads, in 68 us with two and in 86 us
+// with one; 64 tokens in 16 us with four and in 10 us with one.
 constexpr long long kFill = 1 << 19;
 
 struct Launch {
