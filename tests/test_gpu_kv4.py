@@ -387,6 +387,44 @@ def test_another_stream_and_a_graph(ds):
     assert torch.equal(out, now[0]) and torch.equal(lse, now[1])
 
 
+def test_steps_without_a_wait_between_them(ds):
+    """A decode loop enqueued at once equals one that waits after every call: each kernel sees
+    what the one before it left (lengths, table, records), though it may start before that ends."""
+    def loop(wait):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(1)
+        n, hk, dim, page = 5, 2, 64, 16
+        i32 = dict(dtype=torch.int32, device=DEV)
+        pool = torch.zeros((60, hk, page, 80), dtype=torch.uint8, device=DEV)
+        table, lengths = torch.full((n, 12), -1, **i32), torch.zeros(n, **i32)
+        refs, seqs = torch.zeros(60, **i32), torch.arange(n, **i32)
+        grow = torch.tensor([1, 3, 2, 1, 4], **i32)
+        flat = seqs.repeat_interleave(grow.long())
+        within = torch.cat([torch.arange(x, **i32) for x in grow.tolist()])
+        results = []
+        kv = torch.randn((40, len(flat), 2, hk, dim), device=DEV, generator=g).bfloat16()
+        q = torch.randn((40, n, 1, 4, dim), device=DEV, generator=g).bfloat16()
+        torch.cuda.synchronize()
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        for i in range(40):
+            before = lengths.clone()
+            done()
+            ds.pages_reserve(table, lengths, refs, seqs, grow, page)
+            done()
+            ds.kv4_append(pool, table, flat, before[flat.long()] + within, kv[i, :, 0], kv[i, :, 1])
+            done()
+            results.append(ds.kv4_attention(q[i], pool, table, lengths)[0])
+            done()
+            if i % 10 == 9:
+                ds.pages_free(table, lengths, refs, seqs[i // 10:i // 10 + 1], page)
+                done()
+                ds.pages_compact(pool[None], table, refs)
+                done()
+        return torch.stack(results), lengths, pool
+    a, b = loop(True), loop(False)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_streams_and_threads_do_not_share_a_workspace_at_a_time(ds):
     """Calls without a workspace, from several streams and from several host threads on one."""
     import threading
@@ -434,6 +472,7 @@ def test_refusals(ds):
                 dict(indices=torch.zeros((3, 4), dtype=torch.int32, device=DEV)),
                 dict(indices=torch.zeros((3, 1, 4), dtype=torch.int64, device=DEV)),
                 dict(out=torch.zeros((3, 1, 4, 128), device=DEV)), dict(lse=q[..., 0]),
+                dict(table=table[:1].expand(3, -1)), dict(pool=pool[:1].expand(4, -1, -1, -1)),
                 dict(seqs=lengths[:1]), dict(q=torch.cat((q, q)))]:
         with pytest.raises((ValueError, TypeError)):
             ds.kv4_attention(**{**ok, **bad})

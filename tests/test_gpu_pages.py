@@ -188,6 +188,11 @@ def test_refusals(ds):
         ds.pages_copy(b.d_pool.cpu(), *lists)
     with pytest.raises(ValueError):
         ds.pages_copy(b.d_pool[..., ::2], *lists)
+    for overlapping in (b.d_pool[:, :1].expand(-1, 8, -1, -1, -1), b.d_pool[:1].expand(2, -1, -1, -1, -1)):
+        with pytest.raises(ValueError):
+            ds.pages_copy(overlapping, *lists)
+    with pytest.raises(ValueError):
+        ds.pages_free(b.table[:1].expand(4, -1), b.lengths, b.refs, lists[0], 4)
     with pytest.raises(ValueError):
         ds.pages_fork(b.d_pool[0], b.table, b.lengths, b.refs, *lists)
     with pytest.raises(ValueError):

@@ -218,7 +218,11 @@ def _table(table, index):
     stride, unit = table.stride()
     if unit != 1 and columns != 1:
         raise ValueError("table must have unit stride in the last dimension")
-    return table.data_ptr(), stride if stride > columns else columns, rows, columns
+    if stride < columns:
+        if rows > 1:
+            raise ValueError("rows of table must not overlap")
+        stride = columns
+    return table.data_ptr(), stride, rows, columns
 
 
 def _space(name, x, index):
@@ -254,9 +258,13 @@ def _cache(pool, table, head_dim, index):
     page = kv_heads * page_size * rec
     if (unit != 1 or token != rec or head != page_size * rec) and not pool[:1].is_contiguous():
         raise ValueError("each page of pool must be contiguous")
+    if each < page:
+        if n_pages > 1:
+            raise ValueError("pages of pool must not overlap")
+        each = page
     at, row, rows, columns = _table(table, index)
-    return _pack_cache(pool.data_ptr(), each if each > page else page, at, row, n_pages, page_size,
-                       kv_heads, head_dim, rows, columns)
+    return _pack_cache(pool.data_ptr(), each, at, row, n_pages, page_size, kv_heads, head_dim, rows,
+                       columns)
 
 
 def kv4_append(pool, table, seq, pos, k, v, stream=None):
@@ -424,9 +432,12 @@ def _pool(pool, index):
     size = pool.element_size()
     page = math.prod(shape[2:]) * size
     layer, each = pool.stride()[:2]
-    each *= size
-    return _pack_pool(pool.data_ptr(), layer * size, each if each > page else page, page, shape[0],
-                      shape[1])
+    layer, each = layer * size, each * size
+    if each < page or layer < page:
+        if each < page and shape[1] > 1 or layer < page and shape[0] > 1:
+            raise ValueError("pages of pool must not overlap")
+        each, layer = max(each, page), max(layer, page)
+    return _pack_pool(pool.data_ptr(), layer, each, page, shape[0], shape[1])
 
 
 def _book(table, lengths, refs, page_size, index):

@@ -14,7 +14,8 @@ int fail_cuda(cudaError_t e, const char *what);
 
 // Launches with programmatic dependent launch: the grid may be scheduled while
 // the previous kernel on the stream drains.  The kernel calls
-// dependent_grid_wait() before it touches memory and allow_dependent_grid().
+// dependent_grid_wait() before it touches memory, reads that with plain loads
+// (neither __ldg nor const __restrict__), and calls allow_dependent_grid().
 // CTAs come in clusters of `cluster`.
 template <typename... Params, typename... Args>
 cudaError_t launch_clusters(void (*kernel)(Params...), unsigned cluster, unsigned grid, unsigned threads,

@@ -45,6 +45,10 @@ struct Cache {
     Divider by_page;
 };
 
+// Loads below are plain ones on purpose: a kernel that starts while the previous
+// one drains may not read what that one writes through the read-only path, whose
+// loads may also be moved before the wait.
+
 // Page and offset in it of position `pos` of sequence `seq`; page -1 where the
 // sequence, the position or the page is out of range.
 struct Slot {
@@ -58,7 +62,7 @@ __device__ __forceinline__ Slot token_slot(const Cache &c, int seq, int pos)
     const int col = c.by_page(pos);
     if (col >= c.max_pages)
         return {-1, 0};
-    const int page = __ldg(c.table + seq * c.table_stride + col);
+    const int page = c.table[seq * c.table_stride + col];
     return {(unsigned)page < (unsigned)c.n_pages ? page : -1, pos - col * c.page_size};
 }
 

@@ -261,14 +261,14 @@ __device__ __forceinline__ void load_scales(float (&s)[G], const unsigned char *
 
 __device__ __forceinline__ int sequence_of(const AttendArgs &p, int b)
 {
-    return p.a.seqs ? __ldg(p.a.seqs + b) : b;
+    return p.a.seqs ? p.a.seqs[b] : b;
 }
 
 __device__ __forceinline__ int length_of(const AttendArgs &p, int seq)
 {
     if ((unsigned)seq >= (unsigned)p.c.max_seqs)
         return 0;
-    const int n = __ldg(p.a.lengths + seq);
+    const int n = p.a.lengths[seq];
     const long long room = (long long)p.c.max_pages * p.c.page_size;
     return n < 0 ? 0 : n > room ? (int)room : n;
 }
@@ -614,11 +614,11 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             const unsigned e = e0 + lane + i * (S::kWarps * S::kTile);
             int pos = (int)e;
             if (listed)
-                pos = e < (unsigned)p.a.k ? __ldg(part.list + e) : -1;
+                pos = e < (unsigned)p.a.k ? part.list[e] : -1;
             return pos < part.seen ? pos : -1;
         };
         auto page_of = [&](const volatile Part &part, int pos) -> int {
-            return pos >= 0 ? __ldg(part.row_table + p.c.by_page(pos)) : -1;
+            return pos >= 0 ? part.row_table[p.c.by_page(pos)] : -1;
         };
         // Copies the records of a tile: a lane each, or, where `run` neighbours
         // lie side by side in a page, one lane for all of them.  A run's tokens
@@ -653,7 +653,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         auto run_page_of = [&](const volatile Part &part, int i0) -> int {
             const int pos = run_pos(i0);
             return i0 + (lane >> halves) < mine && (unsigned)pos < (unsigned)part.seen
-                       ? __ldg(part.row_table + p.c.by_page(pos)) : -1;
+                       ? part.row_table[p.c.by_page(pos)] : -1;
         };
         auto next_runs = [&](const volatile Part &part, int i0) {
             const int pos = run_pos(i0);

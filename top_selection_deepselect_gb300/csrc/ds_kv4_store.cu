@@ -33,7 +33,7 @@ struct Place {
     bool in;
     Slot slot;
     __device__ __forceinline__ Place(const Cache &c, const Divider &by_runs, int each, int runs,
-                                     const int32_t *__restrict__ seq, const int32_t *__restrict__ pos,
+                                     const int32_t *seq, const int32_t *pos,
                                      int tokens)
     {
         w = threadIdx.x % (D / 8);
@@ -41,7 +41,7 @@ struct Place {
         token = by_runs(row);
         head = (row - token * runs) * each;
         in = token < tokens;
-        slot = in ? token_slot(c, __ldg(seq + token), __ldg(pos + token)) : Slot{-1, 0};
+        slot = in ? token_slot(c, seq[token], pos[token]) : Slot{-1, 0};
     }
 };
 
@@ -149,9 +149,9 @@ __device__ __forceinline__ unsigned encode(const Eight<T> &e, unsigned *bits)
 // own choice; seven and eight spill).
 template <typename T, int D, bool kVec>
 __global__ void __launch_bounds__(kThreads, 6)
-append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__restrict__ seq,
-              const int32_t *__restrict__ pos, int tokens, const T *__restrict__ k, long long k_token,
-              long long k_head, const T *__restrict__ v, long long v_token, long long v_head)
+append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *seq,
+              const int32_t *pos, int tokens, const T *k, long long k_token,
+              long long k_head, const T *v, long long v_token, long long v_head)
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
@@ -221,8 +221,8 @@ __device__ __forceinline__ Eight<T> decode(unsigned word, float scale)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *__restrict__ seq,
-            const int32_t *__restrict__ pos, int tokens, T *__restrict__ k, T *__restrict__ v)
+read_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *seq,
+            const int32_t *pos, int tokens, T *k, T *v)
 {
     constexpr int kWords = D / 8;
     constexpr int n = (D < 128 ? D : 128) / kGroup;
