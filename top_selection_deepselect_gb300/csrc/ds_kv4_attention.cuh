@@ -19,11 +19,11 @@
 // rows the matrix instructions (m16n8k16) have tokens or channels as their 16
 // rows and the query rows as their 8 columns:
 //   S^T = K Q^T,  O^T = V^T P^T
-// and P is transposed between the two by a movmatrix per 8 x 8.  With 16 or 32
-// rows (grouped heads, drafted tokens) the query rows are the 16 rows instead,
+// and P is transposed between the two by a movmatrix per 8 x 8.  With 16 rows
+// (grouped heads, drafted tokens) the query rows are the 16 rows instead,
 //   S = Q K^T,  O = P V
-// the same number of instructions for 16 rows, and P comes out as it goes in.
-// Either way the sum over each group of 32 channels is multiplied by the key
+// which is twice the products from the same expanded codes, and P comes out as it
+// goes in.  Either way the sum over each group of 32 channels is multiplied by the key
 // scale of (token, group) in 32 bits, and the probabilities carry the value
 // scale: fp16(p * scale), the only rounding of the inner loop.  2^-11 relative on
 // each token's share, less than the output's own rounding; 32-bit operands
@@ -53,12 +53,11 @@
 namespace ds {
 namespace kv4 {
 
-// Shape of one instantiation: head dimension, query rows of a unit (8, 16, 32).
+// Shape of one instantiation: head dimension, query rows of a unit (8 or 16).
 template <int D, int Rows>
 struct Shape {
     static constexpr bool kWide = Rows > 8;                      // query rows are the operands' rows
     static constexpr int kRows = Rows;
-    static constexpr int kBlocks = kWide ? Rows / 16 : 1;        // row blocks of an instruction
     static constexpr int kSubs = kWide ? 4 : 2;                  // instructions of a group's values
     static constexpr int kGroups = D / kGroup;
     static constexpr int kStretches = D > 128 ? D / 128 : 1;    // of up to 128 channels
@@ -68,13 +67,11 @@ struct Shape {
     static constexpr unsigned kFullMask = ~0u >> (32 - kTile);
     static constexpr int kRecord = record_bytes(D);
     static constexpr int kStageBytes = kTile * kRecord;
-    static constexpr int kOutRegs = kGroups * kSubs * kBlocks * 4;
+    static constexpr int kOutRegs = kGroups * kSubs * 4;
     // Warps of a CTA and CTAs of an SM, by what the output leaves of the
     // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.
     static constexpr int kWarps = kOutRegs == 64 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
-    // 16-token steps whose scores are made before their values are used (wide)
-    static constexpr int kJoint = kMT == 2 && kBlocks == 1 ? 2 : 1;
     static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
     static constexpr int kStages = D == 64 ? (kCtas == 2 ? 4 : 6) : kCtas == 2 ? 3 : kWarps == 12 ? 4 : 5;
     static constexpr int kOutStride = D + 4;                     // floats of an output row in shared memory
@@ -483,9 +480,9 @@ struct Queries {
                 const int d = lane * kMine + e, w = d / 8, n = d % 8;
                 const int group = d / kGroup, t = w % 4, half = n / 4, reg = n % 2, second = n % 4 / 2;
                 // operand register of the lane that holds row r % 8, place 2 t:
-                // narrow {reg}, wide {reg, row / 8 % 2}
-                const int at = S::kWide ? (((group * 2 + second) * S::kBlocks + r / 16) * 32 + r % 8 * 4 + t) * 4 +
-                                              reg * 2 + r / 8 % 2
+                // narrow {reg}, wide {reg, row / 8}
+                const int at = S::kWide ? ((group * 2 + second) * 32 + r % 8 * 4 + t) * 4 +
+                                              reg * 2 + r / 8
                                         : ((group * 2 + second) * 32 + r * 4 + t) * 2 + reg;
                 frag[at * 2 + half] = __float2half_rn(x[i][e] * lift * (reg ? 0.0625f : 1.f));
             }
@@ -746,23 +743,20 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         }
         __syncthreads();   // query operands and `part` are there
 
-        // Output; two rows of the unit for each block of it that this lane
-        // shares: row(b, c).
-        float o[S::kGroups][S::kSubs][S::kBlocks][4];
-        float top[S::kBlocks][2], sum[S::kBlocks][2], fac[S::kBlocks][2];
-        float low[S::kBlocks][2];     // maximum in base-2 units, 0 while there is none
-        auto row = [&](int b, int c) { return S::kWide ? b * 16 + g + 8 * c : 2 * t + c; };
+        // Output, and the state of the unit's two rows that this lane shares
+        float o[S::kGroups][S::kSubs][4];
+        float top[2], sum[2], fac[2];
+        float low[2];     // maximum in base-2 units, 0 while there is none
+        auto row = [&](int c) { return S::kWide ? g + 8 * c : 2 * t + c; };
         int least = 0x7fffffff;
 #pragma unroll
-        for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                top[b][c] = -INFINITY;
-                sum[b][c] = low[b][c] = 0.f;
-                fac[b][c] = factor[row(b, c)];
-                if (row(b, c) < part.u.rows)
-                    least = min(least, limit[row(b, c)]);
-            }
+        for (int c = 0; c < 2; ++c) {
+            top[c] = -INFINITY;
+            sum[c] = low[c] = 0.f;
+            fac[c] = factor[row(c)];
+            if (row(c) < part.u.rows)
+                least = min(least, limit[row(c)]);
+        }
         // tiles below the lowest limit of any row need no comparison
         least = __reduce_min_sync(~0u, least);
 #pragma unroll
@@ -770,10 +764,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
             for (int s = 0; s < S::kSubs; ++s)
 #pragma unroll
-                for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[i][s][b][e] = 0.f;
+                for (int e = 0; e < 4; ++e)
+                    o[i][s][e] = 0.f;
 
         // largest of the lanes that share a row
         auto row_max = [&](float v) {
@@ -786,32 +778,25 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         auto state = [](int e) { return S::kWide ? e / 2 : e & 1; };
         // New maxima `best` of the lane's scores.  One is rare after the first
         // tiles: only then the rows' maxima are joined and the sums brought down.
-        auto raise = [&](const float (&best)[S::kBlocks][2]) {
-            bool higher = false;
-#pragma unroll
-            for (int b = 0; b < S::kBlocks; ++b)
-                higher |= best[b][0] > top[b][0] || best[b][1] > top[b][1];
-            if (!__any_sync(~0u, higher))
+        auto raise = [&](const float (&best)[2]) {
+            if (!__any_sync(~0u, best[0] > top[0] || best[1] > top[1]))
                 return;
+            float down[2];
 #pragma unroll
-            for (int b = 0; b < S::kBlocks; ++b) {
-                float down[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float m = row_max(fmaxf(best[b][c], top[b][c]));
-                    down[c] = top[b][c] == -INFINITY ? 0.f : exp2_fast((top[b][c] - m) * fac[b][c]);
-                    top[b][c] = m;
-                    low[b][c] = m == -INFINITY ? 0.f : m * fac[b][c];
-                    sum[b][c] *= down[c];
-                }
-#pragma unroll
-                for (int i = 0; i < S::kGroups; ++i)
-#pragma unroll
-                    for (int s = 0; s < S::kSubs; ++s)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[i][s][b][e] *= down[state(e)];
+            for (int c = 0; c < 2; ++c) {
+                const float m = row_max(fmaxf(best[c], top[c]));
+                down[c] = top[c] == -INFINITY ? 0.f : exp2_fast((top[c] - m) * fac[c]);
+                top[c] = m;
+                low[c] = m == -INFINITY ? 0.f : m * fac[c];
+                sum[c] *= down[c];
             }
+#pragma unroll
+            for (int i = 0; i < S::kGroups; ++i)
+#pragma unroll
+                for (int s = 0; s < S::kSubs; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[i][s][e] *= down[state(e)];
         };
         // operands of the four codes of each of two tokens in z: codes j of both
         auto value_codes = [](uint32_t z, int j) {
@@ -865,14 +850,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         }
                     }
                 }
-                float best[1][2] = {{-INFINITY, -INFINITY}};
+                float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
                             sc[mt][e] = -INFINITY;
-                        best[0][e & 1] = fmaxf(best[0][e & 1], sc[mt][e]);
+                        best[e & 1] = fmaxf(best[e & 1], sc[mt][e]);
                     }
                 raise(best);
 #pragma unroll
@@ -883,10 +868,10 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     load_scales(sb, ra + S::kNext * S::kRecord + D + 2 * S::kGroups);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        pr[e] = exp2_fast(sc[mt][e] * fac[0][e & 1] - low[0][e & 1]);
-                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                        pr[e] = exp2_fast(sc[mt][e] * fac[e & 1] - low[e & 1]);
+                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
                             pr[e] = 0.f;
-                        sum[0][e & 1] += pr[e];
+                        sum[e & 1] += pr[e];
                     }
                     const unsigned char *va = tile + (mt * 16 + tok_a) * S::kRecord + D / 2;
                     const unsigned char *vb = tile + (mt * 16 + tok_b) * S::kRecord + D / 2;
@@ -908,142 +893,124 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             for (int e = 0; e < 4; ++e) {
                                 w[e] = pr[e] * (e < 2 ? sa[group] : sb[group]);
                                 // whatever the record holds
-                                if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(0, e & 1)))
+                                if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
                                     w[e] = 0.f;
                             }
                             const uint32_t b0 = transpose8x8(pack_half2(w[0], w[1]));
                             const uint32_t b1 = transpose8x8(pack_half2(w[2], w[3]));
-                            mma16816(o[group][0][0], value_codes(z, 0), value_codes(z, 1),
+                            mma16816(o[group][0], value_codes(z, 0), value_codes(z, 1),
                                      value_codes(y, 0), value_codes(y, 1), b0, b1);
-                            mma16816(o[group][1][0], value_codes(z, 2), value_codes(z, 3),
+                            mma16816(o[group][1], value_codes(z, 2), value_codes(z, 3),
                                      value_codes(y, 2), value_codes(y, 3), b0, b1);
                         }
                     }
                 }
             } else {
-#pragma unroll 1
-                for (int m0 = 0; m0 < S::kMT; m0 += S::kJoint) {
-                    // scores of a step's places 2 t, 2 t + 1 (half 0) and those + 8
-                    float sc[S::kJoint][S::kBlocks][2][4];
-                    const int next = S::kNext * S::kRecord;
-                    auto record = [&](int m, int token) {
-                        return tile + ((m0 + m) * 16 + token) * S::kRecord;
-                    };
+                // scores of a step's places 2 t, 2 t + 1 (half 0) and those + 8
+                float sc[S::kMT][2][4];
+                const int next = S::kNext * S::kRecord;
+                auto record = [&](int m, int token) {
+                    return tile + (m * 16 + token) * S::kRecord;
+                };
 #pragma unroll
-                    for (int m = 0; m < S::kJoint; ++m) {
+                for (int m = 0; m < S::kMT; ++m) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const unsigned char *rk = record(m, tok_row) + half * next;
-                            float sa[S::kGroups], sb[S::kGroups];
-                            load_scales(sa, record(m, tok_a) + half * next + D);
-                            load_scales(sb, record(m, tok_b) + half * next + D);
+                    for (int half = 0; half < 2; ++half) {
+                        const unsigned char *rk = record(m, tok_row) + half * next;
+                        float sa[S::kGroups], sb[S::kGroups];
+                        load_scales(sa, record(m, tok_a) + half * next + D);
+                        load_scales(sb, record(m, tok_b) + half * next + D);
 #pragma unroll
-                            for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    sc[m][b][half][e] = 0.f;
-#pragma unroll
-                            for (int st = 0; st < S::kStretches; ++st) {
-                                uint32_t wk[S::kPer];
-                                load_words(wk, rk + st * 64 + t * S::kPer * 4);
-#pragma unroll
-                                for (int i = 0; i < S::kPer; ++i) {
-                                    const int group = st * S::kPer + i;
-                                    const uint32_t k0 = low_codes(wk[i]), k1 = high_codes(wk[i]);
-                                    const uint32_t k2 = low_codes(wk[i] >> 8), k3 = high_codes(wk[i] >> 8);
-#pragma unroll
-                                    for (int b = 0; b < S::kBlocks; ++b) {
-                                        const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kOffQ) +
-                                                          (group * 2 * S::kBlocks + b) * 32 + lane;
-                                        const uint4 q0 = qf[0], q1 = qf[S::kBlocks * 32];
-                                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                                        mma16816(acc, q0.x, q0.y, q0.z, q0.w, k0, k1);
-                                        mma16816(acc, q1.x, q1.y, q1.z, q1.w, k2, k3);
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e)
-                                            sc[m][b][half][e] += (e & 1 ? sb[group] : sa[group]) * acc[e];
-                                    }
-                                }
-                            }
-                        }
-                    }
-                    auto token = [&](int m, int half, int e) {
-                        return (m0 + m) * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
-                    };
-                    float best[S::kBlocks][2];
-#pragma unroll
-                    for (int b = 0; b < S::kBlocks; ++b) {
-                        best[b][0] = best[b][1] = -INFINITY;
-#pragma unroll
-                        for (int m = 0; m < S::kJoint; ++m)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
-                                        sc[m][b][half][e] = -INFINITY;
-                                    best[b][e / 2] = fmaxf(best[b][e / 2], sc[m][b][half][e]);
-                                }
-                    }
-                    raise(best);
-#pragma unroll
-                    for (int m = 0; m < S::kJoint; ++m) {
-#pragma unroll
-                        for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    float pr = exp2_fast(sc[m][b][half][e] * fac[b][e / 2] - low[b][e / 2]);
-                                    if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
-                                        pr = 0.f;
-                                    sum[b][e / 2] += pr;
-                                    sc[m][b][half][e] = pr;
-                                }
-                        const unsigned char *ra = record(m, tok_a), *rb = record(m, tok_b);
-                        float vs[4][S::kGroups];     // value scales of the lane's four tokens
-                        load_scales(vs[0], ra + D + 2 * S::kGroups);
-                        load_scales(vs[1], rb + D + 2 * S::kGroups);
-                        load_scales(vs[2], ra + next + D + 2 * S::kGroups);
-                        load_scales(vs[3], rb + next + D + 2 * S::kGroups);
+                        for (int e = 0; e < 4; ++e)
+                            sc[m][half][e] = 0.f;
 #pragma unroll
                         for (int st = 0; st < S::kStretches; ++st) {
-                            constexpr int kW = S::kPer / 2;
-                            const int at = D / 2 + st * 64 + g * kW * 4;
-                            uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
-                            load_words(wa, ra + at);
-                            load_words(wb, rb + at);
-                            load_words(xa, ra + next + at);
-                            load_words(xb, rb + next + at);
+                            uint32_t wk[S::kPer];
+                            load_words(wk, rk + st * 64 + t * S::kPer * 4);
 #pragma unroll
                             for (int i = 0; i < S::kPer; ++i) {
                                 const int group = st * S::kPer + i;
-                                const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
-                                const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
-                                uint32_t pa[S::kBlocks][4];
+                                const uint32_t k0 = low_codes(wk[i]), k1 = high_codes(wk[i]);
+                                const uint32_t k2 = low_codes(wk[i] >> 8), k3 = high_codes(wk[i] >> 8);
+                                const uint4 *qf = reinterpret_cast<const uint4 *>(smem + S::kOffQ) +
+                                                  group * 2 * 32 + lane;
+                                const uint4 q0 = qf[0], q1 = qf[32];
+                                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816(acc, q0.x, q0.y, q0.z, q0.w, k0, k1);
+                                mma16816(acc, q1.x, q1.y, q1.z, q1.w, k2, k3);
 #pragma unroll
-                                for (int b = 0; b < S::kBlocks; ++b) {
-                                    float w[2][4];
+                                for (int e = 0; e < 4; ++e)
+                                    sc[m][half][e] += (e & 1 ? sb[group] : sa[group]) * acc[e];
+                            }
+                        }
+                    }
+                }
+                auto token = [&](int m, int half, int e) {
+                    return m * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
+                };
+                float best[2];
+                best[0] = best[1] = -INFINITY;
 #pragma unroll
-                                    for (int half = 0; half < 2; ++half)
+                for (int m = 0; m < S::kMT; ++m)
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            w[half][e] = sc[m][b][half][e] * vs[half * 2 + (e & 1)][group];
-                                            if (kMasked && !seen_by(token(m, half, e), row(b, e / 2)))
-                                                w[half][e] = 0.f;
-                                        }
-                                    pa[b][0] = pack_half2(w[0][0], w[0][1]);
-                                    pa[b][1] = pack_half2(w[0][2], w[0][3]);
-                                    pa[b][2] = pack_half2(w[1][0], w[1][1]);
-                                    pa[b][3] = pack_half2(w[1][2], w[1][3]);
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                                sc[m][half][e] = -INFINITY;
+                            best[e / 2] = fmaxf(best[e / 2], sc[m][half][e]);
+                        }
+                raise(best);
+#pragma unroll
+                for (int m = 0; m < S::kMT; ++m) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float pr = exp2_fast(sc[m][half][e] * fac[e / 2] - low[e / 2]);
+                            if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                                pr = 0.f;
+                            sum[e / 2] += pr;
+                            sc[m][half][e] = pr;
+                        }
+                    const unsigned char *ra = record(m, tok_a), *rb = record(m, tok_b);
+                    float vs[4][S::kGroups];     // value scales of the lane's four tokens
+                    load_scales(vs[0], ra + D + 2 * S::kGroups);
+                    load_scales(vs[1], rb + D + 2 * S::kGroups);
+                    load_scales(vs[2], ra + next + D + 2 * S::kGroups);
+                    load_scales(vs[3], rb + next + D + 2 * S::kGroups);
+#pragma unroll
+                    for (int st = 0; st < S::kStretches; ++st) {
+                        constexpr int kW = S::kPer / 2;
+                        const int at = D / 2 + st * 64 + g * kW * 4;
+                        uint32_t wa[kW], wb[kW], xa[kW], xb[kW];
+                        load_words(wa, ra + at);
+                        load_words(wb, rb + at);
+                        load_words(xa, ra + next + at);
+                        load_words(xb, rb + next + at);
+#pragma unroll
+                        for (int i = 0; i < S::kPer; ++i) {
+                            const int group = st * S::kPer + i;
+                            const uint32_t z = __byte_perm(wa[i / 2], wb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                            const uint32_t y = __byte_perm(xa[i / 2], xb[i / 2], i & 1 ? 0x7632 : 0x5410);
+                            uint32_t pa[4];
+                            float w[2][4];
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    w[half][e] = sc[m][half][e] * vs[half * 2 + (e & 1)][group];
+                                    if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                                        w[half][e] = 0.f;
                                 }
+                            pa[0] = pack_half2(w[0][0], w[0][1]);
+                            pa[1] = pack_half2(w[0][2], w[0][3]);
+                            pa[2] = pack_half2(w[1][0], w[1][1]);
+                            pa[3] = pack_half2(w[1][2], w[1][3]);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint32_t b0 = value_codes(z, j), b1 = value_codes(y, j);
-#pragma unroll
-                                    for (int b = 0; b < S::kBlocks; ++b)
-                                        mma16816(o[group][j][b], pa[b][0], pa[b][1], pa[b][2], pa[b][3], b0, b1);
-                                }
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t b0 = value_codes(z, j), b1 = value_codes(y, j);
+                                mma16816(o[group][j], pa[0], pa[1], pa[2], pa[3], b0, b1);
                             }
                         }
                     }
@@ -1093,39 +1060,37 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         // (a warp without tiles has none)
         const int active = part.active;
 #pragma unroll
-        for (int b = 0; b < S::kBlocks; ++b)
+        for (int c = 0; c < 2; ++c) {
+            if (warp >= active)
+                break;
+            const int r = row(c);
+            float s = lost ? __int_as_float(0x7fffffff) : sum[c];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (warp >= active)
-                    break;
-                const int r = row(b, c);
-                float s = lost ? __int_as_float(0x7fffffff) : sum[b][c];
+            for (int step = S::kWide ? 1 : 4; step < (S::kWide ? 4 : 32); step *= 2)
+                s += __shfl_xor_sync(~0u, s, step);
+            if (S::kWide ? t == 0 : g == 0) {
+                wmax(warp, r) = top[c] == -INFINITY ? -INFINITY : low[c];
+                wsum(warp, r) = s;
+            }
+            // narrow: rows of the instruction are channels 4 g + {0, 1} and
+            // 4 g + {2, 3}; wide: columns 2 t, 2 t + 1 of instruction j are
+            // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large.
+            float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride;
 #pragma unroll
-                for (int step = S::kWide ? 1 : 4; step < (S::kWide ? 4 : 32); step *= 2)
-                    s += __shfl_xor_sync(~0u, s, step);
-                if (S::kWide ? t == 0 : g == 0) {
-                    wmax(warp, r) = top[b][c] == -INFINITY ? -INFINITY : low[b][c];
-                    wsum(warp, r) = s;
-                }
-                // narrow: rows of the instruction are channels 4 g + {0, 1} and
-                // 4 g + {2, 3}; wide: columns 2 t, 2 t + 1 of instruction j are
-                // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large.
-                float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride;
+            for (int i = 0; i < S::kGroups; ++i) {
+                if constexpr (S::kWide) {
 #pragma unroll
-                for (int i = 0; i < S::kGroups; ++i) {
-                    if constexpr (S::kWide) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            *reinterpret_cast<float4 *>(dst + i * kGroup + 8 * t + 4 * k) = make_float4(
-                                o[i][0][b][2 * c + k], o[i][1][b][2 * c + k] * 0.0625f,
-                                o[i][2][b][2 * c + k], o[i][3][b][2 * c + k] * 0.0625f);
-                    } else {
-                        *reinterpret_cast<float4 *>(dst + i * kGroup + 4 * g) =
-                            make_float4(o[i][0][b][c], o[i][0][b][c + 2] * 0.0625f, o[i][1][b][c],
-                                        o[i][1][b][c + 2] * 0.0625f);
-                    }
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<float4 *>(dst + i * kGroup + 8 * t + 4 * k) = make_float4(
+                            o[i][0][2 * c + k], o[i][1][2 * c + k] * 0.0625f,
+                            o[i][2][2 * c + k], o[i][3][2 * c + k] * 0.0625f);
+                } else {
+                    *reinterpret_cast<float4 *>(dst + i * kGroup + 4 * g) =
+                        make_float4(o[i][0][c], o[i][0][c + 2] * 0.0625f, o[i][1][c],
+                                    o[i][1][c + 2] * 0.0625f);
                 }
             }
+        }
         __syncthreads();
 
         Unit u;
@@ -1315,13 +1280,11 @@ join_kernel(const __grid_constant__ AttendArgs p)
 }
 
 // ---- host ----------------------------------------------------------------------
-// Query rows of a unit: as many as there are, up to 32 (16 for D = 256, whose
-// outputs would not fit the registers).
-template <int D>
-int unit_rows(int rows)
-{
-    return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
-}
+// Query rows of a unit: 8, or 16 where there are more.  Further rows are further
+// units.  Units of 32 rows expand a record once instead of twice, but their
+// outputs leave 8 warps an SM that cannot hide each other's waits (32 rows, 16 x
+// 16384 tokens: 197 us in one unit, 186 in two; 80 rows, 4 x 65536: 94 and 72).
+inline int unit_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 // How a call is laid out: sizes of its units, its CTAs, and whether units are
 // cut between CTAs.  They are not, and the join is saved, where a unit is at
@@ -1403,11 +1366,9 @@ AttendArgs attend_args(const Cache &c, const Attend &a)
 template <int D>
 cudaError_t launch_dim(const Cache &c, const Attend &a, int dev, int sms, cudaStream_t stream)
 {
-    constexpr int kMost = D == 256 ? 16 : 32;
     AttendArgs p = attend_args<D>(c, a);
-    const int rows = unit_rows<D>(p.rows);
-    return rows == 8    ? launch_shape<D, 8>(p, dev, sms, stream)
-           : rows == 16 ? launch_shape<D, 16>(p, dev, sms, stream) : launch_shape<D, kMost>(p, dev, sms, stream);
+    return unit_rows(p.rows) == 8 ? launch_shape<D, 8>(p, dev, sms, stream)
+                                  : launch_shape<D, 16>(p, dev, sms, stream);
 }
 
 template <int D, int Rows>
@@ -1420,11 +1381,8 @@ size_t workspace_shape(AttendArgs &p, int sms)
 template <int D>
 size_t workspace_dim(const Cache &c, const Attend &a, int sms)
 {
-    constexpr int kMost = D == 256 ? 16 : 32;
     AttendArgs p = attend_args<D>(c, a);
-    const int rows = unit_rows<D>(p.rows);
-    return rows == 8    ? workspace_shape<D, 8>(p, sms)
-           : rows == 16 ? workspace_shape<D, 16>(p, sms) : workspace_shape<D, kMost>(p, sms);
+    return unit_rows(p.rows) == 8 ? workspace_shape<D, 8>(p, sms) : workspace_shape<D, 16>(p, sms);
 }
 
 }  // namespace kv4
