@@ -1107,13 +1107,21 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             float m, l;
             float4 v;
         };
-        auto add_up = [&](int n, auto maximum, auto sum_of, auto output) {
+        auto add_up = [&](auto most, int n, auto maximum, auto sum_of, auto output) {
+            constexpr int kMost = decltype(most)::value;      // n is at most this
             Four f = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-            for (int i = 0; i < n; ++i)
-                f.m = fmaxf(f.m, maximum(i));
-            for (int i = 0; i < n; ++i) {
+            float m[kMost];
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                m[i] = i < n ? maximum(i) : -INFINITY;
+                f.m = fmaxf(f.m, m[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                if (i >= n)
+                    break;
                 const float s = sum_of(i);
-                const float weight = s == 0.f ? 0.f : s != s ? 1.f : exp2_fast(maximum(i) - f.m);
+                const float weight = s == 0.f ? 0.f : s != s ? 1.f : exp2_fast(m[i] - f.m);
                 const float4 o4 = output(i);
                 f.l += s * weight;
                 f.v.x += o4.x * weight, f.v.y += o4.y * weight;
@@ -1122,7 +1130,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             return f;
         };
         auto of_warps = [&](int r, int d) {
-            return add_up(active, [&](int w) { return wmax(w, r); }, [&](int w) { return wsum(w, r); },
+            return add_up(std::integral_constant<int, S::kWarps>(), active, [&](int w) { return wmax(w, r); }, [&](int w) { return wsum(w, r); },
                           [&](int w) {
                               return *reinterpret_cast<const float4 *>(
                                   smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
@@ -1172,7 +1180,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     if (r >= u.rows)
                         break;
                     auto of = [&](int i) { return cluster.map_shared_rank(mine, i); };
-                    finish(r, d, add_up(p.cluster, [&](int i) { return of(i)[r]; },
+                    finish(r, d, add_up(std::integral_constant<int, 8>(), p.cluster, [&](int i) { return of(i)[r]; },
                                         [&](int i) { return of(i)[S::kRows + r]; },
                                         [&](int i) {
                                             return *reinterpret_cast<const float4 *>(
