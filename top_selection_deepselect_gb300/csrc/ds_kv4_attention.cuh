@@ -75,11 +75,17 @@ struct Shape {
     static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
     static constexpr int kStages = D == 64 ? (kCtas == 2 ? 4 : 6) : kCtas == 2 ? 3 : kWarps == 12 ? 4 : 5;
     static constexpr int kOutStride = D + 4;                     // floats of an output row in shared memory
-    // A warp's ring; at a unit's end its output, the rows' maxima and sums.
-    static constexpr int kOffMax = kRows * kOutStride * 4;
+    // A warp's ring; at a unit's end its tail holds the warp's output, the rows'
+    // maxima and sums, while kEarly stages in front of that are filled for the
+    // next unit.
+    static constexpr int kResultBytes = kRows * (kOutStride + 2) * 4;
+    static constexpr int kWarpBytes =
+        kStages * kStageBytes > kResultBytes ? kStages * kStageBytes : kResultBytes;
+    static constexpr int kTail = kWarpBytes - kResultBytes;
+    static constexpr int kOffMax = kTail + kRows * kOutStride * 4;
     static constexpr int kOffSum = kOffMax + kRows * 4;
-    static constexpr int kWarpBytes = kStages * kStageBytes > kOffSum + kRows * 4
-                                          ? kStages * kStageBytes : kOffSum + kRows * 4;
+    static constexpr int kEarly =
+        kTail / kStageBytes < kStages - 1 ? kTail / kStageBytes : kStages - 1;
     // shared memory behind the rings
     static constexpr int kOffQ = kWarps * kWarpBytes;             // query operands
     static constexpr int kOffFactor = kOffQ + kRows * D * 2;
@@ -88,7 +94,7 @@ struct Shape {
     static constexpr int kOffMask = kOffBarrier + kWarps * kStages * 8;
     static constexpr int kOffScan = (kOffMask + kWarps * kStages * 4 + 15) / 16 * 16;
     static constexpr int kOffPart = kOffScan + 16 * 8;
-    static constexpr int kSmem = kOffPart + 128;
+    static constexpr int kSmem = kOffPart + 2 * 128;
     static constexpr int kPartial = kRows * (D + 2);                    // floats of a partial result
 
     // Order of the 16 tokens of a step in the operands: places 2 t and 2 t + 1
@@ -380,8 +386,8 @@ __device__ __forceinline__ Line line_of(const AttendArgs &p, bool listed, long l
 
 // Which query rows unit u of a batch entry covers.
 struct Unit {
-    int b, head, query, row0, rows;
-    __device__ __forceinline__ Unit() {}
+    int b = 0, head = 0, query = 0, row0 = 0, rows = 0;
+    Unit() = default;
     __device__ __forceinline__ Unit(const AttendArgs &p, int entry, int u, int block_rows)
     {
         b = entry;
@@ -427,7 +433,7 @@ struct Queries {
     using S = Shape<D, Rows>;
     static constexpr int kMine = D / 32;                                    // channels of a lane
     static constexpr int kTurns = (Rows + S::kWarps - 1) / S::kWarps;       // rows of a warp
-    float x[kTurns][kMine];
+    float x[kTurns][kMine] = {};
 
     template <typename T>
     __device__ __forceinline__ void load(const AttendArgs &p, const Unit &u)
@@ -524,12 +530,12 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         return *reinterpret_cast<float *>(smem + w * S::kWarpBytes + S::kOffSum + r * 4);
     };
 
-    // state of the warp's ring: the stage filled and the one used next, the
-    // phase of the latter; lost: a copy did not arrive, the ring is not used any
-    // more and all further results are NaN
+    // state of the warp's ring: tile i of a unit is in stage i % kStages; the
+    // stage filled and the one used next, the phases of all; lost: a copy did not
+    // arrive, the ring is not used any more and all further results are NaN
     const uint32_t barriers = shared_address(smem + S::kOffBarrier) + warp * S::kStages * 8;
     int fill = 0, use = 0;
-    unsigned phase = 0;
+    unsigned phases = 0;
     bool lost = false;
     if (lane == 0) {
         for (int s = 0; s < S::kStages; ++s)
@@ -541,7 +547,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     dependent_grid_wait();
     allow_dependent_grid();
 
-    volatile Part &part = *reinterpret_cast<Part *>(smem + S::kOffPart);
     Split *split = reinterpret_cast<Split *>(p.a.partial) + blockIdx.x;
     const bool clustered = kRun == 0 && p.cluster > 1;
     if (threadIdx.x == 0 && !p.whole && !clustered)
@@ -580,168 +585,209 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     const int tok_row = g & 1 ? S::odd(g / 2) : S::even(g / 2);   // token at place g
     const int tok_a = S::even(t), tok_b = S::odd(t);              // at places 2 t and 2 t + 1
 
-    while (true) {
-        // the part of the unit at x that is this CTA's
-        const int seq = sequence_of(p, entry), len = length_of(p, seq);
-        const long long tiles = tiles_of<S::kTile>(p, listed, entry);
-        const long long zero = start + kUnitCost;     // place of the unit's tile 0
-        const long long tile0 = x > zero ? x - zero : 0;
+    // ---- the next unit: what it is, its first copies ---------------------
+    int mine = 0, slot = 0;       // the warp's tiles; which `Part` is the unit's
+    unsigned e0 = 0;              // first token, or list entry, of the first of them
+    Part now;
+    Unit unit;
+    int len = 0;
+    long long tiles = 0, zero = 0, tile0 = 0, count = 0;
+    Queries<D, Rows> queries;
+    auto part_of = [&](int i) -> volatile Part & {
+        return *reinterpret_cast<Part *>(smem + S::kOffPart + i * 128);
+    };
+
+    // ---- tokens one by one: a lane each -----------------------------
+    // position of this lane's token of the warp's tile i, -1: none
+    auto position = [&](const volatile Part &part, int i) -> int {
+        if (i >= mine || lane >= S::kTile)
+            return -1;
+        const unsigned e = e0 + lane + i * (S::kWarps * S::kTile);
+        int pos = (int)e;
+        if (listed)
+            pos = e < (unsigned)p.a.k ? part.list[e] : -1;
+        return pos < part.seen ? pos : -1;
+    };
+    auto page_of = [&](const volatile Part &part, int pos) -> int {
+        return pos >= 0 ? part.row_table[p.c.by_page(pos)] : -1;
+    };
+    // Copies the records of a tile: a lane each, or, where `run` neighbours
+    // lie side by side in a page, one lane for all of them.  A run's tokens
+    // past the sequence's end are in the page too; the mask leaves them out.
+    auto issue_tokens = [&](const volatile Part &part, int pos, int page) {
+        const uint32_t bar = barriers + fill * 8, dst = shared_address(ring + fill * S::kStageBytes);
+        const bool ok = (unsigned)page < (unsigned)p.c.n_pages;   // page is -1 where pos is
+        const bool leads = ok && (lane & (p.run - 1)) == 0;
+        const unsigned mask = __ballot_sync(~0u, ok), leaders = __ballot_sync(~0u, leads);
+        if (lane == 0) {
+            masks[fill] = mask;
+            barrier_expect(bar, __popc(leaders) * p.run * S::kRecord);
+        }
+        __syncwarp();
+        if (leads) {
+            const int in_page = pos - p.c.by_page(pos) * p.c.page_size;
+            copy_bulk(dst + lane * S::kRecord,
+                      part.head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
+                      p.run * S::kRecord, bar);
+        }
+        fill = fill + 1 == S::kStages ? 0 : fill + 1;
+    };
+    // ---- runs: a lane looks up one of 32 whole runs ------------------
+    // Tile i is run(s) i << halves and the next; 32 runs are looked up at once.
+    constexpr int halves = kRun > 0 && kRun < S::kTile ? 1 : 0, per_look = 32 >> halves;
+    const unsigned char *run_src = nullptr;    // of the lane's run of those under way
+    unsigned tile_mask = 0;                    // of the run's tile
+    int run_page = -1;                         // of the lane's run of the next ones
+    auto run_pos = [&](int i0) {
+        return (int)(e0 + (i0 + (lane >> halves)) * (S::kWarps * S::kTile) + (lane & halves) * kRun);
+    };
+    auto run_page_of = [&](const volatile Part &part, int i0) -> int {
+        const int pos = run_pos(i0);
+        return i0 + (lane >> halves) < mine && (unsigned)pos < (unsigned)part.seen
+                   ? part.row_table[p.c.by_page(pos)] : -1;
+    };
+    auto next_runs = [&](const volatile Part &part, int i0) {
+        const int pos = run_pos(i0);
+        const bool ok = (unsigned)run_page < (unsigned)p.c.n_pages;
+        const int in_page = ok ? pos - p.c.by_page(pos) * p.c.page_size : 0;
+        run_src = ok ? part.head_pool + run_page * p.c.page_stride + (long long)in_page * S::kRecord
+                     : nullptr;
+        const int left = part.seen - pos;      // > 0 where there is a page
+        tile_mask = !ok ? 0u : ~0u >> (32 - (left < kRun ? left : kRun));
+        if (halves) {
+            tile_mask <<= (lane & 1) * 16;
+            tile_mask |= __shfl_xor_sync(~0u, tile_mask, 1);
+        }
+        run_page = run_page_of(part, i0 + per_look);
+    };
+    // tokens past the sequence's end are in the page too
+    auto issue_runs = [&](const volatile Part &part, int i) {
+        const int turn = i & (per_look - 1);
+        if (i > 0 && turn == 0)
+            next_runs(part, i);
+        const uint32_t bar = barriers + fill * 8;
+        if (lane == turn << halves) {
+            masks[fill] = tile_mask;
+            const int runs = !halves ? tile_mask != 0 : ((tile_mask & 0xffffu) != 0) + (tile_mask > 0xffffu);
+            barrier_expect(bar, runs * kRun * S::kRecord);
+        }
+        if (halves)
+            __syncwarp();
+        if (lane >> halves == turn && run_src)
+            copy_bulk(shared_address(ring + fill * S::kStageBytes) + (lane & halves) * kRun * S::kRecord,
+                      run_src, kRun * S::kRecord, bar);
+        fill = fill + 1 == S::kStages ? 0 : fill + 1;
+    };
+
+    // The part of the unit at x that is this CTA's: looks its first tiles up,
+    // starts kEarly copies and the load of its queries.  False: there is none.
+    int pos_next = -1, page_next = -1, pos_after = -1;
+    int early_pos[S::kStages], early_page[S::kStages];
+    auto set_up = [&]() -> bool {
+        // nothing of the last unit is carried through the loop over its tiles
+        now = Part();
+        unit = Unit();
+        queries = Queries<D, Rows>();
+        len = mine = 0;
+        tiles = zero = tile0 = count = 0;
+        e0 = tile_mask = 0;
+        run_src = nullptr;
+        run_page = pos_next = page_next = pos_after = -1;
+#pragma unroll
+        for (int s = 0; s < S::kStages; ++s)
+            early_pos[s] = early_page[s] = -1;
+        if (x >= end)
+            return false;
+        const int seq = sequence_of(p, entry);
+        len = length_of(p, seq);
+        tiles = tiles_of<S::kTile>(p, listed, entry);
+        zero = start + kUnitCost;     // place of the unit's tile 0
+        tile0 = x > zero ? x - zero : 0;
         const long long stop = p.whole || zero + tiles < end ? zero + tiles : end;
-        const long long count = stop - zero - tile0;
+        count = stop - zero - tile0;
         if (count <= 0)
-            break;      // only the unit's first places: its tiles are the next CTA's
-        const Unit unit(p, entry, u_in, S::kRows);
-        Part now;
+            return false;   // only the unit's first places: its tiles are the next CTA's
+        unit = Unit(p, entry, u_in, S::kRows);
         now.list = listed ? p.a.indices + ((long long)entry * p.a.queries + unit.query) * p.a.k : nullptr;
         now.row_table =
             p.c.table + ((unsigned)seq < (unsigned)p.c.max_seqs ? seq * p.c.table_stride : 0);
         now.head_pool = p.c.pool + (long long)unit.head * p.c.page_size * S::kRecord;
         now.seen = listed ? len - p.a.queries + 1 + unit.query : len;
         // the warp's tiles: warp, warp + kWarps, ... of `count`
-        const int mine =
-            count > warp && !lost ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
+        mine = count > warp && !lost ? (int)((count - warp + S::kWarps - 1) / S::kWarps) : 0;
         // tokens and list entries are below 2^31; the last tile may end above
-        const unsigned e0 = (unsigned)((tile0 + warp) * S::kTile);
-
-        // ---- tokens one by one: a lane each -----------------------------
-        // position of this lane's token of the warp's tile i, -1: none
-        auto position = [&](const volatile Part &part, int i) -> int {
-            if (i >= mine || lane >= S::kTile)
-                return -1;
-            const unsigned e = e0 + lane + i * (S::kWarps * S::kTile);
-            int pos = (int)e;
-            if (listed)
-                pos = e < (unsigned)p.a.k ? part.list[e] : -1;
-            return pos < part.seen ? pos : -1;
-        };
-        auto page_of = [&](const volatile Part &part, int pos) -> int {
-            return pos >= 0 ? part.row_table[p.c.by_page(pos)] : -1;
-        };
-        // Copies the records of a tile: a lane each, or, where `run` neighbours
-        // lie side by side in a page, one lane for all of them.  A run's tokens
-        // past the sequence's end are in the page too; the mask leaves them out.
-        auto issue_tokens = [&](const volatile Part &part, int pos, int page) {
-            const uint32_t bar = barriers + fill * 8, dst = shared_address(ring + fill * S::kStageBytes);
-            const bool ok = (unsigned)page < (unsigned)p.c.n_pages;   // page is -1 where pos is
-            const bool leads = ok && (lane & (p.run - 1)) == 0;
-            const unsigned mask = __ballot_sync(~0u, ok), leaders = __ballot_sync(~0u, leads);
-            if (lane == 0) {
-                masks[fill] = mask;
-                barrier_expect(bar, __popc(leaders) * p.run * S::kRecord);
-            }
-            __syncwarp();
-            if (leads) {
-                const int in_page = pos - p.c.by_page(pos) * p.c.page_size;
-                copy_bulk(dst + lane * S::kRecord,
-                          part.head_pool + page * p.c.page_stride + (long long)in_page * S::kRecord,
-                          p.run * S::kRecord, bar);
-            }
-            fill = fill + 1 == S::kStages ? 0 : fill + 1;
-        };
-        // ---- runs: a lane looks up one of 32 whole runs ------------------
-        // Tile i is run(s) i << halves and the next; 32 runs are looked up at once.
-        constexpr int halves = kRun > 0 && kRun < S::kTile ? 1 : 0, per_look = 32 >> halves;
-        const unsigned char *run_src = nullptr;    // of the lane's run of those under way
-        unsigned tile_mask = 0;                    // of the run's tile
-        int run_page = -1;                         // of the lane's run of the next ones
-        auto run_pos = [&](int i0) {
-            return (int)(e0 + (i0 + (lane >> halves)) * (S::kWarps * S::kTile) + (lane & halves) * kRun);
-        };
-        auto run_page_of = [&](const volatile Part &part, int i0) -> int {
-            const int pos = run_pos(i0);
-            return i0 + (lane >> halves) < mine && (unsigned)pos < (unsigned)part.seen
-                       ? part.row_table[p.c.by_page(pos)] : -1;
-        };
-        auto next_runs = [&](const volatile Part &part, int i0) {
-            const int pos = run_pos(i0);
-            const bool ok = (unsigned)run_page < (unsigned)p.c.n_pages;
-            const int in_page = ok ? pos - p.c.by_page(pos) * p.c.page_size : 0;
-            run_src = ok ? part.head_pool + run_page * p.c.page_stride + (long long)in_page * S::kRecord
-                         : nullptr;
-            const int left = part.seen - pos;      // > 0 where there is a page
-            tile_mask = !ok ? 0u : ~0u >> (32 - (left < kRun ? left : kRun));
-            if (halves) {
-                tile_mask <<= (lane & 1) * 16;
-                tile_mask |= __shfl_xor_sync(~0u, tile_mask, 1);
-            }
-            run_page = run_page_of(part, i0 + per_look);
-        };
-        // tokens past the sequence's end are in the page too
-        auto issue_runs = [&](const volatile Part &part, int i) {
-            const int turn = i & (per_look - 1);
-            if (i > 0 && turn == 0)
-                next_runs(part, i);
-            const uint32_t bar = barriers + fill * 8;
-            if (lane == turn << halves) {
-                masks[fill] = tile_mask;
-                const int runs = !halves ? tile_mask != 0 : ((tile_mask & 0xffffu) != 0) + (tile_mask > 0xffffu);
-                barrier_expect(bar, runs * kRun * S::kRecord);
-            }
-            if (halves)
-                __syncwarp();
-            if (lane >> halves == turn && run_src)
-                copy_bulk(shared_address(ring + fill * S::kStageBytes) + (lane & halves) * kRun * S::kRecord,
-                          run_src, kRun * S::kRecord, bar);
-            fill = fill + 1 == S::kStages ? 0 : fill + 1;
-        };
-
-        // first copies and the queries, under way together; the ring held the
-        // last unit's results, which everybody has read by now
-        auto ring_is_free = [&] {
-            __syncthreads();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        };
-        int pos_next = -1, page_next = -1, pos_after = -1;
-        Queries<D, Rows> queries;
+        e0 = (unsigned)((tile0 + warp) * S::kTile);
+        fill = use = 0;
         if constexpr (kRun > 0) {
             run_page = run_page_of(now, 0);
             queries.load(p, unit);
-            ring_is_free();
             next_runs(now, 0);
 #pragma unroll
-            for (int s = 0; s < S::kStages - 1; ++s) {
+            for (int s = 0; s < S::kEarly; ++s)
                 if (s < mine)
                     issue_runs(now, s);
-            }
         } else {
-            int pos[S::kStages], page[S::kStages];
 #pragma unroll
             for (int s = 0; s < S::kStages; ++s)
-                pos[s] = position(now, s);
+                early_pos[s] = position(now, s);
 #pragma unroll
             for (int s = 0; s < S::kStages; ++s)
-                page[s] = page_of(now, pos[s]);
+                early_page[s] = page_of(now, early_pos[s]);
             queries.load(p, unit);
-            ring_is_free();
 #pragma unroll
-            for (int s = 0; s < S::kStages - 1; ++s) {
+            for (int s = 0; s < S::kEarly; ++s)
                 if (s < mine)
-                    issue_tokens(now, pos[s], page[s]);
-            }
-            pos_next = pos[S::kStages - 1];
-            page_next = page[S::kStages - 1];
+                    issue_tokens(now, early_pos[s], early_page[s]);
             pos_after = position(now, S::kStages);
         }
+        return true;
+    };
+    // The unit's query operands and its `Part`, where the last unit's are not
+    // needed any more.
+    auto announce = [&](int i) {
         queries.store(p, unit, len, smem);
-        if (threadIdx.x == 0) {
-            const bool last = u_in + 1 == p.units;
-            part.list = now.list, part.row_table = now.row_table;
-            part.head_pool = now.head_pool, part.seen = now.seen;
-            part.next = zero + tiles;
-            part.next_entry = entry + last;
-            part.next_unit = last ? 0 : u_in + 1;
-            part.active = count < S::kWarps ? (int)count : S::kWarps;
-            part.u.b = unit.b, part.u.head = unit.head, part.u.query = unit.query;
-            part.u.row0 = unit.row0, part.u.rows = unit.rows;
-            part.whole = count == tiles;
-            part.begins = tile0 == 0;
-            if (tile0 == 0 && count < tiles && !clustered) {
-                split->b = entry;
-                split->unit = u_in;
-                split->parts = (int)(divided(zero + tiles - 1, per) - blockIdx.x) + 1;
-            }
+        if (threadIdx.x != 0)
+            return;
+        volatile Part &part = part_of(i);
+        const bool last = u_in + 1 == p.units;
+        part.list = now.list, part.row_table = now.row_table;
+        part.head_pool = now.head_pool, part.seen = now.seen;
+        part.next = zero + tiles;
+        part.next_entry = entry + last;
+        part.next_unit = last ? 0 : u_in + 1;
+        part.active = count < S::kWarps ? (int)count : S::kWarps;
+        part.u.b = unit.b, part.u.head = unit.head, part.u.query = unit.query;
+        part.u.row0 = unit.row0, part.u.rows = unit.rows;
+        part.whole = count == tiles;
+        part.begins = tile0 == 0;
+        if (tile0 == 0 && count < tiles && !clustered) {
+            split->b = entry;
+            split->unit = u_in;
+            split->parts = (int)(divided(zero + tiles - 1, per) - blockIdx.x) + 1;
         }
-        __syncthreads();   // query operands and `part` are there
+    };
+
+    bool more = set_up();
+    if (!more)
+        return;
+    announce(slot);
+    __syncthreads();
+
+    while (true) {
+        // query operands and `part` are there, the last unit's results are read:
+        // the ring's tail can be filled too
+        volatile Part &part = part_of(slot);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+        for (int s = S::kEarly; s < S::kStages - 1; ++s)
+            if (s < mine) {
+                if constexpr (kRun > 0)
+                    issue_runs(part, s);
+                else
+                    issue_tokens(part, early_pos[s], early_page[s]);
+            }
+        if constexpr (kRun == 0)
+            pos_next = early_pos[S::kStages - 1], page_next = early_page[S::kStages - 1];
 
         // Output, and the state of the unit's two rows that this lane shares
         float o[S::kGroups][S::kSubs][4];
@@ -1033,17 +1079,16 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
 
             const unsigned mask = masks[use];
-            const bool came = barrier_wait(barriers + use * 8, phase);
+            const bool came = barrier_wait(barriers + use * 8, phases >> use & 1);
+            phases ^= 1u << use;
             const unsigned char *data = ring + use * S::kStageBytes;
-            if (++use == S::kStages)
-                use = 0, phase ^= 1;
+            use = use + 1 == S::kStages ? 0 : use + 1;
             if (!came) {
                 // the copies after it get as long to end
                 lost = true;
                 for (int left = min(S::kStages - 1, mine - 1 - i); left > 0; --left) {
-                    barrier_wait(barriers + use * 8, phase);
-                    if (++use == S::kStages)
-                        use = 0, phase ^= 1;
+                    barrier_wait(barriers + use * 8, phases >> use & 1);
+                    use = use + 1 == S::kStages ? 0 : use + 1;
                 }
                 break;
             }
@@ -1056,9 +1101,9 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         }
         __syncwarp();
 
-        // ---- the warps' results, side by side in the rings' place ----------
-        // (a warp without tiles has none)
         const int active = part.active;
+        // ---- the warps' results in their rings' tails (a warp without tiles
+        // has none) ----------------------------------------------------------
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (warp >= active)
@@ -1075,7 +1120,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             // narrow: rows of the instruction are channels 4 g + {0, 1} and
             // 4 g + {2, 3}; wide: columns 2 t, 2 t + 1 of instruction j are
             // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large.
-            float *dst = reinterpret_cast<float *>(ring) + r * S::kOutStride;
+            float *dst = reinterpret_cast<float *>(ring + S::kTail) + r * S::kOutStride;
 #pragma unroll
             for (int i = 0; i < S::kGroups; ++i) {
                 if constexpr (S::kWide) {
@@ -1091,7 +1136,15 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 }
             }
         }
+
+        // ---- the unit after this one, under way while the results are joined -
+        x = start = clustered ? end : part.next;
+        entry = part.next_entry;
+        u_in = part.next_unit;
+        more = set_up();
         __syncthreads();
+        if (more)
+            announce(slot ^ 1);
 
         Unit u;
         u.b = part.u.b, u.head = part.u.head, u.query = part.u.query;
@@ -1130,10 +1183,11 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             return f;
         };
         auto of_warps = [&](int r, int d) {
-            return add_up(std::integral_constant<int, S::kWarps>(), active, [&](int w) { return wmax(w, r); }, [&](int w) { return wsum(w, r); },
+            return add_up(std::integral_constant<int, S::kWarps>(), active, [&](int w) { return wmax(w, r); },
+                          [&](int w) { return wsum(w, r); },
                           [&](int w) {
                               return *reinterpret_cast<const float4 *>(
-                                  smem + w * S::kWarpBytes + (r * S::kOutStride + d) * 4);
+                                  smem + w * S::kWarpBytes + S::kTail + (r * S::kOutStride + d) * 4);
                           });
         };
         auto finish = [&](int r, int d, const Four &f) {
@@ -1180,7 +1234,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     if (r >= u.rows)
                         break;
                     auto of = [&](int i) { return cluster.map_shared_rank(mine, i); };
-                    finish(r, d, add_up(std::integral_constant<int, 8>(), p.cluster, [&](int i) { return of(i)[r]; },
+                    finish(r, d, add_up(std::integral_constant<int, 8>(), p.cluster,
+                                        [&](int i) { return of(i)[r]; },
                                         [&](int i) { return of(i)[S::kRows + r]; },
                                         [&](int i) {
                                             return *reinterpret_cast<const float4 *>(
@@ -1206,11 +1261,10 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 }
             }
         }
-        x = start = part.next;
-        entry = part.next_entry;
-        u_in = part.next_unit;
-        if (x >= end)
+        if (!more)
             break;
+        __syncthreads();
+        slot ^= 1;
     }
 }
 
