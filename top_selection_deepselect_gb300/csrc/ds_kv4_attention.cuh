@@ -852,9 +852,26 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
         auto consume = [&](auto masked_tag, const unsigned char *tile, unsigned mask, int base) {
             constexpr bool kMasked = decltype(masked_tag)::value;
-            auto seen_by = [&](int token, int r) -> bool {
-                return (mask >> token & 1) && (listed || base + token < limit[r]);
+            // which of the lane's (token, row) pairs count, a bit each
+            unsigned keep = 0;
+            auto token_of = [&](int m, int half, int e) {
+                return m * 16 + half * S::kNext + (!S::kWide ? tok_row : e & 1 ? tok_b : tok_a);
             };
+            if constexpr (kMasked) {
+                const int seen[2] = {listed ? 0x7fffffff : limit[row(0)] - base,
+                                     listed ? 0x7fffffff : limit[row(1)] - base};
+#pragma unroll
+                for (int m = 0; m < S::kMT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int e = 0; e < (S::kWide ? 4 : 2); ++e) {
+                            const int token = token_of(m, half, e), c = S::kWide ? e / 2 : e;
+                            if ((mask >> token & 1) && token < seen[c])
+                                keep |= 1u << ((m * 2 + half) * 4 + e);
+                        }
+            }
+            auto kept = [&](int m, int half, int e) { return keep >> ((m * 2 + half) * 4 + e) & 1; };
             if constexpr (!S::kWide) {
                 float sc[S::kMT][4], sa[S::kMT][S::kGroups], sb[S::kMT][S::kGroups];
 #pragma unroll
@@ -901,7 +918,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
+                        if (kMasked && !kept(mt, e / 2, e & 1))
                             sc[mt][e] = -INFINITY;
                         best[e & 1] = fmaxf(best[e & 1], sc[mt][e]);
                     }
@@ -915,7 +932,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         pr[e] = exp2_fast(sc[mt][e] * fac[e & 1] - low[e & 1]);
-                        if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
+                        if (kMasked && !kept(mt, e / 2, e & 1))
                             pr[e] = 0.f;
                         sum[e & 1] += pr[e];
                     }
@@ -939,7 +956,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             for (int e = 0; e < 4; ++e) {
                                 w[e] = pr[e] * (e < 2 ? sa[group] : sb[group]);
                                 // whatever the record holds
-                                if (kMasked && !seen_by(mt * 16 + tok_row + e / 2 * S::kNext, row(e & 1)))
+                                if (kMasked && !kept(mt, e / 2, e & 1))
                                     w[e] = 0.f;
                             }
                             const uint32_t b0 = transpose8x8(pack_half2(w[0], w[1]));
@@ -991,9 +1008,6 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         }
                     }
                 }
-                auto token = [&](int m, int half, int e) {
-                    return m * 16 + (e & 1 ? tok_b : tok_a) + half * S::kNext;
-                };
                 float best[2];
                 best[0] = best[1] = -INFINITY;
 #pragma unroll
@@ -1002,7 +1016,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                            if (kMasked && !kept(m, half, e))
                                 sc[m][half][e] = -INFINITY;
                             best[e / 2] = fmaxf(best[e / 2], sc[m][half][e]);
                         }
@@ -1014,7 +1028,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float pr = exp2_fast(sc[m][half][e] * fac[e / 2] - low[e / 2]);
-                            if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                            if (kMasked && !kept(m, half, e))
                                 pr = 0.f;
                             sum[e / 2] += pr;
                             sc[m][half][e] = pr;
@@ -1046,7 +1060,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     w[half][e] = sc[m][half][e] * vs[half * 2 + (e & 1)][group];
-                                    if (kMasked && !seen_by(token(m, half, e), row(e / 2)))
+                                    if (kMasked && !kept(m, half, e))
                                         w[half][e] = 0.f;
                                 }
                             pa[0] = pack_half2(w[0][0], w[0][1]);
