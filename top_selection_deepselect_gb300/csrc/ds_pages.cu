@@ -68,9 +68,13 @@ __device__ __forceinline__ void stretch(int n_pages, int warp, int *lo, int *hi)
     *hi = a + each < n_pages ? (int)(a + each) : n_pages;
 }
 
+// Loads of a warp that are under way at once when it sweeps its stretch.
+constexpr int kSweep = 8;
+
 __device__ int count_live(const int32_t *refs, int lo, int hi)
 {
     int n = 0;
+#pragma unroll 8
     for (int p = lo + (threadIdx.x & 31); p < hi; p += 32)
         n += refs[p] > 0;
     for (int step = 16; step; step /= 2)
@@ -89,13 +93,22 @@ __device__ int list_free(const int32_t *refs, int n_pages, int want, int32_t *li
     const int all = block_scan(lane == 0 ? mine : 0, &before);
     int at = __shfl_sync(~0u, before, 0);
     if (all >= want) {
-        for (int p = lo; p < hi && at < want; p += 32) {
-            const bool is_free = p + lane < hi && refs[p + lane] <= 0;
-            const unsigned m = __ballot_sync(~0u, is_free);
-            const int r = at + __popc(m & ((1u << lane) - 1));
-            if (is_free && r < want)
-                list[r] = p + lane;
-            at += __popc(m);
+        for (int p0 = lo; p0 < hi && at < want; p0 += 32 * kSweep) {
+            int held[kSweep];
+#pragma unroll
+            for (int k = 0; k < kSweep; ++k) {
+                const int p = p0 + 32 * k + lane;
+                held[k] = p < hi ? refs[p] : 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kSweep; ++k) {
+                const bool is_free = held[k] <= 0;
+                const unsigned m = __ballot_sync(~0u, is_free);
+                const int r = at + __popc(m & ((1u << lane) - 1));
+                if (is_free && r < want)
+                    list[r] = p0 + 32 * k + lane;
+                at += __popc(m);
+            }
         }
     }
     __syncthreads();
@@ -375,20 +388,27 @@ compact_plan_kernel(Book book, int32_t *remap, int32_t *status, int32_t *holes, 
     }
     __syncthreads();
     const int moves = live - live_below;
-    for (int p0 = lo, at = before; p0 < hi; p0 += 32) {
-        const int p = p0 + lane;
-        const bool is_live = p < hi && book.refs[p] > 0;
-        const unsigned m = __ballot_sync(~0u, is_live);
-        const int r = at + __popc(m & ((1u << lane) - 1));  // live pages below p
-        at += __popc(m);
-        if (p >= hi)
-            continue;
-        if (is_live && p >= live)
-            movers[r - live_below] = p;
-        else
-            remap[p] = is_live ? p : -1;
-        if (!is_live && p < live)
-            holes[p - r] = p;
+    for (int p0 = lo, at = before; p0 < hi; p0 += 32 * kSweep) {
+        int held[kSweep];
+#pragma unroll
+        for (int k = 0; k < kSweep; ++k) {
+            const int p = p0 + 32 * k + lane;
+            held[k] = p < hi ? book.refs[p] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kSweep; ++k) {
+            const int p = p0 + 32 * k + lane;
+            const bool is_live = held[k] > 0;
+            const unsigned m = __ballot_sync(~0u, is_live);
+            const int r = at + __popc(m & ((1u << lane) - 1));  // live pages below p
+            at += __popc(m);
+            if (is_live && p >= live)
+                movers[r - live_below] = p;
+            else if (p < hi)
+                remap[p] = is_live ? p : -1;
+            if (!is_live && p < hi && p < live)
+                holes[p - r] = p;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < moves; i += kThreads)
