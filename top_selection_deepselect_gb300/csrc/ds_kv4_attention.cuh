@@ -69,7 +69,9 @@ struct Shape {
     static constexpr int kStageBytes = kTile * kRecord;
     static constexpr int kOutRegs = kGroups * kSubs * 4;
     // Warps of a CTA and CTAs of an SM, by what the output leaves of the
-    // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.
+    // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.  (16 warps
+    // in one CTA: 64 x 32768 tokens the same 403 us, 256 x 200 tokens 63 for 41,
+    // because nothing else runs while a unit ends.)
     static constexpr int kWarps = kOutRegs == 64 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
@@ -315,9 +317,9 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
 // The line of work: each unit takes kUnitCost places and one for each of its
 // tiles.  A unit's start and end (its queries, the first copies' latency, the
 // meeting of the warps) cost a CTA as much as some tiles do; without these
-// places the CTA that met 24 empty sequences in a row took four times as long
-// as the others (37 ragged sequences of 5 drafts: 119 us; with 12, 18, 24 and 32
-// places 41, 39, 37 and 37; 16 x 16384 tokens 68, 68, 66 and 68).
+// places the CTA that meets 24 empty sequences in a row takes three times as long
+// as the others (37 ragged sequences of 5 drafts: 80 us; with 12, 18, 24, 32 and 40
+// places 35, 33, 33, 33 and 35; 16 x 16384 tokens 68 with any of them).
 constexpr int kUnitCost = 24;
 
 // Quotient of numbers that are not negative, in 32 bits where that is enough.
@@ -1359,17 +1361,18 @@ join_kernel(const __grid_constant__ AttendArgs p)
 
 // ---- host ----------------------------------------------------------------------
 // Query rows of a unit: 8, or 16 where there are more.  Further rows are further
-// units.  Units of 32 rows expand a record once instead of twice, but their
+// units.  Units of 32 rows would expand a record once instead of twice, but their
 // outputs leave 8 warps an SM that cannot hide each other's waits (32 rows, 16 x
-// 16384 tokens: 197 us in one unit, 186 in two; 80 rows, 4 x 65536: 94 and 72).
+// 16384 tokens: 197 us in one unit where two took 186, which take 174 now; 80
+// rows, 4 x 65536: 94 and 72, now 68).
 inline int unit_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 // How a call is laid out: sizes of its units, its CTAs, and whether units are
 // cut between CTAs.  They are not, and the join is saved, where a unit is at
 // most two tiles a warp, and where tokens are listed, so that all units are of
 // one known size, and whole ones keep at least half of one wave of CTAs or four
-// fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 20.5
-// instead of 26.6 us; 64 units of 2048 tokens for 304 CTAs: 22.5 cut, 30.7 whole).
+// fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 18.4
+// instead of 24.6 us; 64 units of 2048 tokens for 304 CTAs: 22.5 cut, 28.7 whole).
 template <int D, int Rows>
 int lay_out(AttendArgs &p, int sms)
 {

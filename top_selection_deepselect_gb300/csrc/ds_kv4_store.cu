@@ -263,8 +263,8 @@ read_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *seq,
 // Launch shape: heads that a lane takes one after another (1, 2 or 4, a divisor
 // of kv_heads).  More than one saves looking the token up again, but only where
 // the rest still fills the GPU (kFill threads): 28693 tokens of 8 heads of 128
-// are appended and read in 61 us with four heads, in 68 us with two and in 86 us
-// with one; 64 tokens in 16 us with four and in 10 us with one.
+// are appended and read in 61 us with four heads, in 66 us with two and in 80 us
+// with one; 64 tokens in 14 us with four and in 10 us with one.
 constexpr long long kFill = 1 << 19;
 
 struct Launch {

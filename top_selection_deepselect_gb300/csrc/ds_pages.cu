@@ -22,7 +22,7 @@ using Book = ds_page_book_t;
 constexpr int kThreads = 1024;      // bookkeeping CTA
 constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
-constexpr int kLoads = 4;  // 16-byte loads of a thread under way (2: 28.0 us for 500 pages, 4 and 8: 24.4)
+constexpr int kLoads = 4;  // 16-byte loads of a thread under way (2: 28.7 us for 500 pages, 4 and 8: 22.5)
 constexpr int kChunk = kMoveThreads * 16 * kLoads;  // bytes a CTA moves at a time, at most
 
 __device__ __forceinline__ int pages_of(const Book &b, int length)
@@ -512,8 +512,8 @@ int check_work(const void *ws, size_t bytes, size_t need)
 
 // CTAs that move pages: no more than there are chunks, and many more than fit at
 // once, so that SMs nearer to their memory take more of them (500 pages of 37 KB
-// in four layers: 25.5 us with 8 a SM, 24.2 with 64, 24.3 with 1024; a compaction,
-// whose moves the host only knows a bound of: 183, 174 and 221).
+// in four layers: 22.5 us with 8, 64 and 1024 a SM; a compaction of 8192, whose
+// moves the host only knows a bound of: 175, 169 and 216).
 int move_grid(long long items, unsigned *grid)
 {
     int dev = 0, sms = 0;
