@@ -138,7 +138,8 @@ typedef struct {
     int32_t n_pages;
 } ds_page_pool_t;
 
-/* Who holds which page: refs[p] = sequences that hold page p (0: free). */
+/* Who holds which page: refs[p] = sequences that hold page p (0: free).  Pages
+ * and the entries of a list are 2^30 at most. */
 typedef struct {
     int32_t *table;       /* [max_seqs][table_stride], -1 where a sequence has no page */
     int64_t table_stride;

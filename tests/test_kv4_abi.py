@@ -156,6 +156,21 @@ def test_book_checks(lib, kw):
         assert status_of(ds.ds_pages_compact, pool(), b, FAKE, FAKE, FAKE, 4096, None) == EINVAL
 
 
+def test_more_pages_or_entries_than_are_counted_in_32_bits(lib):
+    most, big = 1 << 30, 1 << 60
+    for n in (most + 1, 2 ** 31 - 1):
+        for rc in (status_of(ds.ds_pages_reserve, book(n_pages=n), FAKE, FAKE, 1, FAKE, FAKE, big, None),
+                   status_of(ds.ds_pages_reserve, book(), FAKE, FAKE, n, FAKE, FAKE, big, None),
+                   status_of(ds.ds_pages_fork, pool(n_pages=n), book(n_pages=n), FAKE, FAKE, 1, FAKE, FAKE,
+                             big, None),
+                   status_of(ds.ds_pages_fork, pool(), book(), FAKE, FAKE, n, FAKE, FAKE, big, None),
+                   status_of(ds.ds_pages_free, book(), FAKE, n, None),
+                   status_of(ds.ds_pages_copy, pool(), FAKE, FAKE, n, None),
+                   status_of(ds.ds_pages_compact, pool(n_pages=n), book(n_pages=n), FAKE, FAKE, FAKE, big,
+                             None)):
+            assert rc == EUNSUP
+
+
 def test_page_list_and_workspace_checks(lib):
     need = ds.ds_pages_workspace(4, 2)
     assert ds.ds_pages_workspace(4, 0) > 0

@@ -446,6 +446,10 @@ compact_kernel(Pool pool, Book book, const int32_t *remap, const int32_t *status
 }
 
 // ---- host ---------------------------------------------------------------------
+// Most pages and list entries, so that sweeps that step past the end, by up to
+// kThreads or 32 kSweep, stay in 32 bits.
+constexpr int kMost = 1 << 30;
+
 int check_pool(const Pool *p)
 {
     if (!p)
@@ -475,6 +479,8 @@ int check_book(const Book *b, bool lengths)
         return fail(DS_EINVAL,
                     "max_seqs = %d, max_pages = %d, n_pages = %d and page_size = %d must all be >= 1",
                     b->max_seqs, b->max_pages, b->n_pages, b->page_size);
+    if (b->n_pages > kMost)
+        return fail(DS_EUNSUPPORTED, "n_pages = %d is above 2^30", b->n_pages);
     if ((long long)b->max_pages * b->page_size >= 1LL << 31)
         return fail(DS_EINVAL, "max_pages * page_size = %lld is not below 2^31",
                     (long long)b->max_pages * b->page_size);
@@ -497,6 +503,8 @@ int check_list(int n, bool given)
 {
     if (n < 0)
         return fail(DS_EINVAL, "n = %d is negative", n);
+    if (n > kMost)
+        return fail(DS_EUNSUPPORTED, "n = %d is above 2^30", n);
     if (n > 0 && !given)
         return fail(DS_EINVAL, "the lists must be non-NULL when n > 0");
     return DS_OK;
