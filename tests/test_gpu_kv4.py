@@ -151,6 +151,33 @@ def test_append_of_special_values(ds):
     assert np.array_equal(v.cpu().numpy(), rv.astype(np.float32), equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_ties_and_their_neighbours(ds, dtype):
+    """Channels at and next to (n + 1/2) * scale, for every significand of a scale and exponents
+    from subnormal scales to the largest; values beyond all scales."""
+    step = (np.arange(1024, 2048)[:, None] * 2.0 ** np.array([-34, -25, -12, 0, 3])).reshape(-1)
+    ties = np.concatenate([np.arange(-7, 7) + 0.5, [7.0, -7.0]])
+    x = (step[:, None] * ties).astype(np.float32)
+    t = torch.from_numpy(x).to(DTYPES[dtype])
+    up, down = (torch.nextafter(t, torch.full_like(t, side)) for side in (np.inf, -np.inf))
+    t = torch.stack([t, t, up, down, t, up], 1).reshape(-1, 3, 32)
+    t[:, 1:, 30] = t[:, :1, 30]            # groups of one scale, where the neighbours' is not larger
+    big = torch.finfo(DTYPES[dtype]).max
+    t = torch.cat([t.reshape(-1, 32), torch.linspace(-1, 1, 32)[None].to(t.dtype) * big,
+                   torch.full((1, 32), -big, dtype=t.dtype)])
+    x = t[:len(t) // 4 * 4].reshape(-1, 1, 128).to(DEV)
+    tail = t[-4:].reshape(1, 1, 128).to(DEV)
+    k = torch.cat([x, tail])
+    v = k.flip(0)
+    tokens = len(k)
+    pool = torch.zeros((-(-tokens // 64), 1, 64, 144), dtype=torch.uint8, device=DEV)
+    table = dev(np.arange(len(pool), dtype=np.int32)[None])
+    seq, pos = dev(np.zeros(tokens, np.int32)), dev(np.arange(tokens, dtype=np.int32))
+    ds.kv4_append(pool, table, seq, pos, k, v)
+    want = model.encode(k.float().cpu().numpy(), v.float().cpu().numpy())
+    assert np.array_equal(pool.cpu().numpy().reshape(-1, 144)[:tokens], want[:, 0])
+
+
 def test_tokens_that_are_not_there(ds):
     """Out-of-range sequences, positions and pages: nothing is written, zeros are read."""
     table = np.array([[0, -1, 5], [2, 1, -7]], dtype=np.int32)   # 3 pages in the pool

@@ -3,7 +3,8 @@
 // One lane holds eight channels of one token's key and the same of its value (16
 // bytes each of a 16-bit type), so a vector of D channels takes D/8 neighbouring
 // lanes and a group of 32 channels four of them: the group's largest magnitude
-// is two shuffles away, and the reordering inside the record is a shuffle too,
+// is two shuffles away (one for both the key's and the value's, whose scales are
+// worked out in turn by neighbouring lanes), and the reordering inside the record is a shuffle too,
 // so that codes leave and arrive as whole words.  Both kernels move each byte
 // once and are bound by the bytes only while a lane's eight channels cost few
 // instructions: magnitudes are compared as bits, quotients and integers come
@@ -87,17 +88,16 @@ __device__ __forceinline__ Eight<T> load_eight(const T *src)
     return e;
 }
 
-// Largest magnitude of the group of four lanes, as the bits of a float: the
-// bits of magnitudes are in their order, those that are not finite above all
-// others, in 16-bit types two at a time.
+// Largest magnitude of a lane's eight channels, as the bits of a float: the bits
+// of magnitudes are in their order, those that are not finite above all others,
+// in 16-bit types two at a time.
 __device__ __forceinline__ unsigned largest(const Eight<float> &e)
 {
     unsigned most = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         most = max(most, __float_as_uint(e.x[j]) & 0x7fffffffu);
-    most = max(most, __shfl_xor_sync(~0u, most, 1));
-    return max(most, __shfl_xor_sync(~0u, most, 2));
+    return most;
 }
 
 template <typename T>
@@ -108,45 +108,88 @@ __device__ __forceinline__ unsigned largest(const Eight<T> &e)
 #pragma unroll
     for (int j = 1; j < 4; ++j)
         most = __vmaxu2(most, w[j] & 0x7fff7fffu);
-    most = __vmaxu2(most, __shfl_xor_sync(~0u, most, 1));
-    most = __vmaxu2(most, __shfl_xor_sync(~0u, most, 2));
     const unsigned short top = (unsigned short)max(most & 0xffffu, most >> 16);
     return __float_as_uint(to_float(*reinterpret_cast<const T *>(&top)));
 }
 
-// Codes of the lane's eight channels, and the bits of their group's scale.
-template <typename T>
-__device__ __forceinline__ unsigned encode(const Eight<T> &e, unsigned *bits)
+// Scale of a group: its bits, what codes are made with (0 where the codes are
+// all 8) and the nearest float to 1 / step.
+struct Scale {
+    unsigned bits;
+    float inv;
+};
+
+__device__ __forceinline__ float step_of(unsigned bits)
 {
-    const unsigned most = largest(e);
-    const bool bad = most >= 0x7f800000u;      // a NaN or an infinity poisons the group
+    return __half2float(__ushort_as_half((unsigned short)bits));
+}
+
+__device__ __forceinline__ Scale scale_of(unsigned most)
+{
     __half scale = __float2half_rn(__uint_as_float(most) * (1.f / 7.f));
     if (__hisinf(scale))
         scale = __ushort_as_half(0x7bff);
-    const float step = __half2float(scale);
-    const float inv = __frcp_rn(step);
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        q[j] = quotient(to_float(e.x[j]), step, inv);
-    // subnormal and largest scales: quotients may be beyond 7 (rare, so a branch)
-    if (__any_sync(~0u, step < 6.103515625e-05f || step == 65504.f)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q[j] = fminf(fmaxf(q[j], -7.f), 7.f);
-    }
+    const bool bad = most >= 0x7f800000u;      // a NaN or an infinity poisons the group
+    return {bad ? 0x7fffu : __half_as_ushort(scale), __frcp_rn(__half2float(scale))};
+}
+
+// Bits of the floats round(round(x[i] f + a) + b), a pair in one instruction each.
+__device__ __forceinline__ void multiply_add_add(float x0, float x1, float f, float a, float b,
+                                                 unsigned *y0, unsigned *y1)
+{
+    asm("{\n\t"
+        ".reg .b64 x, f, a, b;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 f, {%4, %4};\n\t"
+        "mov.b64 a, {%5, %5};\n\t"
+        "mov.b64 b, {%6, %6};\n\t"
+        "fma.rn.f32x2 x, x, f, a;\n\t"
+        "add.rn.f32x2 x, x, b;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t"
+        "}"
+        : "=r"(*y0), "=r"(*y1)
+        : "f"(x0), "f"(x1), "f"(f), "f"(a), "f"(b));
+}
+
+// Codes of the lane's eight channels.  wide: some quotient of the warp's may be
+// beyond 7.
+template <typename T>
+__device__ __forceinline__ unsigned encode(const Eight<T> &e, const Scale &s, bool wide)
+{
     // the float q + 12582920 (1.5 2^23 + 8) holds rint(q) + 8 in its low bits,
     // above a constant that the sum takes away once for all eight
     unsigned word = 0;
+    if (sizeof(T) == 2 && !wide) {
+        // q to the nearest multiple of 2^-13 first, by adding 1536.  With 11
+        // significant bits in x and in the scale a quotient that is no tie is
+        // 2^-12.2 away from one at least, so that it stays on its side, and a
+        // tie, whose product may be a little off, is met exactly: the integer
+        // is the rounded quotient's, and the correction is saved.
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        word += __float_as_uint(q[j] + 12582920.f) << (4 * j);
-    *bits = bad ? 0x7fffu : __half_as_ushort(scale);
-    return bad || step == 0.f ? 0x88888888u : word - 0x3f400000u;
+        for (int j = 0; j < 8; j += 2) {
+            unsigned lo, hi;
+            multiply_add_add(to_float(e.x[j]), to_float(e.x[j + 1]), s.inv, 1536.f, 12581384.f, &lo, &hi);
+            word += (lo << (4 * j)) + (hi << (4 * j + 4));
+        }
+    } else {
+        const float step = step_of(s.bits);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float q = quotient(to_float(e.x[j]), step, s.inv);
+            if (wide)
+                q = fminf(fmaxf(q, -7.f), 7.f);
+            word += __float_as_uint(q + 12582920.f) << (4 * j);
+        }
+    }
+    return s.bits == 0 || s.bits == 0x7fffu ? 0x88888888u : word - 0x3f400000u;
 }
 
-// Six CTAs an SM: 63.5 -> 61.4 us for the prefill below (five, the registers'
-// own choice; seven and eight spill).
+// 31.9 us for 28693 tokens of 8 heads of 128 in bf16 (150 MB, 4.7 TB/s), 43.9 in
+// fp32 (268 MB, 6.1 TB/s): in 16-bit types the bound is instructions, some 220 for a
+// lane's 16 channels.  A pair a multiply-add 32.8 -> 31.9, scales shared out and no
+// correction 35.1 -> 32.8; six CTAs an SM (five 33.4; seven and eight spill, 33.1);
+// the next head's loads ahead of this one's codes, or two heads at once, are slower
+// (39.9, 34.5).
 template <typename T, int D, bool kVec>
 __global__ void __launch_bounds__(kThreads, 6)
 append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *seq,
@@ -174,13 +217,25 @@ append_kernel(Cache c, Divider by_runs, int each, int runs, const int32_t *seq,
     const unsigned pick = g & 1 ? 0x7632 : 0x5410;
     // the word of scales that this lane writes, if any: key scales by the first
     // lane of two groups, value scales by the second
-    const bool scales = at.w % 4 == 0;
+    const bool scales = at.w % 4 == 0, right = lane & 1;
 
 #pragma unroll 1
     for (int h = 0; h < each; ++h) {
         const Eight<T> x = load_eight<T, kVec>(k), y = load_eight<T, kVec>(v);
-        unsigned kbits, vbits;
-        const unsigned kc = encode(x, &kbits), vc = encode(y, &vbits);
+        // the group's four lanes: even ones find the key's scale, odd ones the
+        // value's, and neighbours exchange them
+        const unsigned kmost = largest(x), vmost = largest(y);
+        const unsigned given = __shfl_xor_sync(~0u, right ? kmost : vmost, 1);
+        unsigned most = max(right ? vmost : kmost, given);
+        most = max(most, __shfl_xor_sync(~0u, most, 2));
+        const Scale mine = scale_of(most);
+        const Scale its = {__shfl_xor_sync(~0u, mine.bits, 1), __shfl_xor_sync(~0u, mine.inv, 1)};
+        const Scale ks = right ? its : mine, vs = right ? mine : its;
+        // subnormal and largest scales: quotients may be beyond 7 (rare, so a
+        // branch)
+        const bool wide = __any_sync(~0u, mine.bits < 0x400u || mine.bits >= 0x7bffu);
+        const unsigned kbits = ks.bits, vbits = vs.bits;
+        const unsigned kc = encode(x, ks, wide), vc = encode(y, vs, wide);
         const unsigned kw = __shfl_sync(~0u, kc, from_k);
         const unsigned lo = __shfl_sync(~0u, vc, from_v), hi = __shfl_sync(~0u, vc, from_v + 4);
         // groups 2 i and 2 i + 1 are four lanes apart: the even one gets both
