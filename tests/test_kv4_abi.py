@@ -171,6 +171,13 @@ def test_more_pages_or_entries_than_are_counted_in_32_bits(lib):
             assert rc == EUNSUP
 
 
+def test_workspace_bytes_of_the_wrappers(lib):
+    from top_selection_deepselect_gb300 import _kv4
+    for n_pages in (1, 7, 8192, 1 << 30):
+        for n in (0, 1, 1000, 1 << 30):
+            assert _kv4._pages_bytes(n_pages, n) == ds.ds_pages_workspace(n_pages, n)
+
+
 def test_page_list_and_workspace_checks(lib):
     need = ds.ds_pages_workspace(4, 2)
     assert ds.ds_pages_workspace(4, 0) > 0

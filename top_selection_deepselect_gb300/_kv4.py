@@ -455,6 +455,11 @@ def _status(status, table, index):
     return status
 
 
+def _pages_bytes(n_pages, n):
+    """What ds_pages_workspace answers, without the call."""
+    return 4 * (2 * n_pages + 2 * n + 4)
+
+
 def _work(t, index, raw, need, workspace):
     """(workspace, its bytes); called under _order."""
     if workspace is None:
@@ -490,7 +495,7 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     book = _book(table, lengths, refs, page_size, index)
     status = _status(status, table, index)
     seqs_at, tokens_at = _int32("seqs", seqs, index, n), _int32("tokens", tokens, index, n)
-    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(index)
+    need, raw = _pages_bytes(refs.numel(), n), t.raw_stream(index)
     with _order:
         workspace, size = _work(t, index, raw, need, workspace)
         rc = t.reserve(book, seqs_at, tokens_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
@@ -515,7 +520,7 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     book = _book(table, lengths, refs, pool.shape[3], index)
     at, status = _pool(pool, index), _status(status, table, index)
     src_at, dst_at = _int32("src", src, index, n), _int32("dst", dst, index, n)
-    need, raw = ds_pages_workspace(refs.numel(), n), t.raw_stream(index)
+    need, raw = _pages_bytes(refs.numel(), n), t.raw_stream(index)
     with _order:
         workspace, size = _work(t, index, raw, need, workspace)
         rc = t.fork(at, book, src_at, dst_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
@@ -553,7 +558,7 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
         remap = t.empty_like(refs)
     at, status = _pool(pool, index), _status(status, table, index)
     remap_at = _int32("remap", remap, index, n_pages)
-    need, raw = ds_pages_workspace(n_pages, 0), t.raw_stream(index)
+    need, raw = _pages_bytes(n_pages, 0), t.raw_stream(index)
     with _order:
         workspace, size = _work(t, index, raw, need, workspace)
         rc = t.compact(at, book, remap_at, status.data_ptr(), workspace.data_ptr(), size, raw)
