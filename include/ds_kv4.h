@@ -112,7 +112,10 @@ int ds_kv4_read(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t *
  *             exp(scale * q k), or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_attention_workspace bytes
  *             (NULL when that is 0)
- * A query that sees no token gives out = 0 and lse = -inf.  (A copy into shared
+ * A query that sees no token gives out = 0 and lse = -inf.  A probability times
+ * a value scale is rounded to 11 significant bits (below 2^-28 of the largest of
+ * each in its group of channels it is within 2^-39 of that); scores, maxima, sums
+ * and outputs are held in 32 bits until they are rounded to `dtype`.  (A copy into shared
  * memory that does not end within a second, which no working GPU does, is given
  * up, and what depends on it is NaN.)
  */

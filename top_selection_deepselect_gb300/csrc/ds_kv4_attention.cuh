@@ -25,12 +25,16 @@
 // which is twice the products from the same expanded codes, and P comes out as it
 // goes in.  Either way the sum over each group of 32 channels is multiplied by the key
 // scale of (token, group) in 32 bits, and the probabilities carry the value
-// scale: fp16(p * scale), the only rounding of the inner loop.  2^-11 relative on
-// each token's share, less than the output's own rounding; 32-bit operands
-// would halve the rate of the matrix instructions.  Denominators are summed in
-// 32 bits from unrounded p.  Instructions on 64 and more rows (tcgen05) would
-// leave most of them empty and need the operands written back to shared memory
-// after the expansion.
+// scale, fp16(p * scale), the only rounding of the inner loop; 32-bit operands
+// would halve the rate of the matrix instructions.  Scales reach from 2^-24 to
+// 2^16, so a power of two goes with each weight: p is taken 2^23 times, and
+// each warp lifts the scales of a group so that the largest it has met comes to
+// lie in [2^-9, 2^-8).  Weights are then below 2^15 and keep 11 significant bits,
+// 2^-11 relative, while p * scale is above 2^-28 of the group's largest scale
+// (times the largest p); below, they are off by 2^-39 of it at most.  Lifts only
+// fall while a warp goes through a unit; the output is brought down with them,
+// and they are taken back at the unit's end.  Denominators are summed in 32 bits
+// from unrounded p.
 //
 // Work is cut into tiles of kTile tokens; all tiles of all (sequence, head)
 // units stand in one line that is divided evenly among the CTAs, whatever the
@@ -96,7 +100,12 @@ struct Shape {
     static constexpr int kOffMask = kOffBarrier + kWarps * kStages * 8;
     static constexpr int kOffScan = (kOffMask + kWarps * kStages * 4 + 15) / 16 * 16;
     static constexpr int kOffPart = kOffScan + 16 * 8;
-    static constexpr int kSmem = kOffPart + 2 * 128;
+    // a warp's value scales, two groups a word: the largest that its lifts are
+    // good for, and the lifts
+    static constexpr int kOffBound = kOffPart + 2 * 128;
+    static constexpr int kOffLift = kOffBound + kWarps * kGroups * 2;
+    static constexpr int kSmem = kOffLift + kWarps * kGroups * 2;
+    static_assert(kSmem <= (kCtas == 2 ? 115712 : 232448), "shared memory of an SM");
     static constexpr int kPartial = kRows * (D + 2);                    // floats of a partial result
 
     // Order of the 16 tokens of a step in the operands: places 2 t and 2 t + 1
@@ -221,6 +230,20 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w)
     return y;
 }
 
+// Lift of a group whose largest value scale has the bits `most` (a float, not 0):
+// the power of two that brings it to [2^-9, 2^-8), in fp16; weights are made of
+// probabilities times kRaise.  What that makes the output too large by, inverted.
+constexpr float kRaise = 0x1p23f;
+__device__ __forceinline__ unsigned lift_of(unsigned most)
+{
+    return __half_as_ushort(__float2half_rn(__uint_as_float((245u - (most >> 23)) << 23)));
+}
+__device__ __forceinline__ float lift_back(unsigned lift)
+{
+    const float f = __half2float(__ushort_as_half((unsigned short)lift));
+    return __uint_as_float((254u << 23) - __float_as_uint(f)) * (1.f / kRaise);
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
 {
     uint32_t y;
@@ -242,6 +265,14 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const unsigned char
     }
 }
 
+template <int N>
+__device__ __forceinline__ void store_words(unsigned char *p, const uint32_t (&w)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        reinterpret_cast<uint32_t *>(p)[i] = w[i];
+}
+
 template <typename T>
 __device__ __forceinline__ void store_four(T *dst, const float4 &v, float factor)
 {
@@ -249,6 +280,25 @@ __device__ __forceinline__ void store_four(T *dst, const float4 &v, float factor
     from_float(y[0], v.x * factor), from_float(y[1], v.y * factor);
     from_float(y[2], v.z * factor), from_float(y[3], v.w * factor);
     *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
+}
+
+// Scales of G groups, each times its lift, as floats: the product of two fp16
+// numbers is exact there.
+template <int G>
+__device__ __forceinline__ void load_lifted(float (&s)[G], const unsigned char *p,
+                                            const uint32_t (&lift)[G / 2])
+{
+    uint32_t w[G / 2];
+    load_words(w, p);
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i)
+        asm("{\n\t.reg .b16 x, y, f, g;\n\t"
+            "mov.b32 {x, y}, %2;\n\t"
+            "mov.b32 {f, g}, %3;\n\t"
+            "fma.rn.f32.f16 %0, x, f, %4;\n\t"
+            "fma.rn.f32.f16 %1, y, g, %4;\n\t}"
+            : "=f"(s[2 * i]), "=f"(s[2 * i + 1])
+            : "r"(w[i]), "r"(lift[i]), "f"(-0.f));
 }
 
 // Scales of G groups as floats.
@@ -524,6 +574,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     unsigned *masks = reinterpret_cast<unsigned *>(smem + S::kOffMask) + warp * S::kStages;
     const float *factor = reinterpret_cast<const float *>(smem + S::kOffFactor);
     const int *limit = reinterpret_cast<const int *>(smem + S::kOffLimit);
+    unsigned char *bounds = smem + S::kOffBound + warp * S::kGroups * 2;
+    unsigned char *lifts = smem + S::kOffLift + warp * S::kGroups * 2;
     // maximum (later weight) and sum of row r of warp w's result
     auto wmax = [&](int w, int r) -> float & {
         return *reinterpret_cast<float *>(smem + w * S::kWarpBytes + S::kOffMax + r * 4);
@@ -814,6 +866,10 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     o[i][s][e] = 0.f;
+        if (lane < S::kGroups / 2) {
+            reinterpret_cast<uint32_t *>(bounds)[lane] = 0;
+            reinterpret_cast<uint32_t *>(lifts)[lane] = 0x78007800;     // as of the smallest scale
+        }
 
         // largest of the lanes that share a row
         auto row_max = [&](float v) {
@@ -824,11 +880,63 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         };
         // state of accumulator register e: columns 2 t, 2 t + 1 of rows g, g + 8
         auto state = [](int e) { return S::kWide ? e / 2 : e & 1; };
-        // New maxima `best` of the lane's scores.  One is rare after the first
-        // tiles: only then the rows' maxima are joined and the sums brought down.
-        auto raise = [&](const float (&best)[2]) {
-            if (!__any_sync(~0u, best[0] > top[0] || best[1] > top[1]))
+        // Whether a value scale of this lane's token is beyond what the lifts are good
+        // for.
+        auto beyond = [&](const uint32_t (&w)[S::kGroups / 2]) {
+            uint32_t b[S::kGroups / 2];
+            load_words(b, bounds);
+            bool fits = true;       // a NaN fits any lift
+#pragma unroll
+            for (int i = 0; i < S::kGroups / 2; ++i)
+                fits = fits && __hbleu2(*reinterpret_cast<const __half2 *>(&w[i]),
+                                        *reinterpret_cast<const __half2 *>(&b[i]));
+            return !fits;
+        };
+        // New lifts for value scales w of the lanes' tokens, those that count, and the
+        // output brought down to them.
+        auto lower = [&](const uint32_t (&w)[S::kGroups / 2], bool in) {
+            uint32_t b[S::kGroups / 2], bound[S::kGroups / 2] = {}, lift[S::kGroups / 2] = {};
+            unsigned most[S::kGroups];
+            load_words(b, bounds);
+            // (no lift is made for a NaN)
+#pragma unroll
+            for (int i = 0; i < S::kGroups; ++i) {
+                const unsigned s = w[i / 2] >> (i % 2 * 16) & 0xffffu;
+                most[i] = __reduce_max_sync(~0u, in && s <= 0x7bffu ? s : 0u);
+            }
+            auto bits = [](unsigned h) {
+                return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+            };
+#pragma unroll
+            for (int i = 0; i < S::kGroups; ++i) {
+                const unsigned old = max(b[i / 2] >> (i % 2 * 16) & 0xffffu, 1u), now = max(most[i], old);
+                const float down = __uint_as_float((127u + (bits(old) >> 23) - (bits(now) >> 23)) << 23);
+#pragma unroll
+                for (int k = 0; k < S::kSubs; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[i][k][e] *= down;
+                // good for every scale of the same exponent
+                const unsigned same = now < 0x400u ? (1u << (31 - __clz(now))) - 1 : 0x3ffu;
+                bound[i / 2] |= (now | same) << (i % 2 * 16);
+                lift[i / 2] |= lift_of(bits(now)) << (i % 2 * 16);
+            }
+            __syncwarp();       // every lane has read the bounds
+            if (lane == 0) {
+                store_words(bounds, bound);
+                store_words(lifts, lift);
+            }
+            __syncwarp();
+        };
+        // New maxima `best` of the lane's scores, or a value scale beyond the lifts.
+        // Either is rare after the first tiles: only then the rows' maxima are joined
+        // and the sums brought down.  (Looking for the latter and lifting costs 64 x
+        // 32768 tokens 403 -> 421 us.)
+        auto raise = [&](const float (&best)[2], bool grow, const uint32_t (&w)[S::kGroups / 2], bool in) {
+            if (!__any_sync(~0u, best[0] > top[0] || best[1] > top[1] || grow))
                 return;
+            if (__any_sync(~0u, grow))
+                lower(w, in);
             float down[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -874,6 +982,13 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                         }
             }
             auto kept = [&](int m, int half, int e) { return keep >> ((m * 2 + half) * 4 + e) & 1; };
+            // a token each for the lanes: its value scales (the last row sees most tokens)
+            const int token = lane % S::kTile;
+            const bool in = !kMasked || ((mask >> token & 1) &&
+                                         (listed || base + token < limit[part.u.rows - 1]));
+            uint32_t scales[S::kGroups / 2], lift[S::kGroups / 2];
+            load_words(scales, tile + token * S::kRecord + D + 2 * S::kGroups);
+            const bool grow = in && beyond(scales);
             if constexpr (!S::kWide) {
                 float sc[S::kMT][4], sa[S::kMT][S::kGroups], sb[S::kMT][S::kGroups];
 #pragma unroll
@@ -924,21 +1039,23 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             sc[mt][e] = -INFINITY;
                         best[e & 1] = fmaxf(best[e & 1], sc[mt][e]);
                     }
-                raise(best);
+                raise(best, grow, scales, in);
+                load_words(lift, lifts);
                 // (masked tiles are rare: their code is kept short, which the other
                 // tiles gain 2 % from)
 #pragma unroll (kMasked ? 1 : S::kMT)
                 for (int mt = 0; mt < S::kMT; ++mt) {
                     const unsigned char *ra = tile + (mt * 16 + tok_row) * S::kRecord;
                     float sa[S::kGroups], sb[S::kGroups], pr[4];
-                    load_scales(sa, ra + D + 2 * S::kGroups);
-                    load_scales(sb, ra + S::kNext * S::kRecord + D + 2 * S::kGroups);
+                    load_lifted(sa, ra + D + 2 * S::kGroups, lift);
+                    load_lifted(sb, ra + S::kNext * S::kRecord + D + 2 * S::kGroups, lift);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         pr[e] = exp2_fast(sc[mt][e] * fac[e & 1] - low[e & 1]);
                         if (kMasked && !kept(mt, e / 2, e & 1))
                             pr[e] = 0.f;
                         sum[e & 1] += pr[e];
+                        pr[e] *= kRaise;
                     }
                     const unsigned char *va = tile + (mt * 16 + tok_a) * S::kRecord + D / 2;
                     const unsigned char *vb = tile + (mt * 16 + tok_b) * S::kRecord + D / 2;
@@ -1024,7 +1141,8 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                                 sc[m][half][e] = -INFINITY;
                             best[e / 2] = fmaxf(best[e / 2], sc[m][half][e]);
                         }
-                raise(best);
+                raise(best, grow, scales, in);
+                load_words(lift, lifts);
 #pragma unroll
                 for (int m = 0; m < S::kMT; ++m) {
 #pragma unroll
@@ -1035,14 +1153,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                             if (kMasked && !kept(m, half, e))
                                 pr = 0.f;
                             sum[e / 2] += pr;
-                            sc[m][half][e] = pr;
+                            sc[m][half][e] = pr * kRaise;
                         }
                     const unsigned char *ra = record(m, tok_a), *rb = record(m, tok_b);
                     float vs[4][S::kGroups];     // value scales of the lane's four tokens
-                    load_scales(vs[0], ra + D + 2 * S::kGroups);
-                    load_scales(vs[1], rb + D + 2 * S::kGroups);
-                    load_scales(vs[2], ra + next + D + 2 * S::kGroups);
-                    load_scales(vs[3], rb + next + D + 2 * S::kGroups);
+                    load_lifted(vs[0], ra + D + 2 * S::kGroups, lift);
+                    load_lifted(vs[1], rb + D + 2 * S::kGroups, lift);
+                    load_lifted(vs[2], ra + next + D + 2 * S::kGroups, lift);
+                    load_lifted(vs[3], rb + next + D + 2 * S::kGroups, lift);
 #pragma unroll
                     for (int st = 0; st < S::kStretches; ++st) {
                         constexpr int kW = S::kPer / 2;
@@ -1111,8 +1229,7 @@ attend_kernel(const __grid_constant__ AttendArgs p)
                 break;
             }
             const int base = listed ? 0 : (int)(e0 + i * (S::kWarps * S::kTile));
-            if (mask == S::kFullMask &&
-                (listed || base + S::kTile <= least))
+            if (mask == S::kFullMask && (listed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
             else if (mask)
                 consume(std::true_type{}, data, mask, base);
@@ -1137,20 +1254,23 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
             // narrow: rows of the instruction are channels 4 g + {0, 1} and
             // 4 g + {2, 3}; wide: columns 2 t, 2 t + 1 of instruction j are
-            // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large.
+            // channels 8 t + j and 8 t + 4 + j.  Odd ones are 16 times too large, and
+            // all of a group by its lift.
             float *dst = reinterpret_cast<float *>(ring + S::kTail) + r * S::kOutStride;
 #pragma unroll
             for (int i = 0; i < S::kGroups; ++i) {
+                const float back = lift_back(reinterpret_cast<const unsigned short *>(lifts)[i]);
+                const float back16 = back * 0.0625f;
                 if constexpr (S::kWide) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         *reinterpret_cast<float4 *>(dst + i * kGroup + 8 * t + 4 * k) = make_float4(
-                            o[i][0][2 * c + k], o[i][1][2 * c + k] * 0.0625f,
-                            o[i][2][2 * c + k], o[i][3][2 * c + k] * 0.0625f);
+                            o[i][0][2 * c + k] * back, o[i][1][2 * c + k] * back16,
+                            o[i][2][2 * c + k] * back, o[i][3][2 * c + k] * back16);
                 } else {
                     *reinterpret_cast<float4 *>(dst + i * kGroup + 4 * g) =
-                        make_float4(o[i][0][c], o[i][0][c + 2] * 0.0625f, o[i][1][c],
-                                    o[i][1][c + 2] * 0.0625f);
+                        make_float4(o[i][0][c] * back, o[i][0][c + 2] * back16, o[i][1][c] * back,
+                                    o[i][1][c + 2] * back16);
                 }
             }
         }
