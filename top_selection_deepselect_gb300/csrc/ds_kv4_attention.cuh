@@ -1493,6 +1493,9 @@ inline int unit_rows(int rows) { return rows <= 8 ? 8 : 16; }
 // one known size, and whole ones keep at least half of one wave of CTAs or four
 // fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 18.4
 // instead of 24.6 us; 64 units of 2048 tokens for 304 CTAs: 22.5 cut, 28.7 whole).
+// Between one wave and four fifths of two they are cut (1024 tokens: 320 units 38.9
+// us cut, 45.1 whole in persistent CTAs, 41.0 whole in a CTA each; 384 units 43.0,
+// 45.1, 41.0; 440 units 47.1, 45.1, 47.1).
 template <int D, int Rows>
 int lay_out(AttendArgs &p, int sms)
 {
@@ -1513,7 +1516,7 @@ int lay_out(AttendArgs &p, int sms)
     if (p.a.k > 0 && !p.whole) {
         while (p.cluster < 8 && tiles > 2 * S::kWarps * p.cluster && 2 * p.cluster * units <= ctas)
             p.cluster *= 2;
-        if (tiles <= 4 * S::kWarps * p.cluster)
+        if (p.cluster > 1 && tiles <= 4 * S::kWarps * p.cluster)
             return (int)(units * p.cluster);
         p.cluster = 1;
     }
