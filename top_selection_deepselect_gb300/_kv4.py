@@ -3,7 +3,8 @@ tokens live in -- argument marshalling only, as in _binding.
 
 The functions named like C entry points take the same arguments; the kv4_* and
 pages_* functions take torch tensors, allocate outputs and workspaces with
-torch and enqueue on the current stream.
+torch and enqueue on the current stream of the tensors' device, which need not
+be the current device.
 """
 import ctypes
 import math
@@ -153,6 +154,8 @@ class _Torch:
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.capturing = torch.cuda.is_current_stream_capturing
         self.on_stream = torch.cuda.stream
+        self.current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.on_device = torch.cuda.device
         lib = _lib()
 
         def bytes_for(name, at):
@@ -240,6 +243,20 @@ def _cuda(name, x):
     return index
 
 
+def _elsewhere(t, index, stream, call, *args):
+    """The result of call(*args) with `stream`, or else device `index`, made current.
+
+    The library launches on the calling thread's current device, so that a call
+    enters that of its tensors first."""
+    if stream is None:
+        with t.on_device(index):
+            return call(*args)
+    if stream.device_index != index:
+        raise ValueError("stream belongs to cuda:%d, the tensors to cuda:%d" % (stream.device_index, index))
+    with t.on_stream(stream):      # what is allocated belongs to that stream
+        return call(*args)
+
+
 def kv4_record_bytes(head_dim):
     """Bytes of one token's record of one key/value head (head_dim 64, 128 or 256)."""
     return ds_kv4_record_bytes(head_dim)
@@ -275,10 +292,10 @@ def kv4_append(pool, table, seq, pos, k, v, stream=None):
     be in the table (pages_reserve); tokens without one are skipped.
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return kv4_append(pool, table, seq, pos, k, v)
-    shape, dtype, index = k.shape, k.dtype, _cuda("pool", pool)
+    index = _cuda("pool", pool)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, kv4_append, pool, table, seq, pos, k, v)
+    shape, dtype = k.shape, k.dtype
     if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
     tokens, heads, dim = shape
@@ -307,10 +324,10 @@ def kv4_read(pool, table, seq, pos, head_dim, dtype, k=None, v=None, stream=None
     is not there reads as zeros.
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return kv4_read(pool, table, seq, pos, head_dim, dtype, k, v)
-    tokens, index = seq.numel(), _cuda("pool", pool)
+    index = _cuda("pool", pool)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, kv4_read, pool, table, seq, pos, head_dim, dtype, k, v)
+    tokens = seq.numel()
     cache = _cache(pool, table, head_dim, index)
     shape = (tokens, pool.shape[1], head_dim)
     code = t.codes.get(dtype)
@@ -360,10 +377,11 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     0 and -inf.
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return kv4_attention(q, pool, table, lengths, indices, scale, seqs, out, lse, workspace)
-    index, shape, dtype = _cuda("pool", pool), q.shape, q.dtype
+    index = _cuda("pool", pool)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, kv4_attention,
+                          q, pool, table, lengths, indices, scale, seqs, out, lse, workspace)
+    shape, dtype = q.shape, q.dtype
     if len(shape) != 4 or q.get_device() != index:
         raise ValueError("q must be [batch, queries, heads, head_dim] on the pool's device")
     batch, queries, heads, dim = shape
@@ -470,10 +488,10 @@ def _work(t, index, raw, need, workspace):
 def pages_copy(pool, src, dst, stream=None):
     """Page dst[i] of pool [layers, n_pages, ...] := page src[i], in every layer (int32 lists)."""
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return pages_copy(pool, src, dst)
-    n, index = src.numel(), _cuda("pool", pool)
+    index = _cuda("pool", pool)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, pages_copy, pool, src, dst)
+    n = src.numel()
     status = t.copy(_pool(pool, index), _int32("src", src, index, n), _int32("dst", dst, index, n), n,
                     t.raw_stream(index))
     if status:
@@ -488,10 +506,11 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     when above 0), pages taken.
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace, status)
-    n, index = seqs.numel(), _cuda("table", table)
+    index = _cuda("table", table)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, pages_reserve,
+                          table, lengths, refs, seqs, tokens, page_size, workspace, status)
+    n = seqs.numel()
     book = _book(table, lengths, refs, page_size, index)
     status = _status(status, table, index)
     seqs_at, tokens_at = _int32("seqs", seqs, index, n), _int32("tokens", tokens, index, n)
@@ -511,12 +530,13 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     returns status as pages_reserve does.
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return pages_fork(pool, table, lengths, refs, src, dst, workspace, status)
+    index = _cuda("table", table)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, pages_fork,
+                          pool, table, lengths, refs, src, dst, workspace, status)
     if pool.dim() != 5:
         raise ValueError("pool must be [layers, n_pages, kv_heads, page_size, record bytes]")
-    n, index = src.numel(), _cuda("table", table)
+    n = src.numel()
     book = _book(table, lengths, refs, pool.shape[3], index)
     at, status = _pool(pool, index), _status(status, table, index)
     src_at, dst_at = _int32("src", src, index, n), _int32("dst", dst, index, n)
@@ -532,10 +552,10 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
 def pages_free(table, lengths, refs, seqs, page_size, stream=None):
     """The sequences seqs[i] end: their pages' refs go down, their rows become -1."""
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return pages_free(table, lengths, refs, seqs, page_size)
-    n, index = seqs.numel(), _cuda("table", table)
+    index = _cuda("table", table)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, pages_free, table, lengths, refs, seqs, page_size)
+    n = seqs.numel()
     rc = t.free(_book(table, lengths, refs, page_size, index), _int32("seqs", seqs, index, n), n,
                 t.raw_stream(index))
     if rc:
@@ -549,10 +569,11 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
     [2]: live pages, pages moved).
     """
     t = _t if _t.ready else _t.find()
-    if stream is not None:
-        with t.on_stream(stream):      # what is allocated belongs to that stream
-            return pages_compact(pool, table, refs, workspace, remap, status)
-    index, n_pages = _cuda("table", table), refs.numel()
+    index = _cuda("table", table)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, pages_compact,
+                          pool, table, refs, workspace, remap, status)
+    n_pages = refs.numel()
     book = _book(table, None, refs, 1, index)
     if remap is None:
         remap = t.empty_like(refs)
