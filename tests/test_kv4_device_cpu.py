@@ -1,6 +1,7 @@
 """The cache's wrappers launch on their tensors' device, whichever is current, on a host without
 any: devices, streams and the library's functions are stand-ins that note what they are asked."""
 import contextlib
+import weakref
 
 import pytest
 
@@ -126,3 +127,22 @@ def test_a_stream_of_another_device_is_refused(cuda, name, current):
     with pytest.raises(ValueError):
         tensors()[name](stream=Stream(0))
     assert not cuda.calls
+
+
+@pytest.mark.parametrize("name", ["attention", "reserve", "fork", "compact"])
+def test_a_workspace_is_the_calls_own(cuda, name):
+    """What a call allocates beside its results ends with it: memory that is kept by a stream's handle
+    would be another stream's when CUDA gives the handle out again."""
+    given = []
+
+    def empty(shape, dtype, device):
+        x = On(torch.empty(shape, dtype=dtype))
+        if dtype == torch.uint8:
+            given.append(weakref.ref(x))
+        return x
+
+    cuda.empty, cuda.now = empty, MINE
+    call = tensors()[name]
+    for _ in range(3):
+        call()
+    assert len(given) == 3 and all(x() is None for x in given)

@@ -9,7 +9,6 @@ be the current device.
 import ctypes
 import math
 import struct
-import threading
 
 from ._binding import DS_BF16, DS_FP16, DS_FP32, _check, load_library
 
@@ -152,7 +151,6 @@ class _Torch:
         self.codes = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-        self.capturing = torch.cuda.is_current_stream_capturing
         self.on_stream = torch.cuda.stream
         self.current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.on_device = torch.cuda.device
@@ -180,29 +178,6 @@ class _Torch:
 
 
 _t = _Torch()
-
-# Workspaces of calls that are given none: one for each device and stream, grown
-# as needed and kept.  Calls on one stream follow each other, so that they can
-# share it; _order keeps the launches of one call together where several host
-# threads use a stream.  A call that is being captured into a graph gets memory of
-# its own, since the graph may run on any stream.
-_kept = {}
-_order = threading.Lock()
-_KEPT_BYTES = 1 << 20     # at least this much, so that few calls grow it
-
-
-def _workspace(t, index, raw, need):
-    """(workspace, its bytes) for a call on the device's current stream, whose handle is raw."""
-    if t.capturing():
-        return t.empty(need, dtype=t.uint8, device=t.torch.device("cuda", index)), need
-    key = (index, raw)
-    space = _kept.get(key)
-    if space is None or space[1] < need:
-        size = max(need, _KEPT_BYTES)
-        # an old one goes back to its stream's memory, in order
-        space = _kept[key] = (t.empty(size, dtype=t.uint8, device=t.torch.device("cuda", index)), size)
-    return space
-
 
 def _int32(name, x, index, n=None):
     """Address of a contiguous int32 tensor on device `index`, of n entries in one dimension if given."""
@@ -422,19 +397,17 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
     size = _attention_bytes.get(key)
     if size is None:
         size = _attention_workspace(cache, batch, queries, heads, k, key)
-    raw = t.raw_stream(index)
-    with _order:
-        if workspace is None:
-            if size:
-                workspace, size = _workspace(t, index, raw, size)
-        else:
-            given = _space("workspace", workspace, index)
-            if given < size:
-                raise ValueError("workspace has %d bytes, %d needed" % (given, size))
-        status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
-                             _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
-                             out.data_ptr(), lse.data_ptr(),
-                             None if workspace is None else workspace.data_ptr(), size, raw)
+    if workspace is None:
+        if size:
+            workspace = t.empty(size, dtype=t.uint8, device=q.device)
+    else:
+        given = _space("workspace", workspace, index)
+        if given < size:
+            raise ValueError("workspace has %d bytes, %d needed" % (given, size))
+    status = t.attention(cache, at, seqs_at, batch, queries, heads, code, q.data_ptr(),
+                         _pack_3(q0, q1, q2), list_at, k, dim ** -0.5 if scale is None else scale,
+                         out.data_ptr(), lse.data_ptr(),
+                         None if workspace is None else workspace.data_ptr(), size, t.raw_stream(index))
     if status:
         _check(status, "ds_kv4_attention")
     return out, lse
@@ -478,10 +451,11 @@ def _pages_bytes(n_pages, n):
     return 4 * (2 * n_pages + 2 * n + 4)
 
 
-def _work(t, index, raw, need, workspace):
-    """(workspace, its bytes); called under _order."""
+def _work(t, table, index, need, workspace):
+    """(workspace, its bytes): the one that was passed in, or memory of the current stream for this
+    call alone."""
     if workspace is None:
-        return _workspace(t, index, raw, need)
+        return t.empty(need, dtype=t.uint8, device=table.device), need
     return workspace, _space("workspace", workspace, index)
 
 
@@ -514,10 +488,9 @@ def pages_reserve(table, lengths, refs, seqs, tokens, page_size, workspace=None,
     book = _book(table, lengths, refs, page_size, index)
     status = _status(status, table, index)
     seqs_at, tokens_at = _int32("seqs", seqs, index, n), _int32("tokens", tokens, index, n)
-    need, raw = _pages_bytes(refs.numel(), n), t.raw_stream(index)
-    with _order:
-        workspace, size = _work(t, index, raw, need, workspace)
-        rc = t.reserve(book, seqs_at, tokens_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
+    workspace, size = _work(t, table, index, _pages_bytes(refs.numel(), n), workspace)
+    rc = t.reserve(book, seqs_at, tokens_at, n, status.data_ptr(), workspace.data_ptr(), size,
+                   t.raw_stream(index))
     if rc:
         _check(rc, "ds_pages_reserve")
     return status
@@ -540,10 +513,9 @@ def pages_fork(pool, table, lengths, refs, src, dst, workspace=None, status=None
     book = _book(table, lengths, refs, pool.shape[3], index)
     at, status = _pool(pool, index), _status(status, table, index)
     src_at, dst_at = _int32("src", src, index, n), _int32("dst", dst, index, n)
-    need, raw = _pages_bytes(refs.numel(), n), t.raw_stream(index)
-    with _order:
-        workspace, size = _work(t, index, raw, need, workspace)
-        rc = t.fork(at, book, src_at, dst_at, n, status.data_ptr(), workspace.data_ptr(), size, raw)
+    workspace, size = _work(t, table, index, _pages_bytes(refs.numel(), n), workspace)
+    rc = t.fork(at, book, src_at, dst_at, n, status.data_ptr(), workspace.data_ptr(), size,
+                t.raw_stream(index))
     if rc:
         _check(rc, "ds_pages_fork")
     return status
@@ -579,10 +551,9 @@ def pages_compact(pool, table, refs, workspace=None, remap=None, status=None, st
         remap = t.empty_like(refs)
     at, status = _pool(pool, index), _status(status, table, index)
     remap_at = _int32("remap", remap, index, n_pages)
-    need, raw = _pages_bytes(n_pages, 0), t.raw_stream(index)
-    with _order:
-        workspace, size = _work(t, index, raw, need, workspace)
-        rc = t.compact(at, book, remap_at, status.data_ptr(), workspace.data_ptr(), size, raw)
+    workspace, size = _work(t, table, index, _pages_bytes(n_pages, 0), workspace)
+    rc = t.compact(at, book, remap_at, status.data_ptr(), workspace.data_ptr(), size,
+                   t.raw_stream(index))
     if rc:
         _check(rc, "ds_pages_compact")
     return remap, status
