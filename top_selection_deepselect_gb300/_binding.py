@@ -225,6 +225,16 @@ def dtype_code(t):
     raise TypeError("x must be float32, bfloat16 or float16, got %s" % t.dtype)
 
 
+def _enter(x, stream):
+    """None where x's device is current, else a context that makes it so; refuses a stream of
+    another device.  The library launches on the calling thread's current device."""
+    import torch
+    index = x.get_device()
+    if stream is not None and getattr(stream, "device_index", index) != index:
+        raise ValueError("stream belongs to cuda:%d, x to cuda:%d" % (stream.device_index, index))
+    return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
 def topk(x, k, B, B2, seed=0x5EED5EED, row_len=None, splits=0, stats=False, out_idx=None,
          out_val=None, stream=None, order=None):
     """Top-k of every row of a 2-D CUDA tensor x (float32, bfloat16 or float16).
@@ -239,6 +249,10 @@ def topk(x, k, B, B2, seed=0x5EED5EED, row_len=None, splits=0, stats=False, out_
         raise ValueError("x must be a 2-D CUDA tensor")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous (row pitch = N)")
+    there = _enter(x, stream)
+    if there is not None:
+        with there:
+            return topk(x, k, B, B2, seed, row_len, splits, stats, out_idx, out_val, stream, order)
     rows, N = x.shape
     code = dtype_code(x)
     if out_idx is None:
@@ -283,6 +297,10 @@ def topk_long_row(x, k, B, B2, seed=0x5EED5EED, workspace=None, out_idx=None, ou
     import torch
     if x.dim() != 1 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous 1-D CUDA tensor")
+    there = _enter(x, stream)
+    if there is not None:
+        with there:
+            return topk_long_row(x, k, B, B2, seed, workspace, out_idx, out_val, stream)
     N = x.numel()
     code = dtype_code(x)
     need = ds_topk_long_row_workspace(code, N, k, B, B2)
