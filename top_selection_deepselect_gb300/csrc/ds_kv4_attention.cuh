@@ -152,8 +152,8 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, unsigned bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// Whether the phase ended within kPatience nanoseconds (far beyond any copy's
-// time): a copy that never ends must not hang the GPU.
+// Nanoseconds that a copy is waited for, far beyond any copy's time: one that
+// never ends must not hang the GPU.
 constexpr long long kPatience = 1000000000;
 __device__ __forceinline__ bool barrier_done(uint32_t bar, unsigned phase)
 {
@@ -172,15 +172,20 @@ __device__ __forceinline__ long long nanoseconds()
     return t;
 }
 
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, unsigned phase)
+// Waits for a phase to end.  late: this lane has given a phase up, now or before,
+// and waits for none any more.  Other lanes may not have, so that no branch that
+// leads away from them is taken on it.
+__device__ __forceinline__ void barrier_wait(uint32_t bar, unsigned phase, bool &late,
+                                             long long patience = kPatience)
 {
-    if (barrier_done(bar, phase))
-        return true;
+    if (barrier_done(bar, phase) || late)
+        return;
     const long long from = nanoseconds();
     while (!barrier_done(bar, phase))
-        if (nanoseconds() - from > kPatience)
-            return false;
-    return true;
+        if (nanoseconds() - from > patience) {
+            late = true;
+            return;
+        }
 }
 
 // Asynchronous copy of `bytes` (a multiple of 16) from global to shared memory.
@@ -586,11 +591,12 @@ attend_kernel(const __grid_constant__ AttendArgs p)
 
     // state of the warp's ring: tile i of a unit is in stage i % kStages; the
     // stage filled and the one used next, the phases of all; lost: a copy did not
-    // arrive, the ring is not used any more and all further results are NaN
+    // arrive, the ring is not used any more and all further results are NaN; late:
+    // so far only this lane knows, and starts no copies
     const uint32_t barriers = shared_address(smem + S::kOffBarrier) + warp * S::kStages * 8;
     int fill = 0, use = 0;
     unsigned phases = 0;
-    bool lost = false;
+    bool lost = false, late = false;
     if (lane == 0) {
         for (int s = 0; s < S::kStages; ++s)
             barrier_init(barriers + s * 8);
@@ -671,9 +677,9 @@ attend_kernel(const __grid_constant__ AttendArgs p)
     auto issue_tokens = [&](const volatile Part &part, int pos, int page) {
         const uint32_t bar = barriers + fill * 8, dst = shared_address(ring + fill * S::kStageBytes);
         const bool ok = (unsigned)page < (unsigned)p.c.n_pages;   // page is -1 where pos is
-        const bool leads = ok && (lane & (p.run - 1)) == 0;
+        const bool leads = ok && (lane & (p.run - 1)) == 0 && !late;
         const unsigned mask = __ballot_sync(~0u, ok), leaders = __ballot_sync(~0u, leads);
-        if (lane == 0) {
+        if (lane == 0 && !late) {
             masks[fill] = mask;
             barrier_expect(bar, __popc(leaders) * p.run * S::kRecord);
         }
@@ -720,14 +726,14 @@ attend_kernel(const __grid_constant__ AttendArgs p)
         if (i > 0 && turn == 0)
             next_runs(part, i);
         const uint32_t bar = barriers + fill * 8;
-        if (lane == turn << halves) {
+        if (lane == turn << halves && !late) {
             masks[fill] = tile_mask;
             const int runs = !halves ? tile_mask != 0 : ((tile_mask & 0xffffu) != 0) + (tile_mask > 0xffffu);
             barrier_expect(bar, runs * kRun * S::kRecord);
         }
         if (halves)
             __syncwarp();
-        if (lane >> halves == turn && run_src)
+        if (lane >> halves == turn && run_src && !late)
             copy_bulk(shared_address(ring + fill * S::kStageBytes) + (lane & halves) * kRun * S::kRecord,
                       run_src, kRun * S::kRecord, bar);
         fill = fill + 1 == S::kStages ? 0 : fill + 1;
@@ -1215,26 +1221,25 @@ attend_kernel(const __grid_constant__ AttendArgs p)
             }
 
             const unsigned mask = masks[use];
-            const bool came = barrier_wait(barriers + use * 8, phases >> use & 1);
+            barrier_wait(barriers + use * 8, phases >> use & 1, late);
             phases ^= 1u << use;
             const unsigned char *data = ring + use * S::kStageBytes;
             use = use + 1 == S::kStages ? 0 : use + 1;
-            if (!came) {
-                // the copies after it get as long to end
-                lost = true;
-                for (int left = min(S::kStages - 1, mine - 1 - i); left > 0; --left) {
-                    barrier_wait(barriers + use * 8, phases >> use & 1);
-                    use = use + 1 == S::kStages ? 0 : use + 1;
-                }
-                break;
-            }
             const int base = listed ? 0 : (int)(e0 + i * (S::kWarps * S::kTile));
             if (mask == S::kFullMask && (listed || base + S::kTile <= least))
                 consume(std::false_type{}, data, mask, base);
             else if (mask)
                 consume(std::true_type{}, data, mask, base);
         }
-        __syncwarp();
+        // What came too late was taken as it was, by all lanes alike; now they agree
+        // that it was lost, and give what is still under way as long again.
+        if (__any_sync(~0u, late)) {
+            lost = true;
+            late = false;
+            for (int s = 0; s < S::kStages; ++s)
+                barrier_wait(barriers + s * 8, ~phases >> s & 1, late);
+            __syncwarp();
+        }
 
         const int active = part.active;
         // ---- the warps' results in their rings' tails (a warp without tiles
