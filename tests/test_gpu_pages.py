@@ -207,3 +207,16 @@ def test_refusals(ds):
     with pytest.raises(ds.DSError):
         ds.pages_free(b.table, b.lengths, b.refs, dev([0]), -1)
     b.check()
+
+
+def test_reserve_for_negative_lengths(ds):
+    """They count as 0, the smallest ones too."""
+    low = -2 ** 31
+    seqs, tokens = [4, 3, 1, 3, 0, 2], [5, 17, 16, 9, 1, 33]
+    for lengths in ([low, low, low, low, low], [low + 3, low + 2, low + 1, low, -1], [-7, low + 5, 0, low + 1, low + 4]):
+        table, got, refs = dev(np.full((5, 4), -1)), dev(lengths), dev(np.zeros(9))
+        status = ds.pages_reserve(table, got, refs, dev(seqs), dev(tokens), 16)
+        assert status.tolist() == [0, 8]
+        assert got.tolist() == [1, 16, 33, 17, 5]
+        assert table[:, :3].tolist() == [[4, -1, -1], [3, -1, -1], [5, 6, 7], [1, 2, -1], [0, -1, -1]]
+        assert refs.tolist() == [1] * 8 + [0]

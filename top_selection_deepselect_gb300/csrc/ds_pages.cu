@@ -140,7 +140,13 @@ reserve_kernel(Book book, const int32_t *seqs, const int32_t *tokens, int n, int
     // lengths before the call, then the claims
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const int s = seqs[i];
-        w.a[i] = (unsigned)s < (unsigned)book.max_seqs && tokens[i] > 0 ? max(book.lengths[s], 0) : -1;
+        w.a[i] = -1;
+        if ((unsigned)s < (unsigned)book.max_seqs && tokens[i] > 0) {
+            const int len = book.lengths[s];
+            w.a[i] = max(len, 0);
+            if (len < 0)
+                book.lengths[s] = 0;    // below it a claim might not be seen
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads)
