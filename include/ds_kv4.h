@@ -114,10 +114,11 @@ int ds_kv4_read(const ds_kv4_cache_t *cache, const int32_t *seq, const int32_t *
  *             (NULL when that is 0)
  * A query that sees no token gives out = 0 and lse = -inf.  A probability times
  * a value scale is rounded to 11 significant bits (below 2^-28 of the largest of
- * each in its group of channels it is within 2^-39 of that); scores, maxima, sums
- * and outputs are held in 32 bits until they are rounded to `dtype`.  (A copy into shared
- * memory that does not end within a second, which no working GPU does, is given
- * up, and what depends on it is NaN.)
+ * each in its group of channels it is within 2^-39 of that), and q's channels
+ * below 2^-25 of the row's largest are held to within 2^-35 of it; scores, maxima,
+ * sums and outputs are held in 32 bits until they are rounded to `dtype`.  (A copy
+ * into shared memory that does not end within a second, which no working GPU does,
+ * is given up, and what depends on it is NaN.)
  */
 int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const int32_t *seqs,
                      int batch, int queries, int heads, int dtype, const void *q,

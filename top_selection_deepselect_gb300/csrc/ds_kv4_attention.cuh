@@ -74,8 +74,9 @@ struct Shape {
     static constexpr int kOutRegs = kGroups * kSubs * 4;
     // Warps of a CTA and CTAs of an SM, by what the output leaves of the
     // registers: 2 x 8 warps with 128 each, 12 with 168, 8 with 255.  (16 warps
-    // in one CTA: 64 x 32768 tokens the same 403 us, 256 x 200 tokens 63 for 41,
-    // because nothing else runs while a unit ends.)
+    // in one CTA, both timed before scales were lifted: 64 x 32768 tokens the same
+    // 403 us, 256 x 200 tokens 63 for 41, because nothing else runs while a unit
+    // ends.)
     static constexpr int kWarps = kOutRegs == 64 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kCtas = kOutRegs <= 32 ? 2 : 1;
@@ -373,8 +374,8 @@ __device__ __forceinline__ long long scan_cta(long long v, long long *before, lo
 // tiles.  A unit's start and end (its queries, the first copies' latency, the
 // meeting of the warps) cost a CTA as much as some tiles do; without these
 // places the CTA that meets 24 empty sequences in a row takes three times as long
-// as the others (37 ragged sequences of 5 drafts: 80 us; with 12, 18, 24, 32 and 40
-// places 35, 33, 33, 33 and 35; 16 x 16384 tokens 68 with any of them).
+// as the others (37 ragged sequences of 5 drafts: 84 us; with 12, 18, 24, 32 and 40
+// places 37, 35, 33 to 35, 35 and 37; 16 x 16384 tokens 70 with any of them).
 constexpr int kUnitCost = 24;
 
 // Quotient of numbers that are not negative, in 32 bits where that is enough.
@@ -484,7 +485,8 @@ struct alignas(16) Split {
 
 // Query operands of a unit, the rows' factors and limits.  A row is scaled by a
 // power of two to magnitudes of 2^14 to 2^15, so that fp16 holds every bf16 and
-// fp16 value of it (down to 2^-39 of the largest, below which it adds nothing).
+// fp16 value of it down to 2^-25 of the largest; smaller ones are off by 2^-35 of
+// that at most.
 template <int D, int Rows>
 struct Queries {
     using S = Shape<D, Rows>;
@@ -1488,16 +1490,16 @@ join_kernel(const __grid_constant__ AttendArgs p)
 // Query rows of a unit: 8, or 16 where there are more.  Further rows are further
 // units.  Units of 32 rows would expand a record once instead of twice, but their
 // outputs leave 8 warps an SM that cannot hide each other's waits (32 rows, 16 x
-// 16384 tokens: 197 us in one unit where two took 186, which take 174 now; 80
-// rows, 4 x 65536: 94 and 72, now 68).
+// 16384 tokens: 197 us in one unit where two took 186, which take 180 now; 80
+// rows, 4 x 65536: 94 and 72, now 70).
 inline int unit_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 // How a call is laid out: sizes of its units, its CTAs, and whether units are
 // cut between CTAs.  They are not, and the join is saved, where a unit is at
 // most two tiles a warp, and where tokens are listed, so that all units are of
 // one known size, and whole ones keep at least half of one wave of CTAs or four
-// fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 18.4
-// instead of 24.6 us; 64 units of 2048 tokens for 304 CTAs: 22.5 cut, 28.7 whole).
+// fifths of several busy (512 of 32768 tokens, 128 units for 152 CTAs: 20.5
+// instead of 28.7 us; 64 units of 2048 tokens for 304 CTAs: 24.6 cut, 30.7 whole).
 // Between one wave and four fifths of two they are cut (1024 tokens: 320 units 38.9
 // us cut, 45.1 whole in persistent CTAs, 41.0 whole in a CTA each; 384 units 43.0,
 // 45.1, 41.0; 440 units 47.1, 45.1, 47.1).
@@ -1516,7 +1518,7 @@ int lay_out(AttendArgs &p, int sms)
               (p.a.k > 0 && units >= (units <= ctas ? 0.5 * ctas : 0.8 * ctas * waves));
     // Few listed units of middling size: a cluster of CTAs each, which joins its
     // parts in shared memory, while that gives no warp more than four tiles
-    // (64 units of 2048 tokens, four CTAs each: 20.5 us, with a join launch 22.5).
+    // (64 units of 2048 tokens, four CTAs each: 20.5 us, with a join launch 24.6).
     p.cluster = 1;
     if (p.a.k > 0 && !p.whole) {
         while (p.cluster < 8 && tiles > 2 * S::kWarps * p.cluster && 2 * p.cluster * units <= ctas)

@@ -185,8 +185,9 @@ __device__ __forceinline__ unsigned encode(const Eight<T> &e, const Scale &s, bo
 }
 
 // 31.9 us for 28693 tokens of 8 heads of 128 in bf16 (150 MB, 4.7 TB/s), 43.9 in
-// fp32 (268 MB, 6.1 TB/s): in 16-bit types the bound is instructions, some 220 for a
-// lane's 16 channels.  A pair a multiply-add 32.8 -> 31.9, scales shared out and no
+// fp32 (268 MB, 6.1 TB/s).  16-bit types lie between two bounds: some 220
+// instructions for a lane's 16 channels keep issue 69 % and the ALU 67 % busy, and
+// waits for loads are the largest stall.  A pair a multiply-add 32.8 -> 31.9, scales shared out and no
 // correction 35.1 -> 32.8; six CTAs an SM (five 33.4; seven and eight spill, 33.1);
 // the next head's loads ahead of this one's codes, or two heads at once, are slower
 // (39.9, 34.5).
