@@ -11,12 +11,13 @@ SOURCES = [os.path.join(CSRC, f) for f in ("ds_topk.cu", "ds_kernels_fp32.cu", "
                                          "ds_kernels_fp16.cu", "ds_kv4.cu", "ds_kv4_store.cu",
                                          "ds_kv4_attention.cu", "ds_kv4_attention_64.cu",
                                          "ds_kv4_attention_128.cu", "ds_kv4_attention_256.cu",
-                                         "ds_pages.cu")]
+                                         "ds_pages.cu", "ds_logprob.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ds_device.cuh"), os.path.join(CSRC, "ds_kernel.cuh"),
                   os.path.join(CSRC, "ds_stream.cuh"), os.path.join(CSRC, "ds_host.h"),
                   os.path.join(CSRC, "ds_kv4.cuh"), os.path.join(CSRC, "ds_kv4_launch.h"),
                   os.path.join(CSRC, "ds_kv4_attention.cuh"),
-                  os.path.join(INCLUDE, "ds_topk.h"), os.path.join(INCLUDE, "ds_kv4.h")]
+                  os.path.join(INCLUDE, "ds_topk.h"), os.path.join(INCLUDE, "ds_kv4.h"),
+                  os.path.join(INCLUDE, "ds_logprob.h")]
 
 # No fast-math and no flush-to-zero: the prefilter compares denormals exactly.
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",

@@ -1,0 +1,813 @@
+// ds_logprob.cu -- log probabilities of given tokens with entropy and the
+// likeliest alternatives, and their gradient (include/ds_logprob.h).
+//
+// Forward, one pass over a row: with a running maximum m of the logits,
+//   S = sum 2^d,  T = sum 2^d d,  d = (x - m) scale log2 e <= 0
+// give lse = scale m + ln S and entropy = ln 2 (log2 S - T / S), whose two terms
+// are both >= 0, so that nothing cancels.  d is clamped at -200, where 2^d is 0:
+// a logit of -inf, or one that is further below than 32 bits reach, then adds
+// 2^d d = 0 and not NaN.  The alternatives come out of the same pass: the first
+// pieces of a CTA's slice give a value that at least k of its logits reach, later
+// logits above it go to a buffer in shared memory, and the k first of these by
+// (value, index) are found by warps that sort and merge lists of 32.
+//
+// The bound is HBM; what has to be kept off is instructions.  A vector of 16
+// bytes is tested as a whole, by packed maxima, against the value that candidates
+// have to be above (which is at or below the running maximum), so that maxima and
+// candidates cost nothing where there are none; sums are pairs in one instruction.
+//
+// A row is a CTA's, or a cluster's where rows are few: each CTA takes a slice, and
+// the first joins the sums and the sorted lists out of distributed shared memory.
+#include "ds_logprob.h"
+
+#include <cooperative_groups.h>
+
+#include "ds_device.cuh"
+#include "ds_host.h"
+#include "ds_kv4.cuh"
+
+namespace ds {
+namespace logprob {
+namespace {
+
+using kv4::from_float;
+using kv4::to_float;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;          // vectors of a thread under way
+constexpr int kTop = DS_LOGPROB_MAX_K;
+constexpr int kEach = kTop / kWarps;   // of a warp's threads that the first bound is taken from
+constexpr int kCapacity = 2048;    // candidates of a slice
+constexpr float kLow = -200.f;     // 2^d is 0 in 32 bits below -150
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+
+typedef unsigned long long Entry;  // key of the value, then ~index: larger comes first
+
+template <typename T>
+struct alignas(16) Vec {
+    static constexpr int kCount = 16 / sizeof(T);
+    T x[kCount];
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Maxima that keep a NaN.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ __half2 max_nan(__half2 a, __half2 b) { return __hmax2_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat162 max_nan(__nv_bfloat162 a, __nv_bfloat162 b)
+{
+    return __hmax2_nan(a, b);
+}
+
+// Largest element of a vector, NaN if there is one.
+__device__ __forceinline__ float largest(const Vec<float> &v)
+{
+    return max_nan(max_nan(v.x[0], v.x[1]), max_nan(v.x[2], v.x[3]));
+}
+template <typename T, typename T2>
+__device__ __forceinline__ float largest16(const Vec<T> &v)
+{
+    const T2 *w = reinterpret_cast<const T2 *>(v.x);
+    const T2 m = max_nan(max_nan(w[0], w[1]), max_nan(w[2], w[3]));
+    return max_nan(to_float(m.x), to_float(m.y));
+}
+__device__ __forceinline__ float largest(const Vec<__half> &v) { return largest16<__half, __half2>(v); }
+__device__ __forceinline__ float largest(const Vec<__nv_bfloat16> &v)
+{
+    return largest16<__nv_bfloat16, __nv_bfloat162>(v);
+}
+
+// Unsigned key in the order of values: NaN above +inf, -0 equal to +0.
+__device__ __forceinline__ unsigned key_of(float x)
+{
+    if (x != x)
+        return ~0u;
+    const unsigned b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned key)
+{
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);   // the NaN's key gives a NaN
+}
+
+// A row as vectors of 16 aligned bytes: element i is element i + skip of them.
+template <typename T>
+struct Row {
+    const T *at;                  // aligned address at or below the row's start
+    unsigned skip, past;          // the row is elements [skip, past) from there
+    unsigned vectors;
+    __device__ __forceinline__ Row(const T *row, int vocab)
+    {
+        const uintptr_t a = (uintptr_t)row;
+        skip = (unsigned)(a % 16 / sizeof(T));
+        at = reinterpret_cast<const T *>(a & ~(uintptr_t)15);
+        past = skip + (unsigned)vocab;
+        vectors = (past + Vec<T>::kCount - 1) / Vec<T>::kCount;
+    }
+    __device__ __forceinline__ bool whole(unsigned j) const
+    {
+        return j * Vec<T>::kCount >= skip && (j + 1) * Vec<T>::kCount <= past;
+    }
+    // Vector j, -inf in the places that are not the row's (which are not read).
+    __device__ __forceinline__ Vec<T> load(unsigned j, unsigned end) const
+    {
+        Vec<T> v;
+        const T *p = at + (size_t)j * Vec<T>::kCount;
+        if (j < end && whole(j)) {
+            v = *reinterpret_cast<const Vec<T> *>(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < Vec<T>::kCount; ++e) {
+                const unsigned i = j * Vec<T>::kCount + e;
+                if (j < end && i >= skip && i < past)
+                    v.x[e] = p[e];
+                else
+                    from_float(v.x[e], -INFINITY);
+            }
+        }
+        return v;
+    }
+};
+
+// Sums of a thread, a CTA or a row: pairs of partial sums, by parity of the place.
+struct Sums {
+    float most;                   // maximum so far (not a NaN); -inf: nothing but -inf so far
+    float s0, s1, t0, t1;
+};
+
+// Brings sums to another maximum at or above theirs.
+__device__ __forceinline__ void rescale(Sums &a, float most, float c)
+{
+    if (a.most == -INFINITY) {    // then the sums are 0, or a NaN's
+        a.most = most;
+        return;
+    }
+    const float d = max_nan((a.most - most) * c, kLow), f = exp2_fast(d);
+    a.t0 = f * fmaf(d, a.s0, a.t0), a.t1 = f * fmaf(d, a.s1, a.t1);
+    a.s0 *= f, a.s1 *= f;
+    a.most = most;
+}
+
+__device__ __forceinline__ void add_sums(Sums &a, Sums b, float c)
+{
+    const float most = fmaxf(a.most, b.most);
+    rescale(a, most, c);
+    rescale(b, most, c);
+    a.s0 += b.s0, a.s1 += b.s1, a.t0 += b.t0, a.t1 += b.t1;
+}
+
+// Adds two elements, relative to base (a.most, or 0 while that is -inf).
+__device__ __forceinline__ void add_pair(Sums &a, float x0, float x1, float base, float c)
+{
+    float d0, d1;
+    asm("{\n\t.reg .b64 x, m, f;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 m, {%4, %4};\n\t"
+        "mov.b64 f, {%5, %5};\n\t"
+        "sub.rn.f32x2 x, x, m;\n\t"
+        "mul.rn.f32x2 x, x, f;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(base), "f"(c));
+    d0 = max_nan(d0, kLow), d1 = max_nan(d1, kLow);
+    const float e0 = exp2_fast(d0), e1 = exp2_fast(d1);
+    asm("{\n\t.reg .b64 s, t, e, d;\n\t"
+        "mov.b64 s, {%0, %1};\n\t"
+        "mov.b64 t, {%2, %3};\n\t"
+        "mov.b64 e, {%4, %5};\n\t"
+        "mov.b64 d, {%6, %7};\n\t"
+        "add.rn.f32x2 s, s, e;\n\t"
+        "fma.rn.f32x2 t, e, d, t;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t"
+        "mov.b64 {%2, %3}, t;\n\t}"
+        : "+f"(a.s0), "+f"(a.s1), "+f"(a.t0), "+f"(a.t1) : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
+}
+
+template <typename T>
+__device__ __forceinline__ void add_vector(Sums &a, const Vec<T> &v, float c)
+{
+    const float base = a.most == -INFINITY ? 0.f : a.most;
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kCount; e += 2)
+        add_pair(a, to_float(v.x[e]), to_float(v.x[e + 1]), base, c);
+}
+
+// ---- lists of 32 entries, one a lane, largest first ----------------------------
+template <typename K>
+__device__ __forceinline__ K exchange(K x, int step, bool larger)
+{
+    const K y = __shfl_xor_sync(~0u, x, step);
+    return larger == (x > y) ? x : y;
+}
+
+// The larger half of a bitonic sequence's sort, largest first.
+template <typename K>
+__device__ __forceinline__ K order_bitonic(K x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int step = 16; step; step /= 2)
+        x = exchange(x, step, (lane & step) == 0);
+    return x;
+}
+
+template <typename K>
+__device__ __forceinline__ K order_lanes(K x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size < 32; size *= 2)
+#pragma unroll
+        for (int step = size / 2; step; step /= 2)
+            x = exchange(x, step, ((lane & step) == 0) == ((lane & size) == 0));
+    return order_bitonic(x);
+}
+
+// The 32 largest of two lists.
+__device__ __forceinline__ Entry merge_lists(Entry a, Entry b)
+{
+    const Entry r = __shfl_sync(~0u, b, 31 - (threadIdx.x & 31));
+    return order_bitonic(a > r ? a : r);
+}
+
+// The 32 largest of n entries, in warp 0 (in all warps of the first call's
+// threads, something).  `lists`: kWarps * 32 entries of shared memory.
+__device__ Entry select_entries(const Entry *entries, int n, Entry *lists)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    Entry mine = 0;
+    for (int i = warp * 32; i < n; i += kThreads)
+        mine = merge_lists(mine, order_lanes(i + lane < n ? entries[i + lane] : 0));
+#pragma unroll
+    for (int half = kWarps / 2; half; half /= 2) {
+        if (warp >= half && warp < 2 * half)
+            lists[warp * 32 + lane] = mine;
+        __syncthreads();
+        if (warp < half)
+            mine = merge_lists(mine, lists[(warp + half) * 32 + lane]);
+    }
+    return mine;
+}
+
+struct Shared {
+    Entry entries[kCapacity];
+    Entry lists[kWarps * 32];
+    Sums sums[kWarps];
+    unsigned keys[kWarps * kEach];
+    float most[kWarps];
+    int count;
+    // what the cluster's first CTA reads
+    Entry top[kTop];
+    Sums all;
+};
+
+template <typename T>
+__device__ __forceinline__ Entry entry_of(const Row<T> &row, T x, unsigned j, int e)
+{
+    return (Entry)key_of(to_float(x)) << 32 | ~(j * Vec<T>::kCount + e - row.skip);
+}
+
+__device__ __forceinline__ void keep(Shared &sh, Entry x)
+{
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCapacity)
+        sh.entries[at] = x;
+}
+
+// The 32 largest entries of the slice where candidates did not fit: the k-th
+// largest of the threads' largest is a bound that k entries reach, and mostly few
+// more do; where those do not fit either, entry after entry is found by a
+// sweep.  In warp 0.
+template <typename T>
+__device__ __noinline__ Entry select_slowly(const Row<T> &row, unsigned lo, unsigned hi, int k, Shared &sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    // the thread's largest entry below `under`
+    auto largest_below = [&](Entry under) {
+        Entry most = 0;
+        for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
+            const Vec<T> v = row.load(j, hi);
+#pragma unroll
+            for (int e = 0; e < Vec<T>::kCount; ++e) {
+                const unsigned i = j * Vec<T>::kCount + e;
+                const Entry x = entry_of(row, v.x[e], j, e);
+                if (i >= row.skip && i < row.past && x < under && x > most)
+                    most = x;
+            }
+        }
+        return most;
+    };
+    __syncthreads();
+    static_assert(kThreads <= kCapacity, "an entry of each thread");
+    sh.entries[threadIdx.x] = largest_below(~0ULL);    // no entry is ~0: indices are below 2^31
+    __syncthreads();
+    Entry mine = select_entries(sh.entries, kThreads, sh.lists);
+    __syncthreads();
+    if (warp == 0) {
+        const Entry bound = __shfl_sync(~0u, mine, k - 1);
+        if (lane == 0) {
+            sh.top[0] = bound;
+            sh.count = 0;
+        }
+    }
+    __syncthreads();
+    const Entry bound = sh.top[0];
+    for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
+        const Vec<T> v = row.load(j, hi);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::kCount; ++e) {
+            const unsigned i = j * Vec<T>::kCount + e;
+            const Entry x = entry_of(row, v.x[e], j, e);
+            if (i >= row.skip && i < row.past && x >= bound)
+                keep(sh, x);
+        }
+    }
+    __syncthreads();
+    if (sh.count <= kCapacity)
+        return select_entries(sh.entries, sh.count, sh.lists);
+    Entry found = ~0ULL;
+    mine = 0;
+    for (int n = 0; n < k; ++n) {
+        Entry most = largest_below(found);
+#pragma unroll
+        for (int step = 16; step; step /= 2) {
+            const Entry y = __shfl_xor_sync(~0u, most, step);
+            most = y > most ? y : most;
+        }
+        __syncthreads();
+        if (lane == 0)
+            sh.lists[warp] = most;
+        __syncthreads();
+        found = sh.lists[0];
+        for (int w = 1; w < kWarps; ++w)
+            found = sh.lists[w] > found ? sh.lists[w] : found;
+        if (lane == n)
+            mine = found;
+    }
+    return mine;
+}
+
+struct Args {
+    const void *logits;
+    long long stride;
+    const int32_t *tokens;
+    float *logprob, *entropy, *lse, *top;
+    int32_t *idx;
+    int vocab, k, cluster;
+    float scale;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+logprob_kernel(const __grid_constant__ Args p)
+{
+    __shared__ Shared sh;
+    dependent_grid_wait();
+    allow_dependent_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const unsigned r = blockIdx.x / p.cluster, rank = blockIdx.x - r * p.cluster;
+    const T *logits = (const T *)p.logits + (long long)r * p.stride;
+    const Row<T> row(logits, p.vocab);
+    const unsigned lo = (unsigned)((unsigned long long)row.vectors * rank / p.cluster);
+    const unsigned hi = (unsigned)((unsigned long long)row.vectors * (rank + 1) / p.cluster);
+    const float c = p.scale * kLog2e;
+
+    // The first pieces, whose maximum all sums start from.  A candidate has to be
+    // at or above a value that k logits of these pieces reach, and above it after
+    // them (an equal one further on comes later in the order).
+    Vec<T> now[kAhead];
+    unsigned j = lo + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        now[u] = row.load(j + u * kThreads, hi);
+    float mine = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        const float m = largest(now[u]);
+        nan = nan || m != m;
+        mine = fmaxf(mine, m);
+    }
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    const unsigned top_key = __reduce_max_sync(~0u, key_of(mine));
+    if (lane == 0)
+        sh.most[warp] = value_of(top_key);
+    if (p.k > 0) {
+        // four largest of each warp's threads, and the k-th of these; a thread
+        // of places outside the row has -inf, which is at or below all logits
+        const unsigned sorted = order_lanes(nan ? ~0u : key_of(mine));
+        if (lane < kEach)
+            sh.keys[warp * kEach + lane] = sorted;
+    }
+    __syncthreads();
+    mine = sh.most[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w)
+        mine = fmaxf(mine, sh.most[w]);
+    const float bound = p.k > 0 ? value_of(__shfl_sync(~0u, order_lanes(sh.keys[lane]), p.k - 1)) : mine;
+
+    Sums a = {mine, 0.f, 0.f, 0.f, 0.f};
+    // A vector that may hold a candidate or a new maximum.
+    auto look = [&](const Vec<T> &v, unsigned at, bool first) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < Vec<T>::kCount; ++e) {
+            const float x = to_float(v.x[e]);
+            most = fmaxf(most, x);
+            if (p.k > 0 && (first ? !(x < bound) : !(x <= bound))) {
+                const unsigned i = at * Vec<T>::kCount + e;
+                if (i >= row.skip && i < row.past)
+                    keep(sh, entry_of(row, v.x[e], at, e));
+            }
+        }
+        if (most > a.most)
+            rescale(a, most, c);
+    };
+    bool first = true;
+    for (;;) {
+        Vec<T> next[kAhead];
+        const unsigned j_next = j + kAhead * kThreads;
+        const bool more = j_next - threadIdx.x < hi;      // the same for all threads
+        if (more) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                next[u] = row.load(j_next + u * kThreads, hi);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float m = largest(now[u]);
+            if (first ? !(m < bound) : !(m <= bound))
+                if (j + u * kThreads < hi)
+                    look(now[u], j + u * kThreads, first);
+            add_vector(a, now[u], c);
+        }
+        if (!more)
+            break;
+        first = false;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            now[u] = next[u];
+        j = j_next;
+    }
+
+    // the CTA's sums, in a fixed order
+#pragma unroll
+    for (int step = 16; step; step /= 2) {
+        Sums b;
+        b.most = __shfl_xor_sync(~0u, a.most, step);
+        b.s0 = __shfl_xor_sync(~0u, a.s0, step), b.s1 = __shfl_xor_sync(~0u, a.s1, step);
+        b.t0 = __shfl_xor_sync(~0u, a.t0, step), b.t1 = __shfl_xor_sync(~0u, a.t1, step);
+        add_sums(a, b, c);
+    }
+    if (lane == 0)
+        sh.sums[warp] = a;
+    __syncthreads();
+    Entry list = 0;
+    if (p.k > 0)
+        list = sh.count <= kCapacity ? select_entries(sh.entries, sh.count, sh.lists)
+                                     : select_slowly(row, lo, hi, p.k, sh);
+    if (warp == 0) {
+        a = sh.sums[0];
+        for (int w = 1; w < kWarps; ++w)
+            add_sums(a, sh.sums[w], c);
+        if (p.cluster > 1) {
+            sh.top[lane] = list;
+            if (lane == 0)
+                sh.all = a;
+        }
+    }
+    if (p.cluster > 1) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        if (rank == 0 && warp == 0)
+            for (int other = 1; other < p.cluster; ++other) {
+                const Shared *far = cluster.map_shared_rank(&sh, other);
+                add_sums(a, far->all, c);
+                if (p.k > 0)
+                    list = merge_lists(list, far->top[lane]);
+            }
+        cluster.sync();           // the others' shared memory lives until it was read
+    }
+    if (rank != 0 || warp != 0)
+        return;
+    const float s = a.s0 + a.s1, t = a.t0 + a.t1;
+    const float bits = log2f(s);                     // of the sum
+    const bool empty = s == 0.f;                     // nothing but -inf
+    auto log_prob = [&](float x) {       // of a logit
+        return empty ? -INFINITY : (float)(((double)x - a.most) * p.scale - kLn2 * bits);
+    };
+    if (lane == 0) {
+        p.lse[r] = empty ? -INFINITY : (float)((double)p.scale * a.most + kLn2 * bits);
+        p.entropy[r] = empty ? 0.f : (float)(kLn2 * (double)(bits - t / s));
+        const int token = p.tokens[r];
+        p.logprob[r] = (unsigned)token < (unsigned)p.vocab ? log_prob(to_float(logits[token])) : 0.f;
+    }
+    if (lane < p.k) {
+        const long long at = (long long)r * p.k + lane;
+        p.idx[at] = (int)~(unsigned)list;
+        p.top[at] = log_prob(value_of((unsigned)(list >> 32)));
+    }
+}
+
+// ---- gradient --------------------------------------------------------------------
+// dz_i = p_i (g_lse - g_logprob - sum g_top - g_entropy (log p_i + entropy)), plus
+// the token's and the alternatives' own gradients in their places, which are
+// written again by one thread each after the CTA's pass.  One read and one write
+// of the row, a CTA for each piece of it.
+struct GradArgs {
+    const void *logits;
+    void *grad;
+    long long stride, grad_stride;
+    const int32_t *tokens, *idx;
+    const float *lse, *entropy, *g_logprob, *g_entropy, *g_lse, *g_top;
+    int vocab, k, pieces;
+    unsigned each;                // vectors of a piece
+    float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float exponential(float x)
+{
+    // 16-bit results: the fast exponential's 2^-22 is far below their rounding
+    return sizeof(T) == 4 ? expf(x) : exp2_fast(x * kLog2e);
+}
+
+// log p = (x - base) scale - lse: base is 0, or the row's maximum where lse is so
+// large that its rounding would show in p.
+struct Factors {
+    float scale, base, lse, common, g_entropy, entropy;
+    bool empty;
+};
+
+template <typename T>
+__device__ __forceinline__ float slope(const Factors &f, float x)
+{
+    const float logp = fmaf(x - f.base, f.scale, -f.lse);
+    const float prob = exponential<T>(logp);
+    const float g = prob * (f.common - f.g_entropy * (logp + f.entropy));
+    return prob == 0.f || f.empty ? 0.f : g;
+}
+
+// lse is summed again from kLarge on, where its half unit in the last place is
+// 2^-15 of p.
+constexpr float kLarge = 1024.f;
+
+// Maximum of the row and log of its sum relative to that, by the CTA.
+template <typename T>
+__device__ __noinline__ void sum_again(const Row<T> &row, Factors &f, Sums *sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const float c = f.scale * kLog2e;
+    Sums a = {-INFINITY, 0.f, 0.f, 0.f, 0.f};
+    for (unsigned j = threadIdx.x; j < row.vectors; j += kThreads) {
+        const Vec<T> v = row.load(j, row.vectors);
+        const float most = largest(v);
+        if (most > a.most)
+            rescale(a, most, c);
+        add_vector(a, v, c);
+    }
+#pragma unroll
+    for (int step = 16; step; step /= 2) {
+        Sums b;
+        b.most = __shfl_xor_sync(~0u, a.most, step);
+        b.s0 = __shfl_xor_sync(~0u, a.s0, step), b.s1 = __shfl_xor_sync(~0u, a.s1, step);
+        b.t0 = __shfl_xor_sync(~0u, a.t0, step), b.t1 = __shfl_xor_sync(~0u, a.t1, step);
+        add_sums(a, b, c);
+    }
+    if (lane == 0)
+        sums[warp] = a;
+    __syncthreads();
+    a = sums[0];
+    for (int w = 1; w < kWarps; ++w)
+        add_sums(a, sums[w], c);
+    f.empty = a.s0 + a.s1 == 0.f;
+    f.base = f.empty ? 0.f : a.most;
+    f.lse = (float)(kLn2 * (double)log2f(a.s0 + a.s1));
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads)
+gradient_kernel(const __grid_constant__ GradArgs p)
+{
+    __shared__ int place[kTop + 1];
+    __shared__ float share[kTop + 1];
+    __shared__ Sums sums[kWarps];
+    dependent_grid_wait();
+    allow_dependent_grid();
+    const int lane = threadIdx.x & 31;
+    const unsigned r = blockIdx.x / p.pieces, piece = blockIdx.x - r * p.pieces;
+    const T *logits = (const T *)p.logits + (long long)r * p.stride;
+    T *grad = (T *)p.grad + (long long)r * p.grad_stride;
+    const Row<T> row(logits, p.vocab);
+    const unsigned lo = piece * p.each, hi = lo + p.each < row.vectors ? lo + p.each : row.vectors;
+
+    const int token = p.tokens[r];
+    const bool given = (unsigned)token < (unsigned)p.vocab;
+    const float g_logprob = p.g_logprob && given ? p.g_logprob[r] : 0.f;
+    float g_top = 0.f;
+    int top_at = -1;
+    if (lane < p.k) {
+        top_at = p.idx[(long long)r * p.k + lane];
+        if ((unsigned)top_at < (unsigned)p.vocab)
+            g_top = p.g_top[(long long)r * p.k + lane];
+        else
+            top_at = -1;
+    }
+    float sum = g_top;
+#pragma unroll
+    for (int step = 16; step; step /= 2)
+        sum += __shfl_xor_sync(~0u, sum, step);
+    Factors f;
+    f.scale = p.scale;
+    f.lse = p.lse[r];
+    f.base = 0.f;
+    f.empty = false;
+    f.entropy = p.entropy[r];
+    f.g_entropy = p.g_entropy ? p.g_entropy[r] : 0.f;
+    f.common = (p.g_lse ? p.g_lse[r] : 0.f) - g_logprob - sum;
+
+    // the token and the alternatives: their logits are read before anything of
+    // the row is written, which may be in their place
+    float own = 0.f;
+    int at = -1;
+    if (threadIdx.x <= (unsigned)p.k) {
+        at = threadIdx.x < (unsigned)p.k ? top_at : given ? token : -1;
+        place[threadIdx.x] = at;
+        share[threadIdx.x] = threadIdx.x < (unsigned)p.k ? g_top : g_logprob;
+        if (at >= 0)
+            own = to_float(logits[at]);
+    }
+    if (fabsf(f.lse) >= kLarge)
+        sum_again(row, f, sums);
+    __syncthreads();
+
+    for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
+        const Vec<T> v = row.load(j, hi);
+        Vec<T> out;
+#pragma unroll
+        for (int e = 0; e < Vec<T>::kCount; ++e)
+            from_float(out.x[e], slope<T>(f, to_float(v.x[e])) * f.scale);
+        const long long first = (long long)j * Vec<T>::kCount - row.skip;
+        if (kVec && row.whole(j)) {
+            *reinterpret_cast<Vec<T> *>(grad + first) = out;
+        } else {
+#pragma unroll
+            for (int e = 0; e < Vec<T>::kCount; ++e)
+                if (first + e >= 0 && first + e < p.vocab)
+                    grad[first + e] = out.x[e];
+        }
+    }
+    __syncthreads();
+    if (at >= 0) {
+        const unsigned j = (at + row.skip) / Vec<T>::kCount;
+        bool mine = j >= lo && j < hi;
+        for (int i = 0; i < (int)threadIdx.x; ++i)
+            mine = mine && place[i] != at;             // the first of equal ones
+        if (mine) {
+            float g = slope<T>(f, own);
+            for (int i = threadIdx.x; i <= p.k; ++i)
+                if (place[i] == at)
+                    g += share[i];
+            if (f.empty)
+                g = 0.f;
+            from_float(grad[at], g * f.scale);
+        }
+    }
+}
+
+// CTAs of a row: one where rows alone fill the GPU, else as many as give slices of
+// at least kSlice vectors a thread.
+constexpr int kSlice = 2 * kAhead;
+
+template <typename T>
+cudaError_t launch_forward(Args &p, long long rows, int sms, cudaStream_t stream)
+{
+    p.cluster = 1;
+    const long long vectors = (p.vocab + Vec<T>::kCount - 1) / Vec<T>::kCount;
+    while (p.cluster < 8 && rows * p.cluster < 2LL * sms &&
+           vectors >= 2LL * p.cluster * kSlice * kThreads)
+        p.cluster *= 2;
+    return launch_clusters(logprob_kernel<T>, p.cluster, (unsigned)(rows * p.cluster), kThreads, 0, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_gradient(GradArgs &p, long long rows, int sms, cudaStream_t stream)
+{
+    const long long vectors = (p.vocab + 2LL * Vec<T>::kCount - 2) / Vec<T>::kCount;   // at most
+    // in its own place a row is one CTA's, which may have to read it twice
+    long long pieces = 1;
+    while (p.grad != p.logits && rows * pieces < 16LL * sms && vectors > pieces * kThreads * 2)
+        pieces *= 2;
+    p.each = (unsigned)((vectors + pieces - 1) / pieces);
+    p.pieces = (int)pieces;
+    const size_t size = sizeof(T);
+    // rows of the gradient start where those of the logits do within 16 bytes
+    const bool vec = (uintptr_t)p.grad % 16 == (uintptr_t)p.logits % 16 &&
+                     (rows < 2 || p.grad_stride * size % 16 == p.stride * size % 16);
+    auto fn = vec ? gradient_kernel<T, true> : gradient_kernel<T, false>;
+    return launch_overlapped(fn, (unsigned)(rows * pieces), kThreads, 0, stream, p);
+}
+
+int check(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int32_t *tokens,
+          int k, float scale)
+{
+    if (dtype != DS_FP32 && dtype != DS_BF16 && dtype != DS_FP16)
+        return fail(DS_EUNSUPPORTED, "dtype %d is not DS_FP32 (0), DS_BF16 (1) or DS_FP16 (2)", dtype);
+    if (rows < 0 || vocab < 1)
+        return fail(DS_EINVAL, "rows = %lld must be >= 0 and vocab = %lld >= 1", (long long)rows,
+                    (long long)vocab);
+    if (vocab >= DS_LOGPROB_MAX_VOCAB || rows >= 1LL << 27)
+        return fail(DS_EUNSUPPORTED, "rows = %lld and vocab = %lld must be below 2^27 and 2^31 - 64",
+                    (long long)rows, (long long)vocab);
+    if (rows > 1 && stride < vocab)
+        return fail(DS_EINVAL, "row_stride = %lld is below vocab = %lld", (long long)stride, (long long)vocab);
+    if (k < 0 || k > vocab)
+        return fail(DS_EINVAL, "k = %d must be >= 0 and at most vocab = %lld", k, (long long)vocab);
+    if (k > DS_LOGPROB_MAX_K)
+        return fail(DS_EUNSUPPORTED, "k = %d is above %d", k, DS_LOGPROB_MAX_K);
+    if (!(scale > 0.f) || !(scale < INFINITY))
+        return fail(DS_EINVAL, "scale = %g must be finite and above 0", scale);
+    if (rows == 0)
+        return DS_OK;
+    if (!logits || !tokens)
+        return fail(DS_EINVAL, "logits and tokens must be non-NULL when rows > 0");
+    if ((uintptr_t)logits % (dtype == DS_FP32 ? 4 : 2) != 0)
+        return fail(DS_EINVAL, "logits must be aligned to its elements");
+    return DS_OK;
+}
+
+}  // namespace
+}  // namespace logprob
+}  // namespace ds
+
+extern "C" {
+
+int ds_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t vocab,
+                      int64_t row_stride, const int32_t *tokens, int k, float scale,
+                      float *logprob, float *entropy, float *lse, int32_t *idx, float *top,
+                      void *stream)
+{
+    using namespace ds::logprob;
+    ds::g_detail[0] = '\0';
+    int dev = 0, sms = 0, rc = check(logits, dtype, rows, vocab, row_stride, tokens, k, scale);
+    if (rc != DS_OK || rows == 0)
+        return rc;
+    if (!logprob || !entropy || !lse || (k > 0 && (!idx || !top)))
+        return ds::fail(DS_EINVAL, "logprob, entropy and lse, and with k > 0 idx and top, must be non-NULL");
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
+        return rc;
+    Args p = {logits, row_stride, tokens, logprob, entropy, lse, top, idx, (int)vocab, k, 1, scale};
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = dtype == DS_FP32   ? launch_forward<float>(p, rows, sms, s)
+                          : dtype == DS_BF16 ? launch_forward<__nv_bfloat16>(p, rows, sms, s)
+                                             : launch_forward<__half>(p, rows, sms, s);
+    return e == cudaSuccess ? DS_OK : ds::fail_cuda(e, "ds_token_logprobs");
+}
+
+int ds_token_logprobs_backward(const void *logits, int dtype, int64_t rows, int64_t vocab,
+                               int64_t row_stride, const int32_t *tokens, int k,
+                               const int32_t *idx, float scale, const float *lse,
+                               const float *entropy, const float *grad_logprob,
+                               const float *grad_entropy, const float *grad_lse,
+                               const float *grad_top, void *grad, int64_t grad_stride,
+                               void *stream)
+{
+    using namespace ds::logprob;
+    ds::g_detail[0] = '\0';
+    int dev = 0, sms = 0, rc = check(logits, dtype, rows, vocab, row_stride, tokens, k, scale);
+    if (rc != DS_OK)
+        return rc;
+    if (rows > 1 && grad_stride < vocab)
+        return ds::fail(DS_EINVAL, "grad_stride = %lld is below vocab = %lld", (long long)grad_stride,
+                        (long long)vocab);
+    if (rows == 0)
+        return DS_OK;
+    if (!lse || !entropy || !grad || (grad_top && k > 0 && !idx))
+        return ds::fail(DS_EINVAL, "lse, entropy and grad, and with grad_top idx, must be non-NULL");
+    if ((uintptr_t)grad % (dtype == DS_FP32 ? 4 : 2) != 0)
+        return ds::fail(DS_EINVAL, "grad must be aligned to its elements");
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
+        return rc;
+    GradArgs p = {logits, grad, row_stride, grad_stride, tokens, idx, lse, entropy, grad_logprob,
+                  grad_entropy, grad_lse, grad_top, (int)vocab, grad_top ? k : 0, 1, 0, scale};
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = dtype == DS_FP32   ? launch_gradient<float>(p, rows, sms, s)
+                          : dtype == DS_BF16 ? launch_gradient<__nv_bfloat16>(p, rows, sms, s)
+                                             : launch_gradient<__half>(p, rows, sms, s);
+    return e == cudaSuccess ? DS_OK : ds::fail_cuda(e, "ds_token_logprobs_backward");
+}
+
+}  // extern "C"
