@@ -130,6 +130,44 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
 int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queries, int heads,
                                int k, size_t *bytes);
 
+/*
+ * ds_kv4_chunk_attention -- the same for chunks of new tokens, as many for each
+ * sequence as it has: prompts, or parts of them, read after what their sequences
+ * hold already (a few tokens a sequence, one among them, are ds_kv4_attention's).
+ *   starts    device int32[batch + 1]: rows [starts[b], starts[b + 1]) of q and out
+ *             are the newest tokens of entry b's sequence, which ds_kv4_append has
+ *             put into the cache; row j of n of a sequence of L tokens sees the
+ *             tokens below max(0, L - n + 1 + j).  Below 0 they are read as 0,
+ *             beyond `tokens` as that, and where they fall as the largest so far;
+ *             rows of no entry are left as they were
+ *   batch, seqs, lengths  as in ds_kv4_attention
+ *   tokens    rows of q and out
+ *   heads     query heads, a multiple of kv_heads
+ *   dtype     of q and out: DS_BF16 or DS_FP16
+ *   q         device, unit stride in the last dimension, q_stride = {token, head}
+ *             strides in elements; 16 bytes at a time where these allow it
+ *   scale     any number
+ *   out       device [tokens][heads][head_dim], contiguous, 16-byte aligned
+ *   lse       device float[tokens][heads], or NULL
+ *   workspace device, 16-byte aligned, of ds_kv4_chunk_attention_workspace bytes
+ * max_pages * page_size is below 2^31 - 128.  A query that sees no token gives
+ * out = 0 and lse = -inf.  Scores are sums in 32 bits of exact products; with
+ * DS_FP16, a key's channel is exact to 2^-25 at least, and one of a key or value
+ * whose scale is beyond 9352 (channels beyond fp16) is taken with that.  A
+ * probability, and a value, are rounded to `dtype` before they are multiplied;
+ * maxima, sums and outputs are held in 32 bits.  A row with a NaN or an infinity
+ * gives NaN if it sees a token.  (Waits are limited to a second, which no working
+ * GPU takes; after that results are NaN.)
+ */
+int ds_kv4_chunk_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const int32_t *seqs,
+                           const int32_t *starts, int batch, int64_t tokens, int heads, int dtype,
+                           const void *q, const int64_t *q_stride, float scale, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of ds_kv4_chunk_attention on the current device for these sizes. */
+int ds_kv4_chunk_attention_workspace(const ds_kv4_cache_t *cache, int batch, int64_t tokens, int heads,
+                                     size_t *bytes);
+
 /* ---- pages -----------------------------------------------------------------
  * The page functions serve caches of any content: a page is page_bytes bytes
  * in each layer. */

@@ -127,6 +127,50 @@ def attention(q, pool, table, lengths, scale, indices=None, seqs=None):
     return out, lse, spread, reach
 
 
+def rising(starts, tokens):
+    """Starts of chunks as they are read: within [0, tokens], and never falling."""
+    return np.maximum.accumulate(np.clip(np.asarray(starts, dtype=np.int64), 0, tokens))
+
+
+def chunk_attention(q, pool, table, lengths, starts, scale, seqs=None):
+    """(out, lse, spread, reach) in 64 bits of float64 q [tokens, H, D]: rows starts[b] to
+    starts[b + 1] are the newest tokens of entry b's sequence.  Rows of no entry are NaN.
+
+    spread and reach as in attention(), reach without the codes' offset."""
+    tokens, heads, dim = q.shape
+    n_pages, hk, page, _ = pool.shape
+    group = heads // hk
+    out, spread = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
+    lse, reach = np.full(q.shape[:2], np.nan), np.full(q.shape[:2], np.nan)
+    starts = rising(starts, tokens)
+    for b in range(len(starts) - 1):
+        seq = b if seqs is None else int(seqs[b])
+        length = int(lengths[seq]) if 0 <= seq < table.shape[0] else 0
+        length = max(0, min(length, table.shape[1] * page))
+        home, off, there = slots(table, n_pages, page, seq, np.arange(length))
+        k, v = decode(pool[np.where(there, home, 0), :, off], dim)       # [length, hk, D]
+        first, n = starts[b], starts[b + 1] - starts[b]
+        for j in range(n):
+            seen = there[:max(0, length - n + 1 + j)]
+            row = first + j
+            out[row], spread[row], lse[row], reach[row] = 0, 0, -np.inf, 0
+            if not seen.any():
+                continue
+            for g in range(hk):
+                x, kk, vv = q[row, g * group:(g + 1) * group], k[:len(seen), g][seen], v[:len(seen), g][seen]
+                with np.errstate(all="ignore"):
+                    s = scale * (x @ kk.T)
+                    m = s.max(-1, keepdims=True)
+                    p = np.exp(s - m)
+                    total = p.sum(-1, keepdims=True)
+                    at = slice(g * group, (g + 1) * group)
+                    out[row, at] = p @ vv / total
+                    spread[row, at] = p @ np.abs(vv) / total
+                    lse[row, at] = (m + np.log(total))[:, 0]
+                    reach[row, at] = abs(scale) * (np.abs(x) @ np.abs(kk).T).max(-1)
+    return out, lse, spread, reach
+
+
 class Book:
     """The pages' bookkeeping, one step at a time."""
 

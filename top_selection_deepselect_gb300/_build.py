@@ -11,11 +11,14 @@ SOURCES = [os.path.join(CSRC, f) for f in ("ds_topk.cu", "ds_kernels_fp32.cu", "
                                          "ds_kernels_fp16.cu", "ds_kv4.cu", "ds_kv4_store.cu",
                                          "ds_kv4_attention.cu", "ds_kv4_attention_64.cu",
                                          "ds_kv4_attention_128.cu", "ds_kv4_attention_256.cu",
+                                         "ds_kv4_chunk.cu", "ds_kv4_chunk_64.cu",
+                                         "ds_kv4_chunk_128.cu", "ds_kv4_chunk_256.cu",
                                          "ds_pages.cu", "ds_logprob.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ds_device.cuh"), os.path.join(CSRC, "ds_kernel.cuh"),
                   os.path.join(CSRC, "ds_stream.cuh"), os.path.join(CSRC, "ds_host.h"),
                   os.path.join(CSRC, "ds_kv4.cuh"), os.path.join(CSRC, "ds_kv4_launch.h"),
                   os.path.join(CSRC, "ds_kv4_attention.cuh"),
+                  os.path.join(CSRC, "ds_kv4_chunk.cuh"), os.path.join(CSRC, "ds_kv4_chunk.h"),
                   os.path.join(INCLUDE, "ds_topk.h"), os.path.join(INCLUDE, "ds_kv4.h"),
                   os.path.join(INCLUDE, "ds_logprob.h")]
 

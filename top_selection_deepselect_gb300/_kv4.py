@@ -13,7 +13,8 @@ import struct
 from ._binding import DS_BF16, DS_FP16, DS_FP32, _check, load_library
 
 KV4_ENTRY_POINTS = ["ds_kv4_record_bytes", "ds_kv4_append", "ds_kv4_read", "ds_kv4_attention",
-                    "ds_kv4_attention_workspace", "ds_pages_copy", "ds_pages_reserve",
+                    "ds_kv4_attention_workspace", "ds_kv4_chunk_attention",
+                    "ds_kv4_chunk_attention_workspace", "ds_pages_copy", "ds_pages_reserve",
                     "ds_pages_fork", "ds_pages_free", "ds_pages_compact", "ds_pages_workspace"]
 
 
@@ -56,6 +57,9 @@ def _lib():
             "ds_kv4_attention": [cache, vp, vp, i32, i32, i32, i32, vp, _strides3, vp, i32,
                                  ctypes.c_float, vp, vp, vp, size, vp],
             "ds_kv4_attention_workspace": [cache, i32, i32, i32, i32, ctypes.POINTER(size)],
+            "ds_kv4_chunk_attention": [cache, vp, vp, vp, i32, i64, i32, i32, vp, _strides2,
+                                       ctypes.c_float, vp, vp, vp, size, vp],
+            "ds_kv4_chunk_attention_workspace": [cache, i32, i64, i32, ctypes.POINTER(size)],
             "ds_pages_copy": [pool, vp, vp, i32, vp],
             "ds_pages_reserve": [book, vp, vp, i32, vp, vp, size, vp],
             "ds_pages_fork": [pool, book, vp, vp, i32, vp, vp, size, vp],
@@ -98,6 +102,21 @@ def ds_kv4_attention_workspace(cache, batch, queries, heads, k):
     n = ctypes.c_size_t(0)
     _check(_lib().ds_kv4_attention_workspace(cache, batch, queries, heads, k, ctypes.byref(n)),
            "ds_kv4_attention_workspace")
+    return n.value
+
+
+def ds_kv4_chunk_attention(cache, lengths, seqs, starts, batch, tokens, heads, dtype, q, q_stride,
+                           scale, out, lse, workspace, workspace_bytes, stream):
+    return _check(_lib().ds_kv4_chunk_attention(cache, lengths, seqs, starts, batch, tokens, heads,
+                                                dtype, q, _strides2(*q_stride), scale, out, lse,
+                                                workspace, workspace_bytes, stream),
+                  "ds_kv4_chunk_attention")
+
+
+def ds_kv4_chunk_attention_workspace(cache, batch, tokens, heads):
+    n = ctypes.c_size_t(0)
+    _check(_lib().ds_kv4_chunk_attention_workspace(cache, batch, tokens, heads, ctypes.byref(n)),
+           "ds_kv4_chunk_attention_workspace")
     return n.value
 
 
@@ -168,6 +187,8 @@ class _Torch:
         self.read = bytes_for("ds_kv4_read", (0,))
         self.attention = bytes_for("ds_kv4_attention", (0, 8))
         self.workspace = bytes_for("ds_kv4_attention_workspace", (0,))
+        self.chunk = bytes_for("ds_kv4_chunk_attention", (0, 9))
+        self.chunk_workspace = bytes_for("ds_kv4_chunk_attention_workspace", (0,))
         self.copy = bytes_for("ds_pages_copy", (0,))
         self.reserve = bytes_for("ds_pages_reserve", (0,))
         self.fork = bytes_for("ds_pages_fork", (0, 1))
@@ -331,10 +352,14 @@ def _attention_workspace(cache, batch, queries, heads, k, key):
     n = ctypes.c_size_t(0)
     _check(_t.workspace(cache, batch, queries, heads, k, ctypes.byref(n)),
            "ds_kv4_attention_workspace")
+    return _remember(key, n.value)
+
+
+def _remember(key, size):
     if len(_attention_bytes) > 10000:
         _attention_bytes.clear()
-    _attention_bytes[key] = n.value
-    return n.value
+    _attention_bytes[key] = size
+    return size
 
 
 def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, out=None, lse=None,
@@ -410,6 +435,76 @@ def kv4_attention(q, pool, table, lengths, indices=None, scale=None, seqs=None, 
                          None if workspace is None else workspace.data_ptr(), size, t.raw_stream(index))
     if status:
         _check(status, "ds_kv4_attention")
+    return out, lse
+
+
+def kv4_chunk_attention(q, pool, table, lengths, starts, scale=None, seqs=None, out=None, lse=None,
+                        workspace=None, stream=None):
+    """Attention of chunks of new tokens, as many for each sequence as it has, over the cache.
+
+    q: [tokens, heads, head_dim] bfloat16 or float16, unit stride in the last
+    dimension; rows starts[b] to starts[b + 1] (int32 [batch + 1], rising) are the
+    newest tokens of sequence seqs[b] (int32 [batch]), or b, which kv4_append has put
+    into the cache: row j of n of a sequence of L tokens (lengths, int32 [max_seqs])
+    sees those below L - n + 1 + j.  scale defaults to 1 / sqrt(head_dim).  Returns
+    (out, lse): out like q, lse float32 [tokens, heads]; a row that sees nothing gives 0
+    and -inf, rows of no sequence are left as they were.
+    """
+    t = _t if _t.ready else _t.find()
+    index = _cuda("pool", pool)
+    if stream is not None or index != t.current():
+        return _elsewhere(t, index, stream, kv4_chunk_attention,
+                          q, pool, table, lengths, starts, scale, seqs, out, lse, workspace)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or q.get_device() != index:
+        raise ValueError("q must be [tokens, heads, head_dim] on the pool's device")
+    tokens, heads, dim = shape
+    q0, q1, q2 = q.stride()
+    if q2 != 1:
+        raise ValueError("q must have unit stride in the last dimension")
+    cache = _cache(pool, table, dim, index)
+    code = t.codes.get(dtype)
+    if code is None:
+        raise TypeError("q must be bfloat16 or float16, got %s" % dtype)
+    rows = table.shape[0]
+    at, starts_at = _int32("lengths", lengths, index, rows), _int32("starts", starts, index)
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be [batch + 1]")
+    batch = starts.shape[0] - 1
+    seqs_at = None
+    if seqs is not None:
+        seqs_at = _int32("seqs", seqs, index, batch)
+    elif batch > rows:
+        raise ValueError("batch = %d is above the table's %d sequences" % (batch, rows))
+    if out is None:
+        out = t.empty(shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    if lse is None:
+        lse = t.empty((tokens, heads), dtype=t.float32, device=q.device)
+    elif (lse.shape != shape[:2] or lse.dtype != t.float32 or lse.get_device() != index
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    key = (index, shape, batch, pool.shape, table.shape)
+    size = _attention_bytes.get(key)
+    if size is None:
+        n = ctypes.c_size_t(0)
+        _check(t.chunk_workspace(cache, batch, tokens, heads, ctypes.byref(n)),
+               "ds_kv4_chunk_attention_workspace")
+        size = _remember(key, n.value)
+    if workspace is None:
+        if size:
+            workspace = t.empty(size, dtype=t.uint8, device=q.device)
+    else:
+        given = _space("workspace", workspace, index)
+        if given < size:
+            raise ValueError("workspace has %d bytes, %d needed" % (given, size))
+    status = t.chunk(cache, at, seqs_at, starts_at, batch, tokens, heads, code, q.data_ptr(),
+                     _pack_2(q0, q1), dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                     lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
+                     t.raw_stream(index))
+    if status:
+        _check(status, "ds_kv4_chunk_attention")
     return out, lse
 
 

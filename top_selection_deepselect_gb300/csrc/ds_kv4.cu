@@ -86,6 +86,21 @@ int check_attention(const Cache &c, int batch, int queries, int heads, int k)
     return DS_OK;
 }
 
+int check_chunk(const Cache &c, int batch, int64_t tokens, int heads)
+{
+    if (batch < 0 || tokens < 0 || heads < 1)
+        return fail(DS_EINVAL, "batch = %d, tokens = %lld must be >= 0 and heads = %d >= 1", batch,
+                    (long long)tokens, heads);
+    if (heads % c.kv_heads != 0)
+        return fail(DS_EINVAL, "heads = %d is not a multiple of kv_heads = %d", heads, c.kv_heads);
+    if (tokens >= 1LL << 31 || tokens * heads >= 1LL << 31)
+        return fail(DS_EUNSUPPORTED, "tokens * heads = %lld * %d is not below 2^31", (long long)tokens, heads);
+    if ((long long)c.max_pages * c.page_size >= (1LL << 31) - 128)
+        return fail(DS_EUNSUPPORTED, "max_pages * page_size = %lld is not below 2^31 - 128",
+                    (long long)c.max_pages * c.page_size);
+    return DS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +231,75 @@ int ds_kv4_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const 
     const cudaError_t e = ds::kv4::launch_attention(c, cache->head_dim, a, dev, sms,
                                                     (cudaStream_t)stream);
     return e == cudaSuccess ? DS_OK : fail_cuda(e, "ds_kv4_attention");
+}
+
+int ds_kv4_chunk_attention_workspace(const ds_kv4_cache_t *cache, int batch, int64_t tokens, int heads,
+                                     size_t *bytes)
+{
+    ds::g_detail[0] = '\0';
+    Cache c;
+    int rc = check_cache(cache, &c), dev = 0, sms = 0;
+    if (rc == DS_OK)
+        rc = check_chunk(c, batch, tokens, heads);
+    if (rc != DS_OK)
+        return rc;
+    if (!bytes)
+        return fail(DS_EINVAL, "bytes must be non-NULL");
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
+        return rc;
+    ds::kv4::Chunk a = {};
+    a.batch = batch;
+    a.tokens = (int)tokens;
+    a.heads = heads;
+    *bytes = batch == 0 || tokens == 0 ? 0 : ds::kv4::chunk_workspace(c, cache->head_dim, a, sms);
+    return DS_OK;
+}
+
+int ds_kv4_chunk_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, const int32_t *seqs,
+                           const int32_t *starts, int batch, int64_t tokens, int heads, int dtype,
+                           const void *q, const int64_t *q_stride, float scale, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    ds::g_detail[0] = '\0';
+    Cache c;
+    int rc = check_cache(cache, &c), dev = 0, sms = 0;
+    if (rc == DS_OK)
+        rc = check_chunk(c, batch, tokens, heads);
+    if (rc != DS_OK)
+        return rc;
+    if (dtype != DS_BF16 && dtype != DS_FP16)
+        return fail(DS_EUNSUPPORTED, "dtype %d is not DS_BF16 (1) or DS_FP16 (2)", dtype);
+    if (!q_stride)
+        return fail(DS_EINVAL, "q_stride must be non-NULL");
+    if (batch == 0 || tokens == 0)
+        return DS_OK;
+    if (!lengths || !starts || !q || !out)
+        return fail(DS_EINVAL, "lengths, starts, q and out must be non-NULL when batch and tokens are > 0");
+    if ((uintptr_t)q % 2 != 0 || (uintptr_t)out % 16 != 0)
+        return fail(DS_EINVAL, "q must be aligned to its elements and out to 16 bytes");
+    if ((rc = ds::current_device(&dev, &sms)) != DS_OK)
+        return rc;
+    ds::kv4::Chunk a;
+    a.lengths = lengths;
+    a.seqs = seqs;
+    a.starts = starts;
+    a.q = q;
+    a.q_query = q_stride[0];
+    a.q_head = q_stride[1];
+    a.out = out;
+    a.lse = lse;
+    a.scale = scale;
+    a.batch = batch;
+    a.heads = heads;
+    a.tokens = (int)tokens;
+    a.bf16 = dtype == DS_BF16;
+    const size_t need = ds::kv4::chunk_workspace(c, cache->head_dim, a, sms);
+    if (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need)
+        return fail(DS_EINVAL, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)",
+                    need, workspace_bytes);
+    const cudaError_t e = ds::kv4::launch_chunk(c, cache->head_dim, a, workspace, dev, sms,
+                                                (cudaStream_t)stream);
+    return e == cudaSuccess ? DS_OK : fail_cuda(e, "ds_kv4_chunk_attention");
 }
 
 }  // extern "C"

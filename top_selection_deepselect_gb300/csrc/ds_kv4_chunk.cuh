@@ -1,0 +1,1088 @@
+// ds_kv4_chunk.cuh -- attention of chunks of new tokens over the 4-bit cache.
+//
+// A chunk has many query rows for each key/value head, so that the products
+// bound it and not the records: S = Q K^T and O = P V go to the fifth-generation
+// tensor cores, 128 rows and 64 tokens at a time, with Q, S, P and O in tensor
+// memory and the expanded keys and values in shared memory.
+//
+// Rows.  The (query, head) pairs of a key/value head's group, head fastest, are
+// the rows of one problem; a unit is a block of up to kTiles x 128 of them.  With
+// two tiles of rows the tensor cores work on one while the other's softmax is
+// taken; a tile of tokens is expanded once for both.
+//
+// Exact scores.  A key's channel is (u - 8) scale, three bits times eleven, which
+// does not fit a 16-bit operand.  The scale is split into two numbers of few
+// enough bits that both products are exact, and S is the sum of Q times each:
+// half as many operations more, and log-sums as exact as 32-bit arithmetic has
+// them.  Queries stay as they are: the operands' type is theirs.  Values are
+// rounded to that type once, as the probabilities are.
+//
+// Codes become operands by a logical operation and a packed addition: a code u in
+// the low bits of an fp16 of 1024 (bf16 of 128) makes it 1024 + u (128 + u), and
+// subtracting 1032 (136) leaves u - 8.  A word of eight key codes gives channels
+// (j, j + 4) in pairs; the queries are laid out in the same order.  A value's
+// word is taken with that of the next token, so that pairs are (token, token + 1)
+// of one channel: both operands end up with the summed index contiguous.
+//
+// Roles of a CTA's warps: softmax (four warps a tile of rows, a row a thread),
+// expansion of keys and of values (four warps each), one that issues the products,
+// one that copies records.  They meet on arrival barriers in shared memory only.
+//
+// Work is a line of places: every (unit, head) has a place for each of its tiles
+// of tokens and row tiles and kUnitCost for its start and end; CTAs, one an SM,
+// take equal stretches.  Units cut between CTAs leave partial results for a second
+// launch.  Lengths and starts are read on the device by a first, small launch.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "ds_device.cuh"
+#include "ds_host.h"
+#include "ds_kv4.cuh"
+#include "ds_kv4_chunk.h"
+#include "ds_kv4_launch.h"
+
+namespace ds {
+namespace kv4 {
+namespace chunk {
+
+constexpr int kTokens = 64;            // of a tile
+constexpr int kTileRows = 128;         // query rows of a product
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Shape {
+    static constexpr int kTiles = tiles_of_rows(D);
+    static constexpr int kRows = kTiles * kTileRows;
+    static constexpr int kRecord = record_bytes(D);
+    // Records lie in shared memory in groups of eight tokens, 16 bytes further
+    // apart than their size: the eight lanes of a load then meet different banks.
+    static constexpr int kGroupBytes = 8 * kRecord + 16;
+    static constexpr int kRawBytes = kTokens / 8 * kGroupBytes;
+    static constexpr int kKeyBytes = kTokens * D * 2;          // of one part of the split
+    static constexpr int kValueBytes = kTokens * D * 2;
+    static constexpr int kKeyStages = D == 256 ? 2 : 3;
+    static constexpr int kValueStages = D == 256 ? 2 : 3;
+    static constexpr int kRawStages = D == 256 ? 1 : 3;
+    // warps
+    static constexpr int kSoftmaxWarps = 4 * kTiles;
+    static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4;
+    static constexpr int kProductWarp = kValueWarp + 4, kCopyWarp = kProductWarp + 1;
+    static constexpr int kThreads = 32 * (kCopyWarp + 1);
+    // columns of tensor memory
+    static constexpr int kOutColumn = 0;
+    static constexpr int kScoreColumn = kTiles * D;             // two of them
+    static constexpr int kQueryColumn = kScoreColumn + 2 * kTokens;
+    static_assert(kQueryColumn + kTiles * D / 2 <= 512, "tensor memory");
+    // shared memory, from a 1024-byte boundary
+    static constexpr int kOffKeys = 0;
+    static constexpr int kOffValues = kOffKeys + kKeyStages * 2 * kKeyBytes;
+    static constexpr int kOffRaw = kOffValues + kValueStages * kValueBytes;
+    static constexpr int kUsed = kOffRaw + kRawStages * kRawBytes + 1024;
+    // tensor memory is taken whole, so that a second CTA would only wait for it
+    static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static_assert(kSmem <= 230 * 1024, "shared memory of an SM");
+    static constexpr int kPartial = kRows * (D + 2);            // floats of a partial result
+};
+
+// ---- barriers ---------------------------------------------------------------------
+__device__ __forceinline__ uint32_t shared_at(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_done(uint32_t bar, unsigned phase)
+{
+    unsigned done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(phase) : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ long long clock_ns()
+{
+    long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Nanoseconds that anything is waited for, far beyond what a working GPU takes.
+constexpr long long kPatience = 1000000000;
+
+// Waits for a phase to end.  *lost: a wait was given up, by whichever warp; nothing
+// is waited for any more, and results are NaN.
+__device__ __forceinline__ void bar_wait(uint32_t bar, unsigned phase, volatile int *lost)
+{
+    if (bar_done(bar, phase))
+        return;
+    const long long from = clock_ns();
+    while (!bar_done(bar, phase)) {
+        if (*lost)
+            return;
+        if (clock_ns() - from > kPatience) {
+            *lost = 1;
+            return;
+        }
+    }
+}
+
+// Turn of a ring of n stages: which stage, and the phase its next use ends.
+template <int n>
+struct Turn {
+    int stage = 0;
+    unsigned phase = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++stage == n)
+            stage = 0, phase ^= 1;
+    }
+};
+
+// ---- tensor memory and products --------------------------------------------------
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of the warp's 32 rows, a row a lane.
+__device__ __forceinline__ void load_columns(uint32_t (&x)[32], uint32_t at)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+        "%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+          "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]),
+          "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]),
+          "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]),
+          "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+        "%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]),
+        "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(x[16]),
+        "r"(x[17]), "r"(x[18]), "r"(x[19]), "r"(x[20]), "r"(x[21]), "r"(x[22]), "r"(x[23]), "r"(x[24]),
+        "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]), "r"(x[29]), "r"(x[30]), "r"(x[31])
+        : "memory");
+}
+
+// Operand in shared memory: rows of 128 bytes (64 numbers of the summed index),
+// eight of them a block of 1024 bytes, 16-byte pieces at place (piece ^ row % 8).
+__device__ __forceinline__ uint64_t operand_at(uint32_t at)
+{
+    return (uint64_t)((at & 0x3ffff) >> 4) | 1ULL << 16 | (uint64_t)(1024 >> 4) << 32 | 1ULL << 46 | 2ULL << 61;
+}
+// 16-bit operands of one type, 32-bit sums, 128 rows, n columns.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t product_of(int n)
+{
+    constexpr uint32_t type = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTileRows >> 4) << 24;
+}
+// D (+)= A B with A in tensor memory, 16 of the summed index.
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(what), "r"((int)add)
+                 : "memory");
+}
+// An arrival when all products issued so far are done.
+__device__ __forceinline__ void products_arrive(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---- expansion ----------------------------------------------------------------------
+// Pairs of 16-bit numbers, by type.
+template <typename T>
+struct Pair;
+
+template <>
+struct Pair<__half> {
+    // u - 8 of the codes in the low four bits of each half
+    static __device__ __forceinline__ uint32_t codes(uint32_t w)
+    {
+        uint32_t x, y;
+        asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
+        asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xe408e408u));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
+    {
+        uint32_t y;
+        asm("mul.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    // Scales whose values are beyond fp16 are taken as the largest one whose
+    // values are not: 9352 (NaN stays).
+    static __device__ __forceinline__ uint32_t bounded(uint32_t s)
+    {
+        uint32_t y;
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0x70917091u));
+        return y;
+    }
+    // s = hi + lo, eight significant bits and three: times a code of up to three
+    // bits both are exact.
+    static __device__ __forceinline__ void split(uint32_t s, uint32_t &hi, uint32_t &lo)
+    {
+        s = bounded(s);
+        hi = ((s & 0x7fff7fffu) + 0x00040004u) & 0xfff8fff8u;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(s), "r"(hi));
+    }
+    // Scales of two values as value() wants them.
+    struct Scale {
+        uint32_t s;
+    };
+    static __device__ __forceinline__ Scale scale(uint32_t s) { return {bounded(s)}; }
+    static __device__ __forceinline__ uint32_t value(uint32_t code, Scale s) { return times(code, s.s); }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t y;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+        return y;
+    }
+};
+
+template <>
+struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t codes(uint32_t w)
+    {
+        uint32_t x, y;
+        asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(x) : "r"(w));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3f803f80u), "r"(0xc308c308u));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
+    {
+        uint32_t y;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(0x80008000u));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t convert(uint32_t s)     // fp16 pair to bf16 pair
+    {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&s));
+        return pack(f.x, f.y);
+    }
+    // s = hi + lo, five significant bits each (the second with a sign): times a
+    // code of up to three bits both are exact.  (Scales from 65024 on, the last
+    // 32 steps of fp16, have six in lo.)  NaN is in lo.
+    static __device__ __forceinline__ void split(uint32_t s, uint32_t &hi, uint32_t &lo)
+    {
+        const uint32_t h = (__vminu2(s, 0x7bdf7bdfu) + 0x00200020u) & 0xffc0ffc0u;
+        uint32_t l;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(l) : "r"(s), "r"(h));
+        hi = convert(h);
+        lo = convert(l);
+    }
+    struct Scale {
+        uint32_t hi, lo;
+    };
+    static __device__ __forceinline__ Scale scale(uint32_t s)
+    {
+        Scale x;
+        split(s, x.hi, x.lo);
+        return x;
+    }
+    // rounded once: code lo is exact
+    static __device__ __forceinline__ uint32_t value(uint32_t code, Scale s)
+    {
+        uint32_t y;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(code), "r"(s.hi), "r"(times(code, s.lo)));
+        return y;
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t y;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+        return y;
+    }
+};
+
+// ---- the line of work -----------------------------------------------------------------
+// One head's share of a block of rows, and the tiles [t0, t1) of tokens in it that are
+// this CTA's.
+struct Part {
+    Block b;
+    int block, head, rows, row_tiles;
+    int see_lo, see_hi;        // tokens that the block's first and last row see
+    int tiles, t0, t1;
+    int later;                 // CTAs after this one that have tiles of it
+};
+
+struct Walk {
+    const Args &p;
+    long long x, end;
+    int block, head;
+    __device__ __forceinline__ Walk(const Args &args) : p(args)
+    {
+        const long long per = p.head->per;
+        x = per * blockIdx.x;
+        end = x + per < p.head->all ? x + per : p.head->all;
+        block = x < end ? p.first[blockIdx.x] : 0;
+        head = -1;
+    }
+    // The next part, false where there is none.
+    __device__ __forceinline__ bool next(Part &u)
+    {
+        while (x < end && block < p.head->blocks) {
+            const Block b = p.blocks[block];
+            const Span s = span_of(b, p.group, p.rows);
+            const int cost = cost_of(s);
+            const long long first = b.place * p.c.kv_heads;
+            if (head < 0) {
+                const long long h = (x - first) / cost;
+                head = (int)(h < 0 ? 0 : h);
+            }
+            if (head >= p.c.kv_heads) {
+                ++block;
+                head = 0;
+                continue;
+            }
+            const long long at = first + (long long)head * cost;
+            if (at >= end)
+                return false;
+            auto tile_at = [&](long long place) -> int {
+                const long long d = place - at - kUnitCost;
+                const long long t = d <= 0 ? 0 : s.row_tiles == 1 ? d : (d + 1) / 2;
+                return t < s.tiles ? (int)t : s.tiles;
+            };
+            u.b = b;
+            u.block = block;
+            u.head = head;
+            u.rows = s.rows;
+            u.row_tiles = s.row_tiles;
+            u.see_lo = s.see_lo;
+            u.see_hi = s.see_hi;
+            u.tiles = s.tiles;
+            u.t0 = tile_at(x);
+            u.t1 = tile_at(end);
+            u.later = 0;
+            if (u.t1 > u.t0 && u.t1 < s.tiles)
+                u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.row_tiles) / p.head->per) -
+                          (int)blockIdx.x;
+            ++head;
+            if (u.t1 > u.t0 || (s.tiles == 0 && at >= x))
+                return true;
+        }
+        return false;
+    }
+};
+
+constexpr int kSlots = 16;     // of what is known of a tile or a unit: more than any role is ahead
+
+struct Control {
+    unsigned long long raw_full[4], raw_empty[4], key_full[4], key_empty[4], value_full[4], value_empty[4];
+    unsigned long long query[2], score[2], weight[2], output[2], last;
+    unsigned long long there[kSlots];      // tokens of a tile that are there
+    int bad[kSlots][8];                    // of a unit: first position whose value scale is no number, a group
+    uint32_t tensor;
+    int lost;
+};
+
+// Row r of a unit: its query's row in q and out, the query head, how many tokens it sees.
+struct RowAt {
+    int token, head, limit;
+    __device__ __forceinline__ RowAt(const Args &p, const Part &u, int r)
+    {
+        const int e = u.b.row0 + (r < u.rows ? r : 0), j = p.by_group(e);
+        token = u.b.start + j;
+        head = u.head * p.group + (e - j * p.group);
+        const int see = u.b.len - u.b.n + 1 + j;
+        limit = r < u.rows && see > 0 ? see : 0;
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+chunk_kernel(const __grid_constant__ Args p)
+{
+    using S = Shape<D>;
+    constexpr int kGroups = D / kGroup, kPer = kGroups > 4 ? 4 : kGroups;   // groups, of a stretch
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Control ctl;
+    unsigned char *smem = smem_raw + (1024 - (shared_at(smem_raw) & 1023) & 1023);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) {
+            bar_init(shared_at(&ctl.raw_full[i]), 1);
+            bar_init(shared_at(&ctl.raw_empty[i]), 8);
+            bar_init(shared_at(&ctl.key_full[i]), 4);
+            bar_init(shared_at(&ctl.key_empty[i]), 1);
+            bar_init(shared_at(&ctl.value_full[i]), 4);
+            bar_init(shared_at(&ctl.value_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(shared_at(&ctl.query[i]), 4);
+            bar_init(shared_at(&ctl.score[i]), 1);
+            bar_init(shared_at(&ctl.weight[i]), 4);
+            bar_init(shared_at(&ctl.output[i]), 1);
+        }
+        bar_init(shared_at(&ctl.last), 1);
+        ctl.lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x < kSlots * 8)
+        ctl.bad[threadIdx.x / 8][threadIdx.x % 8] = 0x7fffffff;
+    if (warp == S::kProductWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         shared_at(&ctl.tensor)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tensor = ctl.tensor;
+    volatile int *lost = &ctl.lost;
+
+    dependent_grid_wait();
+    allow_dependent_grid();
+    if (threadIdx.x == 0)
+        p.splits[blockIdx.x].parts = 0;
+
+    Walk walk(p);
+    Part u;
+
+    if (warp == S::kCopyWarp) {
+        // ---- records ---------------------------------------------------------------
+        Turn<S::kRawStages> raw;
+        int count = 0;                            // tiles so far
+        const int runs = kTokens / p.run;
+        while (walk.next(u)) {
+            const int32_t *row = p.c.table + u.b.seq * p.c.table_stride;
+            const unsigned char *pool = p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
+            // pages of this lane's runs (at most two) of tile t
+            auto look = [&](int t, int (&page)[2]) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int pos = t * kTokens + (lane + 32 * i) * p.run;
+                    page[i] = -1;
+                    if (lane + 32 * i < runs && t < u.t1 && pos < u.see_hi)
+                        page[i] = row[p.c.by_page(pos)];
+                }
+            };
+            int page[2];
+            look(u.t0, page);
+            for (int t = u.t0; t < u.t1; ++t) {
+                int now[2] = {page[0], page[1]};
+                look(t + 1, page);
+                bar_wait(shared_at(&ctl.raw_empty[raw.stage]), raw.phase ^ 1, lost);
+                const bool stop = __any_sync(~0u, *lost);
+                unsigned long long there = 0;
+                bool ok[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int first = (lane + 32 * i) * p.run, left = u.see_hi - t * kTokens - first;
+                    ok[i] = (unsigned)now[i] < (unsigned)p.c.n_pages && !stop;
+                    if (ok[i])
+                        there |= (~0ULL >> (64 - (left < p.run ? left : p.run))) << first;
+                }
+                const unsigned copies = __popc(__ballot_sync(~0u, ok[0])) + __popc(__ballot_sync(~0u, ok[1]));
+                const unsigned lo = __reduce_or_sync(~0u, (unsigned)there);
+                const unsigned hi = __reduce_or_sync(~0u, (unsigned)(there >> 32));
+                const uint32_t bar = shared_at(&ctl.raw_full[raw.stage]);
+                if (lane == 0) {
+                    ctl.there[count % kSlots] = (unsigned long long)hi << 32 | lo;
+                    if (!stop)
+                        bar_expect(bar, copies * p.run * S::kRecord);
+                }
+                __syncwarp();
+                const uint32_t to = shared_at(smem + S::kOffRaw + raw.stage * S::kRawBytes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok[i])
+                        continue;
+                    const int first = (lane + 32 * i) * p.run, pos = t * kTokens + first;
+                    const int in_page = pos - p.c.by_page(pos) * p.c.page_size;
+                    asm volatile(
+                        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+                            "r"(to + first / 8 * S::kGroupBytes + first % 8 * S::kRecord),
+                        "l"(pool + now[i] * p.c.page_stride + (long long)in_page * S::kRecord),
+                        "r"(p.run * S::kRecord), "r"(bar)
+                        : "memory");
+                }
+                ++count;
+                raw.step();
+            }
+        }
+        // what was started ends before the CTA does (it has, unless a wait was given up)
+        if (*lost) {
+            const long long from = clock_ns();
+            const int n = count < S::kRawStages ? count : S::kRawStages;
+            for (int i = 0; i < n; ++i) {
+                const int k = count - 1 - i;
+                while (!bar_done(shared_at(&ctl.raw_full[k % S::kRawStages]), k / S::kRawStages & 1) &&
+                       clock_ns() - from < kPatience) {
+                }
+            }
+        }
+    } else if (warp == S::kProductWarp) {
+        // ---- products: one thread ------------------------------------------------------
+        if (lane == 0) {
+            Turn<S::kKeyStages> key;
+            Turn<S::kValueStages> value;
+            unsigned query_phase[2] = {0, 0}, weight_phase[2] = {0, 0};
+            constexpr uint32_t score_kind = product_of<T>(kTokens), output_kind = product_of<T>(D);
+            const uint32_t keys = shared_at(smem + S::kOffKeys), values = shared_at(smem + S::kOffValues);
+            // scores of row tile t into buffer s
+            auto scores = [&](int t, int s) {
+                const uint32_t d = tensor + S::kScoreColumn + s * kTokens;
+                const uint32_t a = tensor + S::kQueryColumn + t * (D / 2);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint32_t b = keys + key.stage * 2 * S::kKeyBytes + part * S::kKeyBytes;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        product(d, a + k * 8, operand_at(b + k / 4 * (kTokens * 128) + k % 4 * 32), score_kind,
+                                part > 0 || k > 0);
+                }
+                products_arrive(shared_at(&ctl.score[s]));
+            };
+            // output of row tile t, weights in buffer s
+            auto outputs = [&](int t, int s, bool add) {
+                const uint32_t d = tensor + S::kOutColumn + t * D, a = tensor + S::kScoreColumn + s * kTokens;
+                const uint32_t b = values + value.stage * S::kValueBytes;
+#pragma unroll
+                for (int k = 0; k < kTokens / 16; ++k)
+                    product(d, a + k * 8, operand_at(b + k * 32), output_kind, add || k > 0);
+                products_arrive(shared_at(&ctl.output[t]));
+            };
+            auto wait_key = [&]() {
+                bar_wait(shared_at(&ctl.key_full[key.stage]), key.phase, lost);
+                fence_after();
+            };
+            auto wait_value = [&]() {
+                bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                fence_after();
+            };
+            auto wait_weight = [&](int s) {
+                bar_wait(shared_at(&ctl.weight[s]), weight_phase[s], lost);
+                weight_phase[s] ^= 1;
+                fence_after();
+            };
+            auto release_key = [&]() {
+                products_arrive(shared_at(&ctl.key_empty[key.stage]));
+                key.step();
+            };
+            int spin = 0;                         // buffer of the next scores, one row tile
+            while (walk.next(u)) {
+                const int n = u.t1 - u.t0;
+                if (n == 0)
+                    continue;
+                for (int t = 0; t < u.row_tiles; ++t) {
+                    bar_wait(shared_at(&ctl.query[t]), query_phase[t], lost);
+                    query_phase[t] ^= 1;
+                }
+                if (*lost)
+                    break;
+                fence_after();
+                wait_key();
+                if (S::kTiles == 2) {
+                    for (int t = 0; t < u.row_tiles; ++t)
+                        scores(t, t);
+                    release_key();
+                    for (int j = 0; j < n; ++j) {
+                        for (int t = 0; t < u.row_tiles; ++t) {
+                            if (t == 0)
+                                wait_value();
+                            wait_weight(t);
+                            outputs(t, t, j > 0);
+                            if (j + 1 < n) {
+                                if (t == 0)
+                                    wait_key();
+                                scores(t, t);
+                            }
+                        }
+                        products_arrive(shared_at(&ctl.value_empty[value.stage]));
+                        value.step();
+                        if (j + 1 < n)
+                            release_key();
+                    }
+                } else {
+                    scores(0, spin);
+                    release_key();
+                    for (int j = 0; j < n; ++j) {
+                        if (j + 1 < n) {
+                            wait_key();
+                            scores(0, spin ^ 1);
+                            release_key();
+                        }
+                        wait_value();
+                        wait_weight(spin);
+                        outputs(0, spin, j > 0);
+                        products_arrive(shared_at(&ctl.value_empty[value.stage]));
+                        value.step();
+                        spin ^= 1;
+                    }
+                }
+            }
+            // nothing is under way when tensor memory is given back
+            products_arrive(shared_at(&ctl.last));
+            const long long from = clock_ns();
+            while (!bar_done(shared_at(&ctl.last), 0) && clock_ns() - from < kPatience) {
+            }
+        }
+        __syncwarp();
+    } else if (warp >= S::kValueWarp) {
+        // ---- values: V^T, a row for each channel -----------------------------------------
+        Turn<S::kRawStages> raw;
+        Turn<S::kValueStages> value;
+        int count = 0, unit = 0;
+        const int turn = (warp - S::kValueWarp) * 32 + lane;
+        while (walk.next(u)) {
+            if (u.t1 == u.t0)
+                continue;
+            // the slot of a unit to come, which no one looks at any more: expansion
+            // is at most kValueStages units ahead, row tiles one apart
+            if (turn < 8)
+                ctl.bad[(unit + kSlots / 2) % kSlots][turn] = 0x7fffffff;
+            int *bad = ctl.bad[unit++ % kSlots];
+            for (int t = u.t0; t < u.t1; ++t) {
+                bar_wait(shared_at(&ctl.raw_full[raw.stage]), raw.phase, lost);
+                bar_wait(shared_at(&ctl.value_empty[value.stage]), value.phase ^ 1, lost);
+                const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
+                unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
+                const unsigned long long there = ctl.there[count % kSlots];
+                const bool masked = there != ~0ULL || (t + 1) * kTokens > u.see_lo;
+#pragma unroll 1
+                for (int i = turn; i < 8 * (D / 8); i += 128) {
+                    // eight tokens of one word: four channels of two neighbouring groups
+                    const int eight = i % 8, word = i / 8;
+                    const int stretch = word / (4 * kPer), place = word % (4 * kPer) * 2;
+                    const int g = place / kPer, group = stretch * kPer + place % kPer;
+                    const unsigned char *rec = src + eight * S::kGroupBytes;
+                    uint32_t w[8], s[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        w[k] = *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D / 2 + word * 4);
+                        s[k] = *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D + D / 16 + group * 2);
+                    }
+                    if (masked) {
+                        // tokens that are not there, or that not every row sees, may
+                        // hold anything: their weights are 0, which 0 * NaN is not
+                        const unsigned here = (unsigned)(there >> (8 * eight)) & 255;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (!(here >> k & 1))
+                                s[k] = 0;
+                            const int pos = t * kTokens + 8 * eight + k;
+                            if ((s[k] & 0x7c00u) == 0x7c00u) {
+                                atomicMin(&bad[group], pos);
+                                s[k] &= 0xffff0000u;
+                            }
+                            if ((s[k] & 0x7c000000u) == 0x7c000000u) {
+                                atomicMin(&bad[group + 1], pos);
+                                s[k] &= 0xffffu;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const unsigned pick = half ? 0x7632 : 0x5410;
+                        uint32_t x[4];
+                        typename Pair<T>::Scale f[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            x[m] = __byte_perm(w[2 * m], w[2 * m + 1], pick);
+                            f[m] = Pair<T>::scale(__byte_perm(s[2 * m], s[2 * m + 1], pick));
+                        }
+                        const int channel = (group + half) * kGroup + 4 * g;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int d = channel + c;
+                            uint4 v;
+                            v.x = Pair<T>::value(Pair<T>::codes(x[0] >> (4 * c)), f[0]);
+                            v.y = Pair<T>::value(Pair<T>::codes(x[1] >> (4 * c)), f[1]);
+                            v.z = Pair<T>::value(Pair<T>::codes(x[2] >> (4 * c)), f[2]);
+                            v.w = Pair<T>::value(Pair<T>::codes(x[3] >> (4 * c)), f[3]);
+                            *reinterpret_cast<uint4 *>(dst + d * 128 + ((eight ^ (d & 7)) * 16)) = v;
+                        }
+                    }
+                }
+                fence_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(shared_at(&ctl.raw_empty[raw.stage]));
+                    bar_arrive(shared_at(&ctl.value_full[value.stage]));
+                }
+                ++count;
+                raw.step();
+                value.step();
+            }
+        }
+    } else if (warp >= S::kKeyWarp) {
+        // ---- keys: a row for each token ----------------------------------------------------
+        Turn<S::kRawStages> raw;
+        Turn<S::kKeyStages> key;
+        const int turn = (warp - S::kKeyWarp) * 32 + lane;
+        while (walk.next(u)) {
+            for (int t = u.t0; t < u.t1; ++t) {
+                bar_wait(shared_at(&ctl.raw_full[raw.stage]), raw.phase, lost);
+                bar_wait(shared_at(&ctl.key_empty[key.stage]), key.phase ^ 1, lost);
+                const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
+                unsigned char *dst = smem + S::kOffKeys + key.stage * 2 * S::kKeyBytes;
+#pragma unroll 1
+                for (int i = turn; i < kTokens * (D / 32); i += 128) {
+                    // 16 bytes of one token: four words, of the groups of one stretch in turn
+                    const int quad = i / 8 % (D / 32), token = i / (D / 4) * 8 + i % 8;
+                    const unsigned char *rec = src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord;
+                    const uint4 words = *reinterpret_cast<const uint4 *>(rec + quad * 16);
+                    const int stretch = quad / kPer, first = quad % kPer * 4;     // place in the stretch
+                    uint32_t hi[kPer], lo[kPer];
+                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(rec + D + stretch * kPer * 2);
+#pragma unroll
+                    for (int g = 0; g < kPer; g += 2) {
+                        uint32_t h, l;
+                        Pair<T>::split(scales[g / 2], h, l);
+                        hi[g] = __byte_perm(h, h, 0x1010), hi[g + 1] = __byte_perm(h, h, 0x3232);
+                        lo[g] = __byte_perm(l, l, 0x1010), lo[g + 1] = __byte_perm(l, l, 0x3232);
+                    }
+                    const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int g = k % kPer;                                   // first is a multiple of kPer
+                        const int piece = stretch * 16 + 4 * g + (first + k) / kPer;   // of eight channels
+                        uint32_t x[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            x[c] = Pair<T>::codes(w[k] >> (4 * c));
+                        unsigned char *at = dst + piece / 8 * (kTokens * 128) + token * 128 +
+                                            ((piece & 7) ^ (token & 7)) * 16;
+                        uint4 v;
+                        v.x = Pair<T>::times(x[0], hi[g]), v.y = Pair<T>::times(x[1], hi[g]);
+                        v.z = Pair<T>::times(x[2], hi[g]), v.w = Pair<T>::times(x[3], hi[g]);
+                        *reinterpret_cast<uint4 *>(at) = v;
+                        v.x = Pair<T>::times(x[0], lo[g]), v.y = Pair<T>::times(x[1], lo[g]);
+                        v.z = Pair<T>::times(x[2], lo[g]), v.w = Pair<T>::times(x[3], lo[g]);
+                        *reinterpret_cast<uint4 *>(at + S::kKeyBytes) = v;
+                    }
+                }
+                fence_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(shared_at(&ctl.raw_empty[raw.stage]));
+                    bar_arrive(shared_at(&ctl.key_full[key.stage]));
+                }
+                raw.step();
+                key.step();
+            }
+        }
+    } else {
+        // ---- softmax: a row a thread ---------------------------------------------------------
+        const int tile = warp / 4;
+        const uint32_t rows_at = tensor + ((uint32_t)(warp % 4 * 32) << 16);
+        const int r = tile * kTileRows + warp % 4 * 32 + lane;
+        const uint32_t out_at = rows_at + S::kOutColumn + tile * D;
+        unsigned score_phase[2] = {0, 0}, output_phase = 0;
+        int count = 0, unit = 0, spin = tile;
+        const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
+        const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
+        while (walk.next(u)) {
+            const int n = u.t1 - u.t0, slot = unit % kSlots;
+            unit += n > 0;
+            if (S::kTiles == 2)       // one tile's warps are at most a unit ahead of the other's
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (tile >= u.row_tiles) {
+                count += n;
+                continue;
+            }
+            const RowAt row(p, u, r);
+            const bool in = r < u.rows;
+            float m = -INFINITY, l = 0.f;
+            if (n > 0) {
+                // the row's query, channels (j, j + 4) of each eight in pairs
+                const T *q = (const T *)p.a.q + row.token * p.a.q_query + row.head * p.a.q_head;
+#pragma unroll
+                for (int part = 0; part < D / 64; ++part) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (in) {
+                            if (p.q_vector) {
+                                v = *reinterpret_cast<const uint4 *>(q + part * 64 + e * 8);
+                            } else {
+                                unsigned short y[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    y[k] = *reinterpret_cast<const unsigned short *>(q + part * 64 + e * 8 + k);
+                                v = make_uint4(y[0] | (unsigned)y[1] << 16, y[2] | (unsigned)y[3] << 16,
+                                               y[4] | (unsigned)y[5] << 16, y[6] | (unsigned)y[7] << 16);
+                            }
+                        }
+                        x[4 * e] = __byte_perm(v.x, v.z, 0x5410) ^ flip;
+                        x[4 * e + 1] = __byte_perm(v.x, v.z, 0x7632) ^ flip;
+                        x[4 * e + 2] = __byte_perm(v.y, v.w, 0x5410) ^ flip;
+                        x[4 * e + 3] = __byte_perm(v.y, v.w, 0x7632) ^ flip;
+                    }
+                    __syncwarp();
+                    store_columns(rows_at + S::kQueryColumn + tile * (D / 2) + part * 32, x);
+                }
+                wait_stores();
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(shared_at(&ctl.query[tile]));
+            }
+            for (int t = u.t0; t < u.t1; ++t) {
+                const uint32_t at = rows_at + S::kScoreColumn + spin * kTokens;
+                bar_wait(shared_at(&ctl.score[spin]), score_phase[spin], lost);
+                score_phase[spin] ^= 1;
+                fence_after();
+                __syncwarp();
+                uint32_t s0[32], s1[32];
+                load_columns(s0, at);
+                load_columns(s1, at + 32);
+                wait_loads();
+                const unsigned long long there = ctl.there[count++ % kSlots];
+                if (there != ~0ULL || (t + 1) * kTokens > u.see_lo) {
+                    const int left = row.limit - t * kTokens;
+                    const unsigned long long see = there & (left >= 64 ? ~0ULL : left <= 0 ? 0 : ~0ULL >> (64 - left));
+                    const unsigned lo = (unsigned)see, hi = (unsigned)(see >> 32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        s0[i] = lo >> i & 1 ? s0[i] : 0xff800000u;
+                        s1[i] = hi >> i & 1 ? s1[i] : 0xff800000u;
+                    }
+                }
+                float most = fmaxf(__uint_as_float(s0[0]), __uint_as_float(s1[0]));
+#pragma unroll
+                for (int i = 1; i < 32; ++i)
+                    most = fmaxf(most, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+                most *= c;
+                // The maximum that weights are relative to follows the true one only where
+                // that is 8 above it: weights stay below 2^8 and outputs are seldom scaled.
+                const bool grows = most > m + 8.f || m == -INFINITY;
+                if (__any_sync(~0u, grows && most > m)) {
+                    const float to = grows ? fmaxf(most, m) : m;
+                    const float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
+                    l *= f;
+                    m = to;
+                    if (t > u.t0) {
+                        bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
+                        fence_after();
+                        __syncwarp();
+#pragma unroll 1
+                        for (int part = 0; part < D; part += 32) {
+                            uint32_t x[32];
+                            load_columns(x, out_at + part);
+                            wait_loads();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                            store_columns(out_at + part, x);
+                        }
+                    }
+                }
+                const float low = m == -INFINITY ? 0.f : m;
+                float sum0 = 0.f, sum1 = 0.f;
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a0 = exp2_fast(fmaf(__uint_as_float(s0[2 * i]), c, -low));
+                    const float a1 = exp2_fast(fmaf(__uint_as_float(s0[2 * i + 1]), c, -low));
+                    sum0 += a0, sum1 += a1;
+                    w[i] = Pair<T>::pack(a0, a1);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a0 = exp2_fast(fmaf(__uint_as_float(s1[2 * i]), c, -low));
+                    const float a1 = exp2_fast(fmaf(__uint_as_float(s1[2 * i + 1]), c, -low));
+                    sum0 += a0, sum1 += a1;
+                    w[16 + i] = Pair<T>::pack(a0, a1);
+                }
+                l += sum0 + sum1;
+                store_columns(at, w);
+                wait_stores();
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(shared_at(&ctl.weight[spin]));
+                output_phase ^= 1;
+                if (S::kTiles == 1)
+                    spin ^= 1;
+            }
+            // ---- the unit's end
+            const bool whole = n == u.tiles;
+            float *partial = nullptr;
+            if (!whole) {
+                partial = p.partial + (2LL * blockIdx.x + (u.t0 == 0)) * S::kPartial;
+                if (u.t0 == 0 && r == 0) {
+                    p.splits[blockIdx.x].block = u.block;
+                    p.splits[blockIdx.x].head = u.head;
+                    p.splits[blockIdx.x].parts = 1 + u.later;
+                }
+            }
+            if (n > 0) {
+                // with one row tile scores are a product ahead, so that the last
+                // output but one may be under way too, whose phase comes first
+                if (S::kTiles == 1 && n > 1)
+                    bar_wait(shared_at(&ctl.output[tile]), output_phase, lost);
+                bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
+                fence_after();
+                __syncwarp();
+            }
+            float inv = l == 0.f ? 0.f : 1.f / l;
+            if (*lost)
+                inv = l = m = __uint_as_float(0x7fffffffu);
+            const long long to = (long long)row.token * p.a.heads + row.head;
+#pragma unroll 1
+            for (int part = 0; part < D; part += 32) {
+                uint32_t x[32];
+                __syncwarp();
+                if (n > 0) {
+                    load_columns(x, out_at + part);
+                    wait_loads();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = 0;
+                }
+                const bool nan = n > 0 && row.limit > ctl.bad[slot][part / 32];
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        partial[(part + i) * S::kRows + r] = nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(x[i]);
+                } else if (in) {
+                    const float f = nan ? __uint_as_float(0x7fffffffu) : inv;
+                    // rows that see nothing are 0, whatever the tile before left there
+                    uint32_t y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = f == 0.f ? 0u : Pair<T>::pack(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+                    uint4 *dst = reinterpret_cast<uint4 *>((T *)p.a.out + to * D + part);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                }
+            }
+            if (!whole) {
+                partial[D * S::kRows + r] = m;
+                partial[(D + 1) * S::kRows + r] = l;
+            } else if (in && p.a.lse) {
+                p.a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+            fence_before();
+        }
+    }
+
+    __syncthreads();
+    if (warp == S::kProductWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tensor));
+}
+
+// Joins the parts of the unit that begins in a CTA and goes on in others: 32 of its
+// rows, a row a lane, the channels shared out between the warps.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+join_chunk_kernel(const __grid_constant__ Args p)
+{
+    using S = Shape<D>;
+    constexpr int kMine = D / (kJoinThreads / 32), kSlices = S::kRows / 32;
+    dependent_grid_wait();
+    allow_dependent_grid();
+    const int cta = blockIdx.x / kSlices, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const Split s = p.splits[cta];
+    if (s.parts == 0)
+        return;
+    const Block b = p.blocks[s.block];
+    const Span span = span_of(b, p.group, p.rows);
+    const int r = (blockIdx.x - cta * kSlices) * 32 + lane;
+    if (r - lane >= span.rows)
+        return;
+    auto part_at = [&](int i) { return p.partial + (2LL * (cta + i) + (i == 0)) * S::kPartial; };
+    float m = -INFINITY;
+    for (int i = 0; i < s.parts; ++i)
+        m = fmaxf(m, part_at(i)[D * S::kRows + r]);
+    const float low = m == -INFINITY ? 0.f : m;
+    float l = 0.f, x[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        x[k] = 0.f;
+    for (int i = 0; i < s.parts; ++i) {
+        const float *q = part_at(i);
+        const float pm = q[D * S::kRows + r], pl = q[(D + 1) * S::kRows + r];
+        float v[kMine];
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+            v[k] = q[(warp * kMine + k) * S::kRows + r];
+        const float w = exp2_fast(pm - low);
+        l += pl * w;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+            x[k] = fmaf(v[k], w, x[k]);
+    }
+    if (r >= span.rows)
+        return;
+    Part u;
+    u.b = b;
+    u.head = s.head;
+    u.rows = span.rows;
+    const RowAt row(p, u, r);
+    const long long to = (long long)row.token * p.a.heads + row.head;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t y[kMine / 2];
+#pragma unroll
+    for (int k = 0; k < kMine / 2; ++k)
+        y[k] = Pair<T>::pack(x[2 * k] * inv, x[2 * k + 1] * inv);
+    uint4 *dst = reinterpret_cast<uint4 *>((T *)p.a.out + to * D + warp * kMine);
+#pragma unroll
+    for (int k = 0; k < kMine / 8; ++k)
+        dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    if (warp == 0 && p.a.lse)
+        p.a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D>
+cudaError_t launch_chunk_dim(const Args &p, int dev, int ctas, cudaStream_t stream)
+{
+    using S = Shape<D>;
+    auto fn = p.a.bf16 ? chunk_kernel<__nv_bfloat16, D> : chunk_kernel<__half, D>;
+    auto join = p.a.bf16 ? join_chunk_kernel<__nv_bfloat16, D> : join_chunk_kernel<__half, D>;
+    static std::atomic<unsigned long long> raised[2];       // the kernels' shared memory, once a device
+    cudaError_t e = cudaSuccess;
+    if (!(raised[p.a.bf16].load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess)
+            return e;
+        raised[p.a.bf16].fetch_or(1ULL << dev, std::memory_order_relaxed);
+    }
+    e = launch_overlapped(fn, ctas, S::kThreads, S::kSmem, stream, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_overlapped(join, ctas * (S::kRows / 32), kJoinThreads, 0, stream, p);
+}
+
+}  // namespace chunk
+}  // namespace kv4
+}  // namespace ds

@@ -1,0 +1,73 @@
+// ds_kv4_chunk.h -- how attention of chunks is laid out: what the planning launch,
+// the kernels and the host share.
+#pragma once
+
+#include "ds_kv4.cuh"
+#include "ds_kv4_launch.h"
+
+namespace ds {
+namespace kv4 {
+namespace chunk {
+
+// Tiles of 128 query rows of a block: two, unless their outputs leave no room in
+// tensor memory.
+constexpr int tiles_of_rows(int d) { return d == 256 ? 1 : 2; }
+
+// A block of rows of one batch entry: rows [row0, row0 + Args::rows) of its n * group.
+struct alignas(16) Block {
+    long long place;      // places of the line, for one head, before it
+    int seq, start, n;    // the sequence, its first row of q, its new tokens
+    int len, row0, pad;
+};
+
+struct Head {
+    long long all, per;   // places of the line, of a CTA
+    int blocks, pad;
+};
+
+// Left for the join: the unit that begins in a CTA and goes on in others.
+struct alignas(16) Split {
+    int block, head, parts, pad;
+};
+
+struct Args {
+    Cache c;
+    Chunk a;
+    Head *head;
+    Block *blocks;
+    int *first;           // block that a CTA's first place is in
+    Split *splits;
+    int *starts;          // batch + 1, as far as they rise
+    long long *places;    // of each entry: places, then places before it
+    int *counts;          // of each entry: blocks, then blocks before it
+    float *partial;
+    int group, rows, run, ctas, q_vector;
+    Divider by_group;
+};
+
+// What a block's rows see, and its tiles.
+struct Span {
+    int rows, row_tiles, see_lo, see_hi, tiles;
+};
+
+__host__ __device__ __forceinline__ Span span_of(const Block &b, int group, int block_rows)
+{
+    Span s;
+    const int left = b.n * group - b.row0;
+    s.rows = left < block_rows ? left : block_rows;
+    s.row_tiles = s.rows > 128 ? 2 : 1;
+    const int lo = b.len - b.n + 1 + b.row0 / group, hi = b.len - b.n + 1 + (b.row0 + s.rows - 1) / group;
+    s.see_lo = lo > 0 ? lo : 0;
+    s.see_hi = hi > 0 ? hi : 0;
+    s.tiles = s.see_hi / 64 + (s.see_hi % 64 != 0);
+    return s;
+}
+
+// Places of a unit: one for each tile and row tile, and for its start and end
+// (queries, first copies, outputs) as much as these cost.
+constexpr int kUnitCost = 8;
+__host__ __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.row_tiles; }
+
+}  // namespace chunk
+}  // namespace kv4
+}  // namespace ds

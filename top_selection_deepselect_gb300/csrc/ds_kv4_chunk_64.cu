@@ -1,0 +1,13 @@
+// ds_kv4_chunk_64.cu -- attention of chunks, head dimension 64.
+#include "ds_kv4_chunk.cuh"
+
+namespace ds {
+namespace kv4 {
+
+cudaError_t launch_chunk_64(const chunk::Args &p, int dev, int ctas, cudaStream_t stream)
+{
+    return chunk::launch_chunk_dim<64>(p, dev, ctas, stream);
+}
+
+}  // namespace kv4
+}  // namespace ds

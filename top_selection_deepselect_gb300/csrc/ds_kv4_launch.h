@@ -38,5 +38,21 @@ size_t attention_workspace(const Cache &c, int head_dim, const Attend &a, int sm
 cudaError_t launch_attention(const Cache &c, int head_dim, const Attend &a, int dev, int sms,
                              cudaStream_t stream);
 
+// One call of attention of chunks.
+struct Chunk {
+    const int32_t *lengths, *seqs, *starts;
+    const void *q;
+    long long q_query, q_head;   // strides in elements
+    void *out;
+    float *lse;
+    float scale;
+    int batch, heads, tokens;
+    int bf16;                    // 1: q and out are bf16, 0: fp16
+};
+
+size_t chunk_workspace(const Cache &c, int head_dim, const Chunk &a, int sms);
+cudaError_t launch_chunk(const Cache &c, int head_dim, const Chunk &a, void *workspace, int dev, int sms,
+                         cudaStream_t stream);
+
 }  // namespace kv4
 }  // namespace ds
