@@ -70,6 +70,9 @@ struct Shape {
     static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4;
     static constexpr int kProductWarp = kValueWarp + 4, kCopyWarp = kProductWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + 1);
+    // Registers: 18 warps have 96 each; a softmax row wants 120, which the warps that
+    // expand give: 8 x 120 + 8 x 72 + 2 x 96 = 18 x 96.
+    static constexpr bool kShift = kTiles == 2;
     // columns of tensor memory
     static constexpr int kOutColumn = 0;
     static constexpr int kScoreColumn = kTiles * D;             // two of them
@@ -126,13 +129,16 @@ constexpr long long kPatience = 1000000000;
 // is waited for any more, and results are NaN.
 __device__ __forceinline__ void bar_wait(uint32_t bar, unsigned phase, volatile int *lost)
 {
-    if (bar_done(bar, phase))
-        return;
-    const long long from = clock_ns();
-    while (!bar_done(bar, phase)) {
+    long long from = 0;
+    for (unsigned tries = 1; !bar_done(bar, phase); ++tries) {
+        if (tries % 64 != 0)               // the timer takes longer to read than most waits
+            continue;
         if (*lost)
             return;
-        if (clock_ns() - from > kPatience) {
+        const long long now = clock_ns();
+        if (from == 0)
+            from = now;
+        if (now - from > kPatience) {
             *lost = 1;
             return;
         }
@@ -185,12 +191,29 @@ __device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[3
         : "memory");
 }
 
+__device__ __forceinline__ void load_columns(uint32_t (&x)[16], uint32_t at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+                   "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+                   "=r"(x[14]), "=r"(x[15])
+                 : "r"(at));
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const uint32_t (&x)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
+                 "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+                 : "memory");
+}
+
 // Operand in shared memory: rows of 128 bytes (64 numbers of the summed index),
 // eight of them a block of 1024 bytes, 16-byte pieces at place (piece ^ row % 8).
-__device__ __forceinline__ uint64_t operand_at(uint32_t at)
-{
-    return (uint64_t)((at & 0x3ffff) >> 4) | 1ULL << 16 | (uint64_t)(1024 >> 4) << 32 | 1ULL << 46 | 2ULL << 61;
-}
+// Its descriptor's lower word; the upper one says the blocks' distance, and the order.
+__device__ __forceinline__ uint32_t operand_at(uint32_t at) { return (at >> 4) | 1u << 16; }
+constexpr uint32_t kOperandKind = 1024 >> 4 | 1u << 14 | 2u << 29;
 // 16-bit operands of one type, 32-bit sums, 128 rows, n columns.
 template <typename T>
 __device__ __forceinline__ constexpr uint32_t product_of(int n)
@@ -198,19 +221,33 @@ __device__ __forceinline__ constexpr uint32_t product_of(int n)
     constexpr uint32_t type = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     return 1u << 4 | type << 7 | type << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTileRows >> 4) << 24;
 }
-// D (+)= A B with A in tensor memory, 16 of the summed index.
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add)
+// D (+)= A B with A in tensor memory, 16 of the summed index.  The whole warp comes
+// here, so that addresses stay in uniform registers, and the lane with `lead` issues:
+// with one lane on a branch of its own a product took 110 cycles to issue.
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, uint32_t what, bool add, int lead)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(what), "r"((int)add)
+                 "setp.ne.b32 q, %6, 0;\n\t"
+                 "mov.b64 b, {%2, %5};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(what), "r"((int)add), "r"(kOperandKind), "r"(lead)
                  : "memory");
 }
 // An arrival when all products issued so far are done.
-__device__ __forceinline__ void products_arrive(uint32_t bar)
+__device__ __forceinline__ void products_arrive(uint32_t bar, int lead)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(lead)
+                 : "memory");
+}
+__device__ __forceinline__ int elected()
+{
+    int yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes;
 }
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -218,6 +255,47 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Pairs of 32-bit numbers in one instruction.
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two multiply_add(uint32_t x0, uint32_t x1, float f, float d)
+{
+    Two y;
+    asm("{\n\t.reg .b64 x, f, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 f, {%4, %4};\n\t"
+        "mov.b64 d, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, f, d;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(y.a), "=f"(y.b) : "r"(x0), "r"(x1), "f"(f), "f"(d));
+    return y;
+}
+__device__ __forceinline__ void add_to(Two &sum, float x0, float x1)
+{
+    asm("{\n\t.reg .b64 s, x;\n\t"
+        "mov.b64 s, {%0, %1};\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "add.rn.f32x2 s, s, x;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(sum.a), "+f"(sum.b) : "f"(x0), "f"(x1));
+}
+
+// Largest of 32 numbers, in four chains of three-way maxima.
+__device__ __forceinline__ float largest_of(const uint32_t (&x)[32])
+{
+    float m[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        m[c] = __uint_as_float(x[c]);
+#pragma unroll
+        for (int i = 4; i < 28; i += 8)
+            m[c] = fmaxf(fmaxf(m[c], __uint_as_float(x[i + c])), __uint_as_float(x[i + 4 + c]));
+        m[c] = fmaxf(m[c], __uint_as_float(x[28 + c]));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // ---- expansion ----------------------------------------------------------------------
@@ -326,6 +404,19 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
+// Weights of 32 scores, packed, and their sums.
+template <typename T>
+__device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32], float c, float low, Two (&sum)[2])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const Two x = multiply_add(s[2 * i], s[2 * i + 1], c, -low);
+        const float a = exp2_fast(x.a), b = exp2_fast(x.b);
+        add_to(sum[i % 2], a, b);
+        w[i] = Pair<T>::pack(a, b);
+    }
+}
+
 // ---- the line of work -----------------------------------------------------------------
 // One head's share of a block of rows, and the tiles [t0, t1) of tokens in it that are
 // this CTA's.
@@ -337,64 +428,75 @@ struct Part {
     int later;                 // CTAs after this one that have tiles of it
 };
 
+// A warp's way along its CTA's places, kept in shared memory, so that what works on a
+// part has the registers for itself.
 struct Walk {
-    const Args &p;
+    Part u;
     long long x, end;
     int block, head;
-    __device__ __forceinline__ Walk(const Args &args) : p(args)
-    {
-        const long long per = p.head->per;
-        x = per * blockIdx.x;
-        end = x + per < p.head->all ? x + per : p.head->all;
-        block = x < end ? p.first[blockIdx.x] : 0;
-        head = -1;
-    }
-    // The next part, false where there is none.
-    __device__ __forceinline__ bool next(Part &u)
-    {
-        while (x < end && block < p.head->blocks) {
-            const Block b = p.blocks[block];
-            const Span s = span_of(b, p.group, p.rows);
-            const int cost = cost_of(s);
-            const long long first = b.place * p.c.kv_heads;
-            if (head < 0) {
-                const long long h = (x - first) / cost;
-                head = (int)(h < 0 ? 0 : h);
-            }
-            if (head >= p.c.kv_heads) {
-                ++block;
-                head = 0;
-                continue;
-            }
-            const long long at = first + (long long)head * cost;
-            if (at >= end)
-                return false;
-            auto tile_at = [&](long long place) -> int {
-                const long long d = place - at - kUnitCost;
-                const long long t = d <= 0 ? 0 : s.row_tiles == 1 ? d : (d + 1) / 2;
-                return t < s.tiles ? (int)t : s.tiles;
-            };
-            u.b = b;
-            u.block = block;
-            u.head = head;
-            u.rows = s.rows;
-            u.row_tiles = s.row_tiles;
-            u.see_lo = s.see_lo;
-            u.see_hi = s.see_hi;
-            u.tiles = s.tiles;
-            u.t0 = tile_at(x);
-            u.t1 = tile_at(end);
-            u.later = 0;
-            if (u.t1 > u.t0 && u.t1 < s.tiles)
-                u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.row_tiles) / p.head->per) -
-                          (int)blockIdx.x;
-            ++head;
-            if (u.t1 > u.t0 || (s.tiles == 0 && at >= x))
-                return true;
-        }
-        return false;
-    }
+    int more;                  // u is a part; 0: there are none left
+    int pad;
 };
+
+__device__ __forceinline__ void begin(const Args &p, Walk &w)
+{
+    const long long per = p.head->per, all = p.head->all;
+    w.x = per * blockIdx.x;
+    w.end = w.x + per < all ? w.x + per : all;
+    w.block = w.x < w.end ? p.first[blockIdx.x] : 0;
+    w.head = -1;
+}
+
+// Goes to the next part.  One thread's.
+__device__ __forceinline__ void advance(const Args &p, Walk &w)
+{
+    const long long x = w.x, end = w.end, per = p.head->per;
+    int block = w.block, head = w.head;
+    w.more = 0;
+    while (x < end && block < p.head->blocks) {
+        const Block b = p.blocks[block];
+        const Span s = span_of(b, p.group, p.rows);
+        const int cost = cost_of(s);
+        const long long first = b.place * p.c.kv_heads;
+        if (head < 0)
+            head = x > first ? (int)((x - first) / cost) : 0;
+        if (head >= p.c.kv_heads) {
+            ++block;
+            head = 0;
+            continue;
+        }
+        const long long at = first + (long long)head * cost;
+        if (at >= end)
+            break;
+        auto tile_at = [&](long long place) -> int {
+            const long long d = place - at - kUnitCost;
+            const long long t = d <= 0 ? 0 : s.row_tiles == 1 ? d : (d + 1) / 2;
+            return t < s.tiles ? (int)t : s.tiles;
+        };
+        Part u;
+        u.b = b;
+        u.block = block;
+        u.head = head;
+        u.rows = s.rows;
+        u.row_tiles = s.row_tiles;
+        u.see_lo = s.see_lo;
+        u.see_hi = s.see_hi;
+        u.tiles = s.tiles;
+        u.t0 = tile_at(x);
+        u.t1 = tile_at(end);
+        u.later = 0;
+        if (u.t1 > u.t0 && u.t1 < s.tiles)
+            u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.row_tiles) / per) - (int)blockIdx.x;
+        ++head;
+        if (u.t1 > u.t0 || (s.tiles == 0 && at >= x)) {
+            w.u = u;
+            w.more = 1;
+            break;
+        }
+    }
+    w.block = block;
+    w.head = head;
+}
 
 constexpr int kSlots = 16;     // of what is known of a tile or a unit: more than any role is ahead
 
@@ -428,8 +530,9 @@ chunk_kernel(const __grid_constant__ Args p)
     constexpr int kGroups = D / kGroup, kPer = kGroups > 4 ? 4 : kGroups;   // groups, of a stretch
     extern __shared__ unsigned char smem_raw[];
     __shared__ Control ctl;
+    __shared__ Walk walks[S::kThreads / 32];
     unsigned char *smem = smem_raw + (1024 - (shared_at(smem_raw) & 1023) & 1023);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
@@ -460,7 +563,7 @@ chunk_kernel(const __grid_constant__ Args p)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tensor = ctl.tensor;
+    const uint32_t tensor = __shfl_sync(~0u, ctl.tensor, 0);
     volatile int *lost = &ctl.lost;
 
     dependent_grid_wait();
@@ -468,15 +571,24 @@ chunk_kernel(const __grid_constant__ Args p)
     if (threadIdx.x == 0)
         p.splits[blockIdx.x].parts = 0;
 
-    Walk walk(p);
-    Part u;
+    Walk &walk = walks[warp];
+    const Part &u = walk.u;
+    auto next = [&]() -> bool {        // a warp's
+        __syncwarp();
+        if (lane == 0)
+            advance(p, walk);
+        __syncwarp();
+        return walk.more != 0;
+    };
+    if (lane == 0)
+        begin(p, walk);
 
     if (warp == S::kCopyWarp) {
         // ---- records ---------------------------------------------------------------
         Turn<S::kRawStages> raw;
         int count = 0;                            // tiles so far
         const int runs = kTokens / p.run;
-        while (walk.next(u)) {
+        while (next()) {
             const int32_t *row = p.c.table + u.b.seq * p.c.table_stride;
             const unsigned char *pool = p.c.pool + (long long)u.head * p.c.page_size * S::kRecord;
             // pages of this lane's runs (at most two) of tile t
@@ -491,7 +603,8 @@ chunk_kernel(const __grid_constant__ Args p)
             };
             int page[2];
             look(u.t0, page);
-            for (int t = u.t0; t < u.t1; ++t) {
+            const int t1 = u.t1, see_hi = u.see_hi;
+            for (int t = u.t0; t < t1; ++t) {
                 int now[2] = {page[0], page[1]};
                 look(t + 1, page);
                 bar_wait(shared_at(&ctl.raw_empty[raw.stage]), raw.phase ^ 1, lost);
@@ -500,7 +613,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 bool ok[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int first = (lane + 32 * i) * p.run, left = u.see_hi - t * kTokens - first;
+                    const int first = (lane + 32 * i) * p.run, left = see_hi - t * kTokens - first;
                     ok[i] = (unsigned)now[i] < (unsigned)p.c.n_pages && !stop;
                     if (ok[i])
                         there |= (~0ULL >> (64 - (left < p.run ? left : p.run))) << first;
@@ -545,8 +658,9 @@ chunk_kernel(const __grid_constant__ Args p)
             }
         }
     } else if (warp == S::kProductWarp) {
-        // ---- products: one thread ------------------------------------------------------
-        if (lane == 0) {
+        // ---- products ----------------------------------------------------------------------
+        {
+            const int lead = elected();
             Turn<S::kKeyStages> key;
             Turn<S::kValueStages> value;
             unsigned query_phase[2] = {0, 0}, weight_phase[2] = {0, 0};
@@ -562,9 +676,9 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         product(d, a + k * 8, operand_at(b + k / 4 * (kTokens * 128) + k % 4 * 32), score_kind,
-                                part > 0 || k > 0);
+                                part > 0 || k > 0, lead);
                 }
-                products_arrive(shared_at(&ctl.score[s]));
+                products_arrive(shared_at(&ctl.score[s]), lead);
             };
             // output of row tile t, weights in buffer s
             auto outputs = [&](int t, int s, bool add) {
@@ -572,45 +686,48 @@ chunk_kernel(const __grid_constant__ Args p)
                 const uint32_t b = values + value.stage * S::kValueBytes;
 #pragma unroll
                 for (int k = 0; k < kTokens / 16; ++k)
-                    product(d, a + k * 8, operand_at(b + k * 32), output_kind, add || k > 0);
-                products_arrive(shared_at(&ctl.output[t]));
+                    product(d, a + k * 8, operand_at(b + k * 32), output_kind, add || k > 0, lead);
+                products_arrive(shared_at(&ctl.output[t]), lead);
             };
             auto wait_key = [&]() {
                 bar_wait(shared_at(&ctl.key_full[key.stage]), key.phase, lost);
                 fence_after();
+                __syncwarp();
             };
             auto wait_value = [&]() {
                 bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
                 fence_after();
+                __syncwarp();
             };
             auto wait_weight = [&](int s) {
                 bar_wait(shared_at(&ctl.weight[s]), weight_phase[s], lost);
                 weight_phase[s] ^= 1;
                 fence_after();
+                __syncwarp();
             };
             auto release_key = [&]() {
-                products_arrive(shared_at(&ctl.key_empty[key.stage]));
+                products_arrive(shared_at(&ctl.key_empty[key.stage]), lead);
                 key.step();
             };
             int spin = 0;                         // buffer of the next scores, one row tile
-            while (walk.next(u)) {
-                const int n = u.t1 - u.t0;
+            while (next()) {
+                const int n = u.t1 - u.t0, row_tiles = u.row_tiles;
                 if (n == 0)
                     continue;
-                for (int t = 0; t < u.row_tiles; ++t) {
+                for (int t = 0; t < row_tiles; ++t) {
                     bar_wait(shared_at(&ctl.query[t]), query_phase[t], lost);
                     query_phase[t] ^= 1;
                 }
-                if (*lost)
+                if (__any_sync(~0u, *lost))
                     break;
                 fence_after();
                 wait_key();
                 if (S::kTiles == 2) {
-                    for (int t = 0; t < u.row_tiles; ++t)
+                    for (int t = 0; t < row_tiles; ++t)
                         scores(t, t);
                     release_key();
                     for (int j = 0; j < n; ++j) {
-                        for (int t = 0; t < u.row_tiles; ++t) {
+                        for (int t = 0; t < row_tiles; ++t) {
                             if (t == 0)
                                 wait_value();
                             wait_weight(t);
@@ -621,7 +738,7 @@ chunk_kernel(const __grid_constant__ Args p)
                                 scores(t, t);
                             }
                         }
-                        products_arrive(shared_at(&ctl.value_empty[value.stage]));
+                        products_arrive(shared_at(&ctl.value_empty[value.stage]), lead);
                         value.step();
                         if (j + 1 < n)
                             release_key();
@@ -638,14 +755,14 @@ chunk_kernel(const __grid_constant__ Args p)
                         wait_value();
                         wait_weight(spin);
                         outputs(0, spin, j > 0);
-                        products_arrive(shared_at(&ctl.value_empty[value.stage]));
+                        products_arrive(shared_at(&ctl.value_empty[value.stage]), lead);
                         value.step();
                         spin ^= 1;
                     }
                 }
             }
             // nothing is under way when tensor memory is given back
-            products_arrive(shared_at(&ctl.last));
+            products_arrive(shared_at(&ctl.last), lead);
             const long long from = clock_ns();
             while (!bar_done(shared_at(&ctl.last), 0) && clock_ns() - from < kPatience) {
             }
@@ -653,11 +770,13 @@ chunk_kernel(const __grid_constant__ Args p)
         __syncwarp();
     } else if (warp >= S::kValueWarp) {
         // ---- values: V^T, a row for each channel -----------------------------------------
+        if (S::kShift)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         Turn<S::kRawStages> raw;
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
         const int turn = (warp - S::kValueWarp) * 32 + lane;
-        while (walk.next(u)) {
+        while (next()) {
             if (u.t1 == u.t0)
                 continue;
             // the slot of a unit to come, which no one looks at any more: expansion
@@ -665,13 +784,14 @@ chunk_kernel(const __grid_constant__ Args p)
             if (turn < 8)
                 ctl.bad[(unit + kSlots / 2) % kSlots][turn] = 0x7fffffff;
             int *bad = ctl.bad[unit++ % kSlots];
-            for (int t = u.t0; t < u.t1; ++t) {
+            const int t1 = u.t1, see_lo = u.see_lo;
+            for (int t = u.t0; t < t1; ++t) {
                 bar_wait(shared_at(&ctl.raw_full[raw.stage]), raw.phase, lost);
                 bar_wait(shared_at(&ctl.value_empty[value.stage]), value.phase ^ 1, lost);
                 const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
                 unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
                 const unsigned long long there = ctl.there[count % kSlots];
-                const bool masked = there != ~0ULL || (t + 1) * kTokens > u.see_lo;
+                const bool masked = there != ~0ULL || (t + 1) * kTokens > see_lo;
 #pragma unroll 1
                 for (int i = turn; i < 8 * (D / 8); i += 128) {
                     // eight tokens of one word: four channels of two neighbouring groups
@@ -740,11 +860,14 @@ chunk_kernel(const __grid_constant__ Args p)
         }
     } else if (warp >= S::kKeyWarp) {
         // ---- keys: a row for each token ----------------------------------------------------
+        if (S::kShift)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         Turn<S::kRawStages> raw;
         Turn<S::kKeyStages> key;
         const int turn = (warp - S::kKeyWarp) * 32 + lane;
-        while (walk.next(u)) {
-            for (int t = u.t0; t < u.t1; ++t) {
+        while (next()) {
+            const int t1 = u.t1;
+            for (int t = u.t0; t < t1; ++t) {
                 bar_wait(shared_at(&ctl.raw_full[raw.stage]), raw.phase, lost);
                 bar_wait(shared_at(&ctl.key_empty[key.stage]), key.phase ^ 1, lost);
                 const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
@@ -797,6 +920,8 @@ chunk_kernel(const __grid_constant__ Args p)
         }
     } else {
         // ---- softmax: a row a thread ---------------------------------------------------------
+        if (S::kShift)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int tile = warp / 4;
         const uint32_t rows_at = tensor + ((uint32_t)(warp % 4 * 32) << 16);
         const int r = tile * kTileRows + warp % 4 * 32 + lane;
@@ -805,7 +930,7 @@ chunk_kernel(const __grid_constant__ Args p)
         int count = 0, unit = 0, spin = tile;
         const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
-        while (walk.next(u)) {
+        while (next()) {
             const int n = u.t1 - u.t0, slot = unit % kSlots;
             unit += n > 0;
             if (S::kTiles == 2)       // one tile's warps are at most a unit ahead of the other's
@@ -814,11 +939,12 @@ chunk_kernel(const __grid_constant__ Args p)
                 count += n;
                 continue;
             }
-            const RowAt row(p, u, r);
             const bool in = r < u.rows;
+            const int limit = RowAt(p, u, r).limit;
             float m = -INFINITY, l = 0.f;
             if (n > 0) {
                 // the row's query, channels (j, j + 4) of each eight in pairs
+                const RowAt row(p, u, r);
                 const T *q = (const T *)p.a.q + row.token * p.a.q_query + row.head * p.a.q_head;
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
@@ -852,7 +978,8 @@ chunk_kernel(const __grid_constant__ Args p)
                 if (lane == 0)
                     bar_arrive(shared_at(&ctl.query[tile]));
             }
-            for (int t = u.t0; t < u.t1; ++t) {
+            const int t0 = u.t0, t1 = u.t1, see_lo = u.see_lo;
+            for (int t = t0; t < t1; ++t) {
                 const uint32_t at = rows_at + S::kScoreColumn + spin * kTokens;
                 bar_wait(shared_at(&ctl.score[spin]), score_phase[spin], lost);
                 score_phase[spin] ^= 1;
@@ -863,8 +990,8 @@ chunk_kernel(const __grid_constant__ Args p)
                 load_columns(s1, at + 32);
                 wait_loads();
                 const unsigned long long there = ctl.there[count++ % kSlots];
-                if (there != ~0ULL || (t + 1) * kTokens > u.see_lo) {
-                    const int left = row.limit - t * kTokens;
+                if (there != ~0ULL || (t + 1) * kTokens > see_lo) {
+                    const int left = limit - t * kTokens;
                     const unsigned long long see = there & (left >= 64 ? ~0ULL : left <= 0 ? 0 : ~0ULL >> (64 - left));
                     const unsigned lo = (unsigned)see, hi = (unsigned)(see >> 32);
 #pragma unroll
@@ -873,10 +1000,7 @@ chunk_kernel(const __grid_constant__ Args p)
                         s1[i] = hi >> i & 1 ? s1[i] : 0xff800000u;
                     }
                 }
-                float most = fmaxf(__uint_as_float(s0[0]), __uint_as_float(s1[0]));
-#pragma unroll
-                for (int i = 1; i < 32; ++i)
-                    most = fmaxf(most, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+                float most = fmaxf(largest_of(s0), largest_of(s1));
                 most *= c;
                 // The maximum that weights are relative to follows the true one only where
                 // that is 8 above it: weights stay below 2^8 and outputs are seldom scaled.
@@ -886,42 +1010,36 @@ chunk_kernel(const __grid_constant__ Args p)
                     const float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
                     l *= f;
                     m = to;
-                    if (t > u.t0) {
+                    if (t > t0) {
                         bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                         fence_after();
                         __syncwarp();
 #pragma unroll 1
-                        for (int part = 0; part < D; part += 32) {
-                            uint32_t x[32];
+                        for (int part = 0; part < D; part += 16) {
+                            uint32_t x[16];
                             load_columns(x, out_at + part);
                             wait_loads();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 16; ++i)
                                 x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
                             store_columns(out_at + part, x);
                         }
                     }
                 }
                 const float low = m == -INFINITY ? 0.f : m;
-                float sum0 = 0.f, sum1 = 0.f;
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a0 = exp2_fast(fmaf(__uint_as_float(s0[2 * i]), c, -low));
-                    const float a1 = exp2_fast(fmaf(__uint_as_float(s0[2 * i + 1]), c, -low));
-                    sum0 += a0, sum1 += a1;
-                    w[i] = Pair<T>::pack(a0, a1);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a0 = exp2_fast(fmaf(__uint_as_float(s1[2 * i]), c, -low));
-                    const float a1 = exp2_fast(fmaf(__uint_as_float(s1[2 * i + 1]), c, -low));
-                    sum0 += a0, sum1 += a1;
-                    w[16 + i] = Pair<T>::pack(a0, a1);
-                }
-                l += sum0 + sum1;
+                Two sum[2] = {};
+                uint32_t w[16];
+                weights_of<T>(w, s0, c, low, sum);
                 store_columns(at, w);
+                weights_of<T>(w, s1, c, low, sum);
+                store_columns(at + 16, w);
+                l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
+                // With one row tile scores are a product ahead of outputs.  The output
+                // before this one ends before these weights are given away, so that never
+                // two phases of its barrier are to come, which a parity could not tell.
+                if (S::kTiles == 1 && t > t0)
+                    bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -942,10 +1060,6 @@ chunk_kernel(const __grid_constant__ Args p)
                 }
             }
             if (n > 0) {
-                // with one row tile scores are a product ahead, so that the last
-                // output but one may be under way too, whose phase comes first
-                if (S::kTiles == 1 && n > 1)
-                    bar_wait(shared_at(&ctl.output[tile]), output_phase, lost);
                 bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                 fence_after();
                 __syncwarp();
@@ -953,6 +1067,7 @@ chunk_kernel(const __grid_constant__ Args p)
             float inv = l == 0.f ? 0.f : 1.f / l;
             if (*lost)
                 inv = l = m = __uint_as_float(0x7fffffffu);
+            const RowAt row(p, u, r);
             const long long to = (long long)row.token * p.a.heads + row.head;
 #pragma unroll 1
             for (int part = 0; part < D; part += 32) {
@@ -966,7 +1081,7 @@ chunk_kernel(const __grid_constant__ Args p)
                     for (int i = 0; i < 32; ++i)
                         x[i] = 0;
                 }
-                const bool nan = n > 0 && row.limit > ctl.bad[slot][part / 32];
+                const bool nan = n > 0 && limit > ctl.bad[slot][part / 32];
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
