@@ -25,9 +25,9 @@ def check(ds, q, dtype, pool, table, lengths, starts, scale=None, seqs=None, **k
 
     Bounds.  The result before its last rounding is within t of the model's, so the output lies
     between the roundings of the model's value minus t and plus t.  A value and a probability are
-    rounded to the type before they are multiplied: u = eps / 2 relative each, of fp16 also 2^-25
-    absolute below its normal range, where a probability is at most 2^8 and their sum at least 1:
-    n 2^-25 of the largest value.  Products are exact; a product instruction adds 16 of them to a
+    rounded to fp16 before they are multiplied: 2^-11 relative each, and absolute 2^-24 of the largest
+    value, and for each of n tokens 2^-32 of the largest probability (their sum is at least 1) times
+    that value.  Products are exact; a product instruction adds 16 of them to a
     32-bit sum, which may cut each addend off at 2^-22 of the largest: 2 D / 16 <= 32 instructions
     move a score by 2^-17 reach, a probability as much relative, numerator and sum alike; n / 16 move
     the output by n 2^-26 spread.  exp and the sums: 2^-18."""
@@ -46,13 +46,12 @@ def check(ds, q, dtype, pool, table, lengths, starts, scale=None, seqs=None, **k
     got, glse = out.double().cpu().numpy()[rows], lse.double().cpu().numpy()[rows]
     ref, rlse, spread, reach = ref[rows], rlse[rows], spread[rows], reach[rows]
     n = table.shape[1] * host.shape[2]
-    u = torch.finfo(qt.dtype).eps / 2
+    u = 2.0 ** -11
     move = 2.0 ** -17 * (1 + reach)
     with np.errstate(invalid="ignore"):
-        t = (2 * u + u * u + 2 * move[..., None] + n * 2.0 ** -26) * spread
-        if dtype == "fp16":
-            big = np.abs(model.decode(host, dim)[1])
-            t = t + n * 2.0 ** -25 * np.nanmax(np.where(np.isfinite(big), big, 0)) + 2.0 ** -25
+        big = np.abs(model.decode(host, dim)[1])
+        big = np.max(np.where(np.isfinite(big), big, 0))
+        t = (2 * u + u * u + 2 * move[..., None] + n * 2.0 ** -26) * spread + (n * 2.0 ** -32 + 2.0 ** -24) * big
         lo, hi = (torch.from_numpy(x).to(qt.dtype).double().numpy() for x in (ref - t, ref + t))
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     fine = ~np.isnan(ref)
@@ -196,13 +195,31 @@ def test_scale(ds, scale):
     check(ds, *chunk_args(rng, [70], [100], 2, 1, 256, 16, "fp16"), scale=scale)
 
 
-@pytest.mark.parametrize("dtype,spread", [("bf16", 1e-30), ("bf16", 1e-6), ("bf16", 1e4), ("fp16", 1e-3), ("fp16", 2e3)])
+@pytest.mark.parametrize("dtype,spread", [("bf16", 1e-30), ("bf16", 1e-6), ("bf16", 1e4), ("fp16", 1e-3), ("fp16", 2e3),
+                                          ("fp16", 1e-6)])
 def test_values_of_every_size(ds, dtype, spread):
     """Keys and values far from 1, queries so that scores are not."""
     rng = np.random.default_rng(8)
     q, pool, table, lengths, starts = chunk(rng, [40, 90], [100, 0], 4, 2, 64, 16, spread=spread)
     scale = 0.125 / max(spread, 1e-5)
     check(ds, q, dtype, pool, table, lengths, starts, scale=scale)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_values_that_grow_and_fall(ds, dim, dtype):
+    """Value scales from one end of their range to the other within a sequence: small ones first, so
+    that what is held of them has to make room, then large ones first."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, [70, 140], [450, 450], 2, 1, dim, 16)
+    for seq in range(2):
+        size = np.exp2(np.linspace(-24, 12, int(lengths[seq])))
+        k, v = rng.standard_normal((2, 1, int(lengths[seq]), dim)).astype(np.float32)
+        v *= (size if seq == 0 else size[::-1])[:, None].astype(np.float32)
+        rec = model.encode(k[0], v[0])
+        for pos in range(int(lengths[seq])):
+            pool[table[seq, pos // 16], 0, pos % 16] = rec[pos]
+    check(ds, q, dtype, pool, table, lengths, starts)
 
 
 def test_growing_scores(ds):

@@ -14,8 +14,9 @@
 // does not fit a 16-bit operand.  The scale is split into two numbers of few
 // enough bits that both products are exact, and S is the sum of Q times each:
 // half as many operations more, and log-sums as exact as 32-bit arithmetic has
-// them.  Queries stay as they are: the operands' type is theirs.  Values are
-// rounded to that type once, as the probabilities are.
+// them.  Queries stay as they are: the operands' type is theirs.  Probabilities and
+// values are fp16 in the second product, whatever the queries' type, each rounded
+// to 11 bits once; powers of two keep both within its range.
 //
 // Codes become operands by a logical operation and a packed addition: a code u in
 // the low bits of an fp16 of 1024 (bf16 of 128) makes it 1024 + u (128 + u), and
@@ -335,12 +336,6 @@ struct Pair<__half> {
         hi = ((s & 0x7fff7fffu) + 0x00040004u) & 0xfff8fff8u;
         asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(s), "r"(hi));
     }
-    // Scales of two values as value() wants them.
-    struct Scale {
-        uint32_t s;
-    };
-    static __device__ __forceinline__ Scale scale(uint32_t s) { return {bounded(s)}; }
-    static __device__ __forceinline__ uint32_t value(uint32_t code, Scale s) { return times(code, s.s); }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
         uint32_t y;
@@ -380,22 +375,6 @@ struct Pair<__nv_bfloat16> {
         hi = convert(h);
         lo = convert(l);
     }
-    struct Scale {
-        uint32_t hi, lo;
-    };
-    static __device__ __forceinline__ Scale scale(uint32_t s)
-    {
-        Scale x;
-        split(s, x.hi, x.lo);
-        return x;
-    }
-    // rounded once: code lo is exact
-    static __device__ __forceinline__ uint32_t value(uint32_t code, Scale s)
-    {
-        uint32_t y;
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(code), "r"(s.hi), "r"(times(code, s.lo)));
-        return y;
-    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
         uint32_t y;
@@ -404,8 +383,7 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Weights of 32 scores, packed, and their sums.
-template <typename T>
+// Weights of 32 scores, in fp16, and their sums.
 __device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32], float c, float low, Two (&sum)[2])
 {
 #pragma unroll
@@ -413,7 +391,7 @@ __device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32],
         const Two x = multiply_add(s[2 * i], s[2 * i + 1], c, -low);
         const float a = exp2_fast(x.a), b = exp2_fast(x.b);
         add_to(sum[i % 2], a, b);
-        w[i] = Pair<T>::pack(a, b);
+        w[i] = Pair<__half>::pack(a, b);
     }
 }
 
@@ -504,6 +482,7 @@ struct Control {
     unsigned long long raw_full[4], raw_empty[4], key_full[4], key_empty[4], value_full[4], value_empty[4];
     unsigned long long query[2], score[2], weight[2], output[2], last;
     unsigned long long there[kSlots];      // tokens of a tile that are there
+    int lift[kSlots];                      // of a tile's values, a power of two
     int bad[kSlots][8];                    // of a unit: first position whose value scale is no number, a group
     uint32_t tensor;
     int lost;
@@ -521,6 +500,24 @@ struct RowAt {
         limit = r < u.rows && see > 0 ? see : 0;
     }
 };
+
+// Values are multiplied by a power of two, their lift, that brings the largest scale of a
+// part's first tile to [1/2, 1) (or as far as 2^15 does), and a later tile's that comes
+// out at kHigh or more, so that fp16 holds what any scales make: eleven bits of those
+// down to 2^-13 of the largest, and 2^-24 of that below.
+constexpr unsigned kHigh = 0x6c00;          // 2^12, an fp16: times a code of 8 below 2^16
+__device__ __forceinline__ int lift_of(unsigned most)
+{
+    const int e = 14 - (int)(most >> 10);   // most: bits of an fp16 that is finite
+    return e < 15 ? e : 15;
+}
+__device__ __forceinline__ unsigned lift_bits(int e)      // 2^e as an fp16, e >= -16
+{
+    return e >= -14 ? (unsigned)(e + 15) << 10 : 0x400u >> (-14 - e);
+}
+// Weights are taken 2^7 times: with maxima that lag by 2^8 at most they stay within
+// fp16, and 11 bits of those down to 2^-21 of the row's largest.
+constexpr float kRaise = 7.f;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
@@ -664,7 +661,7 @@ chunk_kernel(const __grid_constant__ Args p)
             Turn<S::kKeyStages> key;
             Turn<S::kValueStages> value;
             unsigned query_phase[2] = {0, 0}, weight_phase[2] = {0, 0};
-            constexpr uint32_t score_kind = product_of<T>(kTokens), output_kind = product_of<T>(D);
+            constexpr uint32_t score_kind = product_of<T>(kTokens), output_kind = product_of<__half>(D);
             const uint32_t keys = shared_at(smem + S::kOffKeys), values = shared_at(smem + S::kOffValues);
             // scores of row tile t into buffer s
             auto scores = [&](int t, int s) {
@@ -784,6 +781,8 @@ chunk_kernel(const __grid_constant__ Args p)
             if (turn < 8)
                 ctl.bad[(unit + kSlots / 2) % kSlots][turn] = 0x7fffffff;
             int *bad = ctl.bad[unit++ % kSlots];
+            int lift = 0;
+            bool fresh = true;
             const int t1 = u.t1, see_lo = u.see_lo;
             for (int t = u.t0; t < t1; ++t) {
                 bar_wait(shared_at(&ctl.raw_full[raw.stage]), raw.phase, lost);
@@ -792,6 +791,31 @@ chunk_kernel(const __grid_constant__ Args p)
                 unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
                 const unsigned long long there = ctl.there[count % kSlots];
                 const bool masked = there != ~0ULL || (t + 1) * kTokens > see_lo;
+                // the tile's largest scale: each warp looks at all of them, and comes to the same
+                unsigned most = 0;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int token = lane + 32 * k;
+                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(
+                        src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord + D + D / 16);
+                    unsigned both = 0;
+#pragma unroll
+                    for (int g = 0; g < kGroups / 2; ++g) {
+                        const unsigned x = scales[g] & 0x7fff7fffu;
+                        both = __vmaxu2(both, x & __vcmpltu2(x, 0x7c007c00u));
+                    }
+                    if (there >> token & 1)
+                        most = max(most, max(both & 0xffffu, both >> 16));
+                }
+                most = __reduce_max_sync(~0u, most);
+                // most 2^lift against kHigh, in exponents: below 2^-14 a scale is far from it
+                if (fresh || (int)(most >> 10) + lift >= (int)(kHigh >> 10)) {
+                    lift = lift_of(most);
+                    fresh = false;
+                }
+                const unsigned lift2 = lift_bits(lift) * 0x10001u;
+                if (turn == 0)
+                    ctl.lift[count % kSlots] = lift;
 #pragma unroll 1
                 for (int i = turn; i < 8 * (D / 8); i += 128) {
                     // eight tokens of one word: four channels of two neighbouring groups
@@ -828,21 +852,21 @@ chunk_kernel(const __grid_constant__ Args p)
                     for (int half = 0; half < 2; ++half) {
                         const unsigned pick = half ? 0x7632 : 0x5410;
                         uint32_t x[4];
-                        typename Pair<T>::Scale f[4];
+                        uint32_t f[4];
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             x[m] = __byte_perm(w[2 * m], w[2 * m + 1], pick);
-                            f[m] = Pair<T>::scale(__byte_perm(s[2 * m], s[2 * m + 1], pick));
+                            f[m] = Pair<__half>::times(__byte_perm(s[2 * m], s[2 * m + 1], pick), lift2);
                         }
                         const int channel = (group + half) * kGroup + 4 * g;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int d = channel + c;
                             uint4 v;
-                            v.x = Pair<T>::value(Pair<T>::codes(x[0] >> (4 * c)), f[0]);
-                            v.y = Pair<T>::value(Pair<T>::codes(x[1] >> (4 * c)), f[1]);
-                            v.z = Pair<T>::value(Pair<T>::codes(x[2] >> (4 * c)), f[2]);
-                            v.w = Pair<T>::value(Pair<T>::codes(x[3] >> (4 * c)), f[3]);
+                            v.x = Pair<__half>::times(Pair<__half>::codes(x[0] >> (4 * c)), f[0]);
+                            v.y = Pair<__half>::times(Pair<__half>::codes(x[1] >> (4 * c)), f[1]);
+                            v.z = Pair<__half>::times(Pair<__half>::codes(x[2] >> (4 * c)), f[2]);
+                            v.w = Pair<__half>::times(Pair<__half>::codes(x[3] >> (4 * c)), f[3]);
                             *reinterpret_cast<uint4 *>(dst + d * 128 + ((eight ^ (d & 7)) * 16)) = v;
                         }
                     }
@@ -873,38 +897,33 @@ chunk_kernel(const __grid_constant__ Args p)
                 const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
                 unsigned char *dst = smem + S::kOffKeys + key.stage * 2 * S::kKeyBytes;
 #pragma unroll 1
-                for (int i = turn; i < kTokens * (D / 32); i += 128) {
-                    // 16 bytes of one token: four words, of the groups of one stretch in turn
-                    const int quad = i / 8 % (D / 32), token = i / (D / 4) * 8 + i % 8;
+                for (int i = turn; i < kTokens * kGroups; i += 128) {
+                    // a group of one token: four words
+                    const int token = i / (8 * kGroups) * 8 + i % 8, group = i / 8 % kGroups;
+                    const int stretch = group / kPer, g = group % kPer;
                     const unsigned char *rec = src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord;
-                    const uint4 words = *reinterpret_cast<const uint4 *>(rec + quad * 16);
-                    const int stretch = quad / kPer, first = quad % kPer * 4;     // place in the stretch
-                    uint32_t hi[kPer], lo[kPer];
-                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(rec + D + stretch * kPer * 2);
+                    const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + stretch * 64) + g;
+                    uint32_t w[4], hi, lo;
 #pragma unroll
-                    for (int g = 0; g < kPer; g += 2) {
-                        uint32_t h, l;
-                        Pair<T>::split(scales[g / 2], h, l);
-                        hi[g] = __byte_perm(h, h, 0x1010), hi[g + 1] = __byte_perm(h, h, 0x3232);
-                        lo[g] = __byte_perm(l, l, 0x1010), lo[g + 1] = __byte_perm(l, l, 0x3232);
-                    }
-                    const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = words[k * kPer];
+                    const unsigned scale = reinterpret_cast<const unsigned short *>(rec + D)[group];
+                    Pair<T>::split(scale * 0x10001u, hi, lo);
+                    const int piece = stretch * 16 + 4 * g;               // of eight channels, the first
+                    unsigned char *row = dst + piece / 8 * (kTokens * 128) + token * 128;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int g = k % kPer;                                   // first is a multiple of kPer
-                        const int piece = stretch * 16 + 4 * g + (first + k) / kPer;   // of eight channels
                         uint32_t x[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             x[c] = Pair<T>::codes(w[k] >> (4 * c));
-                        unsigned char *at = dst + piece / 8 * (kTokens * 128) + token * 128 +
-                                            ((piece & 7) ^ (token & 7)) * 16;
+                        unsigned char *at = row + (((piece + k) & 7) ^ (token & 7)) * 16;
                         uint4 v;
-                        v.x = Pair<T>::times(x[0], hi[g]), v.y = Pair<T>::times(x[1], hi[g]);
-                        v.z = Pair<T>::times(x[2], hi[g]), v.w = Pair<T>::times(x[3], hi[g]);
+                        v.x = Pair<T>::times(x[0], hi), v.y = Pair<T>::times(x[1], hi);
+                        v.z = Pair<T>::times(x[2], hi), v.w = Pair<T>::times(x[3], hi);
                         *reinterpret_cast<uint4 *>(at) = v;
-                        v.x = Pair<T>::times(x[0], lo[g]), v.y = Pair<T>::times(x[1], lo[g]);
-                        v.z = Pair<T>::times(x[2], lo[g]), v.w = Pair<T>::times(x[3], lo[g]);
+                        v.x = Pair<T>::times(x[0], lo), v.y = Pair<T>::times(x[1], lo);
+                        v.z = Pair<T>::times(x[2], lo), v.w = Pair<T>::times(x[3], lo);
                         *reinterpret_cast<uint4 *>(at + S::kKeyBytes) = v;
                     }
                 }
@@ -927,6 +946,7 @@ chunk_kernel(const __grid_constant__ Args p)
         const int r = tile * kTileRows + warp % 4 * 32 + lane;
         const uint32_t out_at = rows_at + S::kOutColumn + tile * D;
         unsigned score_phase[2] = {0, 0}, output_phase = 0;
+        Turn<S::kValueStages> value;
         int count = 0, unit = 0, spin = tile;
         const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
@@ -937,11 +957,14 @@ chunk_kernel(const __grid_constant__ Args p)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             if (tile >= u.row_tiles) {
                 count += n;
+                for (int t = 0; t < n; ++t)
+                    value.step();
                 continue;
             }
             const bool in = r < u.rows;
             const int limit = RowAt(p, u, r).limit;
             float m = -INFINITY, l = 0.f;
+            int lift = 0;              // that the output has
             if (n > 0) {
                 // the row's query, channels (j, j + 4) of each eight in pairs
                 const RowAt row(p, u, r);
@@ -989,7 +1012,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 load_columns(s0, at);
                 load_columns(s1, at + 32);
                 wait_loads();
-                const unsigned long long there = ctl.there[count++ % kSlots];
+                const unsigned long long there = ctl.there[count % kSlots];
                 if (there != ~0ULL || (t + 1) * kTokens > see_lo) {
                     const int left = limit - t * kTokens;
                     const unsigned long long see = there & (left >= 64 ? ~0ULL : left <= 0 ? 0 : ~0ULL >> (64 - left));
@@ -1005,11 +1028,17 @@ chunk_kernel(const __grid_constant__ Args p)
                 // The maximum that weights are relative to follows the true one only where
                 // that is 8 above it: weights stay below 2^8 and outputs are seldom scaled.
                 const bool grows = most > m + 8.f || m == -INFINITY;
-                if (__any_sync(~0u, grows && most > m)) {
+                bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                value.step();
+                __syncwarp();
+                const int lift_now = ctl.lift[count++ % kSlots];
+                if (__any_sync(~0u, (grows && most > m) || lift_now != lift)) {
                     const float to = grows ? fmaxf(most, m) : m;
-                    const float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
+                    float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
                     l *= f;
                     m = to;
+                    f *= __uint_as_float((unsigned)(lift_now - lift + 127) << 23);
+                    lift = lift_now;
                     if (t > t0) {
                         bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                         fence_after();
@@ -1026,12 +1055,12 @@ chunk_kernel(const __grid_constant__ Args p)
                         }
                     }
                 }
-                const float low = m == -INFINITY ? 0.f : m;
+                const float low = (m == -INFINITY ? 0.f : m) - kRaise;
                 Two sum[2] = {};
                 uint32_t w[16];
-                weights_of<T>(w, s0, c, low, sum);
+                weights_of(w, s0, c, low, sum);
                 store_columns(at, w);
-                weights_of<T>(w, s1, c, low, sum);
+                weights_of(w, s1, c, low, sum);
                 store_columns(at + 16, w);
                 l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
@@ -1064,7 +1093,9 @@ chunk_kernel(const __grid_constant__ Args p)
                 fence_after();
                 __syncwarp();
             }
-            float inv = l == 0.f ? 0.f : 1.f / l;
+            m -= kRaise;
+            const float down = __uint_as_float((unsigned)(127 - lift) << 23);
+            float inv = l == 0.f ? 0.f : down / l;
             if (*lost)
                 inv = l = m = __uint_as_float(0x7fffffffu);
             const RowAt row(p, u, r);
@@ -1085,7 +1116,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        partial[(part + i) * S::kRows + r] = nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(x[i]);
+                        partial[(part + i) * S::kRows + r] = nan ? __uint_as_float(0x7fffffffu) : __uint_as_float(x[i]) * down;
                 } else if (in) {
                     const float f = nan ? __uint_as_float(0x7fffffffu) : inv;
                     // rows that see nothing are 0, whatever the tile before left there
