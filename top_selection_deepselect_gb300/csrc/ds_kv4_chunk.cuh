@@ -25,7 +25,7 @@
 // word is taken with that of the next token, so that pairs are (token, token + 1)
 // of one channel: both operands end up with the summed index contiguous.
 //
-// Roles of a CTA's warps: softmax (four warps a tile of rows, a row a thread),
+// Roles of a CTA's warps: softmax (eight warps a tile of rows, half a row a thread),
 // expansion of keys and of values (four warps each), one that issues the products,
 // one that copies records.  They meet on arrival barriers in shared memory only.
 //
@@ -67,13 +67,10 @@ struct Shape {
     static constexpr int kValueStages = D == 256 ? 2 : 3;
     static constexpr int kRawStages = D == 256 ? 1 : 3;
     // warps
-    static constexpr int kSoftmaxWarps = 4 * kTiles;
+    static constexpr int kSoftmaxWarps = 8 * kTiles;
     static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4;
     static constexpr int kProductWarp = kValueWarp + 4, kCopyWarp = kProductWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + 1);
-    // Registers: 18 warps have 96 each; a softmax row wants 120, which the warps that
-    // expand give: 8 x 120 + 8 x 72 + 2 x 96 = 18 x 96.
-    static constexpr bool kShift = kTiles == 2;
     // columns of tensor memory
     static constexpr int kOutColumn = 0;
     static constexpr int kScoreColumn = kTiles * D;             // two of them
@@ -328,13 +325,25 @@ struct Pair<__half> {
         asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0x70917091u));
         return y;
     }
-    // s = hi + lo, eight significant bits and three: times a code of up to three
-    // bits both are exact.
-    static __device__ __forceinline__ void split(uint32_t s, uint32_t &hi, uint32_t &lo)
+    // A key's scale s = hi + lo, eight significant bits and three: times a code of up
+    // to three bits both are exact.
+    struct Key {
+        uint32_t hi, lo;
+    };
+    static __device__ __forceinline__ Key key(uint32_t s)
     {
+        Key k;
         s = bounded(s);
-        hi = ((s & 0x7fff7fffu) + 0x00040004u) & 0xfff8fff8u;
-        asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(s), "r"(hi));
+        k.hi = (s + 0x00040004u) & 0xfff8fff8u;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(k.lo) : "r"(s), "r"(k.hi));
+        return k;
+    }
+    // both products of the codes in places c and c + 4 of a word
+    static __device__ __forceinline__ void keys(uint32_t w, int c, const Key &k, uint32_t &hi, uint32_t &lo)
+    {
+        const uint32_t x = codes(w >> (4 * c));
+        hi = times(x, k.hi);
+        lo = times(x, k.lo);
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
@@ -346,17 +355,10 @@ struct Pair<__half> {
 
 template <>
 struct Pair<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t codes(uint32_t w)
-    {
-        uint32_t x, y;
-        asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(x) : "r"(w));
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3f803f80u), "r"(0xc308c308u));
-        return y;
-    }
-    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
+    static __device__ __forceinline__ uint32_t times_add(uint32_t a, uint32_t b, uint32_t c)
     {
         uint32_t y;
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(0x80008000u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
         return y;
     }
     static __device__ __forceinline__ uint32_t convert(uint32_t s)     // fp16 pair to bf16 pair
@@ -364,16 +366,33 @@ struct Pair<__nv_bfloat16> {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&s));
         return pack(f.x, f.y);
     }
-    // s = hi + lo, five significant bits each (the second with a sign): times a
-    // code of up to three bits both are exact.  (Scales from 65024 on, the last
-    // 32 steps of fp16, have six in lo.)  NaN is in lo.
-    static __device__ __forceinline__ void split(uint32_t s, uint32_t &hi, uint32_t &lo)
+    // A key's scale s = hi + lo, five significant bits each (the second with a sign):
+    // times a code of up to three bits both are exact, and so is either times 24.
+    // (Scales from 65024 on, the last 15 of fp16, have six in lo.)  NaN is in lo.
+    struct Key {
+        uint32_t hi, lo, hi24, lo24;        // and both times -24
+    };
+    static __device__ __forceinline__ Key key(uint32_t s)
     {
+        Key k;
         const uint32_t h = (__vminu2(s, 0x7bdf7bdfu) + 0x00200020u) & 0xffc0ffc0u;
         uint32_t l;
         asm("sub.f16x2 %0, %1, %2;" : "=r"(l) : "r"(s), "r"(h));
-        hi = convert(h);
-        lo = convert(l);
+        k.hi = convert(h);
+        k.lo = convert(l);
+        k.hi24 = times_add(k.hi, 0xc1c0c1c0u, 0x80008000u);
+        k.lo24 = times_add(k.lo, 0xc1c0c1c0u, 0x80008000u);
+        return k;
+    }
+    // Both products of the codes in places c and c + 4 of a word: a code in the upper
+    // bits of the fraction of 16 makes it 16 + u, and (16 + u) s - 24 s is exact.
+    static __device__ __forceinline__ void keys(uint32_t w, int c, const Key &k, uint32_t &hi, uint32_t &lo)
+    {
+        const uint32_t shifted = c == 0 ? w << 3 : w >> (4 * c - 3);
+        uint32_t x;
+        asm("lop3.b32 %0, %1, 0x00780078, 0x41804180, 0xea;" : "=r"(x) : "r"(shifted));
+        hi = times_add(x, k.hi, k.hi24);
+        lo = times_add(x, k.lo, k.lo24);
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
@@ -486,6 +505,7 @@ struct Control {
     int bad[kSlots][8];                    // of a unit: first position whose value scale is no number, a group
     uint32_t tensor;
     int lost;
+    float swap[2][2][2][kTileRows];        // of a row tile's halves: maxima, sums
 };
 
 // Row r of a unit: its query's row in q and out, the query head, how many tokens it sees.
@@ -541,9 +561,9 @@ chunk_kernel(const __grid_constant__ Args p)
             bar_init(shared_at(&ctl.value_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            bar_init(shared_at(&ctl.query[i]), 4);
+            bar_init(shared_at(&ctl.query[i]), 8);
             bar_init(shared_at(&ctl.score[i]), 1);
-            bar_init(shared_at(&ctl.weight[i]), 4);
+            bar_init(shared_at(&ctl.weight[i]), 8);
             bar_init(shared_at(&ctl.output[i]), 1);
         }
         bar_init(shared_at(&ctl.last), 1);
@@ -708,7 +728,8 @@ chunk_kernel(const __grid_constant__ Args p)
             };
             int spin = 0;                         // buffer of the next scores, one row tile
             while (next()) {
-                const int n = u.t1 - u.t0, row_tiles = u.row_tiles;
+                // the same for all lanes, which the compiler cannot know of shared memory
+                const int n = __shfl_sync(~0u, u.t1 - u.t0, 0), row_tiles = __shfl_sync(~0u, u.row_tiles, 0);
                 if (n == 0)
                     continue;
                 for (int t = 0; t < row_tiles; ++t) {
@@ -720,20 +741,23 @@ chunk_kernel(const __grid_constant__ Args p)
                 fence_after();
                 wait_key();
                 if (S::kTiles == 2) {
-                    for (int t = 0; t < row_tiles; ++t)
-                        scores(t, t);
+                    scores(0, 0);
+                    if (row_tiles == 2)
+                        scores(1, 1);
                     release_key();
                     for (int j = 0; j < n; ++j) {
-                        for (int t = 0; t < row_tiles; ++t) {
-                            if (t == 0)
-                                wait_value();
-                            wait_weight(t);
-                            outputs(t, t, j > 0);
-                            if (j + 1 < n) {
-                                if (t == 0)
-                                    wait_key();
-                                scores(t, t);
-                            }
+                        wait_value();
+                        wait_weight(0);
+                        outputs(0, 0, j > 0);
+                        if (j + 1 < n) {
+                            wait_key();
+                            scores(0, 0);
+                        }
+                        if (row_tiles == 2) {
+                            wait_weight(1);
+                            outputs(1, 1, j > 0);
+                            if (j + 1 < n)
+                                scores(1, 1);
                         }
                         products_arrive(shared_at(&ctl.value_empty[value.stage]), lead);
                         value.step();
@@ -767,8 +791,6 @@ chunk_kernel(const __grid_constant__ Args p)
         __syncwarp();
     } else if (warp >= S::kValueWarp) {
         // ---- values: V^T, a row for each channel -----------------------------------------
-        if (S::kShift)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         Turn<S::kRawStages> raw;
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
@@ -791,44 +813,59 @@ chunk_kernel(const __grid_constant__ Args p)
                 unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
                 const unsigned long long there = ctl.there[count % kSlots];
                 const bool masked = there != ~0ULL || (t + 1) * kTokens > see_lo;
-                // the tile's largest scale: each warp looks at all of them, and comes to the same
-                unsigned most = 0;
+                // a lane's work: eight tokens of one word (or two), which is four channels of
+                // two neighbouring groups
+                constexpr int kWords = D / 8, kTurns = kWords > 16 ? 2 : 1;
+                const int eight = turn % 8;
+                const unsigned char *rec = src + eight * S::kGroupBytes;
+                uint32_t s[kTurns][8];
+                unsigned high = 0;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int token = lane + 32 * k;
-                    const uint32_t *scales = reinterpret_cast<const uint32_t *>(
-                        src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord + D + D / 16);
-                    unsigned both = 0;
+                for (int i = 0; i < kTurns; ++i) {
+                    const int word = turn / 8 + 16 * i, place = word % (4 * kPer) * 2;
+                    const int group = word / (4 * kPer) * kPer + place % kPer;
 #pragma unroll
-                    for (int g = 0; g < kGroups / 2; ++g) {
-                        const unsigned x = scales[g] & 0x7fff7fffu;
-                        both = __vmaxu2(both, x & __vcmpltu2(x, 0x7c007c00u));
+                    for (int k = 0; k < 8; ++k) {
+                        s[i][k] = word < kWords ? *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D + D / 16 + group * 2)
+                                                : 0;
+                        high = __vmaxu2(high, s[i][k]);
                     }
-                    if (there >> token & 1)
-                        most = max(most, max(both & 0xffffu, both >> 16));
                 }
-                most = __reduce_max_sync(~0u, most);
-                // most 2^lift against kHigh, in exponents: below 2^-14 a scale is far from it
-                if (fresh || (int)(most >> 10) + lift >= (int)(kHigh >> 10)) {
-                    lift = lift_of(most);
+                // All scales are some lane's of every warp that has work, so that all of
+                // these come to the same lift.  Against kHigh exponents are compared, of
+                // what may not be there, or no number, too: then it is looked at again.
+                if (__any_sync(~0u, fresh || (int)(max(high & 0xffffu, high >> 16) >> 10) + lift >= (int)(kHigh >> 10))) {
+                    unsigned most = 0;
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        const int token = lane + 32 * k;
+                        const unsigned short *scales = reinterpret_cast<const unsigned short *>(
+                            src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord + D + D / 16);
+#pragma unroll 1
+                        for (int g = 0; g < kGroups; ++g) {
+                            const unsigned x = scales[g] & 0x7fffu;
+                            if ((there >> token & 1) && x < 0x7c00u)
+                                most = max(most, x);
+                        }
+                    }
+                    most = __reduce_max_sync(~0u, most);
+                    if (fresh || (int)(most >> 10) + lift >= (int)(kHigh >> 10))
+                        lift = lift_of(most);
                     fresh = false;
                 }
                 const unsigned lift2 = lift_bits(lift) * 0x10001u;
                 if (turn == 0)
                     ctl.lift[count % kSlots] = lift;
-#pragma unroll 1
-                for (int i = turn; i < 8 * (D / 8); i += 128) {
-                    // eight tokens of one word: four channels of two neighbouring groups
-                    const int eight = i % 8, word = i / 8;
-                    const int stretch = word / (4 * kPer), place = word % (4 * kPer) * 2;
-                    const int g = place / kPer, group = stretch * kPer + place % kPer;
-                    const unsigned char *rec = src + eight * S::kGroupBytes;
-                    uint32_t w[8], s[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                for (int i = 0; i < kTurns; ++i) {
+                    const int word = turn / 8 + 16 * i, place = word % (4 * kPer) * 2;
+                    if (word >= kWords)
+                        break;
+                    const int g = place / kPer, group = word / (4 * kPer) * kPer + place % kPer;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
                         w[k] = *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D / 2 + word * 4);
-                        s[k] = *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D + D / 16 + group * 2);
-                    }
                     if (masked) {
                         // tokens that are not there, or that not every row sees, may
                         // hold anything: their weights are 0, which 0 * NaN is not
@@ -836,27 +873,26 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             if (!(here >> k & 1))
-                                s[k] = 0;
+                                s[i][k] = 0;
                             const int pos = t * kTokens + 8 * eight + k;
-                            if ((s[k] & 0x7c00u) == 0x7c00u) {
+                            if ((s[i][k] & 0x7c00u) == 0x7c00u) {
                                 atomicMin(&bad[group], pos);
-                                s[k] &= 0xffff0000u;
+                                s[i][k] &= 0xffff0000u;
                             }
-                            if ((s[k] & 0x7c000000u) == 0x7c000000u) {
+                            if ((s[i][k] & 0x7c000000u) == 0x7c000000u) {
                                 atomicMin(&bad[group + 1], pos);
-                                s[k] &= 0xffffu;
+                                s[i][k] &= 0xffffu;
                             }
                         }
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const unsigned pick = half ? 0x7632 : 0x5410;
-                        uint32_t x[4];
-                        uint32_t f[4];
+                        uint32_t x[4], f[4];
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             x[m] = __byte_perm(w[2 * m], w[2 * m + 1], pick);
-                            f[m] = Pair<__half>::times(__byte_perm(s[2 * m], s[2 * m + 1], pick), lift2);
+                            f[m] = Pair<__half>::times(__byte_perm(s[i][2 * m], s[i][2 * m + 1], pick), lift2);
                         }
                         const int channel = (group + half) * kGroup + 4 * g;
 #pragma unroll
@@ -884,8 +920,6 @@ chunk_kernel(const __grid_constant__ Args p)
         }
     } else if (warp >= S::kKeyWarp) {
         // ---- keys: a row for each token ----------------------------------------------------
-        if (S::kShift)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         Turn<S::kRawStages> raw;
         Turn<S::kKeyStages> key;
         const int turn = (warp - S::kKeyWarp) * 32 + lane;
@@ -903,28 +937,24 @@ chunk_kernel(const __grid_constant__ Args p)
                     const int stretch = group / kPer, g = group % kPer;
                     const unsigned char *rec = src + token / 8 * S::kGroupBytes + token % 8 * S::kRecord;
                     const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + stretch * 64) + g;
-                    uint32_t w[4], hi, lo;
+                    uint32_t w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         w[k] = words[k * kPer];
                     const unsigned scale = reinterpret_cast<const unsigned short *>(rec + D)[group];
-                    Pair<T>::split(scale * 0x10001u, hi, lo);
+                    const typename Pair<T>::Key key_scale = Pair<T>::key(scale * 0x10001u);
                     const int piece = stretch * 16 + 4 * g;               // of eight channels, the first
                     unsigned char *row = dst + piece / 8 * (kTokens * 128) + token * 128;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            x[c] = Pair<T>::codes(w[k] >> (4 * c));
                         unsigned char *at = row + (((piece + k) & 7) ^ (token & 7)) * 16;
-                        uint4 v;
-                        v.x = Pair<T>::times(x[0], hi), v.y = Pair<T>::times(x[1], hi);
-                        v.z = Pair<T>::times(x[2], hi), v.w = Pair<T>::times(x[3], hi);
-                        *reinterpret_cast<uint4 *>(at) = v;
-                        v.x = Pair<T>::times(x[0], lo), v.y = Pair<T>::times(x[1], lo);
-                        v.z = Pair<T>::times(x[2], lo), v.w = Pair<T>::times(x[3], lo);
-                        *reinterpret_cast<uint4 *>(at + S::kKeyBytes) = v;
+                        uint4 x, y;
+                        Pair<T>::keys(w[k], 0, key_scale, x.x, y.x);
+                        Pair<T>::keys(w[k], 1, key_scale, x.y, y.y);
+                        Pair<T>::keys(w[k], 2, key_scale, x.z, y.z);
+                        Pair<T>::keys(w[k], 3, key_scale, x.w, y.w);
+                        *reinterpret_cast<uint4 *>(at) = x;
+                        *reinterpret_cast<uint4 *>(at + S::kKeyBytes) = y;
                     }
                 }
                 fence_proxy();
@@ -938,14 +968,20 @@ chunk_kernel(const __grid_constant__ Args p)
             }
         }
     } else {
-        // ---- softmax: a row a thread ---------------------------------------------------------
-        if (S::kShift)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-        const int tile = warp / 4;
+        // ---- softmax: half a row a thread ------------------------------------------------------
+        const int tile = warp / 8, half = warp / 4 % 2, local = warp % 4 * 32 + lane;
         const uint32_t rows_at = tensor + ((uint32_t)(warp % 4 * 32) << 16);
-        const int r = tile * kTileRows + warp % 4 * 32 + lane;
-        const uint32_t out_at = rows_at + S::kOutColumn + tile * D;
-        unsigned score_phase[2] = {0, 0}, output_phase = 0;
+        const int r = tile * kTileRows + local;
+        const uint32_t out_at = rows_at + S::kOutColumn + tile * D + half * (D / 2);
+        unsigned score_phase[2] = {0, 0}, output_phase = 0, side = 0;
+        // The other half's value for this row: both warps of the rows meet here.
+        auto exchange = [&](float x) -> float {
+            ctl.swap[side][tile][half][local] = x;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + tile * 4 + warp % 4) : "memory");
+            const float y = ctl.swap[side][tile][half ^ 1][local];
+            side ^= 1;
+            return y;
+        };
         Turn<S::kValueStages> value;
         int count = 0, unit = 0, spin = tile;
         const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
@@ -954,7 +990,7 @@ chunk_kernel(const __grid_constant__ Args p)
             const int n = u.t1 - u.t0, slot = unit % kSlots;
             unit += n > 0;
             if (S::kTiles == 2)       // one tile's warps are at most a unit ahead of the other's
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                asm volatile("bar.sync 9, 512;" ::: "memory");
             if (tile >= u.row_tiles) {
                 count += n;
                 for (int t = 0; t < n; ++t)
@@ -971,18 +1007,19 @@ chunk_kernel(const __grid_constant__ Args p)
                 const T *q = (const T *)p.a.q + row.token * p.a.q_query + row.head * p.a.q_head;
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
-                    uint32_t x[32];
+                    const int first = half * (D / 2) + part * 32;
+                    uint32_t x[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (in) {
                             if (p.q_vector) {
-                                v = *reinterpret_cast<const uint4 *>(q + part * 64 + e * 8);
+                                v = *reinterpret_cast<const uint4 *>(q + first + e * 8);
                             } else {
                                 unsigned short y[8];
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)
-                                    y[k] = *reinterpret_cast<const unsigned short *>(q + part * 64 + e * 8 + k);
+                                    y[k] = *reinterpret_cast<const unsigned short *>(q + first + e * 8 + k);
                                 v = make_uint4(y[0] | (unsigned)y[1] << 16, y[2] | (unsigned)y[3] << 16,
                                                y[4] | (unsigned)y[5] << 16, y[6] | (unsigned)y[7] << 16);
                             }
@@ -993,7 +1030,7 @@ chunk_kernel(const __grid_constant__ Args p)
                         x[4 * e + 3] = __byte_perm(v.y, v.w, 0x7632) ^ flip;
                     }
                     __syncwarp();
-                    store_columns(rows_at + S::kQueryColumn + tile * (D / 2) + part * 32, x);
+                    store_columns(rows_at + S::kQueryColumn + tile * (D / 2) + first / 2, x);
                 }
                 wait_stores();
                 fence_before();
@@ -1008,23 +1045,19 @@ chunk_kernel(const __grid_constant__ Args p)
                 score_phase[spin] ^= 1;
                 fence_after();
                 __syncwarp();
-                uint32_t s0[32], s1[32];
-                load_columns(s0, at);
-                load_columns(s1, at + 32);
+                uint32_t s[32];
+                load_columns(s, at + half * 32);
                 wait_loads();
-                const unsigned long long there = ctl.there[count % kSlots];
-                if (there != ~0ULL || (t + 1) * kTokens > see_lo) {
-                    const int left = limit - t * kTokens;
-                    const unsigned long long see = there & (left >= 64 ? ~0ULL : left <= 0 ? 0 : ~0ULL >> (64 - left));
-                    const unsigned lo = (unsigned)see, hi = (unsigned)(see >> 32);
+                const unsigned there = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots])[half];
+                if (there != ~0u || (t + 1) * kTokens > see_lo) {
+                    const int left = limit - t * kTokens - half * 32;
+                    const unsigned see = there & (left >= 32 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - left));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        s0[i] = lo >> i & 1 ? s0[i] : 0xff800000u;
-                        s1[i] = hi >> i & 1 ? s1[i] : 0xff800000u;
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        s[i] = see >> i & 1 ? s[i] : 0xff800000u;
                 }
-                float most = fmaxf(largest_of(s0), largest_of(s1));
-                most *= c;
+                float most = largest_of(s);
+                most = fmaxf(most, exchange(most)) * c;
                 // The maximum that weights are relative to follows the true one only where
                 // that is 8 above it: weights stay below 2^8 and outputs are seldom scaled.
                 const bool grows = most > m + 8.f || m == -INFINITY;
@@ -1044,7 +1077,7 @@ chunk_kernel(const __grid_constant__ Args p)
                         fence_after();
                         __syncwarp();
 #pragma unroll 1
-                        for (int part = 0; part < D; part += 16) {
+                        for (int part = 0; part < D / 2; part += 16) {
                             uint32_t x[16];
                             load_columns(x, out_at + part);
                             wait_loads();
@@ -1058,10 +1091,8 @@ chunk_kernel(const __grid_constant__ Args p)
                 const float low = (m == -INFINITY ? 0.f : m) - kRaise;
                 Two sum[2] = {};
                 uint32_t w[16];
-                weights_of(w, s0, c, low, sum);
-                store_columns(at, w);
-                weights_of(w, s1, c, low, sum);
-                store_columns(at + 16, w);
+                weights_of(w, s, c, low, sum);
+                store_columns(at + half * 16, w);
                 l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
                 // With one row tile scores are a product ahead of outputs.  The output
@@ -1082,13 +1113,14 @@ chunk_kernel(const __grid_constant__ Args p)
             float *partial = nullptr;
             if (!whole) {
                 partial = p.partial + (2LL * blockIdx.x + (u.t0 == 0)) * S::kPartial;
-                if (u.t0 == 0 && r == 0) {
+                if (u.t0 == 0 && r == 0 && half == 0) {
                     p.splits[blockIdx.x].block = u.block;
                     p.splits[blockIdx.x].head = u.head;
                     p.splits[blockIdx.x].parts = 1 + u.later;
                 }
             }
             if (n > 0) {
+                l += exchange(l);
                 bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                 fence_after();
                 __syncwarp();
@@ -1101,11 +1133,11 @@ chunk_kernel(const __grid_constant__ Args p)
             const RowAt row(p, u, r);
             const long long to = (long long)row.token * p.a.heads + row.head;
 #pragma unroll 1
-            for (int part = 0; part < D; part += 32) {
+            for (int part = half * (D / 2); part < (half + 1) * (D / 2); part += 32) {
                 uint32_t x[32];
                 __syncwarp();
                 if (n > 0) {
-                    load_columns(x, out_at + part);
+                    load_columns(x, rows_at + S::kOutColumn + tile * D + part);
                     wait_loads();
                 } else {
 #pragma unroll
@@ -1130,7 +1162,9 @@ chunk_kernel(const __grid_constant__ Args p)
                         dst[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 }
             }
-            if (!whole) {
+            if (half != 0) {
+                // the other half's
+            } else if (!whole) {
                 partial[D * S::kRows + r] = m;
                 partial[(D + 1) * S::kRows + r] = l;
             } else if (in && p.a.lse) {
