@@ -68,8 +68,10 @@ struct Shape {
     static constexpr int kRawStages = D == 256 ? 1 : 3;
     // warps
     static constexpr int kSoftmaxWarps = 8 * kTiles;
-    static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + 4;
-    static constexpr int kProductWarp = kValueWarp + 4, kCopyWarp = kProductWarp + 1;
+    // Of each four warps after them two expand keys and two values: a scheduler (warps
+    // of one number modulo 4) then has one of the two roles' instructions to fetch.
+    static constexpr int kExpandWarp = kSoftmaxWarps, kExpandWarps = 8;
+    static constexpr int kProductWarp = kExpandWarp + kExpandWarps, kCopyWarp = kProductWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + 1);
     // columns of tensor memory
     static constexpr int kOutColumn = 0;
@@ -789,12 +791,12 @@ chunk_kernel(const __grid_constant__ Args p)
             }
         }
         __syncwarp();
-    } else if (warp >= S::kValueWarp) {
+    } else if (warp >= S::kExpandWarp && warp % 4 >= 2) {
         // ---- values: V^T, a row for each channel -----------------------------------------
         Turn<S::kRawStages> raw;
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
-        const int turn = (warp - S::kValueWarp) * 32 + lane;
+        const int turn = ((warp - S::kExpandWarp) / 4 * 2 + warp % 4 - 2) * 32 + lane;
         while (next()) {
             if (u.t1 == u.t0)
                 continue;
@@ -885,7 +887,7 @@ chunk_kernel(const __grid_constant__ Args p)
                             }
                         }
                     }
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const unsigned pick = half ? 0x7632 : 0x5410;
                         uint32_t x[4], f[4];
@@ -918,11 +920,11 @@ chunk_kernel(const __grid_constant__ Args p)
                 value.step();
             }
         }
-    } else if (warp >= S::kKeyWarp) {
+    } else if (warp >= S::kExpandWarp) {
         // ---- keys: a row for each token ----------------------------------------------------
         Turn<S::kRawStages> raw;
         Turn<S::kKeyStages> key;
-        const int turn = (warp - S::kKeyWarp) * 32 + lane;
+        const int turn = ((warp - S::kExpandWarp) / 4 * 2 + warp % 4) * 32 + lane;
         while (next()) {
             const int t1 = u.t1;
             for (int t = u.t0; t < t1; ++t) {
@@ -974,9 +976,8 @@ chunk_kernel(const __grid_constant__ Args p)
         const int r = tile * kTileRows + local;
         const uint32_t out_at = rows_at + S::kOutColumn + tile * D + half * (D / 2);
         unsigned score_phase[2] = {0, 0}, output_phase = 0, side = 0;
-        // The other half's value for this row: both warps of the rows meet here.
-        auto exchange = [&](float x) -> float {
-            ctl.swap[side][tile][half][local] = x;
+        // The other half's value for this row, where both warps of the rows meet.
+        auto meet = [&]() -> float {
             asm volatile("bar.sync %0, 64;" ::"r"(1 + tile * 4 + warp % 4) : "memory");
             const float y = ctl.swap[side][tile][half ^ 1][local];
             side ^= 1;
@@ -1041,6 +1042,13 @@ chunk_kernel(const __grid_constant__ Args p)
             const int t0 = u.t0, t1 = u.t1, see_lo = u.see_lo;
             for (int t = t0; t < t1; ++t) {
                 const uint32_t at = rows_at + S::kScoreColumn + spin * kTokens;
+                // what is known of the tile once its values are expanded, which is mostly
+                // before its scores are there
+                bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                value.step();
+                const int lift_now = ctl.lift[count % kSlots];
+                const unsigned there = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots])[half];
+                ++count;
                 bar_wait(shared_at(&ctl.score[spin]), score_phase[spin], lost);
                 score_phase[spin] ^= 1;
                 fence_after();
@@ -1048,7 +1056,6 @@ chunk_kernel(const __grid_constant__ Args p)
                 uint32_t s[32];
                 load_columns(s, at + half * 32);
                 wait_loads();
-                const unsigned there = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots])[half];
                 if (there != ~0u || (t + 1) * kTokens > see_lo) {
                     const int left = limit - t * kTokens - half * 32;
                     const unsigned see = there & (left >= 32 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - left));
@@ -1056,15 +1063,16 @@ chunk_kernel(const __grid_constant__ Args p)
                     for (int i = 0; i < 32; ++i)
                         s[i] = see >> i & 1 ? s[i] : 0xff800000u;
                 }
+                // Weights are relative to a maximum that follows the true one only where
+                // that is 8 above it, which is seldom: they are worked out before the other
+                // half's maximum is known, and again where it turns out that it grows.
                 float most = largest_of(s);
-                most = fmaxf(most, exchange(most)) * c;
-                // The maximum that weights are relative to follows the true one only where
-                // that is 8 above it: weights stay below 2^8 and outputs are seldom scaled.
+                ctl.swap[side][tile][half][local] = most;
+                Two sum[2] = {};
+                uint32_t w[16];
+                weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
+                most = fmaxf(most, meet()) * c;
                 const bool grows = most > m + 8.f || m == -INFINITY;
-                bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
-                value.step();
-                __syncwarp();
-                const int lift_now = ctl.lift[count++ % kSlots];
                 if (__any_sync(~0u, (grows && most > m) || lift_now != lift)) {
                     const float to = grows ? fmaxf(most, m) : m;
                     float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
@@ -1072,6 +1080,8 @@ chunk_kernel(const __grid_constant__ Args p)
                     m = to;
                     f *= __uint_as_float((unsigned)(lift_now - lift + 127) << 23);
                     lift = lift_now;
+                    sum[0] = sum[1] = Two{0.f, 0.f};
+                    weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
                     if (t > t0) {
                         bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                         fence_after();
@@ -1088,10 +1098,6 @@ chunk_kernel(const __grid_constant__ Args p)
                         }
                     }
                 }
-                const float low = (m == -INFINITY ? 0.f : m) - kRaise;
-                Two sum[2] = {};
-                uint32_t w[16];
-                weights_of(w, s, c, low, sum);
                 store_columns(at + half * 16, w);
                 l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
@@ -1120,7 +1126,8 @@ chunk_kernel(const __grid_constant__ Args p)
                 }
             }
             if (n > 0) {
-                l += exchange(l);
+                ctl.swap[side][tile][half][local] = l;
+                l += meet();
                 bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                 fence_after();
                 __syncwarp();
