@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 // Places of a CTA where units are cut: not more parts to join than the work is worth.
-constexpr int kLeast = 16;
+constexpr int kLeast = 96;
 
 // Of a value a thread: what `combine` makes of all threads', and in *before of those below.
 template <typename V, typename F>
@@ -180,7 +180,7 @@ size_t lay_out(Args &p, int head_dim, int sms, unsigned char *base)
     const long long blocks = (long long)p.a.tokens * p.group / p.rows + p.a.batch;
     // no more CTAs than the largest possible line has work for
     const double room = (double)p.c.max_pages * p.c.page_size;
-    const double most = (double)blocks * p.c.kv_heads * (kUnitCost + 2 * (room / 64 + 1)) / kLeast + 1;
+    const double most = (double)blocks * p.c.kv_heads * (kUnitCost + 8 * (room / 64 + 1)) / kLeast + 1;
     p.ctas = most < sms ? (int)most : sms;
     size_t at = 0;
     auto take = [&](size_t bytes) {

@@ -29,9 +29,9 @@
 // expansion of keys and of values (four warps each), one that issues the products,
 // one that copies records.  They meet on arrival barriers in shared memory only.
 //
-// Work is a line of places: every (unit, head) has a place for each of its tiles
-// of tokens and row tiles and kUnitCost for its start and end; CTAs, one an SM,
-// take equal stretches.  Units cut between CTAs leave partial results for a second
+// Work is a line of places: every (unit, head) has places for each of its tiles of
+// tokens, and for its start and end, by what these take; CTAs, one an SM, have
+// equal stretches.  Units cut between CTAs leave partial results for a second
 // launch.  Lengths and starts are read on the device by a first, small launch.
 #pragma once
 
@@ -64,13 +64,14 @@ struct Shape {
     static constexpr int kKeyBytes = kTokens * D * 2;          // of one part of the split
     static constexpr int kValueBytes = kTokens * D * 2;
     static constexpr int kKeyStages = D == 256 ? 2 : 3;
-    static constexpr int kValueStages = D == 256 ? 2 : 3;
-    static constexpr int kRawStages = D == 256 ? 1 : 3;
+    static constexpr int kValueStages = D == 256 ? 1 : 3;
+    static constexpr int kRawStages = 3;
     // warps
     static constexpr int kSoftmaxWarps = 8 * kTiles;
     // Of each four warps after them two expand keys and two values: a scheduler (warps
     // of one number modulo 4) then has one of the two roles' instructions to fetch.
-    static constexpr int kExpandWarp = kSoftmaxWarps, kExpandWarps = 8;
+    static constexpr int kExpandWarp = kSoftmaxWarps, kExpandWarps = D == 256 ? 16 : 8;
+    static constexpr int kExpandThreads = 16 * kExpandWarps;     // for keys, and for values
     static constexpr int kProductWarp = kExpandWarp + kExpandWarps, kCopyWarp = kProductWarp + 1;
     static constexpr int kThreads = 32 * (kCopyWarp + 1);
     // columns of tensor memory
@@ -469,7 +470,7 @@ __device__ __forceinline__ void advance(const Args &p, Walk &w)
             break;
         auto tile_at = [&](long long place) -> int {
             const long long d = place - at - kUnitCost;
-            const long long t = d <= 0 ? 0 : s.row_tiles == 1 ? d : (d + 1) / 2;
+            const long long t = d <= 0 ? 0 : (d + s.weight - 1) / s.weight;
             return t < s.tiles ? (int)t : s.tiles;
         };
         Part u;
@@ -485,7 +486,7 @@ __device__ __forceinline__ void advance(const Args &p, Walk &w)
         u.t1 = tile_at(end);
         u.later = 0;
         if (u.t1 > u.t0 && u.t1 < s.tiles)
-            u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.row_tiles) / per) - (int)blockIdx.x;
+            u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.weight) / per) - (int)blockIdx.x;
         ++head;
         if (u.t1 > u.t0 || (s.tiles == 0 && at >= x)) {
             w.u = u;
@@ -556,10 +557,10 @@ chunk_kernel(const __grid_constant__ Args p)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             bar_init(shared_at(&ctl.raw_full[i]), 1);
-            bar_init(shared_at(&ctl.raw_empty[i]), 8);
-            bar_init(shared_at(&ctl.key_full[i]), 4);
+            bar_init(shared_at(&ctl.raw_empty[i]), S::kExpandWarps);
+            bar_init(shared_at(&ctl.key_full[i]), S::kExpandWarps / 2);
             bar_init(shared_at(&ctl.key_empty[i]), 1);
-            bar_init(shared_at(&ctl.value_full[i]), 4);
+            bar_init(shared_at(&ctl.value_full[i]), S::kExpandWarps / 2);
             bar_init(shared_at(&ctl.value_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -728,7 +729,6 @@ chunk_kernel(const __grid_constant__ Args p)
                 products_arrive(shared_at(&ctl.key_empty[key.stage]), lead);
                 key.step();
             };
-            int spin = 0;                         // buffer of the next scores, one row tile
             while (next()) {
                 // the same for all lanes, which the compiler cannot know of shared memory
                 const int n = __shfl_sync(~0u, u.t1 - u.t0, 0), row_tiles = __shfl_sync(~0u, u.row_tiles, 0);
@@ -742,10 +742,9 @@ chunk_kernel(const __grid_constant__ Args p)
                     break;
                 fence_after();
                 wait_key();
-                if (S::kTiles == 2) {
+                if (S::kTiles == 2 && row_tiles == 2) {
                     scores(0, 0);
-                    if (row_tiles == 2)
-                        scores(1, 1);
+                    scores(1, 1);
                     release_key();
                     for (int j = 0; j < n; ++j) {
                         wait_value();
@@ -755,32 +754,30 @@ chunk_kernel(const __grid_constant__ Args p)
                             wait_key();
                             scores(0, 0);
                         }
-                        if (row_tiles == 2) {
-                            wait_weight(1);
-                            outputs(1, 1, j > 0);
-                            if (j + 1 < n)
-                                scores(1, 1);
-                        }
+                        wait_weight(1);
+                        outputs(1, 1, j > 0);
+                        if (j + 1 < n)
+                            scores(1, 1);
                         products_arrive(shared_at(&ctl.value_empty[value.stage]), lead);
                         value.step();
                         if (j + 1 < n)
                             release_key();
                     }
                 } else {
-                    scores(0, spin);
+                    // one row tile: the buffers take turns, scores a product ahead
+                    scores(0, 0);
                     release_key();
                     for (int j = 0; j < n; ++j) {
                         if (j + 1 < n) {
                             wait_key();
-                            scores(0, spin ^ 1);
+                            scores(0, (j + 1) % 2);
                             release_key();
                         }
                         wait_value();
-                        wait_weight(spin);
-                        outputs(0, spin, j > 0);
+                        wait_weight(j % 2);
+                        outputs(0, j % 2, j > 0);
                         products_arrive(shared_at(&ctl.value_empty[value.stage]), lead);
                         value.step();
-                        spin ^= 1;
                     }
                 }
             }
@@ -815,25 +812,26 @@ chunk_kernel(const __grid_constant__ Args p)
                 unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
                 const unsigned long long there = ctl.there[count % kSlots];
                 const bool masked = there != ~0ULL || (t + 1) * kTokens > see_lo;
-                // a lane's work: eight tokens of one word (or two), which is four channels of
-                // two neighbouring groups
-                constexpr int kWords = D / 8, kTurns = kWords > 16 ? 2 : 1;
-                const int eight = turn % 8;
+                // a lane's work: eight tokens of one word, which is four channels of two
+                // neighbouring groups
+                constexpr int kWords = D / 8;
+                static_assert(kWords * 8 <= S::kExpandThreads, "a word a lane");
+                const int eight = turn % 8, word = turn / 8, place = word % (4 * kPer) * 2;
+                const int g = place / kPer, group = word / (4 * kPer) * kPer + place % kPer;
                 const unsigned char *rec = src + eight * S::kGroupBytes;
-                uint32_t s[kTurns][8];
+                uint32_t s[8];
                 unsigned high = 0;
-#pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int word = turn / 8 + 16 * i, place = word % (4 * kPer) * 2;
-                    const int group = word / (4 * kPer) * kPer + place % kPer;
+                if (word < kWords) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        s[i][k] = word < kWords ? *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D + D / 16 + group * 2)
-                                                : 0;
-                        high = __vmaxu2(high, s[i][k]);
+                        const unsigned char *scales = rec + k * S::kRecord + D + D / 16;
+                        s[k] = *reinterpret_cast<const uint32_t *>(scales + group * 2);
+                        high = __vmaxu2(high, s[k]);
+                        if (kGroups > kPer)        // the other stretch's, which is other warps' work
+                            high = __vmaxu2(high, *reinterpret_cast<const uint32_t *>(scales + (group ^ kPer) * 2));
                     }
                 }
-                // All scales are some lane's of every warp that has work, so that all of
+                // Every warp that has work meets all scales in some lane, so that all of
                 // these come to the same lift.  Against kHigh exponents are compared, of
                 // what may not be there, or no number, too: then it is looked at again.
                 if (__any_sync(~0u, fresh || (int)(max(high & 0xffffu, high >> 16) >> 10) + lift >= (int)(kHigh >> 10))) {
@@ -858,12 +856,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 const unsigned lift2 = lift_bits(lift) * 0x10001u;
                 if (turn == 0)
                     ctl.lift[count % kSlots] = lift;
-#pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int word = turn / 8 + 16 * i, place = word % (4 * kPer) * 2;
-                    if (word >= kWords)
-                        break;
-                    const int g = place / kPer, group = word / (4 * kPer) * kPer + place % kPer;
+                if (word < kWords) {
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -875,15 +868,15 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             if (!(here >> k & 1))
-                                s[i][k] = 0;
+                                s[k] = 0;
                             const int pos = t * kTokens + 8 * eight + k;
-                            if ((s[i][k] & 0x7c00u) == 0x7c00u) {
+                            if ((s[k] & 0x7c00u) == 0x7c00u) {
                                 atomicMin(&bad[group], pos);
-                                s[i][k] &= 0xffff0000u;
+                                s[k] &= 0xffff0000u;
                             }
-                            if ((s[i][k] & 0x7c000000u) == 0x7c000000u) {
+                            if ((s[k] & 0x7c000000u) == 0x7c000000u) {
                                 atomicMin(&bad[group + 1], pos);
-                                s[i][k] &= 0xffffu;
+                                s[k] &= 0xffffu;
                             }
                         }
                     }
@@ -894,7 +887,7 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             x[m] = __byte_perm(w[2 * m], w[2 * m + 1], pick);
-                            f[m] = Pair<__half>::times(__byte_perm(s[i][2 * m], s[i][2 * m + 1], pick), lift2);
+                            f[m] = Pair<__half>::times(__byte_perm(s[2 * m], s[2 * m + 1], pick), lift2);
                         }
                         const int channel = (group + half) * kGroup + 4 * g;
 #pragma unroll
@@ -933,7 +926,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
                 unsigned char *dst = smem + S::kOffKeys + key.stage * 2 * S::kKeyBytes;
 #pragma unroll 1
-                for (int i = turn; i < kTokens * kGroups; i += 128) {
+                for (int i = turn; i < kTokens * kGroups; i += S::kExpandThreads) {
                     // a group of one token: four words
                     const int token = i / (8 * kGroups) * 8 + i % 8, group = i / 8 % kGroups;
                     const int stretch = group / kPer, g = group % kPer;
@@ -984,7 +977,7 @@ chunk_kernel(const __grid_constant__ Args p)
             return y;
         };
         Turn<S::kValueStages> value;
-        int count = 0, unit = 0, spin = tile;
+        int count = 0, unit = 0;
         const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         while (next()) {
@@ -992,12 +985,19 @@ chunk_kernel(const __grid_constant__ Args p)
             unit += n > 0;
             if (S::kTiles == 2)       // one tile's warps are at most a unit ahead of the other's
                 asm volatile("bar.sync 9, 512;" ::: "memory");
+            const bool ahead = u.row_tiles == 1;      // the buffers take turns
             if (tile >= u.row_tiles) {
+                // what happened without these warps
                 count += n;
                 for (int t = 0; t < n; ++t)
                     value.step();
+                score_phase[0] ^= (n + 1) / 2 & 1;
+                score_phase[1] ^= n / 2 & 1;
                 continue;
             }
+            if (!ahead)
+                score_phase[tile ^ 1] ^= n & 1;
+            int spin = tile;                          // the buffer of the next scores
             const bool in = r < u.rows;
             const int limit = RowAt(p, u, r).limit;
             float m = -INFINITY, l = 0.f;
@@ -1104,14 +1104,14 @@ chunk_kernel(const __grid_constant__ Args p)
                 // With one row tile scores are a product ahead of outputs.  The output
                 // before this one ends before these weights are given away, so that never
                 // two phases of its barrier are to come, which a parity could not tell.
-                if (S::kTiles == 1 && t > t0)
+                if (ahead && t > t0)
                     bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(shared_at(&ctl.weight[spin]));
                 output_phase ^= 1;
-                if (S::kTiles == 1)
+                if (ahead)
                     spin ^= 1;
             }
             // ---- the unit's end

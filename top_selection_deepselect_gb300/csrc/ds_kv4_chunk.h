@@ -48,6 +48,7 @@ struct Args {
 // What a block's rows see, and its tiles.
 struct Span {
     int rows, row_tiles, see_lo, see_hi, tiles;
+    int weight;           // places of a tile
 };
 
 __host__ __device__ __forceinline__ Span span_of(const Block &b, int group, int block_rows)
@@ -60,13 +61,14 @@ __host__ __device__ __forceinline__ Span span_of(const Block &b, int group, int 
     s.see_lo = lo > 0 ? lo : 0;
     s.see_hi = hi > 0 ? hi : 0;
     s.tiles = s.see_hi / 64 + (s.see_hi % 64 != 0);
+    s.weight = s.row_tiles == 2 ? 8 : 5;
     return s;
 }
 
-// Places of a unit: one for each tile and row tile, and for its start and end
-// (queries, first copies, outputs) as much as these cost.
-constexpr int kUnitCost = 8;
-__host__ __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.row_tiles; }
+// Places of a unit: of its tiles, and of its start and end (queries, first copies,
+// outputs), by what they take.
+constexpr int kUnitCost = 40;
+__host__ __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.weight; }
 
 }  // namespace chunk
 }  // namespace kv4
