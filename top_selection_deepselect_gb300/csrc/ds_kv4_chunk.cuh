@@ -448,7 +448,7 @@ __device__ __forceinline__ void begin(const Args &p, Walk &w)
 }
 
 // Goes to the next part.  One thread's.
-__device__ __forceinline__ void advance(const Args &p, Walk &w)
+static __device__ __noinline__ void advance(const Args &p, Walk &w)
 {
     const long long x = w.x, end = w.end, per = p.head->per;
     int block = w.block, head = w.head;
@@ -819,6 +819,29 @@ chunk_kernel(const __grid_constant__ Args p)
                 const int eight = turn % 8, word = turn / 8, place = word % (4 * kPer) * 2;
                 const int g = place / kPer, group = word / (4 * kPer) * kPer + place % kPer;
                 const unsigned char *rec = src + eight * S::kGroupBytes;
+                if (masked && word < kWords) {
+                    // Tokens that are not there, or that not every row sees, may hold
+                    // anything: their weights are 0, which 0 * NaN is not.  Their scales
+                    // are put right in place; other lanes may do the same.
+                    const unsigned here = (unsigned)(there >> (8 * eight)) & 255;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t *scales = reinterpret_cast<uint32_t *>(const_cast<unsigned char *>(rec) + k * S::kRecord + D + D / 16 + group * 2);
+                        const uint32_t given = here >> k & 1 ? *scales : 0u;
+                        uint32_t fine = given;
+                        const int pos = t * kTokens + 8 * eight + k;
+                        if ((given & 0x7c00u) == 0x7c00u) {
+                            atomicMin(&bad[group], pos);
+                            fine &= 0xffff0000u;
+                        }
+                        if ((given & 0x7c000000u) == 0x7c000000u) {
+                            atomicMin(&bad[group + 1], pos);
+                            fine &= 0xffffu;
+                        }
+                        *scales = fine;
+                    }
+                }
+                __syncwarp();
                 uint32_t s[8];
                 unsigned high = 0;
                 if (word < kWords) {
@@ -861,26 +884,7 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         w[k] = *reinterpret_cast<const uint32_t *>(rec + k * S::kRecord + D / 2 + word * 4);
-                    if (masked) {
-                        // tokens that are not there, or that not every row sees, may
-                        // hold anything: their weights are 0, which 0 * NaN is not
-                        const unsigned here = (unsigned)(there >> (8 * eight)) & 255;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            if (!(here >> k & 1))
-                                s[k] = 0;
-                            const int pos = t * kTokens + 8 * eight + k;
-                            if ((s[k] & 0x7c00u) == 0x7c00u) {
-                                atomicMin(&bad[group], pos);
-                                s[k] &= 0xffff0000u;
-                            }
-                            if ((s[k] & 0x7c000000u) == 0x7c000000u) {
-                                atomicMin(&bad[group + 1], pos);
-                                s[k] &= 0xffffu;
-                            }
-                        }
-                    }
-#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const unsigned pick = half ? 0x7632 : 0x5410;
                         uint32_t x[4], f[4];
@@ -1006,29 +1010,28 @@ chunk_kernel(const __grid_constant__ Args p)
                 // the row's query, channels (j, j + 4) of each eight in pairs
                 const RowAt row(p, u, r);
                 const T *q = (const T *)p.a.q + row.token * p.a.q_query + row.head * p.a.q_head;
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < D / 64; ++part) {
                     const int first = half * (D / 2) + part * 32;
+                    uint4 v[4] = {};
+                    if (in && p.q_vector) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = *reinterpret_cast<const uint4 *>(q + first + e * 8);
+                    } else if (in) {
+                        const unsigned short *y = reinterpret_cast<const unsigned short *>(q + first);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e, y += 8)
+                            v[e] = make_uint4(y[0] | (unsigned)y[1] << 16, y[2] | (unsigned)y[3] << 16,
+                                              y[4] | (unsigned)y[5] << 16, y[6] | (unsigned)y[7] << 16);
+                    }
                     uint32_t x[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (in) {
-                            if (p.q_vector) {
-                                v = *reinterpret_cast<const uint4 *>(q + first + e * 8);
-                            } else {
-                                unsigned short y[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    y[k] = *reinterpret_cast<const unsigned short *>(q + first + e * 8 + k);
-                                v = make_uint4(y[0] | (unsigned)y[1] << 16, y[2] | (unsigned)y[3] << 16,
-                                               y[4] | (unsigned)y[5] << 16, y[6] | (unsigned)y[7] << 16);
-                            }
-                        }
-                        x[4 * e] = __byte_perm(v.x, v.z, 0x5410) ^ flip;
-                        x[4 * e + 1] = __byte_perm(v.x, v.z, 0x7632) ^ flip;
-                        x[4 * e + 2] = __byte_perm(v.y, v.w, 0x5410) ^ flip;
-                        x[4 * e + 3] = __byte_perm(v.y, v.w, 0x7632) ^ flip;
+                        x[4 * e] = __byte_perm(v[e].x, v[e].z, 0x5410) ^ flip;
+                        x[4 * e + 1] = __byte_perm(v[e].x, v[e].z, 0x7632) ^ flip;
+                        x[4 * e + 2] = __byte_perm(v[e].y, v[e].w, 0x5410) ^ flip;
+                        x[4 * e + 3] = __byte_perm(v[e].y, v[e].w, 0x7632) ^ flip;
                     }
                     __syncwarp();
                     store_columns(rows_at + S::kQueryColumn + tile * (D / 2) + first / 2, x);
@@ -1068,20 +1071,24 @@ chunk_kernel(const __grid_constant__ Args p)
                 // half's maximum is known, and again where it turns out that it grows.
                 float most = largest_of(s);
                 ctl.swap[side][tile][half][local] = most;
-                Two sum[2] = {};
+                Two sum[2];
                 uint32_t w[16];
-                weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
-                most = fmaxf(most, meet()) * c;
-                const bool grows = most > m + 8.f || m == -INFINITY;
-                if (__any_sync(~0u, (grows && most > m) || lift_now != lift)) {
+#pragma unroll
+                for (bool met = false;; met = true) {
+                    sum[0] = sum[1] = Two{0.f, 0.f};
+                    weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
+                    if (met)
+                        break;
+                    most = fmaxf(most, meet()) * c;
+                    const bool grows = most > m + 8.f || m == -INFINITY;
+                    if (!__any_sync(~0u, (grows && most > m) || lift_now != lift))
+                        break;
                     const float to = grows ? fmaxf(most, m) : m;
                     float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
                     l *= f;
                     m = to;
                     f *= __uint_as_float((unsigned)(lift_now - lift + 127) << 23);
                     lift = lift_now;
-                    sum[0] = sum[1] = Two{0.f, 0.f};
-                    weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
                     if (t > t0) {
                         bar_wait(shared_at(&ctl.output[tile]), output_phase ^ 1, lost);
                         fence_after();
