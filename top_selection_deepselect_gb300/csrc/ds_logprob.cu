@@ -2,25 +2,33 @@
 // likeliest alternatives, and their gradient (include/ds_logprob.h).
 //
 // Forward, one pass over a row: with a running maximum m of the logits,
-//   S = sum 2^d,  T = sum 2^d d,  d = (x - m) scale log2 e <= 0
+//   S = sum 2^d,  T = sum 2^d d,  d = x c - m c,  c = scale log2 e
 // give lse = scale m + ln S and entropy = ln 2 (log2 S - T / S), whose two terms
-// are both >= 0, so that nothing cancels.  d is clamped at -200, where 2^d is 0:
-// a logit of -inf, or one that is further below than 32 bits reach, then adds
-// 2^d d = 0 and not NaN.  The alternatives come out of the same pass: the first
-// pieces of a CTA's slice give a value that at least k of its logits reach, later
-// logits above it go to a buffer in shared memory, and the k first of these by
-// (value, index) are found by warps that sort and merge lists of 32.
+// are both >= 0, so that nothing cancels.  m c is rounded once, which shifts all d
+// alike: that drops out of the entropy and is taken back in lse.  Logits of -inf are
+// lifted to a lowest finite one, whose 2^d is 0, so that 2^d d is 0 and not NaN;
+// where the maximum is too near to that, or so large that x c overflows, the row is
+// summed again with the difference taken first.
 //
-// The bound is HBM; what has to be kept off is instructions.  A vector of 16
-// bytes is tested as a whole, by packed maxima, against the value that candidates
-// have to be above (which is at or below the running maximum), so that maxima and
-// candidates cost nothing where there are none; sums are pairs in one instruction.
+// The alternatives come out of the same pass: the first vectors of a CTA's slice
+// give a value that at least k of its logits reach; where a later vector's largest
+// is above it, the vector's number goes to a list.  At the end the logits of the
+// listed vectors that reach the value are taken out again, and the k first of these
+// by (value, index) are found by warps that sort and merge lists of 32.
+//
+// The bound is HBM; what has to be kept off is instructions and waits.  A lane
+// copies its vectors of 16 bytes to shared memory asynchronously, kDepth ahead, and
+// reads only its own, so that no barrier is needed; a vector is tested as a whole, by
+// packed maxima, against the value that candidates have to be above (which is at or
+// below the running maximum), so that maxima and candidates cost next to nothing;
+// products and sums are pairs in one instruction.
 //
 // A row is a CTA's, or a cluster's where rows are few: each CTA takes a slice, and
 // the first joins the sums and the sorted lists out of distributed shared memory.
 #include "ds_logprob.h"
 
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "ds_device.cuh"
 #include "ds_host.h"
@@ -35,10 +43,10 @@ using kv4::to_float;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;          // vectors of a thread under way
+constexpr int kDepth = 8;          // vectors of a thread under way
 constexpr int kTop = DS_LOGPROB_MAX_K;
 constexpr int kEach = kTop / kWarps;   // of a warp's threads that the first bound is taken from
-constexpr int kCapacity = 2048;    // candidates of a slice
+constexpr int kCapacity = 1024;    // listed vectors of a slice, and candidates among their logits
 constexpr float kLow = -200.f;     // 2^d is 0 in 32 bits below -150
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
@@ -120,22 +128,23 @@ struct Row {
     {
         return j * Vec<T>::kCount >= skip && (j + 1) * Vec<T>::kCount <= past;
     }
-    // Vector j, -inf in the places that are not the row's (which are not read).
+    // Element e of vector j, -inf in the places that are not the row's.
+    __device__ __forceinline__ T element(unsigned j, int e) const
+    {
+        const unsigned i = j * Vec<T>::kCount + e;
+        T x;
+        from_float(x, -INFINITY);
+        return i >= skip && i < past ? at[i] : x;
+    }
     __device__ __forceinline__ Vec<T> load(unsigned j, unsigned end) const
     {
         Vec<T> v;
-        const T *p = at + (size_t)j * Vec<T>::kCount;
         if (j < end && whole(j)) {
-            v = *reinterpret_cast<const Vec<T> *>(p);
+            v = *reinterpret_cast<const Vec<T> *>(at + (size_t)j * Vec<T>::kCount);
         } else {
 #pragma unroll
-            for (int e = 0; e < Vec<T>::kCount; ++e) {
-                const unsigned i = j * Vec<T>::kCount + e;
-                if (j < end && i >= skip && i < past)
-                    v.x[e] = p[e];
-                else
-                    from_float(v.x[e], -INFINITY);
-            }
+            for (int e = 0; e < Vec<T>::kCount; ++e)
+                v.x[e] = element(j < end ? j : 0xfffffff0u / Vec<T>::kCount, e);
         }
         return v;
     }
@@ -262,11 +271,12 @@ __device__ Entry select_entries(const Entry *entries, int n, Entry *lists)
 
 struct Shared {
     Entry entries[kCapacity];
+    unsigned vectors[kCapacity];
     Entry lists[kWarps * 32];
     Sums sums[kWarps];
     unsigned keys[kWarps * kEach];
     float most[kWarps];
-    int count;
+    int listed, count;
     // what the cluster's first CTA reads
     Entry top[kTop];
     Sums all;
@@ -368,11 +378,137 @@ struct Args {
     float scale;
 };
 
+// Waits until all but the newest n groups of this thread's copies have ended.
+template <int n>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// What a logit of -inf is lifted to, and a sum's terms relative to a maximum.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ float lowest()
+{
+    return std::is_same<T, __half>::value ? -65504.f : -1e30f;
+}
+
+// Adds a vector to sums relative to mc = m c.
+__device__ __forceinline__ void add_two(Sums &a, float x0, float x1, float mc, float c)
+{
+    float d0, d1;
+    asm("{\n\t.reg .b64 x, m, f;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 m, {%4, %4};\n\t"
+        "mov.b64 f, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, f, m;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(-mc), "f"(c));
+    const float e0 = exp2_fast(d0), e1 = exp2_fast(d1);
+    asm("{\n\t.reg .b64 s, t, e, d;\n\t"
+        "mov.b64 s, {%0, %1};\n\t"
+        "mov.b64 t, {%2, %3};\n\t"
+        "mov.b64 e, {%4, %5};\n\t"
+        "mov.b64 d, {%6, %7};\n\t"
+        "add.rn.f32x2 s, s, e;\n\t"
+        "fma.rn.f32x2 t, e, d, t;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t"
+        "mov.b64 {%2, %3}, t;\n\t}"
+        : "+f"(a.s0), "+f"(a.s1), "+f"(a.t0), "+f"(a.t1) : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
+}
+__device__ __forceinline__ void add_fast(Sums &a, const Vec<float> &v, float mc, float c)
+{
+    constexpr float low = -1e30f;
+    add_two(a, max_nan(v.x[0], low), max_nan(v.x[1], low), mc, c);
+    add_two(a, max_nan(v.x[2], low), max_nan(v.x[3], low), mc, c);
+}
+template <typename T, typename T2>
+__device__ __forceinline__ void add_fast16(Sums &a, const Vec<T> &v, float mc, float c)
+{
+    T low;
+    from_float(low, lowest<T>());
+    const T2 low2 = {low, low};
+    const T2 *w = reinterpret_cast<const T2 *>(v.x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const T2 x = max_nan(w[i], low2);
+        add_two(a, to_float(x.x), to_float(x.y), mc, c);
+    }
+}
+__device__ __forceinline__ void add_fast(Sums &a, const Vec<__half> &v, float mc, float c)
+{
+    add_fast16<__half, __half2>(a, v, mc, c);
+}
+__device__ __forceinline__ void add_fast(Sums &a, const Vec<__nv_bfloat16> &v, float mc, float c)
+{
+    add_fast16<__nv_bfloat16, __nv_bfloat162>(a, v, mc, c);
+}
+
+// Of a maximum: m c, and 0 for one that there is not yet.
+__device__ __forceinline__ float scaled(float most, float c) { return most == -INFINITY ? 0.f : most * c; }
+
+// Brings fast sums to another maximum at or above theirs.
+__device__ __forceinline__ void lift_fast(Sums &a, float most, float c)
+{
+    const float d = scaled(a.most, c) - scaled(most, c);
+    if (a.most != -INFINITY) {               // else the sums are 0, or a NaN's
+        const float f = exp2_fast(fmaxf(d, -1000.f));
+        a.t0 = f * fmaf(d, a.s0, a.t0), a.t1 = f * fmaf(d, a.s1, a.t1);
+        a.s0 *= f, a.s1 *= f;
+    }
+    a.most = most;
+}
+__device__ __forceinline__ void join_fast(Sums &a, Sums b, float c)
+{
+    const float most = fmaxf(a.most, b.most);
+    lift_fast(a, most, c);
+    lift_fast(b, most, c);
+    a.s0 += b.s0, a.s1 += b.s1, a.t0 += b.t0, a.t1 += b.t1;
+}
+
+__device__ __forceinline__ Sums shuffled(const Sums &a, int step)
+{
+    Sums b;
+    b.most = __shfl_xor_sync(~0u, a.most, step);
+    b.s0 = __shfl_xor_sync(~0u, a.s0, step), b.s1 = __shfl_xor_sync(~0u, a.s1, step);
+    b.t0 = __shfl_xor_sync(~0u, a.t0, step), b.t1 = __shfl_xor_sync(~0u, a.t1, step);
+    return b;
+}
+
+// Sums of vectors [lo, hi) by the CTA, differences taken first, in every thread.
+template <typename T>
+__device__ __noinline__ Sums sum_carefully(const Row<T> &row, unsigned lo, unsigned hi, float c, Sums *sums)
+{
+    Sums a = {-INFINITY, 0.f, 0.f, 0.f, 0.f};
+    for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
+        const Vec<T> v = row.load(j, hi);
+        float most = a.most;
+#pragma unroll
+        for (int e = 0; e < Vec<T>::kCount; ++e)
+            most = fmaxf(most, to_float(v.x[e]));
+        if (most > a.most)
+            rescale(a, most, c);
+        add_vector(a, v, c);
+    }
+#pragma unroll
+    for (int step = 16; step; step /= 2)
+        add_sums(a, shuffled(a, step), c);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        sums[threadIdx.x / 32] = a;
+    __syncthreads();
+    a = sums[0];
+    for (int w = 1; w < kWarps; ++w)
+        add_sums(a, sums[w], c);
+    return a;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
 logprob_kernel(const __grid_constant__ Args p)
 {
     __shared__ Shared sh;
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    Vec<T> *ring = reinterpret_cast<Vec<T> *>(ring_bytes) + threadIdx.x;     // slot i at i * kThreads
     dependent_grid_wait();
     allow_dependent_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -383,24 +519,38 @@ logprob_kernel(const __grid_constant__ Args p)
     const unsigned hi = (unsigned)((unsigned long long)row.vectors * (rank + 1) / p.cluster);
     const float c = p.scale * kLog2e;
 
-    // The first pieces, whose maximum all sums start from.  A candidate has to be
-    // at or above a value that k logits of these pieces reach, and above it after
-    // them (an equal one further on comes later in the order).
-    Vec<T> now[kAhead];
+    // vector j to slot i: a copy, or element by element at the row's ends and past them
+    auto fetch = [&](unsigned j, int i) {
+        if (j < hi && row.whole(j)) {
+            cp_async16((uint32_t)__cvta_generic_to_shared(ring + i * kThreads),
+                       row.at + (size_t)j * Vec<T>::kCount);
+        } else {
+            T *x = ring[i * kThreads].x;
+#pragma unroll 1
+            for (int e = 0; e < Vec<T>::kCount; ++e)
+                x[e] = row.element(j < hi ? j : 0xfffffff0u / Vec<T>::kCount, e);
+        }
+    };
     unsigned j = lo + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        now[u] = row.load(j + u * kThreads, hi);
+    for (int i = 0; i < kDepth; ++i) {
+        fetch(j + i * kThreads, i);
+        cp_async_commit();
+    }
+    if (threadIdx.x == 0)
+        sh.listed = sh.count = 0;
+
+    // The first vectors: their maximum, which all sums start from, and a value that k
+    // of their logits reach.
+    cp_async_wait<0>();
     float mine = -INFINITY;
     bool nan = false;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-        const float m = largest(now[u]);
+    for (int i = 0; i < kDepth; ++i) {
+        const float m = largest(ring[i * kThreads]);
         nan = nan || m != m;
         mine = fmaxf(mine, m);
     }
-    if (threadIdx.x == 0)
-        sh.count = 0;
     const unsigned top_key = __reduce_max_sync(~0u, key_of(mine));
     if (lane == 0)
         sh.most[warp] = value_of(top_key);
@@ -416,77 +566,93 @@ logprob_kernel(const __grid_constant__ Args p)
 #pragma unroll
     for (int w = 1; w < kWarps; ++w)
         mine = fmaxf(mine, sh.most[w]);
-    const float bound = p.k > 0 ? value_of(__shfl_sync(~0u, order_lanes(sh.keys[lane]), p.k - 1)) : mine;
+    // A listed vector's largest has to be above `bound`; among the first ones at it, too:
+    // above the value before it.  (An equal one further on comes later in the order.)
+    float bound = mine, reach = mine;
+    if (p.k > 0) {
+        const unsigned key = __shfl_sync(~0u, order_lanes(sh.keys[lane]), p.k - 1);
+        reach = value_of(key);
+        bound = value_of(key == 0x80000000u ? key - 2 : key - 1);     // 0 has no other sign below it
+    }
 
     Sums a = {mine, 0.f, 0.f, 0.f, 0.f};
-    // A vector that may hold a candidate or a new maximum.
-    auto look = [&](const Vec<T> &v, unsigned at, bool first) {
-        float most = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < Vec<T>::kCount; ++e) {
-            const float x = to_float(v.x[e]);
-            most = fmaxf(most, x);
-            if (p.k > 0 && (first ? !(x < bound) : !(x <= bound))) {
-                const unsigned i = at * Vec<T>::kCount + e;
-                if (i >= row.skip && i < row.past)
-                    keep(sh, entry_of(row, v.x[e], at, e));
+    float mc = scaled(mine, c);
+    const unsigned turns = (hi - lo + kThreads - 1) / kThreads;
+    int slot = 0;
+#pragma unroll 1
+    for (unsigned turn = 0; turn < turns; ++turn) {
+        cp_async_wait<kDepth - 1>();
+        const Vec<T> v = ring[slot * kThreads];
+        const float m = largest(v);
+        if (!(m <= bound)) {
+            if (p.k > 0 && j < hi) {
+                const int at = atomicAdd(&sh.listed, 1);
+                if (at < kCapacity)
+                    sh.vectors[at] = j;
+            }
+            float most = m;
+            if (m != m) {
+                most = a.most;
+                for (int e = 0; e < Vec<T>::kCount; ++e)
+                    most = fmaxf(most, to_float(ring[slot * kThreads].x[e]));
+            }
+            if (most > a.most) {
+                lift_fast(a, most, c);
+                mc = scaled(most, c);
             }
         }
-        if (most > a.most)
-            rescale(a, most, c);
-    };
-    bool first = true;
-    for (;;) {
-        Vec<T> next[kAhead];
-        const unsigned j_next = j + kAhead * kThreads;
-        const bool more = j_next - threadIdx.x < hi;      // the same for all threads
-        if (more) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                next[u] = row.load(j_next + u * kThreads, hi);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const float m = largest(now[u]);
-            if (first ? !(m < bound) : !(m <= bound))
-                if (j + u * kThreads < hi)
-                    look(now[u], j + u * kThreads, first);
-            add_vector(a, now[u], c);
-        }
-        if (!more)
-            break;
-        first = false;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            now[u] = next[u];
-        j = j_next;
+        add_fast(a, v, mc, c);
+        fetch(j + kDepth * kThreads, slot);
+        cp_async_commit();
+        slot = (slot + 1) % kDepth;
+        j += kThreads;
+        if (turn == kDepth - 1)
+            bound = reach;
     }
+    cp_async_wait<0>();
 
     // the CTA's sums, in a fixed order
 #pragma unroll
-    for (int step = 16; step; step /= 2) {
-        Sums b;
-        b.most = __shfl_xor_sync(~0u, a.most, step);
-        b.s0 = __shfl_xor_sync(~0u, a.s0, step), b.s1 = __shfl_xor_sync(~0u, a.s1, step);
-        b.t0 = __shfl_xor_sync(~0u, a.t0, step), b.t1 = __shfl_xor_sync(~0u, a.t1, step);
-        add_sums(a, b, c);
-    }
+    for (int step = 16; step; step /= 2)
+        join_fast(a, shuffled(a, step), c);
     if (lane == 0)
         sh.sums[warp] = a;
     __syncthreads();
+    a = sh.sums[0];
+    for (int w = 1; w < kWarps; ++w)
+        join_fast(a, sh.sums[w], c);
+    // Sums of what the fast form cannot tell from a logit of -inf, or overflows on, are
+    // made again; and all sums are relative to the maximum itself from here on.
+    const bool fine = (a.most - lowest<T>()) * c >= 150.f && a.most < 1e29f && c <= 1e8f;
+    if (fine) {
+        const float off = fmaf(a.most, c, -scaled(a.most, c)), f = exp2f(-off);
+        a.t0 = f * fmaf(-off, a.s0, a.t0), a.t1 = f * fmaf(-off, a.s1, a.t1);
+        a.s0 *= f, a.s1 *= f;
+    } else {
+        a = sum_carefully(row, lo, hi, c, sh.sums);
+    }
     Entry list = 0;
-    if (p.k > 0)
-        list = sh.count <= kCapacity ? select_entries(sh.entries, sh.count, sh.lists)
-                                     : select_slowly(row, lo, hi, p.k, sh);
-    if (warp == 0) {
-        a = sh.sums[0];
-        for (int w = 1; w < kWarps; ++w)
-            add_sums(a, sh.sums[w], c);
-        if (p.cluster > 1) {
-            sh.top[lane] = list;
-            if (lane == 0)
-                sh.all = a;
+    if (p.k > 0) {
+        // the logits of the listed vectors that reach the value
+        const int listed = sh.listed;
+        for (int i0 = 0; i0 < listed * Vec<T>::kCount && listed <= kCapacity; i0 += kThreads) {
+            const int i = i0 + threadIdx.x;
+            if (i < listed * Vec<T>::kCount) {
+                const unsigned at = sh.vectors[i / Vec<T>::kCount];
+                const int e = i % Vec<T>::kCount;
+                const unsigned place = at * Vec<T>::kCount + e;
+                if (place >= row.skip && place < row.past && !(to_float(row.at[place]) < reach))
+                    keep(sh, entry_of(row, row.at[place], at, e));
+            }
         }
+        __syncthreads();
+        list = listed <= kCapacity && sh.count <= kCapacity ? select_entries(sh.entries, sh.count, sh.lists)
+                                                            : select_slowly(row, lo, hi, p.k, sh);
+    }
+    if (p.cluster > 1 && warp == 0) {
+        sh.top[lane] = list;
+        if (lane == 0)
+            sh.all = a;
     }
     if (p.cluster > 1) {
         namespace cg = cooperative_groups;
@@ -565,39 +731,6 @@ __device__ __forceinline__ float slope(const Factors &f, float x)
 // 2^-15 of p.
 constexpr float kLarge = 1024.f;
 
-// Maximum of the row and log of its sum relative to that, by the CTA.
-template <typename T>
-__device__ __noinline__ void sum_again(const Row<T> &row, Factors &f, Sums *sums)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const float c = f.scale * kLog2e;
-    Sums a = {-INFINITY, 0.f, 0.f, 0.f, 0.f};
-    for (unsigned j = threadIdx.x; j < row.vectors; j += kThreads) {
-        const Vec<T> v = row.load(j, row.vectors);
-        const float most = largest(v);
-        if (most > a.most)
-            rescale(a, most, c);
-        add_vector(a, v, c);
-    }
-#pragma unroll
-    for (int step = 16; step; step /= 2) {
-        Sums b;
-        b.most = __shfl_xor_sync(~0u, a.most, step);
-        b.s0 = __shfl_xor_sync(~0u, a.s0, step), b.s1 = __shfl_xor_sync(~0u, a.s1, step);
-        b.t0 = __shfl_xor_sync(~0u, a.t0, step), b.t1 = __shfl_xor_sync(~0u, a.t1, step);
-        add_sums(a, b, c);
-    }
-    if (lane == 0)
-        sums[warp] = a;
-    __syncthreads();
-    a = sums[0];
-    for (int w = 1; w < kWarps; ++w)
-        add_sums(a, sums[w], c);
-    f.empty = a.s0 + a.s1 == 0.f;
-    f.base = f.empty ? 0.f : a.most;
-    f.lse = (float)(kLn2 * (double)log2f(a.s0 + a.s1));
-}
-
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 gradient_kernel(const __grid_constant__ GradArgs p)
@@ -650,8 +783,12 @@ gradient_kernel(const __grid_constant__ GradArgs p)
         if (at >= 0)
             own = to_float(logits[at]);
     }
-    if (fabsf(f.lse) >= kLarge)
-        sum_again(row, f, sums);
+    if (fabsf(f.lse) >= kLarge) {
+        const Sums a = sum_carefully(row, 0, row.vectors, f.scale * kLog2e, sums);
+        f.empty = a.s0 + a.s1 == 0.f;
+        f.base = f.empty ? 0.f : a.most;
+        f.lse = (float)(kLn2 * (double)log2f(a.s0 + a.s1));
+    }
     __syncthreads();
 
     for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
@@ -690,7 +827,7 @@ gradient_kernel(const __grid_constant__ GradArgs p)
 
 // CTAs of a row: one where rows alone fill the GPU, else as many as give slices of
 // at least kSlice vectors a thread.
-constexpr int kSlice = 2 * kAhead;
+constexpr int kSlice = 8;
 
 template <typename T>
 cudaError_t launch_forward(Args &p, long long rows, int sms, cudaStream_t stream)
@@ -700,7 +837,8 @@ cudaError_t launch_forward(Args &p, long long rows, int sms, cudaStream_t stream
     while (p.cluster < 8 && rows * p.cluster < 2LL * sms &&
            vectors >= 2LL * p.cluster * kSlice * kThreads)
         p.cluster *= 2;
-    return launch_clusters(logprob_kernel<T>, p.cluster, (unsigned)(rows * p.cluster), kThreads, 0, stream, p);
+    return launch_clusters(logprob_kernel<T>, p.cluster, (unsigned)(rows * p.cluster), kThreads,
+                           kDepth * kThreads * 16, stream, p);
 }
 
 template <typename T>
