@@ -392,55 +392,66 @@ __device__ __forceinline__ float lowest()
     return std::is_same<T, __half>::value ? -65504.f : -1e30f;
 }
 
-// Adds a vector to sums relative to mc = m c.
-__device__ __forceinline__ void add_two(Sums &a, float x0, float x1, float mc, float c)
+// Pairs of floats, in 64-bit registers so that what does not change is paired once.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two pair(float a, float b)
 {
-    float d0, d1;
-    asm("{\n\t.reg .b64 x, m, f;\n\t"
-        "mov.b64 x, {%2, %3};\n\t"
-        "mov.b64 m, {%4, %4};\n\t"
-        "mov.b64 f, {%5, %5};\n\t"
-        "fma.rn.f32x2 x, x, f, m;\n\t"
-        "mov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(-mc), "f"(c));
-    const float e0 = exp2_fast(d0), e1 = exp2_fast(d1);
-    asm("{\n\t.reg .b64 s, t, e, d;\n\t"
-        "mov.b64 s, {%0, %1};\n\t"
-        "mov.b64 t, {%2, %3};\n\t"
-        "mov.b64 e, {%4, %5};\n\t"
-        "mov.b64 d, {%6, %7};\n\t"
-        "add.rn.f32x2 s, s, e;\n\t"
-        "fma.rn.f32x2 t, e, d, t;\n\t"
-        "mov.b64 {%0, %1}, s;\n\t"
-        "mov.b64 {%2, %3}, t;\n\t}"
-        : "+f"(a.s0), "+f"(a.s1), "+f"(a.t0), "+f"(a.t1) : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
+    Two y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
 }
-__device__ __forceinline__ void add_fast(Sums &a, const Vec<float> &v, float mc, float c)
+__device__ __forceinline__ void apart(Two x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ Two times_add(Two x, Two y, Two z)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ Two sum(Two x, Two y)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// Adds a vector to sums s and t of terms relative to -mc2 = m c.
+__device__ __forceinline__ void add_two(Two &s, Two &t, float x0, float x1, Two mc2, Two c2)
+{
+    const Two d = times_add(pair(x0, x1), c2, mc2);
+    float d0, d1;
+    apart(d, d0, d1);
+    const Two e = pair(exp2_fast(d0), exp2_fast(d1));
+    s = sum(s, e);
+    t = times_add(e, d, t);
+}
+__device__ __forceinline__ void add_fast(Two &s, Two &t, const Vec<float> &v, Two mc2, Two c2)
 {
     constexpr float low = -1e30f;
-    add_two(a, max_nan(v.x[0], low), max_nan(v.x[1], low), mc, c);
-    add_two(a, max_nan(v.x[2], low), max_nan(v.x[3], low), mc, c);
+    add_two(s, t, max_nan(v.x[0], low), max_nan(v.x[1], low), mc2, c2);
+    add_two(s, t, max_nan(v.x[2], low), max_nan(v.x[3], low), mc2, c2);
 }
-template <typename T, typename T2>
-__device__ __forceinline__ void add_fast16(Sums &a, const Vec<T> &v, float mc, float c)
+__device__ __forceinline__ void add_fast(Two &s, Two &t, const Vec<__half> &v, Two mc2, Two c2)
 {
-    T low;
-    from_float(low, lowest<T>());
-    const T2 low2 = {low, low};
-    const T2 *w = reinterpret_cast<const T2 *>(v.x);
+    const __half2 low2 = __half2half2(__ushort_as_half(0xfbff));     // -65504
+    const __half2 *w = reinterpret_cast<const __half2 *>(v.x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const T2 x = max_nan(w[i], low2);
-        add_two(a, to_float(x.x), to_float(x.y), mc, c);
+        const float2 x = __half22float2(max_nan(w[i], low2));
+        add_two(s, t, x.x, x.y, mc2, c2);
     }
 }
-__device__ __forceinline__ void add_fast(Sums &a, const Vec<__half> &v, float mc, float c)
+__device__ __forceinline__ void add_fast(Two &s, Two &t, const Vec<__nv_bfloat16> &v, Two mc2, Two c2)
 {
-    add_fast16<__half, __half2>(a, v, mc, c);
-}
-__device__ __forceinline__ void add_fast(Sums &a, const Vec<__nv_bfloat16> &v, float mc, float c)
-{
-    add_fast16<__nv_bfloat16, __nv_bfloat162>(a, v, mc, c);
+    const unsigned *w = reinterpret_cast<const unsigned *>(v.x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unsigned x;                                                  // lifted to -1e30
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(0xf14af14au));
+        add_two(s, t, __uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u), mc2, c2);
+    }
 }
 
 // Of a maximum: m c, and 0 for one that there is not yet.
@@ -576,8 +587,14 @@ logprob_kernel(const __grid_constant__ Args p)
     }
 
     Sums a = {mine, 0.f, 0.f, 0.f, 0.f};
-    float mc = scaled(mine, c);
+    Two sums = 0, weighted = 0;
+    Two mc2 = pair(-scaled(mine, c), -scaled(mine, c));
+    const Two c2 = pair(c, c);
     const unsigned turns = (hi - lo + kThreads - 1) / kThreads;
+    // the vectors that are whole, and where the next copy comes from
+    const unsigned whole_from = max(lo, row.skip ? 1u : 0u), whole_to = min(hi, row.past / Vec<T>::kCount);
+    unsigned ahead = j + kDepth * kThreads;
+    const T *from = row.at + (size_t)ahead * Vec<T>::kCount;
     int slot = 0;
 #pragma unroll 1
     for (unsigned turn = 0; turn < turns; ++turn) {
@@ -593,23 +610,35 @@ logprob_kernel(const __grid_constant__ Args p)
             float most = m;
             if (m != m) {
                 most = a.most;
+#pragma unroll 1
                 for (int e = 0; e < Vec<T>::kCount; ++e)
                     most = fmaxf(most, to_float(ring[slot * kThreads].x[e]));
             }
             if (most > a.most) {
+                apart(sums, a.s0, a.s1);
+                apart(weighted, a.t0, a.t1);
                 lift_fast(a, most, c);
-                mc = scaled(most, c);
+                sums = pair(a.s0, a.s1);
+                weighted = pair(a.t0, a.t1);
+                mc2 = pair(-scaled(most, c), -scaled(most, c));
             }
         }
-        add_fast(a, v, mc, c);
-        fetch(j + kDepth * kThreads, slot);
+        add_fast(sums, weighted, v, mc2, c2);
+        if (ahead >= whole_from && ahead < whole_to)
+            cp_async16((uint32_t)__cvta_generic_to_shared(ring + slot * kThreads), from);
+        else if (turn + kDepth < turns)
+            fetch(ahead, slot);
         cp_async_commit();
         slot = (slot + 1) % kDepth;
         j += kThreads;
+        ahead += kThreads;
+        from += kThreads * Vec<T>::kCount;
         if (turn == kDepth - 1)
             bound = reach;
     }
     cp_async_wait<0>();
+    apart(sums, a.s0, a.s1);
+    apart(weighted, a.t0, a.t1);
 
     // the CTA's sums, in a fixed order
 #pragma unroll
@@ -625,7 +654,7 @@ logprob_kernel(const __grid_constant__ Args p)
     // made again; and all sums are relative to the maximum itself from here on.
     const bool fine = (a.most - lowest<T>()) * c >= 150.f && a.most < 1e29f && c <= 1e8f;
     if (fine) {
-        const float off = fmaf(a.most, c, -scaled(a.most, c)), f = exp2f(-off);
+        const float mc = scaled(a.most, c), off = fmaf(a.most, c, -mc), f = exp2f(-off);
         a.t0 = f * fmaf(-off, a.s0, a.t0), a.t1 = f * fmaf(-off, a.s1, a.t1);
         a.s0 *= f, a.s1 *= f;
     } else {
