@@ -110,6 +110,19 @@ def test_many_short_sequences(ds, dim, heads, hk):
     check(ds, *args)
 
 
+def test_more_entries_than_planning_threads(ds):
+    """2500 entries, most of them without a new token, over a few sequences."""
+    rng = np.random.default_rng(15)
+    q, pool, table, lengths, _ = chunk(rng, [40, 50, 60], [30, 90, 0], 2, 1, 64, 16)
+    new = np.zeros(2500, dtype=np.int64)
+    new[rng.choice(2500, 90, replace=False)] = 1
+    new[[3, 1023, 1024, 2047, 2048, 2499]] = 10
+    starts = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+    seqs = rng.integers(0, 3, 2500).astype(np.int32)
+    check(ds, q[:starts[-1]] if starts[-1] <= len(q) else np.resize(q, (starts[-1], 2, 64)), "bf16", pool, table,
+          lengths, starts, seqs=seqs)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_entries_of_any_sequence(ds, dtype):
     """seqs in any order, the same sequence twice, sequences that are none, lengths beyond the table."""

@@ -46,127 +46,155 @@ __device__ V scan_all(V v, V none, F combine, V *before, V *scratch)
     return all;
 }
 
-// The block of rows that begins at row0 of entry b.
-__device__ __forceinline__ Block block_of(const Args &p, int b, int row0)
+// What is known of an entry: its sequence, first row, new tokens, length.
+struct Entry {
+    int seq, start, n, len;
+};
+
+__device__ __forceinline__ Entry entry_of(const Args &p, int b)
 {
-    Block k;
-    k.place = 0;
-    k.seq = p.a.seqs ? p.a.seqs[b] : b;
-    k.start = p.starts[b];
-    k.n = p.starts[b + 1] - k.start;
-    k.len = 0;
-    if ((unsigned)k.seq < (unsigned)p.c.max_seqs) {
-        const int n = p.a.lengths[k.seq];
+    Entry e;
+    e.seq = p.a.seqs ? p.a.seqs[b] : b;
+    e.start = e.n = e.len = 0;
+    if ((unsigned)e.seq < (unsigned)p.c.max_seqs) {
+        const int n = p.a.lengths[e.seq];
         const long long room = (long long)p.c.max_pages * p.c.page_size;
-        k.len = n < 0 ? 0 : n > room ? (int)room : n;
+        e.len = n < 0 ? 0 : n > room ? (int)room : n;
     }
-    k.row0 = row0;
-    k.pad = 0;
-    return k;
+    return e;
 }
 
 // Lays the call out: what every entry holds, blocks of rows with their places on
-// the line, and which block each CTA begins in.  A warp an entry.
+// the line, and which block each CTA begins in.  A thread an entry looks it up, a
+// warp an entry works on its blocks.  kPlanThreads entries
+// at a time, in shared memory; where there are more they are looked up twice.
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ Args p)
 {
     __shared__ long long scratch[kPlanThreads / 32];
     __shared__ int scratch_int[kPlanThreads / 32];
-    __shared__ long long per_shared;
+    __shared__ Entry entries[kPlanThreads];
+    __shared__ long long places[kPlanThreads];      // of an entry
+    __shared__ int counts[kPlanThreads];            // blocks of an entry
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = kPlanThreads / 32;
     dependent_grid_wait();
     allow_dependent_grid();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = kPlanThreads / 32;
 
-    // starts as far as they rise, so that no two entries share a row
-    int most = 0;
-    for (int i0 = 0; i0 <= p.a.batch; i0 += kPlanThreads) {
-        const int i = i0 + threadIdx.x;
-        const int given = i <= p.a.batch ? p.a.starts[i] : 0;
-        const int mine = given < 0 ? 0 : given > p.a.tokens ? p.a.tokens : given;
-        int before;
-        auto larger = [](int a, int b) { return a > b ? a : b; };
-        const int all = scan_all(mine, 0, larger, &before, scratch_int);
-        if (i <= p.a.batch)
-            p.starts[i] = larger(most, larger(before, mine));
-        most = larger(most, all);
-    }
-    __syncthreads();
-
-    for (int b = warp; b < p.a.batch; b += warps) {
-        const Block k = block_of(p, b, 0);
-        const int rows = k.n * p.group, blocks = rows / p.rows + (rows % p.rows != 0);
-        long long cost = 0;
-        for (int i = lane; i < blocks; i += 32) {
-            Block x = k;
-            x.row0 = i * p.rows;
-            cost += cost_of(span_of(x, p.group, p.rows));
-        }
-#pragma unroll
-        for (int step = 16; step; step /= 2)
-            cost += __shfl_xor_sync(~0u, cost, step);
-        if (lane == 0) {
-            p.counts[b] = blocks;
-            p.places[b] = cost;
-        }
-    }
-    __syncthreads();
-
-    long long places = 0;
-    int blocks = 0;
-    for (int b0 = 0; b0 < p.a.batch; b0 += kPlanThreads) {
+    // Entries b0 on: looked up, with starts as far as they rise, so that no two share a
+    // row; `most` is the largest start before.  Then their blocks and places.
+    auto look = [&](int b0, int most) -> int {
         const int b = b0 + threadIdx.x;
-        auto sum = [](auto x, auto y) { return x + y; };
+        const bool in = b < p.a.batch;
+        auto bounded = [&](int i) {
+            const int x = p.a.starts[i];
+            return x < 0 ? 0 : x > p.a.tokens ? p.a.tokens : x;
+        };
+        auto larger = [](int x, int y) { return x > y ? x : y; };
+        const int first = in ? bounded(b) : 0, next = in ? bounded(b + 1) : 0;
+        Entry e = {};
+        if (in)
+            e = entry_of(p, b);
+        int before;
+        const int all = scan_all(first, 0, larger, &before, scratch_int);
+        e.start = larger(most, larger(before, first));
+        const int end = larger(e.start, next);
+        e.n = in ? end - e.start : 0;
+        entries[threadIdx.x] = e;
+        __syncthreads();
+        for (int i = warp; i < kPlanThreads && b0 + i < p.a.batch; i += warps) {
+            Block k = {};
+            k.n = entries[i].n;
+            k.len = entries[i].len;
+            const int rows = k.n * p.group, blocks = (int)(((long long)rows + p.rows - 1) / p.rows);
+            long long cost = 0;
+            for (int j = lane; j < blocks; j += 32) {
+                k.row0 = j * p.rows;
+                cost += cost_of(span_of(k, p.by_group, p.group, p.rows));
+            }
+#pragma unroll
+            for (int step = 16; step; step /= 2)
+                cost += __shfl_xor_sync(~0u, cost, step);
+            if (lane == 0) {
+                counts[i] = blocks;
+                places[i] = cost;
+            }
+        }
+        __syncthreads();
+        return larger(most, all);
+    };
+    // Exclusive sums over these entries' places and blocks, and their totals.
+    auto add_up = [&](int b0, long long *place, int *block) {
+        auto plus = [](auto x, auto y) { return x + y; };
+        const bool in = b0 + (int)threadIdx.x < p.a.batch;
         long long place_before;
         int block_before;
-        const long long place_all =
-            scan_all(b < p.a.batch ? p.places[b] : 0LL, 0LL, sum, &place_before, scratch);
-        const int block_all = scan_all(b < p.a.batch ? p.counts[b] : 0, 0, sum, &block_before, scratch_int);
-        if (b < p.a.batch) {
-            p.places[b] = places + place_before;
-            p.counts[b] = blocks + block_before;
-        }
-        places += place_all;
-        blocks += block_all;
-    }
-    if (threadIdx.x == 0) {
-        Head h;
-        h.all = places * p.c.kv_heads;
-        h.per = (h.all + p.ctas - 1) / p.ctas;
-        h.per = h.per > kLeast ? h.per : kLeast;
-        h.blocks = blocks;
-        h.pad = 0;
-        *p.head = h;
-        per_shared = h.per;
-    }
-    __syncthreads();
-
-    const long long per = per_shared;
-    for (int b = warp; b < p.a.batch; b += warps) {
-        const Block k = block_of(p, b, 0);
-        const int rows = k.n * p.group, count = rows / p.rows + (rows % p.rows != 0);
-        long long place = p.places[b];
-        const int number = p.counts[b];
-        for (int i0 = 0; i0 < count; i0 += 32) {
-            const int i = i0 + lane;
-            Block x = k;
-            x.row0 = i * p.rows;
-            const int cost = i < count ? cost_of(span_of(x, p.group, p.rows)) : 0;
-            long long upto = cost;
+        const long long place_all = scan_all(in ? places[threadIdx.x] : 0LL, 0LL, plus, &place_before, scratch);
+        const int block_all = scan_all(in ? counts[threadIdx.x] : 0, 0, plus, &block_before, scratch_int);
+        __syncthreads();
+        places[threadIdx.x] = *place + place_before;
+        counts[threadIdx.x] = *block + block_before;
+        __syncthreads();
+        *place += place_all;
+        *block += block_all;
+    };
+    auto write = [&](int b0, long long per) {
+        for (int e = warp; e < kPlanThreads && b0 + e < p.a.batch; e += warps) {
+            Block k = {};
+            k.seq = entries[e].seq;
+            k.start = entries[e].start;
+            k.n = entries[e].n;
+            k.len = entries[e].len;
+            const int rows = k.n * p.group, count = (int)(((long long)rows + p.rows - 1) / p.rows);
+            long long place = places[e];
+            const int number = counts[e];
+            for (int i0 = 0; i0 < count; i0 += 32) {
+                const int i = i0 + lane;
+                k.row0 = i * p.rows;
+                const int cost = i < count ? cost_of(span_of(k, p.by_group, p.group, p.rows)) : 0;
+                long long upto = cost;
 #pragma unroll
-            for (int step = 1; step < 32; step *= 2) {
-                const long long y = __shfl_up_sync(~0u, upto, step);
-                if (lane >= step)
-                    upto += y;
+                for (int step = 1; step < 32; step *= 2) {
+                    const long long y = __shfl_up_sync(~0u, upto, step);
+                    if (lane >= step)
+                        upto += y;
+                }
+                if (i < count) {
+                    k.place = place + upto - cost;
+                    p.blocks[number + i] = k;
+                    const long long from = k.place * p.c.kv_heads, to = from + (long long)cost * p.c.kv_heads;
+                    for (long long c = (from + per - 1) / per; c * per < to; ++c)
+                        p.first[c] = number + i;
+                }
+                place += __shfl_sync(~0u, upto, 31);
             }
-            if (i < count) {
-                x.place = place + upto - cost;
-                p.blocks[number + i] = x;
-                const long long from = x.place * p.c.kv_heads, to = from + (long long)cost * p.c.kv_heads;
-                for (long long c = (from + per - 1) / per; c * per < to; ++c)
-                    p.first[c] = number + i;
-            }
-            place += __shfl_sync(~0u, upto, 31);
         }
+        __syncthreads();
+    };
+
+    long long place = 0;
+    int block = 0, most = 0;
+    for (int b0 = 0; b0 < p.a.batch; b0 += kPlanThreads) {
+        most = look(b0, most);
+        add_up(b0, &place, &block);
+    }
+    Head h;
+    h.all = place * p.c.kv_heads;
+    h.per = (h.all + p.ctas - 1) / p.ctas;
+    h.per = h.per > kLeast ? h.per : kLeast;
+    h.blocks = block;
+    h.pad = 0;
+    if (threadIdx.x == 0)
+        *p.head = h;
+    if (p.a.batch <= kPlanThreads) {          // all of it is still here
+        write(0, h.per);
+        return;
+    }
+    place = 0;
+    block = most = 0;
+    for (int b0 = 0; b0 < p.a.batch; b0 += kPlanThreads) {
+        most = look(b0, most);
+        add_up(b0, &place, &block);
+        write(b0, h.per);
     }
 }
 
@@ -191,9 +219,6 @@ size_t lay_out(Args &p, int head_dim, int sms, unsigned char *base)
     p.head = (Head *)take(sizeof(Head));
     p.splits = (Split *)take(p.ctas * sizeof(Split));
     p.first = (int *)take(p.ctas * sizeof(int));
-    p.starts = (int *)take((p.a.batch + 1LL) * sizeof(int));
-    p.places = (long long *)take(p.a.batch * sizeof(long long));
-    p.counts = (int *)take(p.a.batch * sizeof(int));
     p.blocks = (Block *)take(blocks * sizeof(Block));
     p.partial = (float *)take(2ULL * p.ctas * p.rows * (head_dim + 2) * sizeof(float));
     return at;

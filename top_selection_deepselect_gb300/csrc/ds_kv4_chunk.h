@@ -37,9 +37,6 @@ struct Args {
     Block *blocks;
     int *first;           // block that a CTA's first place is in
     Split *splits;
-    int *starts;          // batch + 1, as far as they rise
-    long long *places;    // of each entry: places, then places before it
-    int *counts;          // of each entry: blocks, then blocks before it
     float *partial;
     int group, rows, run, ctas, q_vector;
     Divider by_group;
@@ -51,24 +48,24 @@ struct Span {
     int weight;           // places of a tile
 };
 
-__host__ __device__ __forceinline__ Span span_of(const Block &b, int group, int block_rows)
+__device__ __forceinline__ Span span_of(const Block &b, const Divider &by_group, int group, int block_rows)
 {
     Span s;
     const int left = b.n * group - b.row0;
     s.rows = left < block_rows ? left : block_rows;
     s.row_tiles = s.rows > 128 ? 2 : 1;
-    const int lo = b.len - b.n + 1 + b.row0 / group, hi = b.len - b.n + 1 + (b.row0 + s.rows - 1) / group;
+    const int lo = b.len - b.n + 1 + by_group(b.row0), hi = b.len - b.n + 1 + by_group(b.row0 + s.rows - 1);
     s.see_lo = lo > 0 ? lo : 0;
     s.see_hi = hi > 0 ? hi : 0;
     s.tiles = s.see_hi / 64 + (s.see_hi % 64 != 0);
-    s.weight = s.row_tiles == 2 ? 8 : 5;
+    s.weight = s.row_tiles == 2 ? 8 : 7;
     return s;
 }
 
 // Places of a unit: of its tiles, and of its start and end (queries, first copies,
 // outputs), by what they take.
 constexpr int kUnitCost = 40;
-__host__ __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.weight; }
+__device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.weight; }
 
 }  // namespace chunk
 }  // namespace kv4
