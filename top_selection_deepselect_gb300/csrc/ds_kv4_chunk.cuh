@@ -258,29 +258,30 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Pairs of 32-bit numbers, in 64-bit registers so that what does not change is paired once.
-typedef unsigned long long Two;
-__device__ __forceinline__ Two pair(float a, float b)
+// Pairs of 32-bit numbers in one instruction.
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two multiply_add(uint32_t x0, uint32_t x1, float f, float d)
 {
     Two y;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    asm("{\n\t.reg .b64 x, f, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 f, {%4, %4};\n\t"
+        "mov.b64 d, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, f, d;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(y.a), "=f"(y.b) : "r"(x0), "r"(x1), "f"(f), "f"(d));
     return y;
 }
-__device__ __forceinline__ void apart(Two x, float &a, float &b)
+__device__ __forceinline__ void add_to(Two &sum, float x0, float x1)
 {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ Two times_add(Two x, Two y, Two z)
-{
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ Two sum(Two x, Two y)
-{
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
+    asm("{\n\t.reg .b64 s, x;\n\t"
+        "mov.b64 s, {%0, %1};\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "add.rn.f32x2 s, s, x;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(sum.a), "+f"(sum.b) : "f"(x0), "f"(x1));
 }
 
 // Largest of 32 numbers, in four chains of three-way maxima.
@@ -311,14 +312,6 @@ struct Pair<__half> {
         uint32_t x, y;
         asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
         asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xe408e408u));
-        return y;
-    }
-    // 16 (u - 8) of the codes in the four bits above
-    static __device__ __forceinline__ uint32_t codes16(uint32_t w)
-    {
-        uint32_t x, y;
-        asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(x) : "r"(w));
-        asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xe480e480u));
         return y;
     }
     static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b)
@@ -412,21 +405,16 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Weights 2^(s c + low) of 32 scores, in fp16, and their sum.
-__device__ __forceinline__ float weights_of(uint32_t (&w)[16], const uint32_t (&s)[32], Two c, Two low)
+// Weights of 32 scores, in fp16, and their sums.
+__device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32], float c, float low, Two (&sum)[2])
 {
-    Two all[2] = {};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float a, b;
-        apart(times_add(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c, low), a, b);
-        a = exp2_fast(a), b = exp2_fast(b);
-        all[i % 2] = sum(all[i % 2], pair(a, b));
+        const Two x = multiply_add(s[2 * i], s[2 * i + 1], c, -low);
+        const float a = exp2_fast(x.a), b = exp2_fast(x.b);
+        add_to(sum[i % 2], a, b);
         w[i] = Pair<__half>::pack(a, b);
     }
-    float a, b;
-    apart(sum(all[0], all[1]), a, b);
-    return a + b;
 }
 
 // ---- the line of work -----------------------------------------------------------------
@@ -537,18 +525,18 @@ struct RowAt {
 };
 
 // Values are multiplied by a power of two, their lift, that brings the largest scale of a
-// part's first tile to [8, 16) (or as far as 2^15 does), and a later tile's that comes
+// part's first tile to [1/2, 1) (or as far as 2^15 does), and a later tile's that comes
 // out at kHigh or more, so that fp16 holds what any scales make: eleven bits of those
 // down to 2^-13 of the largest, and 2^-24 of that below.
 constexpr unsigned kHigh = 0x6c00;          // 2^12, an fp16: times a code of 8 below 2^16
 __device__ __forceinline__ int lift_of(unsigned most)
 {
-    const int e = 18 - (int)(most >> 10);   // most: bits of an fp16 that is finite
+    const int e = 14 - (int)(most >> 10);   // most: bits of an fp16 that is finite
     return e < 15 ? e : 15;
 }
-__device__ __forceinline__ unsigned lift_bits(int e)      // 2^e as an fp16, e >= -12
+__device__ __forceinline__ unsigned lift_bits(int e)      // 2^e as an fp16, e >= -16
 {
-    return (unsigned)(e + 15) << 10;
+    return e >= -14 ? (unsigned)(e + 15) << 10 : 0x400u >> (-14 - e);
 }
 // Weights are taken 2^7 times: with maxima that lag by 2^8 at most they stay within
 // fp16, and 11 bits of those down to 2^-21 of the row's largest.
@@ -899,28 +887,22 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const unsigned pick = half ? 0x7632 : 0x5410;
-                        uint32_t x[4], f[4], f16[4];
+                        uint32_t x[4], f[4];
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             x[m] = __byte_perm(w[2 * m], w[2 * m + 1], pick);
                             f[m] = Pair<__half>::times(__byte_perm(s[2 * m], s[2 * m + 1], pick), lift2);
-                            f16[m] = Pair<__half>::times(f[m], 0x2c002c00u);       // 1 / 16
                         }
                         const int channel = (group + half) * kGroup + 4 * g;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            // codes of odd places come out 16 times, and meet a sixteenth
                             const int d = channel + c;
-                            uint32_t y[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                if (c == 2)
-                                    x[m] >>= 8;
-                                y[m] = c % 2 ? Pair<__half>::times(Pair<__half>::codes16(x[m]), f16[m])
-                                             : Pair<__half>::times(Pair<__half>::codes(x[m]), f[m]);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + d * 128 + ((eight ^ (d & 7)) * 16)) =
-                                make_uint4(y[0], y[1], y[2], y[3]);
+                            uint4 v;
+                            v.x = Pair<__half>::times(Pair<__half>::codes(x[0] >> (4 * c)), f[0]);
+                            v.y = Pair<__half>::times(Pair<__half>::codes(x[1] >> (4 * c)), f[1]);
+                            v.z = Pair<__half>::times(Pair<__half>::codes(x[2] >> (4 * c)), f[2]);
+                            v.w = Pair<__half>::times(Pair<__half>::codes(x[3] >> (4 * c)), f[3]);
+                            *reinterpret_cast<uint4 *>(dst + d * 128 + ((eight ^ (d & 7)) * 16)) = v;
                         }
                     }
                 }
@@ -1001,7 +983,6 @@ chunk_kernel(const __grid_constant__ Args p)
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
         const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
-        const Two c2 = pair(c, c);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         while (next()) {
             const int n = u.t1 - u.t0, slot = unit % kSlots;
@@ -1090,12 +1071,12 @@ chunk_kernel(const __grid_constant__ Args p)
                 // half's maximum is known, and again where it turns out that it grows.
                 float most = largest_of(s);
                 ctl.swap[side][tile][half][local] = most;
-                float total;
+                Two sum[2];
                 uint32_t w[16];
 #pragma unroll
                 for (bool met = false;; met = true) {
-                    const float low = kRaise - (m == -INFINITY ? 0.f : m);
-                    total = weights_of(w, s, c2, pair(low, low));
+                    sum[0] = sum[1] = Two{0.f, 0.f};
+                    weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
                     if (met)
                         break;
                     most = fmaxf(most, meet()) * c;
@@ -1125,7 +1106,7 @@ chunk_kernel(const __grid_constant__ Args p)
                     }
                 }
                 store_columns(at + half * 16, w);
-                l += total;
+                l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
                 // With one row tile scores are a product ahead of outputs.  The output
                 // before this one ends before these weights are given away, so that never
