@@ -405,8 +405,11 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Weights of 32 scores, in fp16, and their sums.
-__device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32], float c, float low, Two (&sum)[2])
+// Weights of 32 scores, in fp16, and their sums.  Fine: what is left of each, in fp16
+// again.
+template <bool Fine>
+__device__ __forceinline__ void weights_of(uint32_t (&w)[16], uint32_t (&rest)[Fine ? 16 : 1], const uint32_t (&s)[32],
+                                           float c, float low, Two (&sum)[2])
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -414,6 +417,15 @@ __device__ __forceinline__ void weights_of(uint32_t *w, const uint32_t (&s)[32],
         const float a = exp2_fast(x.a), b = exp2_fast(x.b);
         add_to(sum[i % 2], a, b);
         w[i] = Pair<__half>::pack(a, b);
+        if (Fine) {
+            float d, e;
+            asm("{\n\t.reg .b16 x, y;\n\t"
+                "mov.b32 {x, y}, %2;\n\t"
+                "fma.rn.f32.f16 %0, x, %3, %4;\n\t"
+                "fma.rn.f32.f16 %1, y, %3, %5;\n\t}"
+                : "=f"(d), "=f"(e) : "r"(w[i]), "h"((unsigned short)0xbc00), "f"(a), "f"(b));
+            rest[i % (Fine ? 16 : 1)] = Pair<__half>::pack(d, e);
+        }
     }
 }
 
@@ -548,6 +560,8 @@ chunk_kernel(const __grid_constant__ Args p)
 {
     using S = Shape<D>;
     constexpr int kGroups = D / kGroup, kPer = kGroups > 4 ? 4 : kGroups;   // groups, of a stretch
+    // fp16 outputs show the rounding of weights to 11 bits, so that they are two numbers
+    constexpr bool kFine = std::is_same<T, __half>::value;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Control ctl;
     __shared__ Walk walks[S::kThreads / 32];
@@ -705,8 +719,11 @@ chunk_kernel(const __grid_constant__ Args p)
                 const uint32_t d = tensor + S::kOutColumn + t * D, a = tensor + S::kScoreColumn + s * kTokens;
                 const uint32_t b = values + value.stage * S::kValueBytes;
 #pragma unroll
-                for (int k = 0; k < kTokens / 16; ++k)
-                    product(d, a + k * 8, operand_at(b + k * 32), output_kind, add || k > 0, lead);
+                for (int part = 0; part < 1 + kFine; ++part)
+#pragma unroll
+                    for (int k = 0; k < kTokens / 16; ++k)
+                        product(d, a + part * (kTokens / 2) + k * 8, operand_at(b + k * 32), output_kind,
+                                add || part > 0 || k > 0, lead);
                 products_arrive(shared_at(&ctl.output[t]), lead);
             };
             auto wait_key = [&]() {
@@ -1072,11 +1089,11 @@ chunk_kernel(const __grid_constant__ Args p)
                 float most = largest_of(s);
                 ctl.swap[side][tile][half][local] = most;
                 Two sum[2];
-                uint32_t w[16];
+                uint32_t w[16], rest[kFine ? 16 : 1];
 #pragma unroll
                 for (bool met = false;; met = true) {
                     sum[0] = sum[1] = Two{0.f, 0.f};
-                    weights_of(w, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
+                    weights_of<kFine>(w, rest, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
                     if (met)
                         break;
                     most = fmaxf(most, meet()) * c;
@@ -1106,6 +1123,8 @@ chunk_kernel(const __grid_constant__ Args p)
                     }
                 }
                 store_columns(at + half * 16, w);
+                if constexpr (kFine)
+                    store_columns(at + kTokens / 2 + half * 16, rest);
                 l += (sum[0].a + sum[1].a) + (sum[0].b + sum[1].b);
                 wait_stores();
                 // With one row tile scores are a product ahead of outputs.  The output
