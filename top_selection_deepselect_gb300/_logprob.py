@@ -107,23 +107,32 @@ def _forward(t, index, logits, tokens, k, scale, logprob, entropy, lse, idx, top
     at, rows, vocab, stride = _logits(t, "logits", logits, index)
     tokens_at = _kv4._int32("tokens", tokens, index, rows)
     device = logits.device
-    if logprob is None and entropy is None and lse is None:
-        logprob, entropy, lse = t.empty((3, rows), dtype=t.float32, device=device).unbind(0)
-        places = logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr()
+    if logprob is None:
+        logprob = t.empty(rows, dtype=t.float32, device=device)
     else:
-        logprob, entropy, lse = (t.empty(rows, dtype=t.float32, device=device) if x is None else x
-                                 for x in (logprob, entropy, lse))
-        places = [_float32(t, name, x, (rows,), index)
-                  for name, x in (("logprob", logprob), ("entropy", entropy), ("lse", lse))]
+        _float32(t, "logprob", logprob, (rows,), index)
+    if entropy is None:
+        entropy = t.empty(rows, dtype=t.float32, device=device)
+    else:
+        _float32(t, "entropy", entropy, (rows,), index)
+    if lse is None:
+        lse = t.empty(rows, dtype=t.float32, device=device)
+    else:
+        _float32(t, "lse", lse, (rows,), index)
+    width = k if k > 0 else 0
     if idx is None:
-        idx = t.empty((rows, max(k, 0)), dtype=t.int32, device=device)
-    elif idx.shape != (rows, k):
-        raise ValueError("idx must have shape (%d, %d), got %s" % (rows, k, tuple(idx.shape)))
+        idx = t.empty((rows, width), dtype=t.int32, device=device)
+    elif idx.shape != (rows, width):
+        raise ValueError("idx must have shape (%d, %d), got %s" % (rows, width, tuple(idx.shape)))
+    else:
+        _kv4._int32("idx", idx, index)
     if top is None:
-        top = t.empty((rows, max(k, 0)), dtype=t.float32, device=device)
+        top = t.empty((rows, width), dtype=t.float32, device=device)
+    else:
+        _float32(t, "top", top, (rows, width), index)
     status = _lib().ds_token_logprobs(
-        at, code, rows, vocab, stride, tokens_at, k, scale, *places, _kv4._int32("idx", idx, index),
-        _float32(t, "top", top, (rows, max(k, 0)), index), t.raw_stream(index))
+        at, code, rows, vocab, stride, tokens_at, k, scale, logprob.data_ptr(), entropy.data_ptr(),
+        lse.data_ptr(), idx.data_ptr(), top.data_ptr(), t.raw_stream(index))
     if status:
         _check(status, "ds_token_logprobs")
     return logprob, entropy, lse, idx, top
@@ -204,10 +213,8 @@ def _function(t):
     class TokenLogprobs(t.torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, tokens, k, scale):
-            # buffers of their own, not parts of one: each output is saved, or written, by itself
-            each = [t.empty(logits.shape[:1], dtype=t.float32, device=logits.device) for _ in range(3)]
             logprob, entropy, lse, idx, top = _forward(t, logits.get_device(), logits, tokens, k, scale,
-                                                       *each, None, None)
+                                                       None, None, None, None, None)
             ctx.save_for_backward(logits, tokens, lse, entropy, idx)
             ctx.scale = scale
             ctx.mark_non_differentiable(idx)

@@ -16,9 +16,6 @@ namespace chunk {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-// Places of a CTA where units are cut: not more parts to join than the work is worth.
-constexpr int kLeast = 96;
-
 // Of a value a thread: what `combine` makes of all threads', and in *before of those below.
 template <typename V, typename F>
 __device__ V scan_all(V v, V none, F combine, V *before, V *scratch)
@@ -46,24 +43,6 @@ __device__ V scan_all(V v, V none, F combine, V *before, V *scratch)
     return all;
 }
 
-// What is known of an entry: its sequence, first row, new tokens, length.
-struct Entry {
-    int seq, start, n, len;
-};
-
-__device__ __forceinline__ Entry entry_of(const Args &p, int b)
-{
-    Entry e;
-    e.seq = p.a.seqs ? p.a.seqs[b] : b;
-    e.start = e.n = e.len = 0;
-    if ((unsigned)e.seq < (unsigned)p.c.max_seqs) {
-        const int n = p.a.lengths[e.seq];
-        const long long room = (long long)p.c.max_pages * p.c.page_size;
-        e.len = n < 0 ? 0 : n > room ? (int)room : n;
-    }
-    return e;
-}
-
 // Lays the call out: what every entry holds, blocks of rows with their places on
 // the line, and which block each CTA begins in.  A thread an entry looks it up, a
 // warp an entry works on its blocks.  kPlanThreads entries
@@ -85,12 +64,8 @@ plan_kernel(const __grid_constant__ Args p)
     auto look = [&](int b0, int most) -> int {
         const int b = b0 + threadIdx.x;
         const bool in = b < p.a.batch;
-        auto bounded = [&](int i) {
-            const int x = p.a.starts[i];
-            return x < 0 ? 0 : x > p.a.tokens ? p.a.tokens : x;
-        };
         auto larger = [](int x, int y) { return x > y ? x : y; };
-        const int first = in ? bounded(b) : 0, next = in ? bounded(b + 1) : 0;
+        const int first = in ? start_of(p, b) : 0, next = in ? start_of(p, b + 1) : 0;
         Entry e = {};
         if (in)
             e = entry_of(p, b);
@@ -179,8 +154,7 @@ plan_kernel(const __grid_constant__ Args p)
     }
     Head h;
     h.all = place * p.c.kv_heads;
-    h.per = (h.all + p.ctas - 1) / p.ctas;
-    h.per = h.per > kLeast ? h.per : kLeast;
+    h.per = places_of_cta(p, h.all);
     h.blocks = block;
     h.pad = 0;
     if (threadIdx.x == 0)
@@ -208,7 +182,10 @@ size_t lay_out(Args &p, int head_dim, int sms, unsigned char *base)
     const long long blocks = (long long)p.a.tokens * p.group / p.rows + p.a.batch;
     // no more CTAs than the largest possible line has work for
     const double room = (double)p.c.max_pages * p.c.page_size;
-    const double most = (double)blocks * p.c.kv_heads * (kUnitCost + 8 * (room / 64 + 1)) / kLeast + 1;
+    const double units = (double)blocks * p.c.kv_heads;
+    p.few = p.a.batch <= kFew && blocks <= kFew && units * (room / 64 + 1) <= 16.0 * sms;
+    p.whole = room <= 512;                 // eight tiles
+    const double most = p.whole ? units : units * (kUnitCost + 8 * (room / 64 + 1)) / kLeast + 1;
     p.ctas = most < sms ? (int)most : sms;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -220,7 +197,7 @@ size_t lay_out(Args &p, int head_dim, int sms, unsigned char *base)
     p.splits = (Split *)take(p.ctas * sizeof(Split));
     p.first = (int *)take(p.ctas * sizeof(int));
     p.blocks = (Block *)take(blocks * sizeof(Block));
-    p.partial = (float *)take(2ULL * p.ctas * p.rows * (head_dim + 2) * sizeof(float));
+    p.partial = (float *)take(p.whole ? 0 : 2ULL * p.ctas * p.rows * (head_dim + 2) * sizeof(float));
     return at;
 }
 
@@ -247,9 +224,11 @@ cudaError_t launch_chunk(const Cache &c, int head_dim, const Chunk &a, void *wor
     while (p.run < 8 && c.page_size % (2 * p.run) == 0)
         p.run *= 2;
     p.q_vector = ((uintptr_t)a.q | a.q_query * 2 | a.q_head * 2) % 16 == 0;
-    const cudaError_t e = launch_overlapped(chunk::plan_kernel, 1, chunk::kPlanThreads, 0, stream, p);
-    if (e != cudaSuccess)
-        return e;
+    if (!p.few) {
+        const cudaError_t e = launch_overlapped(chunk::plan_kernel, 1, chunk::kPlanThreads, 0, stream, p);
+        if (e != cudaSuccess)
+            return e;
+    }
     return head_dim == 64    ? launch_chunk_64(p, dev, p.ctas, stream)
            : head_dim == 128 ? launch_chunk_128(p, dev, p.ctas, stream)
                              : launch_chunk_256(p, dev, p.ctas, stream);

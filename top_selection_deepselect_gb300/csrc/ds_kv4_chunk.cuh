@@ -444,29 +444,33 @@ struct Part {
 // part has the registers for itself.
 struct Walk {
     Part u;
-    long long x, end;
+    const Block *blocks;       // all of them
+    int count;
+    long long x, end, per;
     int block, head;
     int more;                  // u is a part; 0: there are none left
     int pad;
 };
 
-__device__ __forceinline__ void begin(const Args &p, Walk &w)
+__device__ __forceinline__ void begin(Walk &w, const Head &h, const Block *blocks, int first)
 {
-    const long long per = p.head->per, all = p.head->all;
-    w.x = per * blockIdx.x;
-    w.end = w.x + per < all ? w.x + per : all;
-    w.block = w.x < w.end ? p.first[blockIdx.x] : 0;
+    w.blocks = blocks;
+    w.count = h.blocks;
+    w.per = h.per;
+    w.x = h.per * blockIdx.x;
+    w.end = w.x + h.per < h.all ? w.x + h.per : h.all;
+    w.block = w.x < w.end ? first : 0;
     w.head = -1;
 }
 
 // Goes to the next part.  One thread's.
 static __device__ __noinline__ void advance(const Args &p, Walk &w)
 {
-    const long long x = w.x, end = w.end, per = p.head->per;
+    const long long x = w.x, end = w.end, per = w.per;
     int block = w.block, head = w.head;
     w.more = 0;
-    while (x < end && block < p.head->blocks) {
-        const Block b = p.blocks[block];
+    while (x < end && block < w.count) {
+        const Block b = w.blocks[block];
         const Span s = span_of(b, p.by_group, p.group, p.rows);
         const int cost = cost_of(s);
         const long long first = b.place * p.c.kv_heads;
@@ -494,8 +498,8 @@ static __device__ __noinline__ void advance(const Args &p, Walk &w)
         u.see_lo = s.see_lo;
         u.see_hi = s.see_hi;
         u.tiles = s.tiles;
-        u.t0 = tile_at(x);
-        u.t1 = tile_at(end);
+        u.t0 = p.whole ? (at >= x ? 0 : s.tiles) : tile_at(x);
+        u.t1 = p.whole ? s.tiles : tile_at(end);
         u.later = 0;
         if (u.t1 > u.t0 && u.t1 < s.tiles)
             u.later = (int)((at + kUnitCost + (long long)(s.tiles - 1) * s.weight) / per) - (int)blockIdx.x;
@@ -508,6 +512,79 @@ static __device__ __noinline__ void advance(const Args &p, Walk &w)
     }
     w.block = block;
     w.head = head;
+}
+
+// What the planning launch does, by one warp for few blocks: entries a lane each,
+// then blocks a lane each.
+struct Few {
+    Head head;
+    Block blocks[kFew];
+    int first;                 // block that this CTA's first place is in
+};
+
+static __device__ __noinline__ void lay_out_few(const Args &p, Few &f)
+{
+    const int lane = threadIdx.x & 31;
+    Entry e = {};
+    int start = 0, next = 0;
+    if (lane < p.a.batch) {
+        e = entry_of(p, lane);
+        start = start_of(p, lane);
+        next = start_of(p, lane + 1);
+    }
+    // starts as far as they rise
+#pragma unroll
+    for (int step = 1; step < 32; step *= 2) {
+        const int y = __shfl_up_sync(~0u, start, step);
+        if (lane >= step)
+            start = max(start, y);
+    }
+    e.start = start;
+    e.n = lane < p.a.batch ? max(start, next) - start : 0;
+    const int count = (int)(((long long)e.n * p.group + p.rows - 1) / p.rows);
+    int upto = count;
+#pragma unroll
+    for (int step = 1; step < 32; step *= 2) {
+        const int y = __shfl_up_sync(~0u, upto, step);
+        if (lane >= step)
+            upto += y;
+    }
+    const int blocks = __shfl_sync(~0u, upto, 31);
+    // block `lane`: the entry that it is of
+    int owner = 0;
+    for (int i = 0; i < p.a.batch; ++i)
+        owner += __shfl_sync(~0u, upto, i) <= lane;
+    owner = min(owner, 31);
+    Block b = {};
+    b.seq = __shfl_sync(~0u, e.seq, owner);
+    b.start = __shfl_sync(~0u, e.start, owner);
+    b.n = __shfl_sync(~0u, e.n, owner);
+    b.len = __shfl_sync(~0u, e.len, owner);
+    b.row0 = (lane - __shfl_sync(~0u, upto - count, owner)) * p.rows;
+    const long long cost = lane < blocks ? cost_of(span_of(b, p.by_group, p.group, p.rows)) : 0;
+    long long place = cost;
+#pragma unroll
+    for (int step = 1; step < 32; step *= 2) {
+        const long long y = __shfl_up_sync(~0u, place, step);
+        if (lane >= step)
+            place += y;
+    }
+    Head h;
+    h.all = __shfl_sync(~0u, place, 31) * p.c.kv_heads;
+    h.per = places_of_cta(p, h.all);
+    h.blocks = blocks;
+    h.pad = 0;
+    b.place = place - cost;
+    const long long x = h.per * blockIdx.x;
+    if (lane < blocks) {
+        f.blocks[lane] = b;
+        if (blockIdx.x == 0)
+            p.blocks[lane] = b;            // for the join
+        if (x >= b.place * p.c.kv_heads && x < place * p.c.kv_heads)
+            f.first = lane;
+    }
+    if (lane == 0)
+        f.head = h;
 }
 
 constexpr int kSlots = 16;     // of what is known of a tile or a unit: more than any role is ahead
@@ -554,7 +631,10 @@ __device__ __forceinline__ unsigned lift_bits(int e)      // 2^e as an fp16, e >
 // fp16, and 11 bits of those down to 2^-21 of the row's largest.
 constexpr float kRaise = 7.f;
 
-template <typename T, int D>
+// Small: each CTA lays few blocks out itself, where the planning launch would take as
+// long as the work (one short prompt 15.2 -> 9.7 us).  A kernel of its own, since the
+// code costs the loops 3 to 20 % where they run long, though it is not in them.
+template <typename T, int D, bool Small>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 chunk_kernel(const __grid_constant__ Args p)
 {
@@ -565,6 +645,7 @@ chunk_kernel(const __grid_constant__ Args p)
     extern __shared__ unsigned char smem_raw[];
     __shared__ Control ctl;
     __shared__ Walk walks[S::kThreads / 32];
+    __shared__ Few few[1];
     unsigned char *smem = smem_raw + (1024 - (shared_at(smem_raw) & 1023) & 1023);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
 
@@ -602,8 +683,13 @@ chunk_kernel(const __grid_constant__ Args p)
 
     dependent_grid_wait();
     allow_dependent_grid();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && !p.whole)
         p.splits[blockIdx.x].parts = 0;
+    if (Small) {
+        if (warp == 0)
+            lay_out_few(p, *few);
+        __syncthreads();
+    }
 
     Walk &walk = walks[warp];
     const Part &u = walk.u;
@@ -615,7 +701,8 @@ chunk_kernel(const __grid_constant__ Args p)
         return walk.more != 0;
     };
     if (lane == 0)
-        begin(p, walk);
+        begin(walk, Small ? few->head : *p.head, Small ? few->blocks : p.blocks,
+              Small ? few->first : p.first[blockIdx.x]);
 
     if (warp == S::kCopyWarp) {
         // ---- records ---------------------------------------------------------------
@@ -1280,18 +1367,20 @@ template <int D>
 cudaError_t launch_chunk_dim(const Args &p, int dev, int ctas, cudaStream_t stream)
 {
     using S = Shape<D>;
-    auto fn = p.a.bf16 ? chunk_kernel<__nv_bfloat16, D> : chunk_kernel<__half, D>;
+    auto fn = p.a.bf16 ? (p.few ? chunk_kernel<__nv_bfloat16, D, true> : chunk_kernel<__nv_bfloat16, D, false>)
+                       : (p.few ? chunk_kernel<__half, D, true> : chunk_kernel<__half, D, false>);
     auto join = p.a.bf16 ? join_chunk_kernel<__nv_bfloat16, D> : join_chunk_kernel<__half, D>;
-    static std::atomic<unsigned long long> raised[2];       // the kernels' shared memory, once a device
+    static std::atomic<unsigned long long> raised[4];       // the kernels' shared memory, once a device
+    const int which = 2 * p.few + p.a.bf16;
     cudaError_t e = cudaSuccess;
-    if (!(raised[p.a.bf16].load(std::memory_order_relaxed) >> dev & 1)) {
+    if (!(raised[which].load(std::memory_order_relaxed) >> dev & 1)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess)
             return e;
-        raised[p.a.bf16].fetch_or(1ULL << dev, std::memory_order_relaxed);
+        raised[which].fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
     e = launch_overlapped(fn, ctas, S::kThreads, S::kSmem, stream, p);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess || p.whole)
         return e;
     return launch_overlapped(join, ctas * (S::kRows / 32), kJoinThreads, 0, stream, p);
 }

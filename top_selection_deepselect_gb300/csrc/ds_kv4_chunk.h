@@ -39,8 +39,43 @@ struct Args {
     Split *splits;
     float *partial;
     int group, rows, run, ctas, q_vector;
+    int few;              // few blocks and little work: each CTA lays them out itself, without the
+                          // planning launch
+    int whole;            // short sequences: units are not cut, and there is nothing to join
     Divider by_group;
 };
+
+// Entries and blocks that a warp lays out, a lane each.
+constexpr int kFew = 32;
+// Places of a CTA where units are cut: not more parts to join than the work is worth.
+constexpr int kLeast = 96;
+
+// What is known of entry b: its sequence and length; start and n are left to the caller.
+struct Entry {
+    int seq, start, n, len;
+};
+__device__ __forceinline__ Entry entry_of(const Args &p, int b)
+{
+    Entry e;
+    e.seq = p.a.seqs ? p.a.seqs[b] : b;
+    e.start = e.n = e.len = 0;
+    if ((unsigned)e.seq < (unsigned)p.c.max_seqs) {
+        const int n = p.a.lengths[e.seq];
+        const long long room = (long long)p.c.max_pages * p.c.page_size;
+        e.len = n < 0 ? 0 : n > room ? (int)room : n;
+    }
+    return e;
+}
+__device__ __forceinline__ int start_of(const Args &p, int b)      // of entry b, within the rows
+{
+    const int x = p.a.starts[b];
+    return x < 0 ? 0 : x > p.a.tokens ? p.a.tokens : x;
+}
+__device__ __forceinline__ long long places_of_cta(const Args &p, long long all)
+{
+    const long long even = (all + p.ctas - 1) / p.ctas;
+    return p.whole || even > kLeast ? (even > 1 ? even : 1) : kLeast;
+}
 
 // What a block's rows see, and its tiles.
 struct Span {
