@@ -146,7 +146,7 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
  *   dtype     of q and out: DS_BF16 or DS_FP16
  *   q         device, unit stride in the last dimension, q_stride = {token, head}
  *             strides in elements; 16 bytes at a time where these allow it
- *   scale     any number
+ *   scale     finite
  *   out       device [tokens][heads][head_dim], contiguous, 16-byte aligned
  *   lse       device float[tokens][heads], or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_chunk_attention_workspace bytes
@@ -154,8 +154,8 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
  * out = 0 and lse = -inf.  Scores are sums in 32 bits of exact products; with
  * DS_FP16, a key's channel is exact to 2^-25 at least, and one whose scale is beyond
  * 9352 (channels beyond fp16) is taken with that.  A probability is rounded to 11
- * significant bits (below 2^-21 of the row's largest it is within 2^-32 of that), and
- * so is a value (below 2^-13 of the largest scale of its head, within 2^-24 of that);
+ * significant bits (below 2^-21 of the row's largest it is within 2^-32 of that), with
+ * DS_FP16 to 22, and a value to 11 (below 2^-13 of the largest scale of its head, within 2^-24 of that);
  * maxima, sums and outputs are held in 32 bits.  A row with a NaN or an infinity
  * gives NaN if it sees a token.  (Waits are limited to a second, which no working
  * GPU takes; after that results are NaN.)

@@ -201,11 +201,19 @@ def test_queries_that_are_no_numbers(ds, dtype):
     assert torch.equal(out[~want], other[~want]) and torch.equal(lse[~want], olse[~want])
 
 
-@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0, 1e-4])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0, 1e-4, 1e-38])
 def test_scale(ds, scale):
     rng = np.random.default_rng(7)
     check(ds, *chunk_args(rng, [70], [100], 4, 2, 64, 16, "bf16"), scale=scale)
     check(ds, *chunk_args(rng, [70], [100], 2, 1, 256, 16, "fp16"), scale=scale)
+
+
+def test_no_scale_is_even_attention(ds):
+    """Scores of any size times 0 are 0, and times the smallest numbers what they are."""
+    rng = np.random.default_rng(16)
+    q, pool, table, lengths, starts = chunk(rng, [70], [100], 2, 1, 64, 16, spread=1e4)
+    for scale in (0.0, 1e-40, -1e-36):
+        check(ds, q * np.float32(1e30), "bf16", pool, table, lengths, starts, scale=scale)
 
 
 @pytest.mark.parametrize("dtype,spread", [("bf16", 1e-30), ("bf16", 1e-6), ("bf16", 1e4), ("fp16", 1e-3), ("fp16", 2e3),

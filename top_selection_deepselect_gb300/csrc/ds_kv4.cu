@@ -271,6 +271,8 @@ int ds_kv4_chunk_attention(const ds_kv4_cache_t *cache, const int32_t *lengths, 
         return fail(DS_EUNSUPPORTED, "dtype %d is not DS_BF16 (1) or DS_FP16 (2)", dtype);
     if (!q_stride)
         return fail(DS_EINVAL, "q_stride must be non-NULL");
+    if (!(scale - scale == 0.f))
+        return fail(DS_EINVAL, "scale = %g must be finite", scale);
     if (batch == 0 || tokens == 0)
         return DS_OK;
     if (!lengths || !starts || !q || !out)

@@ -1086,7 +1086,8 @@ chunk_kernel(const __grid_constant__ Args p)
         };
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
-        const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1e-30f);
+        // not 0, which a masked score of -inf times it would not come through
+        const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1.4e-45f);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         while (next()) {
             const int n = u.t1 - u.t0, slot = unit % kSlots;
