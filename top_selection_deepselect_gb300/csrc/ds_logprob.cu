@@ -664,14 +664,14 @@ logprob_kernel(const __grid_constant__ Args p)
     if (p.k > 0) {
         // the logits of the listed vectors that reach the value
         const int listed = sh.listed;
-        for (int i0 = 0; i0 < listed * Vec<T>::kCount && listed <= kCapacity; i0 += kThreads) {
-            const int i = i0 + threadIdx.x;
-            if (i < listed * Vec<T>::kCount) {
-                const unsigned at = sh.vectors[i / Vec<T>::kCount];
-                const int e = i % Vec<T>::kCount;
+        for (int i = threadIdx.x; i < listed && listed <= kCapacity; i += kThreads) {
+            const unsigned at = sh.vectors[i];
+            const Vec<T> v = row.load(at, hi);
+#pragma unroll
+            for (int e = 0; e < Vec<T>::kCount; ++e) {
                 const unsigned place = at * Vec<T>::kCount + e;
-                if (place >= row.skip && place < row.past && !(to_float(row.at[place]) < reach))
-                    keep(sh, entry_of(row, row.at[place], at, e));
+                if (!(to_float(v.x[e]) < reach) && place >= row.skip && place < row.past)
+                    keep(sh, entry_of(row, v.x[e], at, e));
             }
         }
         __syncthreads();
