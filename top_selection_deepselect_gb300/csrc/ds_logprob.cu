@@ -530,26 +530,35 @@ logprob_kernel(const __grid_constant__ Args p)
     const unsigned hi = (unsigned)((unsigned long long)row.vectors * (rank + 1) / p.cluster);
     const float c = p.scale * kLog2e;
 
-    // vector j to slot i: a copy, or element by element at the row's ends and past them
-    auto fetch = [&](unsigned j, int i) {
-        if (j < hi && row.whole(j)) {
-            cp_async16((uint32_t)__cvta_generic_to_shared(ring + i * kThreads),
-                       row.at + (size_t)j * Vec<T>::kCount);
-        } else {
-            T *x = ring[i * kThreads].x;
-#pragma unroll 1
-            for (int e = 0; e < Vec<T>::kCount; ++e)
-                x[e] = row.element(j < hi ? j : 0xfffffff0u / Vec<T>::kCount, e);
-        }
-    };
-    unsigned j = lo + threadIdx.x;
+    // The slice's whole vectors [from, to), a thread's kThreads apart, in rounds of kDepth.
+    // Past them a slot holds -inf, which adds nothing.
+    const unsigned from = max(lo, row.skip ? 1u : 0u), to = max(from, min(hi, row.past / Vec<T>::kCount));
+    unsigned j = from + threadIdx.x;
+    const T *source = row.at + (size_t)j * Vec<T>::kCount;
+    Vec<T> none;
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-        fetch(j + i * kThreads, i);
+    for (int e = 0; e < Vec<T>::kCount; ++e)
+        from_float(none.x[e], -INFINITY);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    auto fetch = [&](int i, int turn) {        // the vector `turn` ahead to slot i
+        if (j + turn * kThreads < to)
+            cp_async16(ring_at + i * kThreads * 16, source + turn * kThreads * Vec<T>::kCount);
+        else
+            ring[i * kThreads] = none;
         cp_async_commit();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i)
+        fetch(i, i);
     if (threadIdx.x == 0)
         sh.listed = sh.count = 0;
+    // The row's first and last vector, where they are not whole, are two threads' besides.
+    unsigned ragged = ~0u;
+    if (threadIdx.x == 0 && lo < from && lo < hi)
+        ragged = lo;
+    if (threadIdx.x == 1 && hi > to && hi - 1 >= from)
+        ragged = hi - 1;
+    const Vec<T> edge = row.load(ragged, hi);
 
     // The first vectors: their maximum, which all sums start from, and a value that k
     // of their logits reach.
@@ -562,13 +571,17 @@ logprob_kernel(const __grid_constant__ Args p)
         nan = nan || m != m;
         mine = fmaxf(mine, m);
     }
+    const unsigned mine_key = nan ? ~0u : key_of(mine);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kCount; ++e)
+        mine = fmaxf(mine, to_float(edge.x[e]));
     const unsigned top_key = __reduce_max_sync(~0u, key_of(mine));
     if (lane == 0)
         sh.most[warp] = value_of(top_key);
     if (p.k > 0) {
         // four largest of each warp's threads, and the k-th of these; a thread
         // of places outside the row has -inf, which is at or below all logits
-        const unsigned sorted = order_lanes(nan ? ~0u : key_of(mine));
+        const unsigned sorted = order_lanes(mine_key);
         if (lane < kEach)
             sh.keys[warp * kEach + lane] = sorted;
     }
@@ -578,7 +591,8 @@ logprob_kernel(const __grid_constant__ Args p)
     for (int w = 1; w < kWarps; ++w)
         mine = fmaxf(mine, sh.most[w]);
     // A listed vector's largest has to be above `bound`; among the first ones at it, too:
-    // above the value before it.  (An equal one further on comes later in the order.)
+    // above the value before it.  (An equal one further on comes later in the order.)  The
+    // vectors at the row's ends are listed anyhow.
     float bound = mine, reach = mine;
     if (p.k > 0) {
         const unsigned key = __shfl_sync(~0u, order_lanes(sh.keys[lane]), p.k - 1);
@@ -590,51 +604,48 @@ logprob_kernel(const __grid_constant__ Args p)
     Two sums = 0, weighted = 0;
     Two mc2 = pair(-scaled(mine, c), -scaled(mine, c));
     const Two c2 = pair(c, c);
-    const unsigned turns = (hi - lo + kThreads - 1) / kThreads;
-    // the vectors that are whole, and where the next copy comes from
-    const unsigned whole_from = max(lo, row.skip ? 1u : 0u), whole_to = min(hi, row.past / Vec<T>::kCount);
-    unsigned ahead = j + kDepth * kThreads;
-    const T *from = row.at + (size_t)ahead * Vec<T>::kCount;
-    int slot = 0;
+    auto list = [&](unsigned at) {
+        const int n = atomicAdd(&sh.listed, 1);
+        if (n < kCapacity)
+            sh.vectors[n] = at;
+    };
+    const unsigned rounds = (to - from + kDepth * kThreads - 1) / (kDepth * kThreads);
 #pragma unroll 1
-    for (unsigned turn = 0; turn < turns; ++turn) {
-        cp_async_wait<kDepth - 1>();
-        const Vec<T> v = ring[slot * kThreads];
-        const float m = largest(v);
-        if (!(m <= bound)) {
-            if (p.k > 0 && j < hi) {
-                const int at = atomicAdd(&sh.listed, 1);
-                if (at < kCapacity)
-                    sh.vectors[at] = j;
-            }
-            float most = m;
-            if (m != m) {
-                most = a.most;
+    for (unsigned round = 0; round < rounds; ++round) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            cp_async_wait<kDepth - 1>();
+            const Vec<T> v = ring[i * kThreads];
+            const float m = largest(v);
+            if (!(m <= bound)) {
+                if (p.k > 0 && j + i * kThreads < to)
+                    list(j + i * kThreads);
+                float most = fmaxf(a.most, m);
+                if (m != m) {
 #pragma unroll 1
-                for (int e = 0; e < Vec<T>::kCount; ++e)
-                    most = fmaxf(most, to_float(ring[slot * kThreads].x[e]));
+                    for (int e = 0; e < Vec<T>::kCount; ++e)
+                        most = fmaxf(most, to_float(ring[i * kThreads].x[e]));
+                }
+                if (most > a.most) {
+                    apart(sums, a.s0, a.s1);
+                    apart(weighted, a.t0, a.t1);
+                    lift_fast(a, most, c);
+                    sums = pair(a.s0, a.s1);
+                    weighted = pair(a.t0, a.t1);
+                    mc2 = pair(-scaled(most, c), -scaled(most, c));
+                }
             }
-            if (most > a.most) {
-                apart(sums, a.s0, a.s1);
-                apart(weighted, a.t0, a.t1);
-                lift_fast(a, most, c);
-                sums = pair(a.s0, a.s1);
-                weighted = pair(a.t0, a.t1);
-                mc2 = pair(-scaled(most, c), -scaled(most, c));
-            }
+            add_fast(sums, weighted, v, mc2, c2);
+            fetch(i, kDepth + i);
         }
-        add_fast(sums, weighted, v, mc2, c2);
-        if (ahead >= whole_from && ahead < whole_to)
-            cp_async16((uint32_t)__cvta_generic_to_shared(ring + slot * kThreads), from);
-        else if (turn + kDepth < turns)
-            fetch(ahead, slot);
-        cp_async_commit();
-        slot = (slot + 1) % kDepth;
-        j += kThreads;
-        ahead += kThreads;
-        from += kThreads * Vec<T>::kCount;
-        if (turn == kDepth - 1)
-            bound = reach;
+        j += kDepth * kThreads;
+        source += kDepth * kThreads * Vec<T>::kCount;
+        bound = reach;
+    }
+    if (ragged != ~0u) {
+        add_fast(sums, weighted, edge, mc2, c2);
+        if (p.k > 0)
+            list(ragged);
     }
     cp_async_wait<0>();
     apart(sums, a.s0, a.s1);
@@ -660,7 +671,7 @@ logprob_kernel(const __grid_constant__ Args p)
     } else {
         a = sum_carefully(row, lo, hi, c, sh.sums);
     }
-    Entry list = 0;
+    Entry best = 0;
     if (p.k > 0) {
         // the logits of the listed vectors that reach the value
         const int listed = sh.listed;
@@ -675,11 +686,11 @@ logprob_kernel(const __grid_constant__ Args p)
             }
         }
         __syncthreads();
-        list = listed <= kCapacity && sh.count <= kCapacity ? select_entries(sh.entries, sh.count, sh.lists)
+        best = listed <= kCapacity && sh.count <= kCapacity ? select_entries(sh.entries, sh.count, sh.lists)
                                                             : select_slowly(row, lo, hi, p.k, sh);
     }
     if (p.cluster > 1 && warp == 0) {
-        sh.top[lane] = list;
+        sh.top[lane] = best;
         if (lane == 0)
             sh.all = a;
     }
@@ -692,7 +703,7 @@ logprob_kernel(const __grid_constant__ Args p)
                 const Shared *far = cluster.map_shared_rank(&sh, other);
                 add_sums(a, far->all, c);
                 if (p.k > 0)
-                    list = merge_lists(list, far->top[lane]);
+                    best = merge_lists(best, far->top[lane]);
             }
         cluster.sync();           // the others' shared memory lives until it was read
     }
@@ -712,8 +723,8 @@ logprob_kernel(const __grid_constant__ Args p)
     }
     if (lane < p.k) {
         const long long at = (long long)r * p.k + lane;
-        p.idx[at] = (int)~(unsigned)list;
-        p.top[at] = log_prob(value_of((unsigned)(list >> 32)));
+        p.idx[at] = (int)~(unsigned)best;
+        p.top[at] = log_prob(value_of((unsigned)(best >> 32)));
     }
 }
 
