@@ -18,21 +18,36 @@
 // values are fp16 in the second product, whatever the queries' type, each rounded
 // to 11 bits once; powers of two keep both within its range.
 //
-// Codes become operands by a logical operation and a packed addition: a code u in
-// the low bits of an fp16 of 1024 (bf16 of 128) makes it 1024 + u (128 + u), and
-// subtracting 1032 (136) leaves u - 8.  A word of eight key codes gives channels
-// (j, j + 4) in pairs; the queries are laid out in the same order.  A value's
+// Codes become operands by a logical operation and a packed multiply-add or addition:
+// a code u in the low bits of an fp16 of 1024 makes it 1024 + u, and subtracting 1032
+// leaves u - 8; in the upper bits of the fraction of a bf16 of 16 it makes 16 + u, and
+// (16 + u) s - 24 s is exact for a part s of a scale.  A word of eight key codes gives
+// channels (j, j + 4) in pairs; the queries are laid out in the same order.  A value's
 // word is taken with that of the next token, so that pairs are (token, token + 1)
 // of one channel: both operands end up with the summed index contiguous.
 //
+// What bounds it.  For 64 tokens and 256 rows of 128 channels the products take 1536
+// cycles of the tensor cores, a third of them for the keys' second part, and the four
+// schedulers issue some 1600 instructions each: 330 a tile of rows for weights and
+// maxima, 290 for keys, 230 for values, the rest for waits and what surrounds them.
+// 2048 tokens of 32768 (64 query heads, 8 key/value heads of 128, bf16) take 1.96 ms:
+// 1090 TFLOP/s, 1630 with the second part, which is 85 % of what a large bf16 library
+// product reaches in a burst; over many calls in turn the power limit brings it to
+// 2.05 ms.  Heads of 64 and 256 stay at 500 and 600 TFLOP/s, by issue: there the
+// expansion and the softmax are as large for a half of the products, or serve 128 rows.
+//
 // Roles of a CTA's warps: softmax (eight warps a tile of rows, half a row a thread),
-// expansion of keys and of values (four warps each), one that issues the products,
-// one that copies records.  They meet on arrival barriers in shared memory only.
+// expansion of keys and of values (four warps each, eight for D = 256), one that issues
+// the products, one that copies records.  They meet on arrival barriers in shared
+// memory.  (A whole row a thread, with registers shifted between the roles, was 5 %
+// slower; 64-bit register pairs for the weights 3 %; rolled loops for less code, in any
+// of the roles' inner loops, 5 to 8 %.)
 //
 // Work is a line of places: every (unit, head) has places for each of its tiles of
 // tokens, and for its start and end, by what these take; CTAs, one an SM, have
-// equal stretches.  Units cut between CTAs leave partial results for a second
-// launch.  Lengths and starts are read on the device by a first, small launch.
+// equal stretches.  Units cut between CTAs leave partial results for a last launch.
+// Lengths and starts are read on the device by a first, small launch, or where there is
+// little to do by each CTA.
 #pragma once
 
 #include <atomic>
@@ -63,6 +78,9 @@ struct Shape {
     static constexpr int kRawBytes = kTokens / 8 * kGroupBytes;
     static constexpr int kKeyBytes = kTokens * D * 2;          // of one part of the split
     static constexpr int kValueBytes = kTokens * D * 2;
+    // Stages, as many as there is room for.  Two or four for D <= 128 change nothing
+    // (2.00 and 2.02 ms where three took 2.01); for D = 256 a second stage of values, with
+    // records in pieces of half a tile to make room, took 478 us where one takes 433.
     static constexpr int kKeyStages = D == 256 ? 2 : 3;
     static constexpr int kValueStages = D == 256 ? 1 : 3;
     static constexpr int kRawStages = 3;

@@ -93,12 +93,14 @@ __device__ __forceinline__ Span span_of(const Block &b, const Divider &by_group,
     s.see_lo = lo > 0 ? lo : 0;
     s.see_hi = hi > 0 ? hi : 0;
     s.tiles = s.see_hi / 64 + (s.see_hi % 64 != 0);
+    // measured on 2 x 129 tokens after 130943, of whose rows one block in five is small:
+    // 7 of 8 1.23 ms, 6 1.36, 5 1.52
     s.weight = s.row_tiles == 2 ? 8 : 7;
     return s;
 }
 
 // Places of a unit: of its tiles, and of its start and end (queries, first copies,
-// outputs), by what they take.
+// outputs), by what they take: ragged prompts 174 us with 40, 187 with 16, 176 with 64.
 constexpr int kUnitCost = 40;
 __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.weight; }
 
