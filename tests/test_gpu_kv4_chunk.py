@@ -243,6 +243,21 @@ def test_values_that_grow_and_fall(ds, dim, dtype):
     check(ds, q, dtype, pool, table, lengths, starts)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_scales_of_either_sign_and_every_code(ds, dim, dtype):
+    """Records that kv4_append does not make: any codes, scales below 0, 0, subnormal and the smallest."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, [80, 130], [70, 0], 2, 1, dim, 16)
+    pool = rng.integers(0, 256, pool.shape, dtype=np.uint8)
+    n = dim // 32
+    scales = (rng.standard_normal((*pool.shape[:-1], 2 * n)) * 0.2).astype(np.float16)
+    scales[rng.random(scales.shape) < 0.1] = 0
+    scales[rng.random(scales.shape) < 0.1] *= np.float16(2.0 ** -14)
+    pool[..., dim:dim + 4 * n] = scales.view(np.uint8)
+    check(ds, q, dtype, pool, table, lengths, starts)
+
+
 def test_growing_scores(ds):
     """Each tile's largest score is well above the last one's, so that outputs are scaled again and again."""
     rng = np.random.default_rng(9)

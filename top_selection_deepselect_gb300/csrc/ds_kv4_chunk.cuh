@@ -150,10 +150,12 @@ __device__ __forceinline__ void bar_wait(uint32_t bar, unsigned phase, volatile 
 {
     long long from = 0;
     for (unsigned tries = 1; !bar_done(bar, phase); ++tries) {
-        if (tries % 64 != 0)               // the timer takes longer to read than most waits
+        if (tries % 8 != 0)
             continue;
         if (*lost)
             return;
+        if (tries % 64 != 0)               // the timer takes longer to read than most waits
+            continue;
         const long long now = clock_ns();
         if (from == 0)
             from = now;
@@ -396,7 +398,7 @@ struct Pair<__nv_bfloat16> {
     static __device__ __forceinline__ Key key(uint32_t s)
     {
         Key k;
-        const uint32_t h = (__vminu2(s, 0x7bdf7bdfu) + 0x00200020u) & 0xffc0ffc0u;
+        const uint32_t h = ((__vminu2(s & 0x7fff7fffu, 0x7bdf7bdfu) + 0x00200020u) & 0xffc0ffc0u) | (s & 0x80008000u);
         uint32_t l;
         asm("sub.f16x2 %0, %1, %2;" : "=r"(l) : "r"(s), "r"(h));
         k.hi = convert(h);
@@ -1096,8 +1098,11 @@ chunk_kernel(const __grid_constant__ Args p)
         const uint32_t out_at = rows_at + S::kOutColumn + tile * D + half * (D / 2);
         unsigned score_phase[2] = {0, 0}, output_phase = 0, side = 0;
         // The other half's value for this row, where both warps of the rows meet.
+        // Past it both have their scores, whose columns either's weights go to.
         auto meet = [&]() -> float {
+            fence_before();
             asm volatile("bar.sync %0, 64;" ::"r"(1 + tile * 4 + warp % 4) : "memory");
+            fence_after();
             const float y = ctl.swap[side][tile][half ^ 1][local];
             side ^= 1;
             return y;
