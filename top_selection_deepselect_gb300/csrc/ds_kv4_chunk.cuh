@@ -1173,17 +1173,27 @@ chunk_kernel(const __grid_constant__ Args p)
             const int t0 = u.t0, t1 = u.t1, see_lo = u.see_lo;
             for (int t = t0; t < t1; ++t) {
                 const uint32_t at = rows_at + S::kScoreColumn + spin * kTokens;
-                // what is known of the tile once its values are expanded, which is mostly
-                // before its scores are there
-                bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
-                value.step();
-                const int lift_now = ctl.lift[count % kSlots];
-                const unsigned there = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots])[half];
+                // The lift is known when the values are expanded, which is mostly before the
+                // scores are there.  With one stage of values it is not, and is waited for when
+                // the weights are worked out (D = 256 410 us for 437; the others 6 to 10 % slower).
+                constexpr bool kLate = S::kValueStages == 1;
+                int lift_now = 0;
+                if (!kLate) {
+                    bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                    value.step();
+                    lift_now = ctl.lift[count % kSlots];
+                }
+                const unsigned *known = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots]) + half;
+                unsigned there = 0;
+                if (!kLate)
+                    there = *known;
                 ++count;
                 bar_wait(shared_at(&ctl.score[spin]), score_phase[spin], lost);
                 score_phase[spin] ^= 1;
                 fence_after();
                 __syncwarp();
+                if (kLate)
+                    there = *known;
                 uint32_t s[32];
                 load_columns(s, at + half * 32);
                 wait_loads();
@@ -1207,6 +1217,11 @@ chunk_kernel(const __grid_constant__ Args p)
                     weights_of<kFine>(w, rest, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
                     if (met)
                         break;
+                    if (kLate) {
+                        bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                        value.step();
+                        lift_now = ctl.lift[(count - 1) % kSlots];
+                    }
                     most = fmaxf(most, meet()) * c;
                     const bool grows = most > m + 8.f || m == -INFINITY;
                     if (!__any_sync(~0u, (grows && most > m) || lift_now != lift))
