@@ -33,7 +33,7 @@
 // 2048 tokens of 32768 (64 query heads, 8 key/value heads of 128, bf16) take 1.96 ms:
 // 1090 TFLOP/s, 1630 with the second part, which is 85 % of what a large bf16 library
 // product reaches in a burst; over many calls in turn the power limit brings it to
-// 2.05 ms.  Heads of 64 and 256 stay at 500 and 600 TFLOP/s, by issue: there the
+// 2.05 ms.  Heads of 64 and 256 stay at 500 and 630 TFLOP/s, by issue: there the
 // expansion and the softmax are as large for a half of the products, or serve 128 rows.
 //
 // Roles of a CTA's warps: softmax (eight warps a tile of rows, half a row a thread),
@@ -79,8 +79,9 @@ struct Shape {
     static constexpr int kKeyBytes = kTokens * D * 2;          // of one part of the split
     static constexpr int kValueBytes = kTokens * D * 2;
     // Stages, as many as there is room for.  Two or four for D <= 128 change nothing
-    // (2.00 and 2.02 ms where three took 2.01); for D = 256 a second stage of values, with
-    // records in pieces of half a tile to make room, took 478 us where one takes 433.
+    // (2.00 and 2.02 ms where three took 2.01).  For D = 256 a second stage of values took
+    // 461 us in the place of a second of keys, and 488 us in the place of two of records,
+    // where one takes 409 (1024 tokens after 7168).
     static constexpr int kKeyStages = D == 256 ? 2 : 3;
     static constexpr int kValueStages = D == 256 ? 1 : 3;
     static constexpr int kRawStages = 3;

@@ -515,9 +515,9 @@ __device__ __noinline__ Sums sum_carefully(const Row<T> &row, unsigned lo, unsig
     return a;
 }
 
-// 2048 x 128000 bf16: 112 us alone, 103 in turn (5.1 TB/s, 76 % of the measured copy rate),
+// 2048 x 128000 bf16: 112 us alone, 97 in turn (5.4 TB/s, 81 % of the measured copy rate),
 // issue slots 73 % busy: some 63 instructions for eight logits, 26 of them for the sums
-// themselves.  256 x 128000 with 20 alternatives 27 us in turn.  Loads to registers, four
+// themselves.  256 x 128000 with 20 alternatives 25 us in turn.  Loads to registers, four
 // ahead, took 304 and 69: the lanes' waits, not HBM.  Two or four vectors a step 116 and
 // 114 where one took 115; five CTAs an SM the same.
 template <typename T>
@@ -739,7 +739,7 @@ logprob_kernel(const __grid_constant__ Args p)
 // dz_i = p_i (g_lse - g_logprob - sum g_top - g_entropy (log p_i + entropy)), plus
 // the token's and the alternatives' own gradients in their places, which are
 // written again by one thread each after the CTA's pass.  One read and one write
-// of the row, a CTA for each piece of it: 1024 x 128000 bf16 101 us (5.2 TB/s, 78 % of
+// of the row, a CTA for each piece of it: 1024 x 128000 bf16 102 us (5.1 TB/s, 77 % of
 // the measured copy rate), waiting for loads.  Two vectors ahead of the work 140 us,
 // four 220, because of the registers; loads past L1 105.
 struct GradArgs {
@@ -876,7 +876,7 @@ gradient_kernel(const __grid_constant__ GradArgs p)
 
 // CTAs of a row: one where rows alone fill the GPU twice, else as many as give slices of
 // at least kSlice vectors a thread.  8 x 128000 17.5 us in clusters of eight, 25.8 in one
-// CTA a row; 256 rows 34 in clusters of two, 34 in one, 42 in clusters of four.
+// CTA a row; 256 rows 32 in clusters of two, 32 in one, 40 in clusters of four.
 constexpr int kSlice = 8;
 
 template <typename T>
