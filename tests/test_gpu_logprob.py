@@ -417,3 +417,39 @@ def test_refusals(ds):
         ds.token_logprobs(x.requires_grad_(), tokens, lse=lse)
     empty = ds.token_logprobs(torch.zeros((0, 8), device=DEV), tokens[:0], 2)
     assert [tuple(t.shape) for t in empty] == [(0,), (0,), (0,), (0, 2), (0, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("rows,scale", [(1, 1.0), (1, 0.01), (310, 1.0)])
+@pytest.mark.parametrize("k", [0, 5])
+def test_rows_that_start_masked(ds, dtype, rows, scale, k):
+    """The type's lowest value, or one as good as that, in all of a slice's first logits, and in
+    all of a slice: what -inf is taken as in sums may not stand above the maximum so far."""
+    rng = np.random.default_rng(rows + k)
+    vocab = 40000
+    lowest = torch.finfo(DTYPES[dtype]).min
+    other = -6e4 if dtype == "fp16" else -1e31
+    x = logits(rng, 6, vocab, dtype)
+    x[0, :20000] = lowest
+    x[1, :-1] = lowest
+    x[2, :20000], x[2, 20000:39990] = other, -float("inf")
+    x[3, :10000], x[3, 10000:30000] = -float("inf"), lowest
+    x[4, ::2] = other
+    x[5, 1:] = torch.linspace(lowest, other, vocab - 1, dtype=torch.float64).to(x.dtype)
+    tokens = dev(np.array([30000, vocab - 1, 39995, 35000, 1, 0], dtype=np.int32))
+    if rows == 1:
+        for r in range(6):
+            idx = check_forward(ds, x[r:r + 1], tokens[r:r + 1], k, scale)[3]
+            check_backward(ds, x[r:r + 1], tokens[r:r + 1], idx, scale, some_grads(rng, 1, k))
+        return
+    one = check_forward(ds, x, tokens, k, scale)
+    pick = torch.arange(rows, device=DEV) % 6
+    all_rows = ds.token_logprobs(x[pick], tokens[pick], k, scale=scale)
+    ref = model.forward(x.double().cpu().numpy(), tokens.cpu().numpy(), k, scale)
+    tl, tp, te = bounds(x.double().cpu().numpy(), scale)
+    for r in range(rows):
+        a = r % 6
+        assert abs(all_rows[2][r].item() - ref[2][a]) <= tl[a] + 2.0 ** -22 * abs(ref[2][a])
+        assert abs(all_rows[0][r].item() - ref[0][a]) <= tp[a] + 2.0 ** -21 * abs(ref[0][a])
+        assert abs(all_rows[1][r].item() - ref[1][a]) <= te[a] + 2.0 ** -22 * abs(ref[1][a])
+    assert torch.equal(all_rows[3], one[3][pick])
