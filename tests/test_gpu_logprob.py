@@ -453,3 +453,39 @@ def test_rows_that_start_masked(ds, dtype, rows, scale, k):
         assert abs(all_rows[0][r].item() - ref[0][a]) <= tp[a] + 2.0 ** -21 * abs(ref[0][a])
         assert abs(all_rows[1][r].item() - ref[1][a]) <= te[a] + 2.0 ** -22 * abs(ref[1][a])
     assert torch.equal(all_rows[3], one[3][pick])
+
+
+@pytest.mark.parametrize("size", [2.0 ** 21, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24, 1e9, 1e10, 1e15, 1e20, 1e28, 1e35])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rows_so_far_from_zero_that_products_round(ds, size, sign):
+    """Neighbouring numbers around a maximum whose product with the scale is known to some units,
+    or to 2^100, only: differences are taken first."""
+    rng = np.random.default_rng(13)
+    lift = np.float32(sign * size)
+    steps = rng.integers(0, 3, (3, 2000)).astype(np.float32) * np.spacing(np.abs(lift))
+    steps[2] *= 1000
+    x = dev(lift + steps)
+    tokens = some_tokens(rng, 3, 2000)
+    idx = check_forward(ds, x, tokens, 4)[3]
+    check_backward(ds, x, tokens, idx, 1.0, some_grads(rng, 3, 4))
+    check_forward(ds, x.to(torch.bfloat16), tokens, 4)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 6])
+@pytest.mark.parametrize("mask", [-1e7, -1e9, -1e10, -1e15, -1e20, -1e28])
+def test_masks_of_any_size(ds, dtype, rows, mask):
+    """A large negative number in all of a slice's first logits, or in all logits, or a mixture."""
+    rng = np.random.default_rng(14)
+    vocab = 40000
+    x = logits(rng, 6, vocab, dtype)
+    x[0, :20000] = mask
+    x[1, :-1] = mask
+    x[2] = mask
+    x[3, 1::2] = mask
+    x[4, :20000], x[4, 20000:30000], x[4, 30000:] = mask, -float("inf"), mask / 2
+    x[5, :30000], x[5, 30000:] = mask, -mask
+    tokens = dev(np.array([30000, vocab - 1, 7, 0, 39995, 35000], dtype=np.int32))
+    for r in range(0, 6, rows):
+        idx = check_forward(ds, x[r:r + rows], tokens[r:r + rows], 3)[3]
+        check_backward(ds, x[r:r + rows], tokens[r:r + rows], idx, 1.0, some_grads(rng, rows, 3))

@@ -5,12 +5,13 @@
 //   S = sum 2^d,  T = sum 2^d d,  d = x c - m c,  c = scale log2 e
 // give lse = scale m + ln S and entropy = ln 2 (log2 S - T / S), whose two terms
 // are both >= 0, so that nothing cancels.  m c is rounded once, which shifts all d
-// alike: that drops out of the entropy and is taken back in lse.  Logits of -inf are
+// alike: that drops out of the entropy and is taken back in lse, as long as m c is below
+// 2^22 and 2^d near 1 for the maximum itself.  Logits of -inf are
 // lifted to a lowest finite one, whose 2^d is 0, so that 2^d d is 0 and not NaN.  For
 // that no maximum is taken from logits as low as that, masks of the type's lowest value
 // for one: until another comes sums are relative to 0, which such logits add nothing to.
-// Where the maximum is too near to the lowest, or so large that x c overflows, the row
-// is summed again with the difference taken first.
+// Where the maximum is too near to the lowest, or too large, the row is summed again
+// with the difference taken first.
 //
 // The alternatives come out of the same pass: the first vectors of a CTA's slice
 // give a value that at least k of its logits reach; where a later vector's largest
@@ -389,12 +390,16 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-// What the fast sums take a maximum from is above this.  Logits of -inf, and lower ones,
-// are lifted to -65504 with fp16 and -1e30 otherwise, at or below it.
+// Products of a maximum and c that are rounded by 2^-3 at most.
+constexpr float kFar = 4194304.f;
+
+// What the fast sums take a maximum from is above this: above what logits of -inf, and
+// lower ones, are lifted to (-65504 with fp16 and -1e30 otherwise), and not so far below 0
+// that the rounding of m c would show in 2^d.
 template <typename T>
-__device__ __forceinline__ float floor_of()
+__device__ __forceinline__ float floor_of(float c)
 {
-    return std::is_same<T, __half>::value ? -65504.f : -1e29f;
+    return fmaxf(std::is_same<T, __half>::value ? -65504.f : -1e29f, -kFar / c);
 }
 
 // Pairs of floats, in 64-bit registers so that what does not change is paired once.
@@ -610,7 +615,7 @@ logprob_kernel(const __grid_constant__ Args p)
         bound = value_of(key == 0x80000000u ? key - 2 : key - 1);     // 0 has no other sign below it
     }
 
-    const float floor = floor_of<T>();
+    const float floor = floor_of<T>(c);
     Sums a = {mine > floor ? mine : -INFINITY, 0.f, 0.f, 0.f, 0.f};
     Two sums = 0, weighted = 0;
     Two mc2 = pair(-scaled(a.most, c), -scaled(a.most, c));
@@ -674,7 +679,7 @@ logprob_kernel(const __grid_constant__ Args p)
         join_fast(a, sh.sums[w], c);
     // Sums of what the fast form cannot tell from a logit of -inf, or overflows on, are
     // made again; and all sums are relative to the maximum itself from here on.
-    const bool fine = (a.most - floor) * c >= 150.f && a.most < 1e29f && c <= 1e8f;
+    const bool fine = (a.most - floor) * c >= 150.f && a.most * c < kFar && a.most < 1e29f && c <= 1e8f;
     if (fine) {
         const float mc = scaled(a.most, c), off = fmaf(a.most, c, -mc), f = exp2f(-off);
         a.t0 = f * fmaf(-off, a.s0, a.t0), a.t1 = f * fmaf(-off, a.s1, a.t1);
