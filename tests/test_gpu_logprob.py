@@ -489,3 +489,32 @@ def test_masks_of_any_size(ds, dtype, rows, mask):
     for r in range(0, 6, rows):
         idx = check_forward(ds, x[r:r + rows], tokens[r:r + rows], 3)[3]
         check_backward(ds, x[r:r + rows], tokens[r:r + rows], idx, 1.0, some_grads(rng, rows, 3))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 310])
+def test_alternatives_found_one_by_one(ds, dtype, rows):
+    """Ever larger logits in the places of 31 threads and none elsewhere: the 32nd of any threads'
+    largest is 0, which thousands reach, so that each alternative is swept for.  Beside it the
+    same with a NaN at token 0, which comes first, and in a place of the middle."""
+    rng = np.random.default_rng(16)
+    vocab, each = 102400, 4 if dtype == "fp32" else 8
+    base = torch.zeros((vocab // (256 * each), 256, each), device=DEV)
+    n = len(base)
+    base[:, :31] = 1 + torch.arange(n, device=DEV)[:, None, None] + torch.from_numpy(
+        rng.random((n, 31, each), dtype=np.float32)).to(DEV)
+    kinds = torch.stack([base.reshape(-1)] * 4).to(DTYPES[dtype])
+    kinds[1, 0] = float("nan")
+    kinds[2, 50001] = float("nan")
+    kinds[3, 0] = kinds[3, 1] = kinds[3, vocab - 1] = float("nan")
+    want = [model.order(x.double().cpu().numpy())[:32] for x in kinds]
+    for k in (1, 31, 32):
+        if rows == 1:
+            for kind, ref in zip(kinds, want):
+                got = ds.token_logprobs(kind[None], some_tokens(rng, 1, vocab), k)[3].cpu().numpy()
+                assert got[0].tolist() == ref[:k].tolist()
+            continue
+        got = ds.token_logprobs(kinds[torch.arange(rows, device=DEV) % 4], some_tokens(rng, rows, vocab), k)
+        got = got[3].cpu().numpy()
+        for r in range(rows):
+            assert got[r].tolist() == want[r % 4][:k].tolist()

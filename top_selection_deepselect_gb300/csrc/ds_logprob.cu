@@ -56,7 +56,8 @@ constexpr float kLow = -200.f;     // 2^d is 0 in 32 bits below -150
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 
-typedef unsigned long long Entry;  // key of the value, then ~index: larger comes first
+// Key of the value, then 2^31 - 1 - index: larger comes first.  None is ~0, and 0 is none.
+typedef unsigned long long Entry;
 
 template <typename T>
 struct alignas(16) Vec {
@@ -290,7 +291,7 @@ struct Shared {
 template <typename T>
 __device__ __forceinline__ Entry entry_of(const Row<T> &row, T x, unsigned j, int e)
 {
-    return (Entry)key_of(to_float(x)) << 32 | ~(j * Vec<T>::kCount + e - row.skip);
+    return (Entry)key_of(to_float(x)) << 32 | (0x7fffffffu - (j * Vec<T>::kCount + e - row.skip));
 }
 
 __device__ __forceinline__ void keep(Shared &sh, Entry x)
@@ -325,7 +326,7 @@ __device__ __noinline__ Entry select_slowly(const Row<T> &row, unsigned lo, unsi
     };
     __syncthreads();
     static_assert(kThreads <= kCapacity, "an entry of each thread");
-    sh.entries[threadIdx.x] = largest_below(~0ULL);    // no entry is ~0: indices are below 2^31
+    sh.entries[threadIdx.x] = largest_below(~0ULL);
     __syncthreads();
     Entry mine = select_entries(sh.entries, kThreads, sh.lists);
     __syncthreads();
@@ -739,7 +740,7 @@ logprob_kernel(const __grid_constant__ Args p)
     }
     if (lane < p.k) {
         const long long at = (long long)r * p.k + lane;
-        p.idx[at] = (int)~(unsigned)best;
+        p.idx[at] = (int)(0x7fffffffu - (unsigned)best);
         p.top[at] = log_prob(value_of((unsigned)(best >> 32)));
     }
 }
