@@ -518,3 +518,15 @@ def test_alternatives_found_one_by_one(ds, dtype, rows):
         got = got[3].cpu().numpy()
         for r in range(rows):
             assert got[r].tolist() == want[r % 4][:k].tolist()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 1e9, 1e30, 2.5e38, 3.4e38])
+def test_scales_at_the_ends_of_their_range(ds, scale):
+    """Logits so that their products with the scale are some units, or nothing."""
+    rng = np.random.default_rng(17)
+    size = 1.0 if scale < 1 else 3.0 / scale
+    x = dev((rng.standard_normal((3, 3001)) * size).astype(np.float32))
+    x[1, 5:900] = -float("inf")
+    tokens = some_tokens(rng, 3, 3001)
+    idx = check_forward(ds, x, tokens, 3, scale)[3]
+    check_backward(ds, x, tokens, idx, scale, [g * 0.1 for g in some_grads(rng, 3, 3)])

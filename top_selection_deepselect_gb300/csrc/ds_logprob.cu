@@ -162,40 +162,35 @@ struct Sums {
     float s0, s1, t0, t1;
 };
 
+// A difference of logits in powers of 2.  scale log2 e may be beyond 32 bits where
+// this is not.
+__device__ __forceinline__ float exponent(float d, float scale) { return max_nan(d * scale * kLog2e, kLow); }
+
 // Brings sums to another maximum at or above theirs.
-__device__ __forceinline__ void rescale(Sums &a, float most, float c)
+__device__ __forceinline__ void rescale(Sums &a, float most, float scale)
 {
     if (a.most == -INFINITY) {    // then the sums are 0, or a NaN's
         a.most = most;
         return;
     }
-    const float d = max_nan((a.most - most) * c, kLow), f = exp2_fast(d);
+    const float d = exponent(a.most - most, scale), f = exp2_fast(d);
     a.t0 = f * fmaf(d, a.s0, a.t0), a.t1 = f * fmaf(d, a.s1, a.t1);
     a.s0 *= f, a.s1 *= f;
     a.most = most;
 }
 
-__device__ __forceinline__ void add_sums(Sums &a, Sums b, float c)
+__device__ __forceinline__ void add_sums(Sums &a, Sums b, float scale)
 {
     const float most = fmaxf(a.most, b.most);
-    rescale(a, most, c);
-    rescale(b, most, c);
+    rescale(a, most, scale);
+    rescale(b, most, scale);
     a.s0 += b.s0, a.s1 += b.s1, a.t0 += b.t0, a.t1 += b.t1;
 }
 
 // Adds two elements, relative to base (a.most, or 0 while that is -inf).
-__device__ __forceinline__ void add_pair(Sums &a, float x0, float x1, float base, float c)
+__device__ __forceinline__ void add_pair(Sums &a, float x0, float x1, float base, float scale)
 {
-    float d0, d1;
-    asm("{\n\t.reg .b64 x, m, f;\n\t"
-        "mov.b64 x, {%2, %3};\n\t"
-        "mov.b64 m, {%4, %4};\n\t"
-        "mov.b64 f, {%5, %5};\n\t"
-        "sub.rn.f32x2 x, x, m;\n\t"
-        "mul.rn.f32x2 x, x, f;\n\t"
-        "mov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(base), "f"(c));
-    d0 = max_nan(d0, kLow), d1 = max_nan(d1, kLow);
+    const float d0 = exponent(x0 - base, scale), d1 = exponent(x1 - base, scale);
     const float e0 = exp2_fast(d0), e1 = exp2_fast(d1);
     asm("{\n\t.reg .b64 s, t, e, d;\n\t"
         "mov.b64 s, {%0, %1};\n\t"
@@ -210,12 +205,12 @@ __device__ __forceinline__ void add_pair(Sums &a, float x0, float x1, float base
 }
 
 template <typename T>
-__device__ __forceinline__ void add_vector(Sums &a, const Vec<T> &v, float c)
+__device__ __forceinline__ void add_vector(Sums &a, const Vec<T> &v, float scale)
 {
     const float base = a.most == -INFINITY ? 0.f : a.most;
 #pragma unroll
     for (int e = 0; e < Vec<T>::kCount; e += 2)
-        add_pair(a, to_float(v.x[e]), to_float(v.x[e + 1]), base, c);
+        add_pair(a, to_float(v.x[e]), to_float(v.x[e + 1]), base, scale);
 }
 
 // ---- lists of 32 entries, one a lane, largest first ----------------------------
@@ -498,7 +493,7 @@ __device__ __forceinline__ Sums shuffled(const Sums &a, int step)
 
 // Sums of vectors [lo, hi) by the CTA, differences taken first, in every thread.
 template <typename T>
-__device__ __noinline__ Sums sum_carefully(const Row<T> &row, unsigned lo, unsigned hi, float c, Sums *sums)
+__device__ __noinline__ Sums sum_carefully(const Row<T> &row, unsigned lo, unsigned hi, float scale, Sums *sums)
 {
     Sums a = {-INFINITY, 0.f, 0.f, 0.f, 0.f};
     for (unsigned j = lo + threadIdx.x; j < hi; j += kThreads) {
@@ -508,19 +503,19 @@ __device__ __noinline__ Sums sum_carefully(const Row<T> &row, unsigned lo, unsig
         for (int e = 0; e < Vec<T>::kCount; ++e)
             most = fmaxf(most, to_float(v.x[e]));
         if (most > a.most)
-            rescale(a, most, c);
-        add_vector(a, v, c);
+            rescale(a, most, scale);
+        add_vector(a, v, scale);
     }
 #pragma unroll
     for (int step = 16; step; step /= 2)
-        add_sums(a, shuffled(a, step), c);
+        add_sums(a, shuffled(a, step), scale);
     __syncthreads();
     if ((threadIdx.x & 31) == 0)
         sums[threadIdx.x / 32] = a;
     __syncthreads();
     a = sums[0];
     for (int w = 1; w < kWarps; ++w)
-        add_sums(a, sums[w], c);
+        add_sums(a, sums[w], scale);
     return a;
 }
 
@@ -686,7 +681,7 @@ logprob_kernel(const __grid_constant__ Args p)
         a.t0 = f * fmaf(-off, a.s0, a.t0), a.t1 = f * fmaf(-off, a.s1, a.t1);
         a.s0 *= f, a.s1 *= f;
     } else {
-        a = sum_carefully(row, lo, hi, c, sh.sums);
+        a = sum_carefully(row, lo, hi, p.scale, sh.sums);
     }
     Entry best = 0;
     if (p.k > 0) {
@@ -718,7 +713,7 @@ logprob_kernel(const __grid_constant__ Args p)
         if (rank == 0 && warp == 0)
             for (int other = 1; other < p.cluster; ++other) {
                 const Shared *far = cluster.map_shared_rank(&sh, other);
-                add_sums(a, far->all, c);
+                add_sums(a, far->all, p.scale);
                 if (p.k > 0)
                     best = merge_lists(best, far->top[lane]);
             }
@@ -843,7 +838,7 @@ gradient_kernel(const __grid_constant__ GradArgs p)
             own = to_float(logits[at]);
     }
     if (fabsf(f.lse) >= kLarge) {
-        const Sums a = sum_carefully(row, 0, row.vectors, f.scale * kLog2e, sums);
+        const Sums a = sum_carefully(row, 0, row.vectors, f.scale, sums);
         f.empty = a.s0 + a.s1 == 0.f;
         f.base = f.empty ? 0.f : a.most;
         f.lse = (float)(kLn2 * (double)log2f(a.s0 + a.s1));
