@@ -530,3 +530,16 @@ def test_scales_at_the_ends_of_their_range(ds, scale):
     tokens = some_tokens(rng, 3, 3001)
     idx = check_forward(ds, x, tokens, 3, scale)[3]
     check_backward(ds, x, tokens, idx, scale, [g * 0.1 for g in some_grads(rng, 3, 3)])
+
+
+@pytest.mark.parametrize("lift", [40.7, 60.1, 100.3, 300.3, 500.3, 777.7, 1000.1, -90.6, -1016.9, 1024.3])
+def test_gradient_does_not_show_how_lse_is_rounded(ds, lift):
+    """Equal logits: p is 1 / vocab = 2^-10, log p = -10 ln 2.  lse is summed again from 64 on,
+    relative to the maximum, where it is 10 ln 2 and not off by up to 2^-15 as that of 777.7 is; below,
+    half a unit of it in its last place is 2^-19.  Besides, log2 may be off by a unit in the 10, which
+    is 0.7 2^-20, and rounding log p, expf and the product by 2^-22 each: together below 2^-18."""
+    x = torch.full((2, 1024), lift, device=DEV)
+    tokens = dev(np.array([-1, -1], dtype=np.int32))
+    _, h, lse, _, _ = ds.token_logprobs(x, tokens)
+    got = ds.token_logprobs_backward(x, tokens, lse, h, grad_lse=torch.ones(2, device=DEV))
+    assert (got.double() * 1024 - 1).abs().max().item() <= 2.0 ** -18
