@@ -71,3 +71,19 @@ def test_a_stream_of_another_device_is_refused(device, name, current):
     with pytest.raises(ValueError):
         calls()[name](stream=Stream(0))
     assert not device.calls
+
+
+def test_a_tangent_is_refused(device, monkeypatch):
+    """There is no forward-mode derivative, and a result without one would say that it is 0."""
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(_kv4, "_cuda", lambda name, x: MINE)
+    device.now = MINE
+    tokens = On(torch.zeros(3, dtype=torch.int32))
+    with forward_ad.dual_level():
+        for primal in (torch.zeros((3, 50)), torch.zeros((3, 50), requires_grad=True)):
+            x = forward_ad.make_dual(primal, torch.ones((3, 50)))
+            with pytest.raises(NotImplementedError):
+                ds.token_logprobs(x, tokens, 2)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                ds.token_logprobs(x, tokens, 2)
+    assert not device.calls

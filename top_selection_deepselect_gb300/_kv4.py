@@ -173,6 +173,7 @@ class _Torch:
         self.on_stream = torch.cuda.stream
         self.current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.on_device = torch.cuda.device
+        self.unpack_dual = torch.autograd.forward_ad.unpack_dual
         lib = _lib()
 
         def bytes_for(name, at):

@@ -86,13 +86,16 @@ def token_logprobs(logits, tokens, k=0, scale=1.0, logprob=None, entropy=None, l
     ascending) and their log probabilities.
 
     Where logits requires a gradient, logprob, entropy, lse and top have one
-    (outputs are then allocated, not given).
+    (outputs are then allocated, not given).  There is no forward-mode derivative:
+    logits that carry a tangent are refused.
     """
     t = _t if _t.ready else _t.find()
     index = _kv4._cuda("logits", logits)
     if stream is not None or index != t.current():
         return _kv4._elsewhere(t, index, stream, token_logprobs,
                                logits, tokens, k, scale, logprob, entropy, lse, idx, top)
+    if t.unpack_dual(logits).tangent is not None:
+        raise NotImplementedError("token_logprobs has no forward-mode derivative")
     if logits.requires_grad and t.torch.is_grad_enabled():
         if any(x is not None for x in (logprob, entropy, lse, idx, top)):
             raise ValueError("outputs cannot be given where logits requires a gradient")
