@@ -378,3 +378,34 @@ def test_refusals(ds):
         call(q.float(), pool, table, lengths, starts)
     with pytest.raises(ds.DSError):
         call(torch.cat((q, q), 1)[:, :3], pool.repeat(1, 2, 1, 1), table, lengths, starts)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new,before", [([3, 70, 1], [0, 40, 0]), ([5, 2], [6001, 130])])
+def test_infinite_queries_whose_scores_have_one_sign(ds, dim, dtype, new, before):
+    """Every key's channel is 7 (1 + 2^-10), or -8 times that, whose parts both have its sign: an
+    infinite channel of a query makes all scores -inf, of one token or of thousands and over
+    several CTAs, and no NaN comes up by itself.  Rows that see a token are NaN, others are not."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, new, before, 4, 2, dim, 16)
+    n = dim // 32
+    pool[:, 0, :, :dim // 2], pool[:, 1, :, :dim // 2] = 0xff, 0x00
+    pool[..., dim:dim + 2 * n] = np.full(n, 0x3c01, dtype=np.uint16).view(np.uint8)
+    q[0, 0, 3], q[1, 1, dim - 1], q[-1, 2, 5] = -np.inf, -np.inf, np.inf
+    q[2, 0, 7], q[2, 3, 1] = np.inf, -np.inf
+    out, lse = check(ds, q, dtype, pool, table, lengths, starts)
+    assert torch.isnan(out[0, 0].float()).all() and torch.isnan(lse[-1, 2])
+    # the tokens that such a row sees are not there: it sees nothing
+    table = table.copy()
+    table[:, 0] = -1
+    if before[0] == 0:
+        out, lse = check(ds, q, dtype, pool, table, lengths, starts)
+        assert (out[:3] == 0).all() and (lse[:3] == -float("inf")).all()
+    else:
+        table[0, :] = len(pool)
+        out, lse = check(ds, q, dtype, pool, table, lengths, starts)
+        assert (out[:5] == 0).all() and (lse[:5] == -float("inf")).all()
+        table[0, 200] = 0               # one page of all
+        out, lse = check(ds, q, dtype, pool, table, lengths, starts)
+        assert torch.isnan(out[0, 0].float()).all() and torch.isnan(lse[1, 1])

@@ -634,6 +634,20 @@ struct RowAt {
     }
 };
 
+// First position of a part's that is there, or one beyond all.  A warp's.
+static __device__ __noinline__ int first_there(const Args &p, const Part &u)
+{
+    const int from = u.t0 * kTokens, to = min(u.t1 * kTokens, u.see_hi), last = p.c.by_page(to - 1);
+    const int32_t *row = p.c.table + u.b.seq * p.c.table_stride;
+    for (int page = p.c.by_page(from); page <= last; page += 32) {
+        const int mine = page + (int)(threadIdx.x & 31);
+        const unsigned there = __ballot_sync(~0u, mine <= last && (unsigned)row[mine] < (unsigned)p.c.n_pages);
+        if (there)
+            return max(from, (page + __ffs(there) - 1) * p.c.page_size);
+    }
+    return 0x7fffffff;
+}
+
 // Values are multiplied by a power of two, their lift, that brings the largest scale of a
 // part's first tile to [1/2, 1) (or as far as 2^15 does), and a later tile's that comes
 // out at kHigh or more, so that fp16 holds what any scales make: eleven bits of those
@@ -1285,6 +1299,14 @@ chunk_kernel(const __grid_constant__ Args p)
                 fence_after();
                 __syncwarp();
             }
+            // No weight at all: nothing was seen, or all scores were -inf, as an infinite
+            // query's may be, which gives NaN.  For the join that is a sum of -0.
+            const bool none = l == 0.f && limit > u.t0 * kTokens;
+            if (__any_sync(~0u, none)) {
+                const int first = first_there(p, u);
+                if (none && limit > first)
+                    l = whole ? __uint_as_float(0x7fffffffu) : -0.f;
+            }
             m -= kRaise;
             const float down = __uint_as_float((unsigned)(127 - lift) << 23);
             float inv = l == 0.f ? 0.f : down / l;
@@ -1366,6 +1388,7 @@ join_chunk_kernel(const __grid_constant__ Args p)
         m = fmaxf(m, part_at(i)[D * S::kRows + r]);
     const float low = m == -INFINITY ? 0.f : m;
     float l = 0.f, x[kMine];
+    bool seen = false;             // something that had no weight
 #pragma unroll
     for (int k = 0; k < kMine; ++k)
         x[k] = 0.f;
@@ -1378,6 +1401,7 @@ join_chunk_kernel(const __grid_constant__ Args p)
             v[k] = q[(warp * kMine + k) * S::kRows + r];
         const float w = exp2_fast(pm - low);
         l += pl * w;
+        seen = seen || __float_as_uint(pl) == 0x80000000u;
 #pragma unroll
         for (int k = 0; k < kMine; ++k)
             x[k] = fmaf(v[k], w, x[k]);
@@ -1390,6 +1414,8 @@ join_chunk_kernel(const __grid_constant__ Args p)
     u.rows = span.rows;
     const RowAt row(p, u, r);
     const long long to = (long long)row.token * p.a.heads + row.head;
+    if (l == 0.f && seen)
+        l = __uint_as_float(0x7fffffffu);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint32_t y[kMine / 2];
 #pragma unroll
