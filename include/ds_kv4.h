@@ -151,9 +151,10 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
  *   lse       device float[tokens][heads], or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_chunk_attention_workspace bytes
  * max_pages * page_size is below 2^31 - 128.  A query that sees no token gives
- * out = 0 and lse = -inf.  Scores are sums in 32 bits of exact products; with
- * DS_FP16, a key's channel is exact to 2^-25 at least, and one whose scale is beyond
- * 9352 (channels beyond fp16) is taken with that.  A probability is rounded to 11
+ * out = 0 and lse = -inf.  Scores are sums in 32 bits of exact products, but for
+ * channels beyond 16 bits: with DS_FP16, those of a token that has a key scale of 4096
+ * or more are exact to 2^-18, and with DS_BF16 those of key scales from 64672 on to
+ * 2^-13 of the channel.  A probability is rounded to 11
  * significant bits (below 2^-21 of the row's largest it is within 2^-32 of that), with
  * DS_FP16 to 22, and a value to 11 (below 2^-13 of the largest scale of its head, within 2^-24 of that);
  * maxima, sums and outputs are held in 32 bits.  A row with a NaN or an infinity

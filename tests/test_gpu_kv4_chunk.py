@@ -409,3 +409,44 @@ def test_infinite_queries_whose_scores_have_one_sign(ds, dim, dtype, new, before
         table[0, 200] = 0               # one page of all
         out, lse = check(ds, q, dtype, pool, table, lengths, starts)
         assert torch.isnan(out[0, 0].float()).all() and torch.isnan(lse[1, 1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("most", [65504.0, 9000.0])
+def test_keys_beyond_16_bits(ds, dim, dtype, most):
+    """Key scales of either sign up to fp16's largest, with any codes: channels up to 2^19.  Most of
+    them, one in thirty, and one group of one token.  (With bf16 queries scales are exact up to
+    64640.)"""
+    rng = np.random.default_rng(dim)
+    most = min(most, 64640.0) if dtype == "bf16" else most
+    q, pool, table, lengths, starts = chunk(rng, [80, 130, 9], [70, 0, 300], 2, 1, dim, 16)
+    n = dim // 32
+    pool[..., :dim // 2] = rng.integers(0, 256, (*pool.shape[:-1], dim // 2), dtype=np.uint8)
+    plain = pool.copy()
+    for some in (0.7, 1 / 30):
+        scales = (rng.standard_normal((*pool.shape[:-1], n)) * 0.2).astype(np.float16)
+        large = rng.random(scales.shape) < some
+        scales[large] = rng.choice([-1.0, 1.0], large.sum()) * np.exp2(rng.uniform(11, np.log2(most), large.sum()))
+        scales[0, 0, :8, 0], scales[1, 0, :8, n - 1] = most, -most
+        pool[..., dim:dim + 2 * n] = scales.view(np.uint8)
+        for scale in (1e-6, 1e-4):
+            check(ds, q, dtype, pool, table, lengths, starts, scale=scale)
+    pool = plain
+    pool[table[2, 18], 0, 3, dim:dim + 2] = np.array([most], dtype=np.float16).view(np.uint8)
+    check(ds, q, dtype, pool, table, lengths, starts, scale=1e-5)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("bits", [0x7c00, 0xfc00, 0x7fff, 0xffff, 0x7e00])
+def test_key_scales_that_are_no_numbers(ds, dim, dtype, bits):
+    """An infinite scale is as good as a NaN: rows that see it are NaN, rows before it are not."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, [90], [30], 2, 1, dim, 16)
+    clean = check(ds, q, dtype, pool, table, lengths, starts)
+    at = dim + 2 * (dim // 32 - 1)
+    pool[table[0, 4], 0, 6, at:at + 2] = np.array([bits], dtype=np.uint16).view(np.uint8)      # token 70
+    out, lse = ds.kv4_chunk_attention(dev(q).to(DTYPES[dtype]), dev(pool), dev(table), dev(lengths), dev(starts))
+    assert torch.isnan(out[40:].float()).all() and torch.isnan(lse[40:]).all()
+    assert torch.equal(out[:40], clean[0][:40]) and torch.equal(lse[:40], clean[1][:40])

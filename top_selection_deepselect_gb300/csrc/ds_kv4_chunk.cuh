@@ -341,23 +341,15 @@ struct Pair<__half> {
         asm("mul.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
         return y;
     }
-    // Scales whose values are beyond fp16 are taken as the largest one whose
-    // values are not: 9352 (NaN stays).
-    static __device__ __forceinline__ uint32_t bounded(uint32_t s)
-    {
-        uint32_t y;
-        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0x70917091u));
-        return y;
-    }
     // A key's scale s = hi + lo, eight significant bits and three: times a code of up
-    // to three bits both are exact.
+    // to three bits both are exact, and within fp16 for s below kLarge.  An infinity's lo
+    // is NaN.
     struct Key {
         uint32_t hi, lo;
     };
     static __device__ __forceinline__ Key key(uint32_t s)
     {
         Key k;
-        s = bounded(s);
         k.hi = (s + 0x00040004u) & 0xfff8fff8u;
         asm("sub.f16x2 %0, %1, %2;" : "=r"(k.lo) : "r"(s), "r"(k.hi));
         return k;
@@ -392,7 +384,8 @@ struct Pair<__nv_bfloat16> {
     }
     // A key's scale s = hi + lo, five significant bits each (the second with a sign):
     // times a code of up to three bits both are exact, and so is either times 24.
-    // (Scales from 65024 on, the last 15 of fp16, have six in lo.)  NaN is in lo.
+    // (From 64544 on lo may have six, and 14 scales from 64672 on have codes whose
+    // channels are rounded, by 2^-13 at most.)  NaN, of an infinity too, is in lo.
     struct Key {
         uint32_t hi, lo, hi24, lo24;        // and both times -24
     };
@@ -448,6 +441,32 @@ __device__ __forceinline__ void weights_of(uint32_t (&w)[16], uint32_t (&rest)[F
             rest[i % (Fine ? 16 : 1)] = Pair<__half>::pack(d, e);
         }
     }
+}
+
+// With fp16 queries all keys of a token that has a scale of kLarge or more (bits of an
+// fp16: 4096) are taken 2^-4 times, and its scores 2^4 times: they are within fp16 then,
+// and exact but for scales below 2^-10, which are rounded by 2^-21.  A key's scale is one
+// of its group and place in the warp's work; lanes of a token are eight apart.  (1024
+// tokens after 7168: heads of 64 301 us and 293 without, of 128 376 and 390, of 256 470
+// and 460.  With a word of its own for the tokens it was 316, 392 and 469.)
+constexpr unsigned kLarge = 0x6c00;
+template <int Groups>
+__device__ __forceinline__ unsigned lowered(const unsigned short *scales, int group, int token, unsigned long long &plain)
+{
+    unsigned scale = scales[group], most = scale & 0x7fffu;
+    if (Groups > 4)                        // half of a token's groups are another warp's
+        most = max(most, scales[group ^ 4] & 0x7fffu);
+    if (__any_sync(~0u, most >= kLarge)) {
+#pragma unroll
+        for (int step = 8; step < 8 * Groups && step < 32; step *= 2)
+            most = max(most, __shfl_xor_sync(~0u, most, step));
+        if (most >= kLarge) {
+            scale = __half_as_ushort(__hmul(__ushort_as_half((unsigned short)scale), __ushort_as_half(0x2c00)));
+            if (group == 0)
+                atomicAnd(reinterpret_cast<unsigned *>(&plain) + token / 32, ~(1u << token % 32));
+        }
+    }
+    return scale;
 }
 
 // ---- the line of work -----------------------------------------------------------------
@@ -613,7 +632,9 @@ constexpr int kSlots = 16;     // of what is known of a tile or a unit: more tha
 struct Control {
     unsigned long long raw_full[4], raw_empty[4], key_full[4], key_empty[4], value_full[4], value_empty[4];
     unsigned long long query[2], score[2], weight[2], output[2], last;
-    unsigned long long there[kSlots];      // tokens of a tile that are there
+    struct alignas(16) {
+        unsigned long long there, plain;   // tokens of a tile that are there, and whose keys are as they are
+    } tokens[kSlots];
     int lift[kSlots];                      // of a tile's values, a power of two
     int bad[kSlots][8];                    // of a unit: first position whose value scale is no number, a group
     uint32_t tensor;
@@ -779,7 +800,8 @@ chunk_kernel(const __grid_constant__ Args p)
                 const unsigned hi = __reduce_or_sync(~0u, (unsigned)(there >> 32));
                 const uint32_t bar = shared_at(&ctl.raw_full[raw.stage]);
                 if (lane == 0) {
-                    ctl.there[count % kSlots] = (unsigned long long)hi << 32 | lo;
+                    const unsigned long long all = (unsigned long long)hi << 32 | lo;
+                    ctl.tokens[count % kSlots] = {all, all};
                     if (!stop)
                         bar_expect(bar, copies * p.run * S::kRecord);
                 }
@@ -949,7 +971,7 @@ chunk_kernel(const __grid_constant__ Args p)
                 bar_wait(shared_at(&ctl.value_empty[value.stage]), value.phase ^ 1, lost);
                 const unsigned char *src = smem + S::kOffRaw + raw.stage * S::kRawBytes;
                 unsigned char *dst = smem + S::kOffValues + value.stage * S::kValueBytes;
-                const unsigned long long there = ctl.there[count % kSlots];
+                const unsigned long long there = ctl.tokens[count % kSlots].there;
                 const bool masked = there != ~0ULL || (t + 1) * kTokens > see_lo;
                 // a lane's work: eight tokens of one word, which is four channels of two
                 // neighbouring groups
@@ -1060,6 +1082,7 @@ chunk_kernel(const __grid_constant__ Args p)
         // ---- keys: a row for each token ----------------------------------------------------
         Turn<S::kRawStages> raw;
         Turn<S::kKeyStages> key;
+        int count = 0;
         const int turn = ((warp - S::kExpandWarp) / 4 * 2 + warp % 4) * 32 + lane;
         while (next()) {
             const int t1 = u.t1;
@@ -1079,7 +1102,9 @@ chunk_kernel(const __grid_constant__ Args p)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         w[k] = words[k * kPer];
-                    const unsigned scale = reinterpret_cast<const unsigned short *>(rec + D)[group];
+                    const unsigned short *scales = reinterpret_cast<const unsigned short *>(rec + D);
+                    const unsigned scale =
+                        kFine ? lowered<kGroups>(scales, group, token, ctl.tokens[count % kSlots].plain) : scales[group];
                     const typename Pair<T>::Key key_scale = Pair<T>::key(scale * 0x10001u);
                     const int piece = stretch * 16 + 4 * g;               // of eight channels, the first
                     unsigned char *row = dst + piece / 8 * (kTokens * 128) + token * 128;
@@ -1101,6 +1126,7 @@ chunk_kernel(const __grid_constant__ Args p)
                     bar_arrive(shared_at(&ctl.raw_empty[raw.stage]));
                     bar_arrive(shared_at(&ctl.key_full[key.stage]));
                 }
+                ++count;
                 raw.step();
                 key.step();
             }
@@ -1198,21 +1224,33 @@ chunk_kernel(const __grid_constant__ Args p)
                     value.step();
                     lift_now = ctl.lift[count % kSlots];
                 }
-                const unsigned *known = reinterpret_cast<const unsigned *>(&ctl.there[count % kSlots]) + half;
+                // With fp16 queries keys are looked at, too, which are expanded when the scores
+                // are there.
+                constexpr bool kEarly = !kLate && !kFine;
+                const unsigned *known = reinterpret_cast<const unsigned *>(&ctl.tokens[count % kSlots]) + half;
                 unsigned there = 0;
-                if (!kLate)
+                if (kEarly)
                     there = *known;
                 ++count;
                 bar_wait(shared_at(&ctl.score[spin]), score_phase[spin], lost);
                 score_phase[spin] ^= 1;
                 fence_after();
                 __syncwarp();
-                if (kLate)
-                    there = *known;
+                if (!kEarly)
+                    there = known[kFine ? 2 : 0];
                 uint32_t s[32];
                 load_columns(s, at + half * 32);
                 wait_loads();
                 if (there != ~0u || (t + 1) * kTokens > see_lo) {
+                    if constexpr (kFine) {
+                        const unsigned plain = there;
+                        there = *known;
+                        if (there != plain) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                s[i] = (there & ~plain) >> i & 1 ? __float_as_uint(__uint_as_float(s[i]) * 16.f) : s[i];
+                        }
+                    }
                     const int left = limit - t * kTokens - half * 32;
                     const unsigned see = there & (left >= 32 ? ~0u : left <= 0 ? 0u : ~0u >> (32 - left));
 #pragma unroll
