@@ -146,7 +146,7 @@ int ds_kv4_attention_workspace(const ds_kv4_cache_t *cache, int batch, int queri
  *   dtype     of q and out: DS_BF16 or DS_FP16
  *   q         device, unit stride in the last dimension, q_stride = {token, head}
  *             strides in elements; 16 bytes at a time where these allow it
- *   scale     finite
+ *   scale     finite (from 2.35e38 on it is taken as that)
  *   out       device [tokens][heads][head_dim], contiguous, 16-byte aligned
  *   lse       device float[tokens][heads], or NULL
  *   workspace device, 16-byte aligned, of ds_kv4_chunk_attention_workspace bytes

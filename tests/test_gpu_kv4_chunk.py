@@ -450,3 +450,48 @@ def test_key_scales_that_are_no_numbers(ds, dim, dtype, bits):
     out, lse = ds.kv4_chunk_attention(dev(q).to(DTYPES[dtype]), dev(pool), dev(table), dev(lengths), dev(starts))
     assert torch.isnan(out[40:].float()).all() and torch.isnan(lse[40:]).all()
     assert torch.equal(out[:40], clean[0][:40]) and torch.equal(lse[:40], clean[1][:40])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [2.0 ** 8, 2.0 ** 10, 2.0 ** 12, 2.0 ** 14, 2.0 ** 18, 2.0 ** 21, -2.0 ** 23, 2.0 ** 30,
+                                   2.0 ** 90, 3e38])
+@pytest.mark.parametrize("new,before", [([40, 3], [300, 4001]), ([4, 30], [2900, 0])])
+def test_scores_far_from_zero(ds, dim, dtype, scale, new, before):
+    """Scores of up to 2^13 times scales up to the largest, whose products round to 2^100 and are
+    beyond 32 bits at last.  Queries have one channel and key scales are 1, so that scores are
+    exact: they differ by 2^10 times the scale, and a row's output is the mean of the values of
+    its largest scores' tokens.  Half of the rows' scores grow along the sequence from far below 0,
+    or fall; long sequences are many CTAs'.
+
+    Bounds: the weights of these tokens are equal, so that their mean is off by one weight's
+    rounding 2^-11, the values' 2^-11 and the sums' 2^-18; lse by 2^-21 of it."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, new, before, 4, 1, dim, 16)
+    n = dim // 32
+    q[:] = 0
+    rows = np.arange(len(q))
+    q[:, 0, 5], q[:, 1, 5], q[:, 2, dim - 2], q[:, 3, dim - 2] = 1024, -1024, 1024, -1024
+    places = model.channel_places(dim)[0]
+    codes = rng.integers(0, 16, (*pool.shape[:-1], dim))
+    for seq, (a, b) in enumerate(((5, dim - 2), (dim - 2, 5))):
+        pos = np.arange(lengths[seq])
+        for channel, rising in ((a, True), (b, False)):
+            c = pos * 15 // lengths[seq] if rising else rng.integers(0, 16, len(pos))
+            codes[table[seq, pos // 16], 0, pos % 16, places[channel]] = c
+    pool[..., :dim // 2] = codes[..., 0::2] | codes[..., 1::2] << 4
+    pool[..., dim:dim + 2 * n] = np.ones(n, dtype=np.float16).view(np.uint8)
+    qt = dev(q).to(DTYPES[dtype])
+    out, lse = ds.kv4_chunk_attention(qt, dev(pool), dev(table), dev(lengths), dev(starts), scale=scale)
+    ref, rlse, spread, _ = model.chunk_attention(qt.double().cpu().numpy(), pool, table, lengths, starts,
+                                                 float(np.float32(scale)))
+    t = (2.0 ** -10 + 2.0 ** -18) * spread + 2.0 ** -24 * 8
+    lo, hi = (torch.from_numpy(x).to(qt.dtype).double().numpy() for x in (ref - t, ref + t))
+    got = out.double().cpu().numpy()
+    assert ((lo <= got) & (got <= hi)).all()
+    with np.errstate(over="ignore"):
+        wide = rlse.astype(np.float32)
+    glse = lse.cpu().numpy()
+    f = np.isfinite(wide)
+    assert np.array_equal(glse[~f], wide[~f])
+    assert (np.abs(glse[f].astype(np.float64) - rlse[f]) <= 2.0 ** -21 * (1 + np.abs(rlse[f]))).all()

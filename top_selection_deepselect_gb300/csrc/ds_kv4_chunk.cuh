@@ -105,7 +105,7 @@ struct Shape {
     static constexpr int kUsed = kOffRaw + kRawStages * kRawBytes + 1024;
     // tensor memory is taken whole, so that a second CTA would only wait for it
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static_assert(kSmem <= 230 * 1024, "shared memory of an SM");
+    static_assert(kSmem <= 217 * 1024, "shared memory of an SM, less what is not of the stages");
     static constexpr int kPartial = kRows * (D + 2);            // floats of a partial result
 };
 
@@ -419,15 +419,19 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-// Weights of 32 scores, in fp16, and their sums.  Fine: what is left of each, in fp16
-// again.
-template <bool Fine>
+// Weights 2^((s - base) c - low) of 32 scores, in fp16, and their sums.  Fine: what is left
+// of each, in fp16 again.  Apart: base is not 0.
+template <bool Fine, bool Apart>
 __device__ __forceinline__ void weights_of(uint32_t (&w)[16], uint32_t (&rest)[Fine ? 16 : 1], const uint32_t (&s)[32],
-                                           float c, float low, Two (&sum)[2])
+                                           float base, float c, float low, Two (&sum)[2])
 {
+    sum[0] = sum[1] = Two{0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const Two x = multiply_add(s[2 * i], s[2 * i + 1], c, -low);
+        Two y = {__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])};
+        if (Apart)
+            add_to(y, -base, -base);
+        const Two x = multiply_add(__float_as_uint(y.a), __float_as_uint(y.b), c, -low);
         const float a = exp2_fast(x.a), b = exp2_fast(x.b);
         add_to(sum[i % 2], a, b);
         w[i] = Pair<__half>::pack(a, b);
@@ -687,6 +691,37 @@ __device__ __forceinline__ unsigned lift_bits(int e)      // 2^e as an fp16, e >
 // fp16, and 11 bits of those down to 2^-21 of the row's largest.
 constexpr float kRaise = 7.f;
 
+// Scores times c = |scale| log2 e are exponents of 2.  A row's weights are relative to a
+// score, its base: to its product with c, where that is known to 2^-3, and from kFar on to
+// the score itself, before the product.
+constexpr float kFar = 4194304.f;
+__device__ __forceinline__ float factor_of(const Args &p)
+{
+    // not 0, which a masked score of -inf times it would not come through, nor infinite
+    return fminf(fmaxf(fabsf(p.a.scale) * kLog2e, 1.4e-45f), 3.4028234e38f);
+}
+// A base times c, rounded: all that is relative to it has the same rounding, which an addition
+// that takes the product in would not.
+__device__ __forceinline__ float scaled(float base, float c) { return __fmul_rn(base, c); }
+__device__ __forceinline__ bool is_near(float m) { return fabsf(m) < kFar; }
+// What a weight relative to `from` has to be taken times, for one relative to `to`.  (A
+// call, as log_sum is: what is seldom run is kept out of the loops' code.)
+static __device__ __noinline__ float shift_of(float from, float to, float c)
+{
+    const float a = scaled(from, c), b = scaled(to, c);
+    const float d = is_near(a) ? (is_near(b) ? a - b : -fmaf(to, c, -a)) : (is_near(b) ? fmaf(from, c, -b) : (from - to) * c);
+    return from == -INFINITY ? 0.f : exp2_fast(d);
+}
+// Log of a row's sum l of weights.
+static __device__ __noinline__ float log_sum(const Args &p, float base, float c, float l)
+{
+    constexpr float kLn2 = 0.6931471805599453f;
+    if (l == 0.f)
+        return -INFINITY;
+    const float m = scaled(base, c);
+    return is_near(m) ? (m - kRaise + log2f(l)) * kLn2 : fmaf(base, fabsf(p.a.scale), (log2f(l) - kRaise) * kLn2);
+}
+
 // Small: each CTA lays few blocks out itself, where the planning launch would take as
 // long as the work (one short prompt 15.2 -> 9.7 us).  A kernel of its own, since the
 // code costs the loops 3 to 20 % where they run long, though it is not in them.
@@ -702,6 +737,7 @@ chunk_kernel(const __grid_constant__ Args p)
     __shared__ Control ctl;
     __shared__ Walk walks[S::kThreads / 32];
     __shared__ Few few[1];
+    __shared__ float bases[S::kTiles][2][kTileRows];      // each thread's own
     unsigned char *smem = smem_raw + (1024 - (shared_at(smem_raw) & 1023) & 1023);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
 
@@ -1150,8 +1186,7 @@ chunk_kernel(const __grid_constant__ Args p)
         };
         Turn<S::kValueStages> value;
         int count = 0, unit = 0;
-        // not 0, which a masked score of -inf times it would not come through
-        const float c = fmaxf(fabsf(p.a.scale) * kLog2e, 1.4e-45f);
+        const float c = factor_of(p);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         while (next()) {
             const int n = u.t1 - u.t0, slot = unit % kSlots;
@@ -1173,6 +1208,9 @@ chunk_kernel(const __grid_constant__ Args p)
             int spin = tile;                          // the buffer of the next scores
             const bool in = r < u.rows;
             const int limit = RowAt(p, u, r).limit;
+            // What the row's weights are relative to is seldom looked at, and kept in shared
+            // memory; m is its product with c where that is near, else -inf.
+            bases[tile][half][local] = -INFINITY;
             float m = -INFINITY, l = 0.f;
             int lift = 0;              // that the output has
             if (n > 0) {
@@ -1259,30 +1297,28 @@ chunk_kernel(const __grid_constant__ Args p)
                 }
                 // Weights are relative to a maximum that follows the true one only where
                 // that is 8 above it, which is seldom: they are worked out before the other
-                // half's maximum is known, and again where it turns out that it grows.
+                // half's maximum is known, and again where it turns out that it grows, or
+                // that the row is far from 0.
                 float most = largest_of(s);
                 ctl.swap[side][tile][half][local] = most;
                 Two sum[2];
                 uint32_t w[16], rest[kFine ? 16 : 1];
-#pragma unroll
-                for (bool met = false;; met = true) {
-                    sum[0] = sum[1] = Two{0.f, 0.f};
-                    weights_of<kFine>(w, rest, s, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
-                    if (met)
-                        break;
-                    if (kLate) {
-                        bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
-                        value.step();
-                        lift_now = ctl.lift[(count - 1) % kSlots];
-                    }
-                    most = fmaxf(most, meet()) * c;
-                    const bool grows = most > m + 8.f || m == -INFINITY;
-                    if (!__any_sync(~0u, (grows && most > m) || lift_now != lift))
-                        break;
-                    const float to = grows ? fmaxf(most, m) : m;
-                    float f = m == -INFINITY ? 0.f : exp2_fast(m - to);
+                weights_of<kFine, false>(w, rest, s, 0.f, c, (m == -INFINITY ? 0.f : m) - kRaise, sum);
+                if (kLate) {
+                    bar_wait(shared_at(&ctl.value_full[value.stage]), value.phase, lost);
+                    value.step();
+                    lift_now = ctl.lift[(count - 1) % kSlots];
+                }
+                most = fmaxf(most, meet());
+                const bool grows = most * c > m + 8.f || (m == -INFINITY && most > -INFINITY);
+                if (__any_sync(~0u, grows || lift_now != lift)) {
+                    const float from = bases[tile][half][local], base = (most - from) * c > 8.f ? most : from;
+                    float f = shift_of(from, base, c);
                     l *= f;
-                    m = to;
+                    bases[tile][half][local] = base;
+                    m = scaled(base, c);
+                    const bool near = is_near(m) || base == -INFINITY;
+                    m = near ? m : -INFINITY;
                     f *= __uint_as_float((unsigned)(lift_now - lift + 127) << 23);
                     lift = lift_now;
                     if (t > t0) {
@@ -1300,6 +1336,8 @@ chunk_kernel(const __grid_constant__ Args p)
                             store_columns(out_at + part, x);
                         }
                     }
+                    weights_of<kFine, true>(w, rest, s, near ? 0.f : base, c, (m == -INFINITY ? 0.f : m) - kRaise,
+                                            sum);
                 }
                 store_columns(at + half * 16, w);
                 if constexpr (kFine)
@@ -1345,11 +1383,11 @@ chunk_kernel(const __grid_constant__ Args p)
                 if (none && limit > first)
                     l = whole ? __uint_as_float(0x7fffffffu) : -0.f;
             }
-            m -= kRaise;
+            float base = bases[tile][half][local];
             const float down = __uint_as_float((unsigned)(127 - lift) << 23);
             float inv = l == 0.f ? 0.f : down / l;
             if (*lost)
-                inv = l = m = __uint_as_float(0x7fffffffu);
+                inv = l = base = __uint_as_float(0x7fffffffu);
             const RowAt row(p, u, r);
             const long long to = (long long)row.token * p.a.heads + row.head;
 #pragma unroll 1
@@ -1385,10 +1423,10 @@ chunk_kernel(const __grid_constant__ Args p)
             if (half != 0) {
                 // the other half's
             } else if (!whole) {
-                partial[D * S::kRows + r] = m;
+                partial[D * S::kRows + r] = base;
                 partial[(D + 1) * S::kRows + r] = l;
             } else if (in && p.a.lse) {
-                p.a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                p.a.lse[to] = log_sum(p, base, c, l);
             }
             fence_before();
         }
@@ -1421,10 +1459,10 @@ join_chunk_kernel(const __grid_constant__ Args p)
     if (r - lane >= span.rows)
         return;
     auto part_at = [&](int i) { return p.partial + (2LL * (cta + i) + (i == 0)) * S::kPartial; };
-    float m = -INFINITY;
+    const float c = factor_of(p);
+    float base = -INFINITY;
     for (int i = 0; i < s.parts; ++i)
-        m = fmaxf(m, part_at(i)[D * S::kRows + r]);
-    const float low = m == -INFINITY ? 0.f : m;
+        base = fmaxf(base, part_at(i)[D * S::kRows + r]);
     float l = 0.f, x[kMine];
     bool seen = false;             // something that had no weight
 #pragma unroll
@@ -1432,12 +1470,12 @@ join_chunk_kernel(const __grid_constant__ Args p)
         x[k] = 0.f;
     for (int i = 0; i < s.parts; ++i) {
         const float *q = part_at(i);
-        const float pm = q[D * S::kRows + r], pl = q[(D + 1) * S::kRows + r];
+        const float from = q[D * S::kRows + r], pl = q[(D + 1) * S::kRows + r];
         float v[kMine];
 #pragma unroll
         for (int k = 0; k < kMine; ++k)
             v[k] = q[(warp * kMine + k) * S::kRows + r];
-        const float w = exp2_fast(pm - low);
+        const float w = shift_of(from, base, c);
         l += pl * w;
         seen = seen || __float_as_uint(pl) == 0x80000000u;
 #pragma unroll
@@ -1464,7 +1502,7 @@ join_chunk_kernel(const __grid_constant__ Args p)
     for (int k = 0; k < kMine / 8; ++k)
         dst[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
     if (warp == 0 && p.a.lse)
-        p.a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        p.a.lse[to] = log_sum(p, base, c, l);
 }
 
 template <int D>
