@@ -495,3 +495,36 @@ def test_scores_far_from_zero(ds, dim, dtype, scale, new, before):
     f = np.isfinite(wide)
     assert np.array_equal(glse[~f], wide[~f])
     assert (np.abs(glse[f].astype(np.float64) - rlse[f]) <= 2.0 ** -21 * (1 + np.abs(rlse[f]))).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,before", [([90], [30]), ([20], [100]), ([130], [0])])
+def test_weights_of_fp16_queries_hold_22_bits(ds, dim, new, before):
+    """Values that fp16 holds (codes times a power of two), in pairs that nearly cancel: an output
+    is a difference of weights.  What is left of its bound is 2^-22 of a weight, the sums' cut-offs
+    and the scores' (as in `check`; scores are small here).  With weights of 11 bits the 64-bit
+    model itself is outside it."""
+    rng = np.random.default_rng(dim)
+    q, pool, table, lengths, starts = chunk(rng, new, before, 2, 1, dim, 16)
+    n = dim // 32
+    pos = np.arange(lengths[0])
+    codes = np.where(pos % 2 == 0, 0xff, 0x11).astype(np.uint8)            # 15 and 1: 7 and -7
+    pool[table[0, pos // 16], 0, pos % 16, dim // 2:dim] = codes[:, None]
+    pool[..., dim + 2 * n:dim + 4 * n] = np.ones(n, dtype=np.float16).view(np.uint8)
+    qt = (dev(q) * 0.25).half()
+    scale = dim ** -0.5 * 0.125
+    out, _ = ds.kv4_chunk_attention(qt, dev(pool), dev(table), dev(lengths), dev(starts), scale=scale)
+    x = qt.double().cpu().numpy()
+    ref, _, spread, reach = model.chunk_attention(x, pool, table, lengths, starts, float(np.float32(scale)))
+    t = (2.0 ** -22 + 2 * 2.0 ** -17 * reach[..., None] + 2.0 ** -18 + lengths[0] * 2.0 ** -26) * spread
+    lo, hi = (torch.from_numpy(y).half().double().numpy() for y in (ref - t, ref + t))
+    got = out.double().cpu().numpy()
+    assert ((lo <= got) & (got <= hi)).all(), np.max(np.abs(got - ref) / t)
+    # the mistake, in the model
+    k, v = model.decode(pool[table[0, pos // 16], 0, pos % 16], dim)
+    coarse = np.zeros_like(ref)
+    for j in range(len(x)):
+        see = lengths[0] - len(x) + 1 + j
+        w = np.exp(float(np.float32(scale)) * (x[j] @ k[:see].T))
+        coarse[j] = w.astype(np.float16).astype(np.float64) @ v[:see] / w.sum(-1, keepdims=True)
+    assert not ((lo <= coarse) & (coarse <= hi)).all()
