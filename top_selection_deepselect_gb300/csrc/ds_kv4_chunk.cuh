@@ -81,7 +81,7 @@ struct Shape {
     // Stages, as many as there is room for.  Two or four for D <= 128 change nothing
     // (2.00 and 2.02 ms where three took 2.01).  For D = 256 a second stage of values took
     // 461 us in the place of a second of keys, and 488 us in the place of two of records,
-    // where one takes 409 (1024 tokens after 7168).
+    // where one takes 412 (1024 tokens after 7168).
     static constexpr int kKeyStages = D == 256 ? 2 : 3;
     static constexpr int kValueStages = D == 256 ? 1 : 3;
     static constexpr int kRawStages = 3;

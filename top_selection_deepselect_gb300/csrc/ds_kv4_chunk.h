@@ -93,14 +93,17 @@ __device__ __forceinline__ Span span_of(const Block &b, const Divider &by_group,
     s.see_lo = lo > 0 ? lo : 0;
     s.see_hi = hi > 0 ? hi : 0;
     s.tiles = s.see_hi / 64 + (s.see_hi % 64 != 0);
-    // measured on 2 x 129 tokens after 130943, of whose rows one block in five is small:
-    // 7 of 8 1.23 ms, 6 1.36, 5 1.52
+    // A rule from 2 x 129 tokens after 130943 with heads of 128, of whose rows one block in
+    // five is small: 1232 us, with 6 1290 and with 8 1274.  With heads of 64 8 is better
+    // (1108 and 1061), of 256 there is one row tile a block anyhow.
     s.weight = s.row_tiles == 2 ? 8 : 7;
     return s;
 }
 
 // Places of a unit: of its tiles, and of its start and end (queries, first copies,
-// outputs), by what they take: ragged prompts 174 us with 40, 187 with 16, 176 with 64.
+// outputs), by what they take: ragged prompts of 9 x 701 tokens at most, heads of 64, fp16
+// 176 us with 40, 196 with 16, 180 with 64; bf16 160, 176 and 154; of 128 bf16 203, 224 and
+// 186; of 256 bf16 412, 484 and 420.  One number for all, at most 9 % off the better one.
 constexpr int kUnitCost = 40;
 __device__ __forceinline__ int cost_of(const Span &s) { return kUnitCost + s.tiles * s.weight; }
 
