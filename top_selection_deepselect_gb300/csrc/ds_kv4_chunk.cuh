@@ -30,11 +30,13 @@
 // cycles of the tensor cores, a third of them for the keys' second part, and the four
 // schedulers issue some 1600 instructions each: 330 a tile of rows for weights and
 // maxima, 290 for keys, 230 for values, the rest for waits and what surrounds them.
-// 2048 tokens of 32768 (64 query heads, 8 key/value heads of 128, bf16) take 1.96 ms:
-// 1090 TFLOP/s, 1630 with the second part, which is 85 % of what a large bf16 library
+// 2048 tokens of 32768 (64 query heads, 8 key/value heads of 128, bf16) take 1.97 ms:
+// 1080 TFLOP/s, 1620 with the second part, which is 84 % of what a large bf16 library
 // product reaches in a burst; over many calls in turn the power limit brings it to
-// 2.05 ms.  Heads of 64 and 256 stay at 500 and 630 TFLOP/s, by issue: there the
-// expansion and the softmax are as large for a half of the products, or serve 128 rows.
+// 2.05 to 2.12 ms.  Heads of 64 and 256 stay at 500 and 630 TFLOP/s: there the expansion
+// and the softmax are as large for a half of the products, or serve 128 rows (1024 tokens
+// after 7168: issue slots 62 and 53 % busy, the tensor pipe 37 and 44 %, else the roles'
+// waits for each other).
 //
 // Roles of a CTA's warps: softmax (eight warps a tile of rows, half a row a thread),
 // expansion of keys and of values (four warps each, eight for D = 256), one that issues
